@@ -405,6 +405,192 @@ nf4_status nf4_dequantize_ex(const uint8_t *codes, int64_t n, const nf4_format *
                              const float *absmax_scale, const float *absmax_offset, void *out,
                              int32_t out_dtype, void *stream);
 
+/* ---- The training step around the linears ----
+ * What a QLoRA step runs besides its 4-bit linears: the optimizer over the
+ * adapters, the norms and residual additions between blocks, the token
+ * embedding. The conventions above hold, with these additions: rows may have
+ * any width, so element buffers of rows (activations, tables, gradients) are
+ * 16-byte aligned at their start only; fp32 statistics and scales are 4-byte
+ * aligned.
+ *
+ * AdamW over a list of tensors, for step t = 1, 2, ...:
+ *   g  = clip * grad,  clip = max_norm / norm where norm > max_norm > 0, else 1
+ *   m' = beta1 m + (1 - beta1) g
+ *   v' = beta2 v + (1 - beta2) g^2
+ *   w' = w (1 - lr weight_decay) - lr / (1 - beta1^t) * m' / (sqrt(v' / (1 - beta2^t)) + eps)
+ * in fp32, w' rounded once to its type; clip is fl32(max_norm * fl32(1 / norm)),
+ * and the moments are the fp32 results of exactly these operations, so that
+ * their 8-bit codes are defined to the bit. [MF] "Paged
+ * Optimizers" and [QP] train the adapters with AdamW in 8 bits; what follows
+ * is this library's own 8-bit storage.
+ *
+ * NF4_MOMENTS_8 keeps each moment as OCP FP8 E4M3FN codes and one fp32 scale
+ * per block of 256 consecutive elements of a tensor (the last block may be
+ * partial): x = decode(code) * scale. Storing x[block]:
+ *   scale = fl32(max |x| * fl32(1 / 448)), 0 where that is below 2^-126
+ *   t     = fl32(x * fl32(1 / scale)), 0 where the scale is 0, clamped to
+ *           [-448, 448], for v to [2^-9, 448]
+ *   code  = t rounded stochastically to E4M3: up in magnitude with the
+ *           probability that the dropped fraction of the step has (20 bits)
+ * A second moment therefore never falls to zero under a first moment that is
+ * still stored, and neither moment stalls where a step changes it by less than
+ * half a code. The random bits of element i of entry e of a call are
+ *   mix(u32(i) * 0x9E3779B9 + key_e),  key_e = mix(mix(e * 0x9E3779B9 + (seed >> 32)) + u32(seed)),
+ *   mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15; x *= 0xBB67AE85; x ^= x >> 16
+ * (modulo 2^32); m takes the upper 16 bits and v the lower 16, each as the top
+ * bits of the 20. The same seed gives the same codes. */
+typedef enum { NF4_MOMENTS_8 = 8, NF4_MOMENTS_32 = 32 } nf4_moments;
+
+/* One tensor of an optimizer call.
+ *   w        device in/out, n elements of the call's w_dtype (16-byte aligned)
+ *   master   device in/out, n floats, or NULL: the fp32 weight that the step
+ *            updates; w then only receives its rounding (w_dtype NF4_BF16)
+ *   grad     device, n elements of the call's grad_dtype
+ *   m, v     device in/out, n E4M3FN bytes (NF4_MOMENTS_8) or n floats; zeros
+ *            (with any scales) before the first step
+ *   m_scale, v_scale  device in/out, ceil(n / 256) floats (NF4_MOMENTS_8), else
+ *            ignored
+ *   n        elements, 0 .. 2^33 (an entry with n == 0 is skipped)
+ *   lr, weight_decay  of this tensor */
+typedef struct {
+    void *w;
+    float *master;
+    const void *grad;
+    void *m;
+    void *v;
+    float *m_scale;
+    float *v_scale;
+    int64_t n;
+    float lr;
+    float weight_decay;
+} nf4_adamw_entry;
+
+typedef struct {
+    double beta1, beta2; /* 0 <= beta < 1; beta and 1 - beta are rounded to fp32 once each */
+    float eps;           /* >= 0 */
+    float max_norm;      /* > 0 clips by grad_norm; <= 0: no clipping */
+    int64_t step;        /* t >= 1 */
+    uint64_t seed;       /* of the stochastic rounding (NF4_MOMENTS_8) */
+} nf4_adamw_config;
+
+/* Bytes of device workspace of nf4_grad_norm; (size_t)-1 for invalid arguments. */
+size_t nf4_grad_norm_workspace_size(const nf4_adamw_entry *entries, int32_t count);
+
+/* norm = sqrt(sum of grad^2 over all elements of all entries) (only grad and n
+ * of an entry are read). The squares are summed in fp64, in an order that
+ * depends on the sizes alone, and rounded once. A gradient that is not finite
+ * makes the norm NaN or infinite.
+ *   norm  device out, one float;  workspace  256-byte aligned */
+nf4_status nf4_grad_norm(const nf4_adamw_entry *entries, int32_t count, int32_t grad_dtype,
+                         float *norm, void *workspace, size_t workspace_bytes, void *stream);
+
+/* One AdamW step of every entry, up to 48 per launch (see above).
+ *   entries    host array, read during the call only
+ *   moments    an nf4_moments
+ *   grad_norm  device, one float, or NULL (no clipping; required where
+ *              max_norm > 0). Where it is not finite the step changes nothing.
+ * Every entry is validated before anything is launched. Buffers of different
+ * entries must not overlap. Gradients that are not finite are outside the
+ * contract unless grad_norm is given. The step number and the seed are
+ * arguments: a captured call replays the same step. */
+nf4_status nf4_adamw_step(const nf4_adamw_entry *entries, int32_t count, int32_t w_dtype,
+                          int32_t grad_dtype, int32_t moments, const nf4_adamw_config *config,
+                          const float *grad_norm, void *stream);
+
+/* The residual step between two blocks, one row of `dim` at a time:
+ *   z  = w_post' y rsqrt(mean y^2 + eps)     (z = y where w_post is NULL)
+ *   h' = h + alpha gate z                    (gate 1 where gate_kind is NONE)
+ *   x  = w_pre' h' rsqrt(mean h'^2 + eps)
+ * with w' = w + w_offset: the norm after a block, its gate and residual scale,
+ * and the norm before the next block in one pass. Everything is computed in
+ * fp32; x is computed from the h' before its rounding. y may be NULL: then
+ * h' = h, nothing is written to h_out and x = norm(h). */
+typedef enum { NF4_GATE_NONE = 0, NF4_GATE_CHANNEL = 1, NF4_GATE_TOKEN = 2 } nf4_gate_kind;
+
+typedef struct {
+    int64_t rows;       /* >= 0 */
+    int64_t dim;        /* 1 .. 32768 */
+    int32_t dtype;      /* of y, x, dx, dy and a token gate */
+    int32_t res_dtype;  /* of h, h', dh: dtype, or NF4_F32 with dtype NF4_BF16 */
+    int32_t w_dtype;    /* of w_pre, w_post, a channel gate and their gradients */
+    int32_t gate_kind;  /* channel: gate [dim]; token: gate [rows x dim] */
+    float eps;          /* >= 0 */
+    float alpha;
+    float w_offset;
+} nf4_residual_norm_shape;
+
+/* Forward. y, h, gate as above; h_out [rows x dim] (res_dtype) may be h itself;
+ * x_out [rows x dim] (dtype); rstd_post (with w_post) and rstd_pre: device out,
+ * `rows` floats each, for the backward pass, or NULL. */
+nf4_status nf4_residual_norm_forward(const nf4_residual_norm_shape *shape, const void *y,
+                                     const void *h, const void *w_post, const void *gate,
+                                     const void *w_pre, void *h_out, void *x_out,
+                                     float *rstd_post, float *rstd_pre, void *stream);
+
+/* Bytes of device workspace of the backward pass (fp32 partial sums of the
+ * weights' gradients, one row for each workgroup); (size_t)-1 for invalid
+ * arguments. */
+size_t nf4_residual_norm_backward_workspace_size(const nf4_residual_norm_shape *shape);
+
+/* Backward: given dx and dh_out, the gradients of x and h',
+ *   n1 = h' rstd_pre,  dh = dh_out + rstd_pre (dx w_pre' - n1 mean(dx w_pre' n1))
+ *   dz = alpha gate dh,  dgate = alpha dh z  (summed over the rows for a channel gate)
+ *   n2 = y rstd_post,  dy = rstd_post (dz w_post' - n2 mean(dz w_post' n2))  (dz without w_post)
+ *   dw_pre = sum_rows dx n1,  dw_post = sum_rows dz n2
+ * dh is the gradient of h. The sums over rows run in fp32 in an order that
+ * depends on the sizes alone.
+ *   dx, dh_out  either may be NULL (zero)
+ *   y     NULL: as in the forward; then dy, dgate, dw_post are not written
+ *   h_out the forward's h' (h where y is NULL)
+ *   dy, dh, dgate, dw_pre, dw_post  device out, each may be NULL to skip it;
+ *         dw_pre, dw_post and a channel dgate have w_dtype and `dim` elements
+ *   workspace  256-byte aligned; needed where a summed gradient is asked for
+ * With rows == 0 the summed gradients that are given are zero. */
+nf4_status nf4_residual_norm_backward(const nf4_residual_norm_shape *shape, const void *dx,
+                                      const void *dh_out, const void *y, const void *h_out,
+                                      const void *w_post, const void *gate, const void *w_pre,
+                                      const float *rstd_post, const float *rstd_pre, void *dy,
+                                      void *dh, void *dgate, void *dw_pre, void *dw_post,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Token numbers. */
+typedef enum { NF4_I32 = 0, NF4_I64 = 1 } nf4_index_dtype;
+
+/* out[t][:] = scale * table[ids[t]][:], in fp32, rounded once. A row whose id is
+ * outside 0 .. vocab - 1 is zero.
+ *   ids    device, `tokens` numbers;  table  device [vocab x dim] (dtype)
+ *   out    device out [tokens x dim] (out_dtype) */
+nf4_status nf4_embedding_forward(const void *ids, int32_t id_dtype, int64_t tokens,
+                                 const void *table, int32_t dtype, int64_t vocab, int64_t dim,
+                                 float scale, void *out, int32_t out_dtype, void *stream);
+
+/* The same from an NF4 table (n_out = vocab, k_in = dim): each element is
+ * fl32(scale * w'), w' the fp32 value that nf4_dequantize gives. */
+nf4_status nf4_embedding_forward_packed(const void *ids, int32_t id_dtype, int64_t tokens,
+                                        const nf4_weight *table, float scale, void *out,
+                                        int32_t out_dtype, void *stream);
+
+/* Bytes of device workspace of nf4_embedding_backward (the sorted tokens and
+ * the fp32 sums of runs of equal tokens that cross a chunk); (size_t)-1 for
+ * invalid sizes. */
+size_t nf4_embedding_backward_workspace_size(int64_t tokens, int64_t vocab, int64_t dim);
+
+/* Gradient of the table:
+ *   grad[v][:] = scale * sum over t with ids[t] == v of dy[t][:]   (+ grad[v][:] where accumulate != 0)
+ * The tokens are sorted by their id, equal ids in the order of the tokens, and
+ * each row's sum runs in fp32 over that order, cut at places that depend on the
+ * ids and sizes alone: the same call gives the same bits. Ids outside
+ * 0 .. vocab - 1 and padding_id (-1: none) give nothing. Without `accumulate`
+ * every row of grad is written; with it, only rows that a token names are read
+ * and written.
+ *   dy    device [tokens x dim] (dtype);  grad  device [vocab x dim] (grad_dtype)
+ *   workspace  256-byte aligned. tokens <= 2^28, vocab <= 2^28. */
+nf4_status nf4_embedding_backward(const void *ids, int32_t id_dtype, int64_t tokens,
+                                  const void *dy, int32_t dtype, int64_t vocab, int64_t dim,
+                                  float scale, int64_t padding_id, void *grad, int32_t grad_dtype,
+                                  int32_t accumulate, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
 #ifdef __cplusplus
 }
 #endif

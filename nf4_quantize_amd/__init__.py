@@ -59,6 +59,16 @@ EXPORTS = (
     "nf4_storage_bytes_ex",
     "nf4_quantize_batched",
     "nf4_dequantize_batched",
+    "nf4_grad_norm_workspace_size",
+    "nf4_grad_norm",
+    "nf4_adamw_step",
+    "nf4_residual_norm_forward",
+    "nf4_residual_norm_backward_workspace_size",
+    "nf4_residual_norm_backward",
+    "nf4_embedding_forward",
+    "nf4_embedding_forward_packed",
+    "nf4_embedding_backward_workspace_size",
+    "nf4_embedding_backward",
 )
 
 # nf4_dq_format: the 8-bit code of double quantization.
@@ -182,6 +192,7 @@ def lib():
     L.nf4_merge_lora.argtypes = [ctypes.POINTER(nf4_weight), p, p, i32, f32, p, p, p, p, p,
                                  ctypes.c_size_t, p]
     L.nf4_merge_lora.restype = ctypes.c_int
+    declare(L)
     _lib = L
     return L
 
@@ -936,3 +947,17 @@ def make_lora_linear_module():
             return merge_lora(self.weight, self.lora_a.detach(), self.lora_b.detach(), self.scale)
 
     return NF4LoRALinear
+
+
+# ------------------------------------------------- the training step around the linears
+
+from .training import (  # noqa: E402
+    NF4AdamW,
+    declare,
+    embedding_backward,
+    embedding_forward,
+    nf4_embedding,
+    residual_norm,
+    residual_norm_backward,
+    residual_norm_forward,
+)

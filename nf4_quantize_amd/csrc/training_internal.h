@@ -1,0 +1,144 @@
+// training_internal.h - internal declarations of the training-step operators
+// (optimizer.hip, residual_norm.hip, embedding.hip); their contracts are in
+// nf4.h. Shared by the library's own sources only.
+#pragma once
+
+#include "nf4_internal.h"
+
+namespace nf4 {
+
+constexpr int kMomentBlock = 256;  // elements per scale of the 8-bit moments
+
+// Host-side launchers; each validates nothing.
+size_t grad_norm_workspace(const nf4_adamw_entry *e, int32_t count);
+hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype gt, float *norm,
+                            void *workspace, hipStream_t s);
+hipError_t launch_adamw(const nf4_adamw_entry *e, int32_t count, nf4_dtype wt, nf4_dtype gt,
+                        bool eight, const nf4_adamw_config &c, const float *grad_norm,
+                        hipStream_t s);
+
+struct ResidualNormIn {
+    const void *dx, *dh_out;  // backward only
+    const void *y, *h;        // h: the input (forward), the output (backward)
+    const void *w_post, *gate, *w_pre;
+    const float *rstd_post, *rstd_pre;  // backward only
+};
+struct ResidualNormOut {
+    void *h, *x;                   // forward
+    float *rstd_post, *rstd_pre;   // forward
+    void *dy, *dh, *dgate, *dw_pre, *dw_post;  // backward
+};
+hipError_t launch_residual_norm_forward(const nf4_residual_norm_shape &sh, const ResidualNormIn &in,
+                                        const ResidualNormOut &out, hipStream_t s);
+size_t residual_norm_workspace(const nf4_residual_norm_shape &sh);
+hipError_t launch_residual_norm_backward(const nf4_residual_norm_shape &sh, const ResidualNormIn &in,
+                                         const ResidualNormOut &out, void *workspace, hipStream_t s);
+
+hipError_t launch_embedding_forward(const void *ids, bool i64, int64_t tokens, const void *table,
+                                    nf4_dtype dt, int64_t vocab, int64_t dim, float scale, void *out,
+                                    nf4_dtype ot, hipStream_t s);
+hipError_t launch_embedding_packed(const void *ids, bool i64, int64_t tokens, const nf4_weight &w,
+                                   float scale, void *out, nf4_dtype ot, hipStream_t s);
+size_t embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t dim);
+hipError_t launch_embedding_backward(const void *ids, bool i64, int64_t tokens, const void *dy,
+                                     nf4_dtype dt, int64_t vocab, int64_t dim, float scale,
+                                     int64_t padding_id, void *grad, nf4_dtype gt, bool accumulate,
+                                     void *workspace, hipStream_t s);
+
+// ---- device helpers ----
+
+// Eight consecutive elements of a row that may start at any element: bf16 rows
+// of odd width put 16-byte groups at 2-byte boundaries, which the global
+// memory path of gfx950 takes in one instruction.
+struct __attribute__((packed, aligned(2))) u32x4_any2 { u32x4 v; };
+struct __attribute__((packed, aligned(4))) f32x4_any4 { f32x4 v; };
+
+struct Bf16 {
+    uint16_t bits;
+};
+
+__device__ __forceinline__ void load8(const Bf16 *p, float (&x)[8]) {
+    const u32x4 r = reinterpret_cast<const u32x4_any2 *>(p)->v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = bf16_lo(r[j]);
+        x[2 * j + 1] = bf16_hi(r[j]);
+    }
+}
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+    const f32x4 a = reinterpret_cast<const f32x4_any4 *>(p)->v;
+    const f32x4 b = reinterpret_cast<const f32x4_any4 *>(p + 4)->v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
+}
+__device__ __forceinline__ void store8(Bf16 *p, const float (&x)[8]) {
+    u32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+    reinterpret_cast<u32x4_any2 *>(p)->v = r;
+}
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+    reinterpret_cast<f32x4_any4 *>(p)->v = f32x4{x[0], x[1], x[2], x[3]};
+    reinterpret_cast<f32x4_any4 *>(p + 4)->v = f32x4{x[4], x[5], x[6], x[7]};
+}
+__device__ __forceinline__ float load1(const Bf16 *p) { return bf16_lo(p->bits); }
+__device__ __forceinline__ float load1(const float *p) { return *p; }
+__device__ __forceinline__ void store1(Bf16 *p, float x) {
+    p->bits = (uint16_t)(pack_bf16x2(x, 0.0f) & 0xFFFFu);
+}
+__device__ __forceinline__ void store1(float *p, float x) { *p = x; }
+
+// The first `live` (1 .. 8) of the eight; the others are zero / not written.
+template <typename T>
+__device__ __forceinline__ void load_upto8(const T *p, int64_t live, float (&x)[8]) {
+    if (live >= 8) return load8(p, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = j < live ? load1(p + j) : 0.0f;
+}
+template <typename T>
+__device__ __forceinline__ void store_upto8(T *p, int64_t live, const float (&x)[8]) {
+    if (live >= 8) return store8(p, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < live) store1(p + j, x[j]);
+}
+
+// Sum and maximum over aligned groups of `lanes` lanes of a wave (a power of
+// two, uniform; every lane active): every lane receives its group's result.
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), kCtrl, 0xF, 0xF, true));
+}
+// v_permlane16_swap / v_permlane32_swap of a register with itself: a holds the
+// even 16-lane rows (the lower half) in both rows of each pair, b the odd ones.
+__device__ __forceinline__ void rows16(float x, float &a, float &b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    a = __uint_as_float(r[0]), b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void rows32(float x, float &a, float &b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    a = __uint_as_float(r[0]), b = __uint_as_float(r[1]);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+__device__ __forceinline__ float group_sum(float x, int lanes) {
+    float a, b;
+    if (lanes > 1) x += dpp<kXor1>(x);
+    if (lanes > 2) x += dpp<kXor2>(x);
+    if (lanes > 4) x += dpp<kHalfMirror>(x);
+    if (lanes > 8) x += dpp<kMirror>(x);
+    if (lanes > 16) rows16(x, a, b), x = a + b;
+    if (lanes > 32) rows32(x, a, b), x = a + b;
+    return x;
+}
+// Maximum of non-negative values over aligned groups of 32 lanes.
+__device__ __forceinline__ float max32(float x) {
+    float a, b;
+    x = fmaxf(x, dpp<kXor1>(x));
+    x = fmaxf(x, dpp<kXor2>(x));
+    x = fmaxf(x, dpp<kHalfMirror>(x));
+    x = fmaxf(x, dpp<kMirror>(x));
+    rows16(x, a, b);
+    return fmaxf(a, b);
+}
+
+}  // namespace nf4

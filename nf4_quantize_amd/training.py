@@ -1,0 +1,487 @@
+"""The training step around the 4-bit linears: AdamW over a list of adapter
+tensors (``NF4AdamW``), the residual norms between blocks (``residual_norm``)
+and the token embedding (``nf4_embedding``). Formulas, storage and limits are
+in ``include/nf4.h``; every step of the computation runs in the library's HIP
+kernels, torch supplies device memory and the current stream.
+"""
+import ctypes
+
+import numpy as np
+
+import nf4_quantize_amd as _nq
+
+MOMENT_BLOCK = 256
+GATE_KINDS = {"none": 0, "channel": 1, "token": 2}
+
+# nf4_adamw_entry, as one row of a host array.
+_ENTRY = np.dtype([("w", "u8"), ("master", "u8"), ("grad", "u8"), ("m", "u8"), ("v", "u8"), ("m_scale", "u8"),
+                   ("v_scale", "u8"), ("n", "i8"), ("lr", "f4"), ("weight_decay", "f4")])
+
+
+class nf4_adamw_config(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_float),
+                ("max_norm", ctypes.c_float), ("step", ctypes.c_int64), ("seed", ctypes.c_uint64)]
+
+
+class nf4_residual_norm_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("gate_kind", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("alpha", ctypes.c_float), ("w_offset", ctypes.c_float)]
+
+
+def declare(L):
+    """argtypes and restypes of this module's entry points."""
+    p, i64, i32, f32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+    shape, weight = ctypes.POINTER(nf4_residual_norm_shape), ctypes.POINTER(_nq.nf4_weight)
+    for name, restype, args in (
+            ("nf4_grad_norm_workspace_size", sz, [p, i32]),
+            ("nf4_grad_norm", i32, [p, i32, i32, p, p, sz, p]),
+            ("nf4_adamw_step", i32, [p, i32, i32, i32, i32, ctypes.POINTER(nf4_adamw_config), p, p]),
+            ("nf4_residual_norm_forward", i32, [shape] + [p] * 10),
+            ("nf4_residual_norm_backward_workspace_size", sz, [shape]),
+            ("nf4_residual_norm_backward", i32, [shape] + [p] * 15 + [sz, p]),
+            ("nf4_embedding_forward", i32, [p, i32, i64, p, i32, i64, i64, f32, p, i32, p]),
+            ("nf4_embedding_forward_packed", i32, [p, i32, i64, weight, f32, p, i32, p]),
+            ("nf4_embedding_backward_workspace_size", sz, [i64, i64, i64]),
+            ("nf4_embedding_backward", i32, [p, i32, i64, p, i32, i64, i64, f32, i64, p, i32, i32, p, sz, p])):
+        fn = getattr(L, name)
+        fn.restype, fn.argtypes = restype, args
+
+
+def _size(value, what):
+    if value == ctypes.c_size_t(-1).value:
+        raise _nq.NF4Error(2, what)
+    return int(value)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(dev, *ts):
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors of one call are on one device, got {dev} and {t.device}")
+
+
+# ------------------------------------------------------------------ AdamW
+
+class NF4AdamW:
+    """AdamW over a list of device tensors in a few launches, with the moments in
+    8 bits (E4M3 codes with one fp32 scale per 256 elements, rounded
+    stochastically) or in 32, and clipping by the gradients' global norm.
+
+    ``params``: tensors, or groups ``dict(params=[...], lr=..., weight_decay=...,
+    masters=[...])``; all have one dtype (bfloat16 or float32). ``masters`` are
+    the fp32 weights of bfloat16 parameters: the step updates them and rounds
+    them into the parameters (``masters=True``: made here from the parameters).
+    ``max_grad_norm`` > 0 clips; the step then changes nothing when the norm is
+    not finite. ``seed`` starts the random bits of the stochastic rounding; each
+    step takes the next ones.
+
+    ``m``, ``v`` (and ``m_scale``, ``v_scale``) are the lists of the tensors'
+    moments in the order of the parameters, ``grad_norm`` the last norm (a device
+    tensor of one float)."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=8,
+                 max_grad_norm=0.0, seed=0, masters=None):
+        import torch
+
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits is 8 or 32")
+        params = list(params)
+        if not params:
+            raise ValueError("no parameters")
+        if not isinstance(params[0], dict):
+            params = [dict(params=params, masters=masters)]
+        elif masters is not None:
+            raise ValueError("masters belong to the groups")
+        self.groups = []
+        self.params, self.masters, self._master_rounds = [], [], []
+        for g in params:
+            ps = list(g["params"])
+            ms = g.get("masters")
+            if ms is True:
+                ms = [p.detach().float().contiguous() for p in ps]
+            ms = [None] * len(ps) if ms is None else list(ms)
+            if len(ms) != len(ps):
+                raise ValueError(f"{len(ms)} masters for {len(ps)} parameters")
+            self.groups.append(dict(lr=float(g.get("lr", lr)), weight_decay=float(g.get("weight_decay", weight_decay)),
+                                    first=len(self.params), count=len(ps)))
+            self.params += ps
+            self.masters += ms
+        if not self.params:
+            raise ValueError("no parameters")
+        self.dtype, self.device = self.params[0].dtype, self.params[0].device
+        _nq._dtype_code(self.dtype)
+        for p, mw in zip(self.params, self.masters):
+            if p.dtype != self.dtype:
+                raise TypeError(f"parameters of one dtype, got {self.dtype} and {p.dtype}")
+            _nq._need_cuda(p, mw)
+            _same_device(self.device, p, mw)
+            if mw is not None and (mw.dtype != torch.float32 or self.dtype != torch.bfloat16 or mw.numel() != p.numel()):
+                raise TypeError("a master weight is float32, of a bfloat16 parameter of its size")
+        self.betas, self.eps, self.state_bits = (float(betas[0]), float(betas[1])), float(eps), state_bits
+        self.max_grad_norm, self.seed, self.steps = float(max_grad_norm), int(seed), 0
+        self.grad_norm = torch.zeros(1, dtype=torch.float32, device=self.device)
+        self._entries = np.zeros(len(self.params), _ENTRY)
+        self._numels = [p.numel() for p in self.params]
+        e = self._entries
+        e["w"] = [p.data_ptr() for p in self.params]
+        e["master"] = [0 if mw is None else mw.data_ptr() for mw in self.masters]
+        e["n"] = self._numels
+        self._norm_ws = torch.empty(max(1, self._norm_bytes()), dtype=torch.uint8, device=self.device)
+        self._new_state()
+
+    def _norm_bytes(self):
+        return _size(_nq.lib().nf4_grad_norm_workspace_size(self._entries.ctypes.data, len(self._entries)),
+                     "nf4_grad_norm_workspace_size")
+
+    def _new_state(self):
+        import torch
+
+        # one buffer for each part of the state; a tensor's share starts at a whole block
+        starts = np.concatenate(([0], np.cumsum([-(-n // MOMENT_BLOCK) * MOMENT_BLOCK for n in self._numels])))
+        dt = torch.float8_e4m3fn if self.state_bits == 8 else torch.float32
+
+        def part(dtype, per):
+            flat = torch.zeros(int(starts[-1]) // per, dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype,
+                               device=self.device).view(dtype)
+            return [flat[int(a) // per:int(a) // per + -(-n // per)] for a, n in zip(starts, self._numels)]
+
+        state = [part(dt, 1), part(dt, 1)]
+        if self.state_bits == 8:
+            state += [part(torch.float32, MOMENT_BLOCK), part(torch.float32, MOMENT_BLOCK)]
+        self.bind_state(*state)
+
+    def bind_state(self, m, v, m_scale=None, v_scale=None):
+        """Uses these tensors as the moments (a checkpoint's, or shares of buffers of
+        the caller's): per parameter, m and v of its number of elements (E4M3
+        codes, or float32), with 8-bit moments one float32 scale per 256."""
+        import torch
+
+        lists = dict(m=list(m), v=list(v))
+        if self.state_bits == 8:
+            if m_scale is None or v_scale is None:
+                raise ValueError("8-bit moments have scales")
+            lists.update(m_scale=list(m_scale), v_scale=list(v_scale))
+        dt = torch.float8_e4m3fn if self.state_bits == 8 else torch.float32
+        for name, ts in lists.items():
+            if len(ts) != len(self.params):
+                raise ValueError(f"{name}: {len(ts)} tensors for {len(self.params)} parameters")
+            scale = name.endswith("scale")
+            want = torch.float32 if scale else dt
+            for t, n in zip(ts, self._numels):
+                _nq._need_cuda(t)
+                _same_device(self.device, t)
+                if t.dtype != want or t.numel() != (-(-n // MOMENT_BLOCK) if scale else n):
+                    raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} for a parameter of {n} elements")
+            setattr(self, name, ts)
+            self._entries[name] = [t.data_ptr() for t in ts]
+
+    def zero_grad(self, set_to_none=True):
+        for p in self.params:
+            if set_to_none:
+                p.grad = None
+            elif p.grad is not None:
+                p.grad.zero_()
+
+    def step(self, grads=None, step=None, seed=None):
+        """One step with the parameters' ``.grad``, or with ``grads`` (a tensor for
+        each parameter, all bfloat16 or all float32). ``step`` and ``seed``
+        override the step number (the count of calls) and the random seed."""
+        import torch
+
+        L = _nq.lib()
+        grads = [p.grad for p in self.params] if grads is None else grads
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        if any(g is None for g in grads):
+            raise ValueError("a parameter has no gradient")
+        dt, dev = grads[0].dtype, self.device
+        for g, n in zip(grads, self._numels):
+            if g.dtype is not dt or g.numel() != n or not g.is_contiguous() or g.device != dev:
+                raise ValueError(f"a gradient {tuple(g.shape)} {g.dtype} on {g.device}: contiguous, {n} elements of {dt} "
+                                 f"on {dev} are wanted")
+        grad_dtype = _nq._dtype_code(dt)
+        e, count = self._entries, len(grads)
+        e["grad"] = [g.data_ptr() for g in grads]
+        for g in self.groups:
+            part = slice(g["first"], g["first"] + g["count"])
+            e["lr"][part], e["weight_decay"][part] = g["lr"], g["weight_decay"]
+        at = e.ctypes.data
+        number = self.steps + 1 if step is None else int(step)
+        stream = _nq._stream(dev)
+        clip = self.max_grad_norm > 0
+        with torch.cuda.device(dev):
+            if clip:
+                _nq._check(L.nf4_grad_norm(at, count, grad_dtype, self.grad_norm.data_ptr(), self._norm_ws.data_ptr(),
+                                           self._norm_ws.numel(), stream), "nf4_grad_norm")
+            config = nf4_adamw_config(*self.betas, self.eps, self.max_grad_norm, number,
+                                      (self.seed + number if seed is None else int(seed)) & 0xFFFFFFFFFFFFFFFF)
+            _nq._check(L.nf4_adamw_step(at, count, _nq._dtype_code(self.dtype), grad_dtype, self.state_bits,
+                                        ctypes.byref(config), self.grad_norm.data_ptr() if clip else None, stream),
+                       "nf4_adamw_step")
+        self.steps = number
+
+    def state_dict(self):
+        d = dict(steps=self.steps, seed=self.seed, state_bits=self.state_bits,
+                 groups=[dict(lr=g["lr"], weight_decay=g["weight_decay"]) for g in self.groups],
+                 m=[t.clone() for t in self.m], v=[t.clone() for t in self.v],
+                 masters=[None if t is None else t.clone() for t in self.masters])
+        if self.state_bits == 8:
+            d.update(m_scale=[t.clone() for t in self.m_scale], v_scale=[t.clone() for t in self.v_scale])
+        return d
+
+    def load_state_dict(self, d):
+        import torch
+
+        if d["state_bits"] != self.state_bits or len(d["m"]) != len(self.params) or len(d["groups"]) != len(self.groups):
+            raise ValueError("the state of another optimizer")
+        names = ["m", "v"] + (["m_scale", "v_scale"] if self.state_bits == 8 else [])
+        pairs = [(x, y) for k in names for x, y in zip(getattr(self, k), d[k])]
+        for x, y in zip(self.masters, d["masters"]):
+            if (x is None) != (y is None):
+                raise ValueError("the state of another optimizer: master weights")
+            pairs += [] if x is None else [(x, y)]
+        for x, y in pairs:
+            if x.dtype != y.dtype or x.numel() != y.numel():
+                raise ValueError("the state of another optimizer: sizes")
+        for x, y in pairs:
+            x.view(torch.uint8).copy_(y.reshape(x.shape).to(x.device).view(torch.uint8))
+        self.steps, self.seed = int(d["steps"]), int(d["seed"])
+        for g, new in zip(self.groups, d["groups"]):
+            g.update(lr=float(new["lr"]), weight_decay=float(new["weight_decay"]))
+
+
+# ------------------------------------------------------------------ residual norms
+
+def _norm_shape(y, h, w_pre, w_post, gate, alpha, eps, w_offset):
+    """The call's shape: y None leaves only the norm of h."""
+    act = h if y is None else y
+    if h.dim() < 1 or act.shape != h.shape:
+        raise ValueError(f"y {tuple(act.shape)} and h {tuple(h.shape)} have one shape")
+    dim = h.shape[-1]
+    rows = h.numel() // max(dim, 1)
+    kind = "none"
+    if gate is not None and y is not None:
+        kind = "token" if gate.dim() == act.dim() and act.dim() > 1 and gate.shape == act.shape else "channel"
+        if kind == "channel" and tuple(gate.shape) != (dim,):
+            raise ValueError(f"gate {tuple(gate.shape)}: ({dim},) or the shape of y")
+        if gate.dtype != (act.dtype if kind == "token" else w_pre.dtype):
+            raise TypeError("a token gate has the dtype of y, a channel gate that of the norms' weights")
+    for w in (w_pre, w_post):
+        if w is not None and (tuple(w.shape) != (dim,) or w.dtype != w_pre.dtype):
+            raise ValueError(f"norm weights are ({dim},) of one dtype, got {tuple(w.shape)} {w.dtype}")
+    return nf4_residual_norm_shape(rows, dim, _nq._dtype_code(act.dtype), _nq._dtype_code(h.dtype),
+                                   _nq._dtype_code(w_pre.dtype), GATE_KINDS[kind], float(eps), float(alpha),
+                                   float(w_offset))
+
+
+def residual_norm_forward(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6, w_offset=0.0, h_out=None, x_out=None):
+    """h' = h + alpha gate norm(y; w_post), x = norm(h'; w_pre) over the last
+    dimension (nf4_residual_norm_forward). ``y`` bfloat16 or float32, ``h`` the
+    same or float32; without ``w_post`` y is added as it is; ``y=None``: x =
+    norm(h) and h' = h. ``gate``: one value a channel, or one an element. Returns
+    (h', x, rstd_pre, rstd_post or None); ``h_out=h`` updates the residual stream
+    in place."""
+    import torch
+
+    _nq._need_cuda(y, h, w_pre, w_post, gate, h_out, x_out)
+    _same_device(h.device, y, w_pre, w_post, gate, h_out, x_out)
+    shape = _norm_shape(y, h, w_pre, w_post, gate, alpha, eps, w_offset)
+    act = h if y is None else y
+    if h_out is None and y is not None:
+        h_out = torch.empty_like(h)
+    if x_out is None:
+        x_out = torch.empty_like(act)
+    for t, like in ((h_out, h), (x_out, act)):
+        if t is not None and (t.shape != like.shape or t.dtype != like.dtype):
+            raise ValueError("outputs have the shape and dtype of h and y")
+    post = w_post is not None and y is not None
+    stats = torch.empty((2 if post else 1, shape.rows), dtype=torch.float32, device=h.device)
+    rstd_pre, rstd_post = stats[0], stats[1] if post else None
+    st = _nq.lib().nf4_residual_norm_forward(ctypes.byref(shape), _addr(y), _addr(h), _addr(w_post), _addr(gate),
+                                             _addr(w_pre), _addr(h_out), _addr(x_out), _addr(rstd_post),
+                                             _addr(rstd_pre), _nq._stream(h.device))
+    _nq._check(st, "nf4_residual_norm_forward")
+    return (h if y is None else h_out), x_out, rstd_pre, rstd_post
+
+
+def residual_norm_backward(dx, dh_out, y, h_out, rstd_pre, w_pre, rstd_post=None, w_post=None, gate=None, alpha=1.0,
+                           w_offset=0.0, want=(True, True, True, True, True)):
+    """Gradients of residual_norm_forward from those of x and h' (either may be
+    None) and the forward's h' and statistics: (dy, dh, dw_pre, dw_post, dgate),
+    None where ``want`` is false or the input is absent."""
+    import torch
+
+    _nq._need_cuda(dx, dh_out, y, h_out, rstd_pre, w_pre, rstd_post, w_post, gate)
+    _same_device(h_out.device, dx, dh_out, y, rstd_pre, w_pre, rstd_post, w_post, gate)
+    shape = _norm_shape(y, h_out, w_pre, w_post, gate, alpha, 0.0, w_offset)
+    act = h_out if y is None else y
+    for t, like in ((dx, act), (dh_out, h_out)):
+        if t is not None and (t.shape != like.shape or t.dtype != like.dtype):
+            raise ValueError("dx has the shape and dtype of y, dh_out those of h")
+    post = w_post is not None and y is not None
+    for r, need in ((rstd_pre, True), (rstd_post, post)):
+        if need and (r is None or r.dtype != torch.float32 or r.numel() != shape.rows):
+            raise ValueError("rstd_pre and, with w_post, rstd_post hold one float32 a row")
+    gated = shape.gate_kind != 0
+    dy = torch.empty_like(y) if want[0] and y is not None else None
+    dh = torch.empty_like(h_out) if want[1] else None
+    dw_pre = torch.empty_like(w_pre) if want[2] else None
+    dw_post = torch.empty_like(w_post) if want[3] and post else None
+    dgate = torch.empty_like(gate) if want[4] and gated else None
+    L = _nq.lib()
+    ws = None
+    if dw_pre is not None or dw_post is not None or (dgate is not None and shape.gate_kind == 1):
+        size = _size(L.nf4_residual_norm_backward_workspace_size(ctypes.byref(shape)),
+                     "nf4_residual_norm_backward_workspace_size")
+        ws = torch.empty(max(size, 1), dtype=torch.uint8, device=h_out.device)
+    st = L.nf4_residual_norm_backward(ctypes.byref(shape), _addr(dx), _addr(dh_out), _addr(y), _addr(h_out),
+                                      _addr(w_post), _addr(gate), _addr(w_pre), _addr(rstd_post), _addr(rstd_pre),
+                                      _addr(dy), _addr(dh), _addr(dgate), _addr(dw_pre), _addr(dw_post), _addr(ws),
+                                      0 if ws is None else ws.numel(), _nq._stream(h_out.device))
+    _nq._check(st, "nf4_residual_norm_backward")
+    return dy, dh, dw_pre, dw_post, dgate
+
+
+# ------------------------------------------------------------------ token embedding
+
+_INDEX = {"torch.int32": 0, "torch.int64": 1}
+
+
+def _index_code(ids):
+    code = _INDEX.get(str(ids.dtype))
+    if code is None:
+        raise TypeError(f"token numbers are int32 or int64, got {ids.dtype}")
+    return code
+
+
+def embedding_forward(ids, table, scale=1.0, out_dtype=None, out=None):
+    """scale * table[ids] (nf4_embedding_forward): ``table`` a [vocab x dim] tensor,
+    or an NF4Tensor of that shape whose rows are dequantized as they are read.
+    Ids outside the table give rows of zeros. The output has ``out_dtype``, by
+    default the table's (bfloat16 for an NF4 table)."""
+    import torch
+
+    packed = isinstance(table, _nq.NF4Tensor)
+    if len(table.shape) != 2:
+        raise ValueError("a table is 2-D [vocab x dim]")
+    vocab, dim = table.shape
+    if out is None:
+        out_dtype = out_dtype or (torch.bfloat16 if packed else table.dtype)
+        out = torch.empty((*ids.shape, dim), dtype=out_dtype, device=ids.device)
+    elif tuple(out.shape) != (*ids.shape, dim) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"out: {(*ids.shape, dim)} is wanted")
+    _nq._need_cuda(ids, out, *((table.codes, table.absmax, table.absmax_q, table.absmax_scale) if packed else (table,)))
+    _same_device(ids.device, out, table.codes if packed else table)
+    L, args = _nq.lib(), (ids.data_ptr(), _index_code(ids), ids.numel())
+    od, stream = _nq._dtype_code(out.dtype), _nq._stream(ids.device)
+    if packed:
+        w = table.weight_struct()
+        st = L.nf4_embedding_forward_packed(*args, ctypes.byref(w), float(scale), out.data_ptr(), od, stream)
+    else:
+        st = L.nf4_embedding_forward(*args, table.data_ptr(), _nq._dtype_code(table.dtype), vocab, dim, float(scale),
+                                     out.data_ptr(), od, stream)
+    _nq._check(st, "nf4_embedding_forward")
+    return out
+
+
+def embedding_backward(ids, dy, vocab, scale=1.0, padding_id=None, grad=None, grad_dtype=None, workspace=None):
+    """Gradient of a [vocab x dim] table from dy [*ids.shape x dim]
+    (nf4_embedding_backward): a new tensor of ``grad_dtype`` (by default dy's), or
+    added to ``grad`` where one is given. Deterministic."""
+    import torch
+
+    dim = dy.shape[-1]
+    if tuple(dy.shape) != (*ids.shape, dim):
+        raise ValueError(f"dy {tuple(dy.shape)} for ids {tuple(ids.shape)}")
+    accumulate = grad is not None
+    if not accumulate:
+        grad = torch.empty((vocab, dim), dtype=grad_dtype or dy.dtype, device=dy.device)
+    elif tuple(grad.shape) != (vocab, dim) or (grad_dtype is not None and grad.dtype != grad_dtype):
+        raise ValueError(f"grad {tuple(grad.shape)} {grad.dtype}: ({vocab}, {dim}) is wanted")
+    _nq._need_cuda(ids, dy, grad, workspace)
+    _same_device(dy.device, ids, grad, workspace)
+    L = _nq.lib()
+    if workspace is None:
+        size = _size(L.nf4_embedding_backward_workspace_size(ids.numel(), vocab, dim),
+                     "nf4_embedding_backward_workspace_size")
+        workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=dy.device)
+    st = L.nf4_embedding_backward(ids.data_ptr(), _index_code(ids), ids.numel(), dy.data_ptr(),
+                                  _nq._dtype_code(dy.dtype), vocab, dim, float(scale),
+                                  -1 if padding_id is None else int(padding_id), grad.data_ptr(),
+                                  _nq._dtype_code(grad.dtype), 1 if accumulate else 0, workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _nq._stream(dy.device))
+    _nq._check(st, "nf4_embedding_backward")
+    return grad
+
+
+# ------------------------------------------------------------------ autograd
+
+_FUNCTIONS = None
+
+
+def _functions():
+    """The autograd functions (made on first use: importing this module does not
+    import torch)."""
+    global _FUNCTIONS
+    if _FUNCTIONS is not None:
+        return _FUNCTIONS
+    import torch
+
+    class ResidualNormFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, y, h, w_pre, w_post, gate, alpha, eps, w_offset):
+            y = None if y is None else y.contiguous()
+            h = h.contiguous()
+            gate = None if gate is None else gate.contiguous()
+            h_out, x, rstd_pre, rstd_post = residual_norm_forward(y, h, w_pre, w_post, gate, alpha, eps, w_offset)
+            ctx.save_for_backward(y, h_out, rstd_pre, w_pre, rstd_post, w_post, gate)
+            ctx.alpha, ctx.w_offset = alpha, w_offset
+            ctx.set_materialize_grads(False)
+            return (h_out if y is not None else h.view_as(h)), x
+
+        @staticmethod
+        def backward(ctx, dh_out, dx):
+            y, h_out, rstd_pre, w_pre, rstd_post, w_post, gate = ctx.saved_tensors
+            act = h_out if y is None else y
+            dx = None if dx is None else dx.to(act.dtype).contiguous()
+            dh_out = None if dh_out is None else dh_out.to(h_out.dtype).contiguous()
+            need = ctx.needs_input_grad
+            dy, dh, dw_pre, dw_post, dgate = residual_norm_backward(
+                dx, dh_out, y, h_out, rstd_pre, w_pre, rstd_post, w_post, gate, ctx.alpha, ctx.w_offset,
+                want=(need[0], need[1], need[2], need[3], need[4]))
+            return dy, dh, dw_pre, dw_post, dgate, None, None, None
+
+    class EmbeddingFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, ids, table, scale, padding_id, out_dtype):
+            ids = ids.contiguous()
+            ctx.save_for_backward(ids)
+            ctx.scale, ctx.padding_id, ctx.vocab, ctx.dtype = scale, padding_id, table.shape[0], table.dtype
+            return embedding_forward(ids, table.contiguous(), scale, out_dtype)
+
+        @staticmethod
+        def backward(ctx, dy):
+            grad = embedding_backward(ctx.saved_tensors[0], dy.contiguous(), ctx.vocab, ctx.scale, ctx.padding_id,
+                                      grad_dtype=ctx.dtype)
+            return None, grad, None, None, None
+
+    _FUNCTIONS = (ResidualNormFunction, EmbeddingFunction)
+    return _FUNCTIONS
+
+
+def residual_norm(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6, w_offset=0.0):
+    """Differentiable residual step: (h', x) of residual_norm_forward. Gradients
+    flow to y, h, both norms' weights and the gate."""
+    return _functions()[0].apply(y, h, w_pre, w_post, gate, float(alpha), float(eps), float(w_offset))
+
+
+def nf4_embedding(ids, table, scale=1.0, padding_id=None, out_dtype=None):
+    """Differentiable scale * table[ids]. A dense table receives a dense gradient
+    (none for ``padding_id``); an NF4Tensor is frozen."""
+    if isinstance(table, _nq.NF4Tensor):
+        return embedding_forward(ids.contiguous(), table, scale, out_dtype)
+    return _functions()[1].apply(ids, table, float(scale), padding_id, out_dtype)
