@@ -4,9 +4,8 @@
 //
 // The forward moves each looked-up row once in and once out. The backward
 // sorts the tokens by their id (stable, so that a row's gradient is summed in
-// the order of the tokens), sums runs of equal ids chunk by chunk, joins the
-// runs that cross chunks and, for a dense gradient, clears the rows that no
-// token names. It is bound by reading dy and writing the table's gradient.
+// the order of the tokens), sums runs of equal ids chunk by chunk and joins the
+// runs that cross chunks; a dense gradient is cleared beside the sort. It is bound by reading dy and writing the table's gradient.
 #include "linear_common.h"
 #include "training_internal.h"
 
@@ -14,6 +13,7 @@ namespace nf4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kInFlight = 4;
 
 // The row of token t, or `vocab` where it has none.
 __device__ __forceinline__ uint32_t token_key(const void *ids, bool i64, int64_t t, int64_t vocab, int64_t skip) {
@@ -23,7 +23,8 @@ __device__ __forceinline__ uint32_t token_key(const void *ids, bool i64, int64_t
 
 // ---- forward ----
 
-template <typename T, typename O>
+// A group of `lanes` lanes moves one row, four vectors of a lane in flight.
+template <typename T, typename O, bool kNarrow>
 __global__ __launch_bounds__(kThreads) void lookup_kernel(const void *ids, bool i64, int64_t tokens, const T *table,
                                                           int64_t vocab, int32_t dim, float scale, O *out, int lanes) {
     const int each = kThreads / lanes;
@@ -31,16 +32,20 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(const void *ids, bool 
         const uint32_t row = token_key(ids, i64, t, vocab, -1);
         const T *src = table + (int64_t)row * dim;
         O *dst = out + t * dim;
-        for (int col = (threadIdx.x & (lanes - 1)) * 8; col < dim; col += lanes * 8) {
-            float x[8];
+        for (int c0 = (threadIdx.x & (lanes - 1)) * 8; c0 < dim; c0 += lanes * 8 * kInFlight) {
+            Raw8<T> raw[kInFlight];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-            if (row < vocab) {
-                load_upto8(src + col, dim - col, x);
+            for (int u = 0; u < kInFlight; ++u)
+                if (row < vocab) raw[u] = load_cols(src, Cols<kNarrow>(c0 + u * lanes * 8, dim));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= scale;
+            for (int u = 0; u < kInFlight; ++u) {
+                const Cols<kNarrow> c(c0 + u * lanes * 8, dim);
+                float x[8];
+                cols_values(raw[u], c, x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = row < vocab ? x[j] * scale : 0.0f;
+                store_cols(dst, c, x);
             }
-            store_upto8(dst + col, dim - col, x);
         }
     }
 }
@@ -88,37 +93,162 @@ dim3 lookup_grid(int64_t tokens, int lanes) {
 
 // ---- sorting the tokens ----
 
-constexpr int64_t kRankTokens = 8192;  // up to here ranks are counted, above the sort is by digits
-constexpr int kTiles = 64;             // workgroups of a digit pass
+constexpr int kOneTile = 4096;      // up to here each token counts its place among all
+constexpr int kTile = 2048;         // up to kRankTokens: in its tile, and searches the others
+constexpr int kRankTokens = 32768;
+constexpr int kTiles = 64;          // workgroups of a digit pass above
 constexpr int kMaxBins = 1024;
 
-// Rank of each token by counting the tokens before it: id below its own, or
-// equal and at an earlier place. 64 tokens a workgroup, each wave counts over a
-// quarter of the others.
-__global__ __launch_bounds__(kThreads) void rank_kernel(const void *ids, bool i64, int32_t tokens, int64_t vocab,
-                                                        int64_t skip, uint32_t *skey, uint32_t *sidx) {
-    __shared__ uint32_t s_key[kRankTokens];
-    __shared__ int32_t s_count[4][64];
-    const int padded = (tokens + 255) / 256 * 256;
-    for (int t = threadIdx.x; t < padded; t += kThreads)
-        s_key[t] = t < tokens ? token_key(ids, i64, t, vocab, skip) : 0xFFFFFFFFu;
+// Lanes of the wave whose digit (of `width` bits) equals this lane's, among the
+// live lanes.
+__device__ __forceinline__ uint64_t same_digit(uint32_t d, int width, bool live) {
+    uint64_t same = __ballot(live);
+    for (int b = 0; b < width; ++b) {
+        const bool bit = (d >> b) & 1u;
+        const uint64_t set = __ballot(bit);
+        same &= bit ? set : ~set;
+    }
+    return same;
+}
+
+// Exclusive sum over the workgroup's threads (1024), in the order of the threads.
+__device__ __forceinline__ uint32_t scan1024(uint32_t x, uint32_t *s_wave) {
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    uint32_t scan = x;
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t up = __shfl_up(scan, o);
+        scan += lane >= o ? up : 0u;
+    }
+    if (lane == 63) s_wave[wave] = scan;
+    __syncthreads();
+    uint32_t before = scan - x;
+    for (int w = 0; w < wave; ++w) before += s_wave[w];
+    return before;
+}
+
+// A dense gradient is cleared beside the sort's first launch, which hardly
+// uses the memory.
+template <typename G>
+__device__ __forceinline__ void clear_share(G *grad, int64_t n, int64_t wg, int64_t wgs) {
+    const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    __builtin_amdgcn_s_setprio(3);  // few instructions, all of them stores: ahead of the sort's comparisons
+    for (int64_t i = (wg * 1024 + threadIdx.x) * 8; i < n; i += wgs * 1024 * 8) store_upto8(grad + i, n - i, zero);
+}
+
+struct RankParams {
+    const void *ids;
+    bool i64;
+    int32_t tokens, tile;
+    int32_t wgs, each;  // workgroups that rank (those above clear the gradient), of `each` tokens: 16, 32 or 64
+    int64_t vocab, skip;
+    uint32_t *key_out, *idx_out;
+    void *grad;
+    int64_t n;
+};
+
+// Keys of s_key[0 .. 15] that are below `key`, or (kEqual) not above it.
+template <bool kEqual>
+__device__ __forceinline__ int count_below(const uint4 *s_key, uint32_t key) {
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 k = s_key[j];
+        count += kEqual ? k.x <= key : k.x < key;
+        count += kEqual ? k.y <= key : k.y < key;
+        count += kEqual ? k.z <= key : k.z < key;
+        count += kEqual ? k.w <= key : k.w < key;
+    }
+    return count;
+}
+
+// The place of each token in its tile's stable order, by counting the tokens
+// before it: those with a smaller key, and earlier ones with its own. A
+// workgroup takes `each` tokens; its 16 waves, and the 64 / each lanes of a token,
+// compare with a share of the tile's keys in LDS, two instructions a pair. The
+// work grows with the tile, but it is one launch on the whole chip.
+template <typename G>
+__global__ __launch_bounds__(1024) void rank_tokens_kernel(RankParams p) {
+    __shared__ uint4 s_key4[kOneTile / 4];
+    __shared__ int32_t s_count[16][64];
+    if ((int)blockIdx.x >= p.wgs) {
+        clear_share(static_cast<G *>(p.grad), p.n, blockIdx.x - p.wgs, gridDim.x - p.wgs);
+        return;
+    }
+    uint32_t *s_key = reinterpret_cast<uint32_t *>(s_key4);
+    const int first_token = blockIdx.x * p.each, tile0 = first_token / p.tile * p.tile;
+    const int tokens = p.tokens - tile0 < p.tile ? p.tokens - tile0 : p.tile;
+    const int padded = (tokens + 1023) / 1024 * 1024;  // at most kOneTile
+    uint32_t k[kOneTile / 1024];
+#pragma unroll
+    for (int u = 0; u < kOneTile / 1024; ++u) {
+        const int t = threadIdx.x + u * 1024;
+        k[u] = token_key(p.ids, p.i64, tile0 + (t < tokens ? t : 0), p.vocab, p.skip);
+    }
+#pragma unroll
+    for (int u = 0; u < kOneTile / 1024; ++u) {
+        const int t = threadIdx.x + u * 1024;
+        if (t < padded) s_key[t] = t < tokens ? k[u] : 0xFFFFFFFFu;
+    }
     __syncthreads();
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const int me = blockIdx.x * 64 + lane;  // < padded
+    const int own = first_token - tile0, me = own + lane % p.each;
     const uint32_t key = s_key[me];
-    const int quarter = padded / 4, begin = wave * quarter;
+    // groups of 16 keys; the workgroup's own tokens are whole groups
+    const int first = own / 16, last = first + p.each / 16, parts = 64 / p.each;
+    const int shares = 16 * parts, share = wave * parts + lane / p.each;
     int count = 0;
-    for (int j = begin; j < begin + quarter; ++j) {
-        const uint32_t k = s_key[j];
-        count += (k < key || (k == key && j < me)) ? 1 : 0;
+    for (int t = share; t < padded / 16; t += shares) {
+        if (t < first) count += count_below<true>(s_key4 + t * 4, key);
+        else if (t >= last) count += count_below<false>(s_key4 + t * 4, key);
+        else
+#pragma unroll 1
+            for (int j = t * 16; j < t * 16 + 16; ++j) count += s_key[j] < key || (s_key[j] == key && j < me);
     }
     s_count[wave][lane] = count;
     __syncthreads();
-    if (wave == 0 && me < tokens) {
-        const int r = s_count[0][lane] + s_count[1][lane] + s_count[2][lane] + s_count[3][lane];
-        skey[r] = key;
-        sidx[r] = (uint32_t)me;
+    if ((int)threadIdx.x < p.each && me < tokens) {
+        int r = tile0;
+        for (int w = 0; w < 16; ++w)
+            for (int q = 0; q < parts; ++q) r += s_count[w][q * p.each + lane];
+        p.key_out[r] = key;
+        p.idx_out[r] = (uint32_t)(tile0 + me);
     }
+}
+
+// From sorted tiles to one order: a token's place is its place in its own tile
+// and, in each other tile, the number of keys below its own (or equal, in
+// earlier tiles). `lanes` lanes a token, one a tile, each with a binary search.
+__global__ __launch_bounds__(kThreads) void merge_tiles_kernel(const uint32_t *key, const uint32_t *idx, int32_t tokens,
+                                                               int32_t tile, int32_t lanes, uint32_t *key_out,
+                                                               uint32_t *idx_out) {
+    const int i = (int)((blockIdx.x * kThreads + threadIdx.x) / lanes), other = threadIdx.x & (lanes - 1);
+    if (i >= tokens) return;
+    const uint32_t k = key[i];
+    const int mine = i / tile;
+    int place = 0;
+    if (other == mine) {
+        place = i - mine * tile;
+    } else if (other * tile < tokens) {
+        const uint32_t *at = key + other * tile;
+        const uint32_t bound = k + (other < mine ? 1u : 0u);
+        int n = tokens - other * tile < tile ? tokens - other * tile : tile;
+        while (n > 0) {  // place: so many are known to be below
+            const int half = n / 2;
+            const bool below = at[place + half] < bound;
+            place += below ? half + 1 : 0;
+            n = below ? n - half - 1 : half;
+        }
+    }
+    for (int o = 1; o < lanes; o <<= 1) place += __shfl_xor(place, o);
+    if (other == 0) {
+        key_out[place] = k;
+        idx_out[place] = idx[i];
+    }
+}
+
+template <typename G>
+__global__ __launch_bounds__(1024) void clear_kernel(G *grad, int64_t n) {
+    clear_share(grad, n, blockIdx.x, gridDim.x);
 }
 
 struct DigitPass {
@@ -126,17 +256,25 @@ struct DigitPass {
     const uint32_t *key, *idx;  // later passes: the last pass's output
     bool i64, first;
     int64_t tokens, tile, vocab, skip;
-    int shift, bins;
+    int tiles, shift, width, bins;
     uint32_t *hist;         // [tiles][bins]
     uint32_t *key_out, *idx_out;
+    void *grad;             // cleared beside the count, n elements (none: nullptr)
+    int64_t n;
 };
 
 __device__ __forceinline__ uint32_t pass_key(const DigitPass &p, int64_t t) {
     return p.first ? token_key(p.ids, p.i64, t, p.vocab, p.skip) : p.key[t];
 }
 
+// The digits of each tile; the workgroups past the tiles clear the gradient.
+template <typename G>
 __global__ __launch_bounds__(1024) void digit_count_kernel(DigitPass p) {
     __shared__ uint32_t s_bin[kMaxBins];
+    if ((int)blockIdx.x >= p.tiles) {
+        clear_share(static_cast<G *>(p.grad), p.n, blockIdx.x - p.tiles, gridDim.x - p.tiles);
+        return;
+    }
     s_bin[threadIdx.x] = 0u;
     __syncthreads();
     const int64_t begin = blockIdx.x * p.tile, end = begin + p.tile < p.tokens ? begin + p.tile : p.tokens;
@@ -147,10 +285,9 @@ __global__ __launch_bounds__(1024) void digit_count_kernel(DigitPass p) {
 }
 
 // Stable scatter of one tile by one digit. Each of the 16 waves owns a run of
-// the tile and a row of next places, which starts at the digit's place after
-// all lower digits, all earlier tiles and the earlier waves of this tile. A
-// wave takes 64 keys at a time in order: lanes with the same digit find each
-// other by ballots over its bits.
+// the tile and a row of next places, which starts after all lower digits, all
+// earlier tiles and the earlier waves; it takes 64 tokens at a time in order,
+// and lanes with the same digit find each other by ballots over its bits.
 __global__ __launch_bounds__(1024) void digit_scatter_kernel(DigitPass p) {
     __shared__ uint32_t s_next[16][kMaxBins];
     __shared__ uint32_t s_wave[16];
@@ -164,20 +301,12 @@ __global__ __launch_bounds__(1024) void digit_scatter_kernel(DigitPass p) {
         atomicAdd(&s_next[wave][(pass_key(p, t) >> p.shift) & (p.bins - 1)], 1u);
     uint32_t total = 0u, before = 0u;
     if ((int)threadIdx.x < p.bins)
-        for (uint32_t t = 0; t < gridDim.x; ++t) {
+        for (int t = 0; t < p.tiles; ++t) {
             const uint32_t c = p.hist[(int64_t)t * p.bins + threadIdx.x];
-            before += t < blockIdx.x ? c : 0u;
+            before += t < (int)blockIdx.x ? c : 0u;
             total += c;
         }
-    uint32_t scan = total;  // inclusive over the wave's digits
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t up = __shfl_up(scan, o);
-        scan += lane >= o ? up : 0u;
-    }
-    if (lane == 63) s_wave[wave] = scan;
-    __syncthreads();
-    uint32_t place = scan - total + before;
-    for (int w = 0; w < wave; ++w) place += s_wave[w];
+    uint32_t place = scan1024(total, s_wave) + before;  // its barrier also ends the counting
     for (int w = 0; w < 16; ++w) {
         const uint32_t c = s_next[w][threadIdx.x];
         s_next[w][threadIdx.x] = place;
@@ -191,11 +320,7 @@ __global__ __launch_bounds__(1024) void digit_scatter_kernel(DigitPass p) {
         const uint32_t key = live ? pass_key(p, t) : 0u;
         const uint32_t idx = !live || p.first ? (uint32_t)t : p.idx[t];
         const uint32_t d = (key >> p.shift) & (p.bins - 1);
-        uint64_t same = __ballot(live);
-        for (int b = 1; b < p.bins; b <<= 1) {
-            const uint64_t set = __ballot((d & b) != 0u);
-            same &= (d & b) ? set : ~set;
-        }
+        const uint64_t same = same_digit(d, p.width, live);
         const uint32_t rank = __popcll(same & ((1ull << lane) - 1ull));
         const uint32_t at = live ? next[d] + rank : 0u;
         __builtin_amdgcn_wave_barrier();
@@ -210,13 +335,14 @@ __global__ __launch_bounds__(1024) void digit_scatter_kernel(DigitPass p) {
 
 // ---- the gradient ----
 
-constexpr int kChunk = 16;  // sorted places of a wave
+constexpr int kMostChunk = 16;  // sorted places of a wave
 constexpr int kCols = 512;  // columns of a wave
+constexpr int kRows = 8;    // rows of dy, or shares of a run, in flight
 
 struct GradParams {
     const uint32_t *key, *idx;  // sorted
     int64_t tokens, vocab, chunks;
-    int32_t dim, slices;
+    int32_t dim, slices, chunk;
     float scale;
     const void *dy;
     void *grad;
@@ -225,58 +351,72 @@ struct GradParams {
 };
 
 template <typename G>
-__device__ __forceinline__ void write_row(const GradParams &p, uint32_t key, int col, float (&acc)[8]) {
-    G *dst = static_cast<G *>(p.grad) + (int64_t)key * p.dim + col;
-    const int live = p.dim - col;
-    if (live <= 0) return;
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-    if (p.accumulate) load_upto8(dst, live, x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] += acc[j] * p.scale;
-    store_upto8(dst, live, x);
+__device__ __forceinline__ G *grad_row(const GradParams &p, uint32_t key) {
+    return static_cast<G *>(p.grad) + (int64_t)key * p.dim;
 }
 
-template <typename T, typename G>
+// Each wave sums the runs of up to 16 sorted places in 512 columns. dy is read once, so
+// where a wave's columns are whole cache lines (kStream) it is read past the
+// caches: beside a gradient that the sort's launch has just cleared, 16384 x 4096
+// bf16 into 32000 rows take 86 us in all instead of 109. With lines that two
+// waves share it costs instead (5003 x 1601: 38 us for 36).
+template <typename T, typename G, bool kNarrow, bool kStream, bool kAdd>
 __global__ __launch_bounds__(kThreads) void run_sum_kernel(GradParams p) {
     const int lane = threadIdx.x % 64;
     const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
     const int64_t c = unit / p.slices;
     if (c >= p.chunks) return;
-    const int col = (int)(unit % p.slices) * kCols + lane * 8;
-    const int64_t start = c * kChunk;
-    const int len = (int)(p.tokens - start < kChunk ? p.tokens - start : kChunk);
+    const Cols<kNarrow> cols((int)(unit % p.slices) * kCols + lane * 8, p.dim);
+    const int64_t start = c * p.chunk;
+    const int len = (int)(p.tokens - start < p.chunk ? p.tokens - start : p.chunk);
     // lane j holds place start - 1 + j
     const int64_t place = start - 1 + lane;
-    const bool there = lane < kChunk + 2 && place >= 0 && place < p.tokens;
+    const bool there = lane < p.chunk + 2 && place >= 0 && place < p.tokens;
     const uint32_t vkey = there ? p.key[place] : 0xFFFFFFFFu, vidx = there ? p.idx[place] : 0u;
     float acc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
     bool entered = __builtin_amdgcn_readlane((int)vkey, 0) == __builtin_amdgcn_readlane((int)vkey, 1);
-    for (int i = 0; i < len; ++i) {
-        const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)vkey, i + 1);
-        if (key >= p.vocab) return;
-        const uint32_t idx = (uint32_t)__builtin_amdgcn_readlane((int)vidx, i + 1);
-        const uint32_t after = (uint32_t)__builtin_amdgcn_readlane((int)vkey, i + 2);
-        if (col < p.dim) {
+    for (int i0 = 0; i0 < len; i0 += kRows) {
+        Raw8<T> raw[kRows];
+        Raw8<G> old[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            // places past the tokens and keys that name no row load token 0 and are left below
+            const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)vkey, i0 + u + 1);
+            const uint32_t at = (uint32_t)__builtin_amdgcn_readlane((int)vidx, i0 + u + 1);
+            const uint32_t idx = key < p.vocab ? at : 0u;
+            const T *row = static_cast<const T *>(p.dy) + (int64_t)idx * p.dim;
+            if constexpr (kStream) raw[u] = load_stream(row + cols.base);
+            else raw[u] = load_cols(row, cols);
+            // the row that a run ending here is added to; no other wave writes it
+            const uint32_t after = (uint32_t)__builtin_amdgcn_readlane((int)vkey, i0 + u + 2);
+            if (kAdd && after != key && key < p.vocab) old[u] = load_cols(grad_row<G>(p, key), cols);
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int i = i0 + u;
+            const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)vkey, i + 1);
+            const uint32_t after = (uint32_t)__builtin_amdgcn_readlane((int)vkey, i + 2);
+            if (i >= len || key >= p.vocab) return;  // keys that name no row come last
             float x[8];
-            load_upto8(static_cast<const T *>(p.dy) + (int64_t)idx * p.dim + col, p.dim - col, x);
+            cols_values(raw[u], cols, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] += x[j];
-        }
-        const bool leaves = after == key;
-        if (leaves && i + 1 < len) continue;
-        if (entered || leaves) {
-            float *dst = p.partial + (c * 2 + (entered ? 0 : 1)) * p.dim + col;
-            if (col < p.dim) store_upto8(dst, p.dim - col, acc);
-        } else {
-            write_row<G>(p, key, col, acc);
-        }
-        entered = false;
+            const bool leaves = after == key;
+            if (leaves && i + 1 < len) continue;
+            if (entered || leaves) {
+                store_cols(p.partial + (c * 2 + (entered ? 0 : 1)) * p.dim, cols, acc);
+            } else {
+                if constexpr (kAdd) cols_values(old[u], cols, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+                for (int j = 0; j < 8; ++j) x[j] = kAdd ? x[j] + acc[j] * p.scale : acc[j] * p.scale;
+                store_cols(grad_row<G>(p, key), cols, x);
+            }
+            entered = false;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+        }
     }
 }
 
@@ -298,61 +438,40 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t *keys, int64_t n, 
 }
 
 // The runs that leave the chunk they begin in: their shares, chunk after chunk.
-template <typename G>
+template <typename G, bool kNarrow>
 __global__ __launch_bounds__(kThreads) void run_join_kernel(GradParams p) {
     const int lane = threadIdx.x % 64;
     const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
     const int64_t c = unit / p.slices;
     if (c + 1 >= p.chunks) return;
-    const int col = (int)(unit % p.slices) * kCols + lane * 8;
-    const int64_t start = c * kChunk, end = start + kChunk;
+    const Cols<kNarrow> cols((int)(unit % p.slices) * kCols + lane * 8, p.dim);
+    const int64_t start = c * p.chunk, end = start + p.chunk;
     const uint32_t key = p.key[end - 1];
     if (p.key[end] != key || key >= p.vocab) return;
     if (p.key[start] == key && start > 0 && p.key[start - 1] == key) return;  // begins before
     const int64_t stop = end + lower_bound(p.key + end, p.tokens - end, key + 1);
-    const int64_t last = (stop - 1) / kChunk;
+    const int64_t last = (stop - 1) / p.chunk;
     float acc[8];
+    cols_values(load_cols(p.partial + (c * 2 + 1) * p.dim, cols), cols, acc);
+    for (int64_t d = c + 1; d <= last; d += kRows) {
+        Raw8<float> raw[kRows];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-    if (col < p.dim) {
-        load_upto8(p.partial + (c * 2 + 1) * p.dim + col, p.dim - col, acc);
-        for (int64_t d = c + 1; d <= last; ++d) {
+        for (int u = 0; u < kRows; ++u)
+            raw[u] = load_cols(p.partial + (d + u < last ? d + u : last) * 2 * p.dim, cols);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            if (d + u > last) break;
             float x[8];
-            load_upto8(p.partial + d * 2 * p.dim + col, p.dim - col, x);
+            cols_values(raw[u], cols, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] += x[j];
         }
     }
-    write_row<G>(p, key, col, acc);
-}
-
-constexpr int kClearRows = 64;
-
-// Rows that no token names, 64 rows a workgroup.
-template <typename G>
-__global__ __launch_bounds__(kThreads) void clear_rows_kernel(GradParams p) {
-    __shared__ uint32_t s_named[2];
-    if (threadIdx.x < 2) s_named[threadIdx.x] = 0u;
-    __syncthreads();
-    const int64_t row0 = (int64_t)blockIdx.x * kClearRows;
-    const int64_t rows = p.vocab - row0 < kClearRows ? p.vocab - row0 : kClearRows;
-    if (threadIdx.x < 64) {
-        const int64_t from = lower_bound(p.key, p.tokens, (uint32_t)row0);
-        for (int64_t t0 = from; t0 < p.tokens; t0 += 64) {
-            const int64_t t = t0 + threadIdx.x;
-            const uint32_t off = t < p.tokens ? p.key[t] - (uint32_t)row0 : 0xFFFFFFFFu;
-            if (off < rows) atomicOr(&s_named[off / 32], 1u << (off % 32));
-            if (__ballot(off >= rows) != 0ull) break;
-        }
-    }
-    __syncthreads();
-    const uint64_t named = (uint64_t)s_named[0] | ((uint64_t)s_named[1] << 32);
-    float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int r = 0; r < rows; ++r) {
-        if ((named >> r) & 1ull) continue;
-        G *dst = static_cast<G *>(p.grad) + (row0 + r) * p.dim;
-        for (int col = threadIdx.x * 8; col < p.dim; col += kThreads * 8) store_upto8(dst + col, p.dim - col, zero);
-    }
+    float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (p.accumulate) cols_values(load_cols(grad_row<G>(p, key), cols), cols, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] += acc[j] * p.scale;
+    store_cols(grad_row<G>(p, key), cols, x);
 }
 
 // ---- host side ----
@@ -362,6 +481,7 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 struct Layout {
     size_t key, idx, key2, idx2, hist, partial, bytes;
     int64_t chunks;
+    int32_t chunk, slices;
 };
 Layout layout_of(int64_t tokens, int64_t dim) {
     Layout l{};
@@ -371,36 +491,83 @@ Layout layout_of(int64_t tokens, int64_t dim) {
         at += up256(b);
         return was;
     };
-    l.chunks = (tokens + kChunk - 1) / kChunk;
+    l.slices = (int32_t)((dim + kCols - 1) / kCols);
+    // A wave's places are one after the other, so few tokens are cut finer: down to
+    // 8 places as long as the chip is not full of waves.
+    l.chunk = kMostChunk;
+    while (l.chunk > 8 && tokens / l.chunk * l.slices < 8192) l.chunk /= 2;
+    l.chunks = (tokens + l.chunk - 1) / l.chunk;
     l.key = take((size_t)tokens * 4), l.idx = take((size_t)tokens * 4);
-    if (tokens > kRankTokens) {
-        l.key2 = take((size_t)tokens * 4), l.idx2 = take((size_t)tokens * 4);
-        l.hist = take((size_t)kTiles * kMaxBins * 4);
-    }
+    if (tokens > kOneTile) l.key2 = take((size_t)tokens * 4), l.idx2 = take((size_t)tokens * 4);
+    if (tokens > kRankTokens) l.hist = take((size_t)kTiles * kMaxBins * 4);
     l.partial = take((size_t)(l.chunks * 2 * dim) * 4);
     l.bytes = at;
     return l;
 }
 
-// Sorts by digits of equal width, at most 10 bits each; the keys are 0 .. vocab.
-hipError_t sort_by_digits(const void *ids, bool i64, int64_t tokens, int64_t vocab, int64_t skip, uint32_t *key,
-                          uint32_t *idx, uint32_t *key2, uint32_t *idx2, uint32_t *hist, hipStream_t s) {
+constexpr int kClearWgs = 1024;  // of 1024 threads, four for each CU
+
+// Workgroups that clear n elements.
+uint32_t clear_wgs(int64_t n) {
+    const int64_t need = (n + 8191) / 8192;
+    return (uint32_t)(need < kClearWgs ? need : kClearWgs);
+}
+
+int bits_of(int64_t vocab) {  // the keys are 0 .. vocab
     int bits = 1;
     while ((vocab >> bits) != 0) ++bits;
-    const int passes = (bits + 9) / 10, width = (bits + passes - 1) / passes;
+    return bits;
+}
+
+struct Sort {
+    const void *ids;
+    bool i64;
+    int64_t tokens, vocab, skip;
+    uint32_t *key, *idx, *key2, *idx2, *hist;
+    void *clear;  // a gradient of n elements to clear beside the sort, or nullptr
+    int64_t n;
+};
+
+template <typename G>
+hipError_t sort_tokens(const Sort &q, hipStream_t s) {
+    const uint32_t clear = q.clear ? clear_wgs(q.n) : 0u;
+    if (q.tokens == 0) {
+        if (clear) clear_kernel<G><<<dim3(clear), dim3(1024), 0, s>>>(static_cast<G *>(q.clear), q.n);
+        return hipGetLastError();
+    }
+    if (q.tokens <= kRankTokens) {
+        const bool one = q.tokens <= kOneTile;
+        RankParams p{};
+        p.ids = q.ids, p.i64 = q.i64, p.tokens = (int32_t)q.tokens, p.vocab = q.vocab, p.skip = q.skip;
+        p.tile = one ? kOneTile : kTile;
+        // as many workgroups as there are CUs, where there are tokens for them
+        p.each = p.tokens > 8192 ? 64 : p.tokens > 4096 ? 32 : 16;
+        p.wgs = (p.tokens + p.each - 1) / p.each;
+        p.key_out = one ? q.key : q.key2, p.idx_out = one ? q.idx : q.idx2, p.grad = q.clear, p.n = q.n;
+        rank_tokens_kernel<G><<<dim3(p.wgs + clear), dim3(1024), 0, s>>>(p);
+        if (!one) {
+            int lanes = 2;
+            while (lanes * kTile < p.tokens) lanes *= 2;
+            merge_tiles_kernel<<<dim3((uint32_t)((q.tokens * lanes + kThreads - 1) / kThreads)), dim3(kThreads), 0, s>>>(
+                q.key2, q.idx2, p.tokens, kTile, lanes, q.key, q.idx);
+        }
+        return hipGetLastError();
+    }
+    const int bits = bits_of(q.vocab), passes = (bits + 9) / 10;
     DigitPass p{};
-    p.ids = ids, p.i64 = i64, p.tokens = tokens, p.vocab = vocab, p.skip = skip;
-    p.tile = ((tokens + kTiles - 1) / kTiles + 1023) / 1024 * 1024;
-    p.bins = 1 << width, p.hist = hist;
-    const uint32_t tiles = (uint32_t)((tokens + p.tile - 1) / p.tile);
+    p.ids = q.ids, p.i64 = q.i64, p.tokens = q.tokens, p.vocab = q.vocab, p.skip = q.skip;
+    p.tile = ((q.tokens + kTiles - 1) / kTiles + 1023) / 1024 * 1024;
+    p.tiles = (int)((q.tokens + p.tile - 1) / p.tile);
+    p.width = (bits + passes - 1) / passes, p.bins = 1 << p.width;
+    p.hist = q.hist, p.grad = q.clear, p.n = q.n;
     hipError_t err = hipSuccess;
     for (int i = 0; i < passes; ++i) {
         const bool to_main = (passes - 1 - i) % 2 == 0;  // the last pass ends in (key, idx)
-        p.first = i == 0, p.shift = i * width;
-        p.key = to_main ? key2 : key, p.idx = to_main ? idx2 : idx;
-        p.key_out = to_main ? key : key2, p.idx_out = to_main ? idx : idx2;
-        digit_count_kernel<<<dim3(tiles), dim3(1024), 0, s>>>(p);
-        digit_scatter_kernel<<<dim3(tiles), dim3(1024), 0, s>>>(p);
+        p.first = i == 0, p.shift = i * p.width;
+        p.key = to_main ? q.key2 : q.key, p.idx = to_main ? q.idx2 : q.idx;
+        p.key_out = to_main ? q.key : q.key2, p.idx_out = to_main ? q.idx : q.idx2;
+        digit_count_kernel<G><<<dim3(p.tiles + (i == 0 ? clear : 0u)), dim3(1024), 0, s>>>(p);
+        digit_scatter_kernel<<<dim3(p.tiles), dim3(1024), 0, s>>>(p);
         const hipError_t r = hipGetLastError();
         if (err == hipSuccess) err = r;
     }
@@ -408,31 +575,29 @@ hipError_t sort_by_digits(const void *ids, bool i64, int64_t tokens, int64_t voc
 }
 
 template <typename T, typename G>
-hipError_t gradient(const GradParams &p, hipStream_t s) {
-    hipError_t err = hipSuccess;
-    if (p.tokens > 0) {
-        const uint32_t wgs = (uint32_t)((p.chunks * p.slices + 3) / 4);
-        run_sum_kernel<T, G><<<dim3(wgs), dim3(kThreads), 0, s>>>(p);
-        err = hipGetLastError();
-        if (p.chunks > 1) {
-            run_join_kernel<G><<<dim3(wgs), dim3(kThreads), 0, s>>>(p);
-            const hipError_t r = hipGetLastError();
-            if (err == hipSuccess) err = r;
-        }
+hipError_t gradient(const Sort &q, const GradParams &p, hipStream_t s) {
+    hipError_t err = sort_tokens<G>(q, s);
+    if (err != hipSuccess || p.tokens == 0) return err;
+    const uint32_t wgs = (uint32_t)((p.chunks * p.slices + 3) / 4);
+    const bool narrow = p.dim < 8, lines = p.dim * sizeof(T) % 128 == 0;
+    const bool add = p.accumulate;
+    auto sum = narrow ? (add ? run_sum_kernel<T, G, true, false, true> : run_sum_kernel<T, G, true, false, false>)
+               : lines ? (add ? run_sum_kernel<T, G, false, true, true> : run_sum_kernel<T, G, false, true, false>)
+                       : (add ? run_sum_kernel<T, G, false, false, true> : run_sum_kernel<T, G, false, false, false>);
+    sum<<<dim3(wgs), dim3(kThreads), 0, s>>>(p);
+    if (p.chunks > 1) {
+        auto join = narrow ? run_join_kernel<G, true> : run_join_kernel<G, false>;
+        join<<<dim3(wgs), dim3(kThreads), 0, s>>>(p);
     }
-    if (!p.accumulate) {
-        clear_rows_kernel<G><<<dim3((uint32_t)((p.vocab + kClearRows - 1) / kClearRows)), dim3(kThreads), 0, s>>>(p);
-        const hipError_t r = hipGetLastError();
-        if (err == hipSuccess) err = r;
-    }
-    return err;
+    return hipGetLastError();
 }
 
 template <typename T, typename O>
 hipError_t lookup(const void *ids, bool i64, int64_t tokens, const void *table, int64_t vocab, int64_t dim,
                   float scale, void *out, hipStream_t s) {
     const int lanes = lanes_for(dim);
-    lookup_kernel<T, O><<<lookup_grid(tokens, lanes), dim3(kThreads), 0, s>>>(
+    auto kernel = dim < 8 ? lookup_kernel<T, O, true> : lookup_kernel<T, O, false>;
+    kernel<<<lookup_grid(tokens, lanes), dim3(kThreads), 0, s>>>(
         ids, i64, tokens, static_cast<const T *>(table), vocab, (int32_t)dim, scale, static_cast<O *>(out), lanes);
     return hipGetLastError();
 }
@@ -468,25 +633,19 @@ hipError_t launch_embedding_backward(const void *ids, bool i64, int64_t tokens, 
                                      nf4_dtype gt, bool accumulate, void *workspace, hipStream_t s) {
     const Layout l = layout_of(tokens, dim);
     char *ws = static_cast<char *>(workspace);
-    uint32_t *key = reinterpret_cast<uint32_t *>(ws + l.key), *idx = reinterpret_cast<uint32_t *>(ws + l.idx);
-    hipError_t err = hipSuccess;
-    if (tokens > kRankTokens) {
-        err = sort_by_digits(ids, i64, tokens, vocab, padding_id, key, idx, reinterpret_cast<uint32_t *>(ws + l.key2),
-                             reinterpret_cast<uint32_t *>(ws + l.idx2), reinterpret_cast<uint32_t *>(ws + l.hist), s);
-    } else if (tokens > 0) {
-        rank_kernel<<<dim3((uint32_t)((tokens + 63) / 64)), dim3(kThreads), 0, s>>>(ids, i64, (int32_t)tokens, vocab,
-                                                                                   padding_id, key, idx);
-        err = hipGetLastError();
-    }
-    if (err != hipSuccess) return err;
+    auto words = [ws](size_t at) { return reinterpret_cast<uint32_t *>(ws + at); };
+    Sort q{};
+    q.ids = ids, q.i64 = i64, q.tokens = tokens, q.vocab = vocab, q.skip = padding_id;
+    q.key = words(l.key), q.idx = words(l.idx), q.key2 = words(l.key2), q.idx2 = words(l.idx2), q.hist = words(l.hist);
+    q.clear = accumulate ? nullptr : grad, q.n = vocab * dim;
     GradParams p{};
-    p.key = key, p.idx = idx;
+    p.key = q.key, p.idx = q.idx;
     p.tokens = tokens, p.vocab = vocab, p.chunks = l.chunks;
-    p.dim = (int32_t)dim, p.slices = (int32_t)((dim + kCols - 1) / kCols);
+    p.dim = (int32_t)dim, p.slices = l.slices, p.chunk = l.chunk;
     p.scale = scale, p.dy = dy, p.grad = grad;
     p.partial = reinterpret_cast<float *>(ws + l.partial), p.accumulate = accumulate;
-    if (dt == NF4_BF16) return gt == NF4_BF16 ? gradient<Bf16, Bf16>(p, s) : gradient<Bf16, float>(p, s);
-    return gt == NF4_BF16 ? gradient<float, Bf16>(p, s) : gradient<float, float>(p, s);
+    if (dt == NF4_BF16) return gt == NF4_BF16 ? gradient<Bf16, Bf16>(q, p, s) : gradient<Bf16, float>(q, p, s);
+    return gt == NF4_BF16 ? gradient<float, Bf16>(q, p, s) : gradient<float, float>(q, p, s);
 }
 
 }  // namespace nf4

@@ -103,6 +103,90 @@ __device__ __forceinline__ void store_upto8(T *p, int64_t live, const float (&x)
         if (j < live) store1(p + j, x[j]);
 }
 
+// Eight elements as they lie in memory, and their values. Loads are kept apart
+// from the conversions so that several can be in flight.
+template <typename T> struct Raw8;
+template <> struct Raw8<Bf16> {
+    u32x4 v;
+};
+template <> struct Raw8<float> {
+    f32x4 a, b;
+};
+__device__ __forceinline__ Raw8<Bf16> load_raw(const Bf16 *p) {
+    return {reinterpret_cast<const u32x4_any2 *>(p)->v};
+}
+__device__ __forceinline__ Raw8<float> load_raw(const float *p) {
+    return {reinterpret_cast<const f32x4_any4 *>(p)->v, reinterpret_cast<const f32x4_any4 *>(p + 4)->v};
+}
+// The same from 16-byte aligned addresses, past the caches' usual order: for
+// data that no one reads again.
+__device__ __forceinline__ Raw8<Bf16> load_stream(const Bf16 *p) {
+    return {__builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p))};
+}
+__device__ __forceinline__ Raw8<float> load_stream(const float *p) {
+    return {__builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p)),
+            __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p + 4))};
+}
+__device__ __forceinline__ void values(const Raw8<Bf16> &r, float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = bf16_lo(r.v[j]);
+        x[2 * j + 1] = bf16_hi(r.v[j]);
+    }
+}
+__device__ __forceinline__ void values(const Raw8<float> &r, float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = r.a[j], x[4 + j] = r.b[j];
+}
+
+// The eight columns from `col` of a row of `dim`. Where fewer are left, the
+// load takes the row's last eight instead, and the values move down by `shift`
+// with zeros above, so that no lane leaves the row and none waits in a branch
+// of its own; lanes past the row load the same and get zeros. Rows of fewer
+// than eight elements (kNarrow) are loaded one by one.
+template <bool kNarrow> struct Cols {
+    int dim, col, base, live;
+    __device__ __forceinline__ Cols(int c, int d)
+        : dim(d), col(c), base(kNarrow ? 0 : (c < d - 8 ? c : d - 8)), live(d - c) {}
+};
+__device__ __forceinline__ Raw8<Bf16> raw_of(const float (&x)[8], const Bf16 *) {
+    Raw8<Bf16> r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+    return r;
+}
+__device__ __forceinline__ Raw8<float> raw_of(const float (&x)[8], const float *) {
+    return {f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]}};
+}
+template <typename T, bool kNarrow>
+__device__ __forceinline__ Raw8<T> load_cols(const T *row, const Cols<kNarrow> &c) {
+    if constexpr (!kNarrow) {
+        return load_raw(row + c.base);
+    } else {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = j < c.dim ? load1(row + j) : 0.0f;
+        return raw_of(x, row);
+    }
+}
+template <typename T, bool kNarrow>
+__device__ __forceinline__ void cols_values(const Raw8<T> &r, const Cols<kNarrow> &c, float (&x)[8]) {
+    values(r, x);
+    if ((c.dim & 7) == 0 && c.live > 0) return;
+    const int shift = c.col - c.base;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = (shift & o) ? (j + o < 8 ? x[j + o] : 0.0f) : x[j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = shift >= 8 ? 0.0f : x[j];
+}
+template <typename T, bool kNarrow>
+__device__ __forceinline__ void store_cols(T *row, const Cols<kNarrow> &c, const float (&x)[8]) {
+    if (c.live >= 8) return store8(row + c.col, x);
+    if (c.live > 0) store_upto8(row + c.col, c.live, x);
+}
+
 // Sum and maximum over aligned groups of `lanes` lanes of a wave (a power of
 // two, uniform; every lane active): every lane receives its group's result.
 template <int kCtrl>

@@ -79,10 +79,12 @@ def check_gradient(ids, dy, vocab, scale, grad0, got, padding=None):
     inside = (ids >= 0) & (ids < vocab)
     if padding is not None:
         inside &= ids != padding
-    at, rows = ids[inside], dy[inside].double() * scale
-    want = torch.zeros(vocab, dy.shape[1], dtype=torch.float64, device=dy.device).index_add_(0, at, rows)
-    size = torch.zeros_like(want).index_add_(0, at, rows.abs())
-    count = torch.bincount(at, minlength=vocab).double().unsqueeze(1)
+    # on the host, where many equal ids cost nothing
+    at, rows = ids[inside].cpu(), dy[inside].double().cpu() * scale
+    want = torch.zeros(vocab, dy.shape[1], dtype=torch.float64).index_add_(0, at, rows)
+    size = torch.zeros_like(want).index_add_(0, at, rows.abs()).to(dy.device)
+    count = torch.bincount(at, minlength=vocab).double().unsqueeze(1).to(dy.device)
+    want = want.to(dy.device)
     if grad0 is not None:
         want += grad0.double()
         size += grad0.double().abs()
