@@ -484,18 +484,26 @@ size_t nf4_grad_norm_workspace_size(const nf4_adamw_entry *entries, int32_t coun
 nf4_status nf4_grad_norm(const nf4_adamw_entry *entries, int32_t count, int32_t grad_dtype,
                          float *norm, void *workspace, size_t workspace_bytes, void *stream);
 
-/* One AdamW step of every entry, up to 48 per launch (see above).
+/* Bytes of device workspace of nf4_adamw_step: the table of the entries, where
+ * there are more than 48 (0 up to there); (size_t)-1 for count < 0. */
+size_t nf4_adamw_workspace_size(int32_t count);
+
+/* One AdamW step of every entry, in one launch (see above). Up to 48 entries travel
+ * in the kernel arguments; more are first copied into a table in the workspace.
  *   entries    host array, read during the call only
  *   moments    an nf4_moments
  *   grad_norm  device, one float, or NULL (no clipping; required where
  *              max_norm > 0). Where it is not finite the step changes nothing.
+ *   workspace  256-byte aligned, >= nf4_adamw_workspace_size(count) bytes (may be
+ *              NULL when that is 0); calls that overlap must not share one
  * Every entry is validated before anything is launched. Buffers of different
  * entries must not overlap. Gradients that are not finite are outside the
  * contract unless grad_norm is given. The step number and the seed are
  * arguments: a captured call replays the same step. */
 nf4_status nf4_adamw_step(const nf4_adamw_entry *entries, int32_t count, int32_t w_dtype,
                           int32_t grad_dtype, int32_t moments, const nf4_adamw_config *config,
-                          const float *grad_norm, void *stream);
+                          const float *grad_norm, void *workspace, size_t workspace_bytes,
+                          void *stream);
 
 /* The residual step between two blocks, one row of `dim` at a time:
  *   z  = w_post' y rsqrt(mean y^2 + eps)     (z = y where w_post is NULL)

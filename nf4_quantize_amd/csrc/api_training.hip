@@ -64,10 +64,12 @@ NF4_API nf4_status nf4_grad_norm(const nf4_adamw_entry *entries, int32_t count, 
                                           stream_of(stream)));
 }
 
+NF4_API size_t nf4_adamw_workspace_size(int32_t count) { return count < 0 ? (size_t)-1 : adamw_workspace(count); }
+
 NF4_API nf4_status nf4_adamw_step(const nf4_adamw_entry *entries, int32_t count, int32_t w_dtype, int32_t grad_dtype,
                                   int32_t moments, const nf4_adamw_config *config, const float *grad_norm,
-                                  void *stream) {
-    const nf4_status st = check_grads(entries, count);
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    nf4_status st = check_grads(entries, count);
     if (st != NF4_OK) return st;
     if (!config) return NF4_ERR_NULL;
     if (!is_dtype(w_dtype) || !is_dtype(grad_dtype)) return NF4_ERR_UNSUPPORTED;
@@ -89,8 +91,10 @@ NF4_API nf4_status nf4_adamw_step(const nf4_adamw_entry *entries, int32_t count,
             return NF4_ERR_ALIGN;
         if (eight && (!aligned(e.m_scale, 4) || !aligned(e.v_scale, 4))) return NF4_ERR_ALIGN;
     }
+    if ((st = check_workspace(adamw_workspace(count), workspace, workspace_bytes)) != NF4_OK) return st;
     return launch_status(launch_adamw(entries, count, static_cast<nf4_dtype>(w_dtype),
-                                      static_cast<nf4_dtype>(grad_dtype), eight, c, grad_norm, stream_of(stream)));
+                                      static_cast<nf4_dtype>(grad_dtype), eight, c, grad_norm, workspace,
+                                      stream_of(stream)));
 }
 
 namespace {

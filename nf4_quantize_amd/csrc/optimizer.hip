@@ -33,36 +33,67 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 }
 constexpr uint32_t kWeyl = 0x9E3779B9u;
 
+// One entry as the kernel reads it.
+struct AdamwItem {
+    void *w;
+    float *master;
+    const void *g;
+    void *m, *v;
+    float *ms, *vs;
+    int64_t n;
+    float step;      // lr / (1 - beta1^t)
+    float keep;      // 1 - lr weight_decay
+    uint32_t key;
+    uint32_t first;  // the entry's first workgroup in the launch
+};
+static_assert(sizeof(AdamwItem) == 80, "packed without holes");
 struct AdamwBatch {
-    void *w[kBatch];
-    float *master[kBatch];
-    const void *g[kBatch];
-    void *m[kBatch];
-    void *v[kBatch];
-    float *ms[kBatch];
-    float *vs[kBatch];
-    int64_t n[kBatch];
-    float step[kBatch];   // lr / (1 - beta1^t)
-    float keep[kBatch];   // 1 - lr weight_decay
-    uint32_t key[kBatch];
-    uint32_t first[kBatch];  // the entry's first workgroup in the launch
+    AdamwItem item[kBatch];
 };
 struct AdamwScalars {
     float beta1, one_beta1, beta2, one_beta2, eps, rbias2, max_norm;
-    int32_t passes;  // passes of kPass elements of a workgroup
+    int32_t count;  // entries of the table
     const float *norm;
+    const AdamwItem *table;   // in the workspace, where there are more than kBatch entries
+    const uint32_t *firsts;   // their `first`, one after the other
 };
 static_assert(sizeof(AdamwBatch) + sizeof(AdamwScalars) <= 4096, "kernel arguments");
 
-// The entry of workgroup wg: the last one whose first workgroup is not above it.
-template <int N>
-__device__ __forceinline__ int find_entry(const uint32_t (&first)[N], uint32_t wg) {
-    int k = 0;
-#pragma unroll
-    for (int j = 1; j < N; ++j) k = (wg >= first[j]) ? j : k;
-    return k;
+// Copies a batch of entries from the kernel arguments into the table.
+__global__ __launch_bounds__(kThreads) void adamw_table_kernel(AdamwBatch b, int32_t count, AdamwItem *table,
+                                                               uint32_t *firsts) {
+    for (int i = threadIdx.x; i < count; i += kThreads) {
+        table[i] = b.item[i];
+        firsts[i] = b.item[i].first;
+    }
 }
 
+// The entry of workgroup wg: the last one whose first workgroup is not above it.
+// All of the wave's lanes probe; the result is uniform.
+__device__ __forceinline__ int find_in_table(const uint32_t *firsts, int count, uint32_t wg) {
+    int lo = 0, hi = count;  // firsts[lo] <= wg, and firsts[hi] is above it or past the end
+    const int lane = threadIdx.x % 64;
+    while (hi - lo > 1) {
+        const int stride = (hi - lo + 63) / 64;
+        const int at = lo + lane * stride;
+        const uint64_t not_above = __ballot(at < hi && firsts[at] <= wg);  // a prefix that holds lane 0
+        lo += ((int)__popcll(not_above) - 1) * stride;
+        hi = lo + stride < hi ? lo + stride : hi;
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+template <typename B, int N>
+__device__ __forceinline__ int find_in_batch(const B (&item)[N], uint32_t wg) {
+    // eight at a time, then within the eight
+    int k = 0;
+#pragma unroll
+    for (int j = 8; j < N; j += 8) k = (wg >= item[j].first) ? j : k;
+    const B *eight = &item[k];
+    int in = 0;
+#pragma unroll
+    for (int j = 1; j < 8; ++j) in = (wg >= eight[j].first) ? j : in;
+    return k + in;
+}
 
 // Stochastic rounding of four values to packed E4M3 codes: gfx950's conversion
 // adds the top 20 random bits below the kept mantissa bits and cuts (subnormal
@@ -81,6 +112,8 @@ __device__ __forceinline__ void unpack_e4m3(uint32_t c, float scale, float *x) {
     x[0] = lo[0] * scale, x[1] = lo[1] * scale, x[2] = hi[0] * scale, x[3] = hi[1] * scale;
 }
 
+__device__ __forceinline__ float decode_e4m3(uint8_t c) { return __builtin_amdgcn_cvt_f32_fp8((int)c, 0); }
+
 // Scale of a block's storage and its reciprocal.
 __device__ __forceinline__ float storage_scale(float amax, float *inv) {
     float s = amax * (1.0f / kE4m3Max);
@@ -89,10 +122,13 @@ __device__ __forceinline__ float storage_scale(float amax, float *inv) {
     return s;
 }
 
-// One workgroup: passes x 2048 consecutive elements of one entry. A half-wave
-// holds one block of 256, eight elements a lane, so the block's maximum is a
-// reduction over 32 lanes in registers and every byte is moved once.
-template <typename W, typename G, bool kMaster, bool kEight>
+// One workgroup: 2048 consecutive elements of one entry. A half-wave holds one block of 256, eight elements a lane, so the block's maximum is a
+// reduction over 32 lanes in registers and every byte is moved once. Weights and
+// moments go past the caches' usual order (they are not read again before the
+// next step), gradients do not, and the workgroups run from the end of the list:
+// what the norm's pass read last is still in the memory-side cache. The 448
+// tensors take 365 us with both, 424 without.
+template <typename W, typename G, bool kMaster, bool kEight, bool kTable>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b, AdamwScalars c) {
     float clip = 1.0f;
     if (c.norm != nullptr) {
@@ -100,116 +136,123 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b, AdamwScal
         if (!(fabsf(norm) < INFINITY)) return;
         if (c.max_norm > 0.0f && norm > c.max_norm) clip = c.max_norm * (1.0f / norm);
     }
-    const int k = find_entry(b.first, blockIdx.x);
-    const int64_t n = b.n[k];
-    W *w = static_cast<W *>(b.w[k]);
-    float *master = b.master[k];
-    const G *g = static_cast<const G *>(b.g[k]);
-    const float step = b.step[k], keep = b.keep[k];
-    const uint32_t key = b.key[k];
-    const int64_t begin = (int64_t)(blockIdx.x - b.first[k]) * c.passes * kPass;
-
-    for (int p = 0; p < c.passes; ++p) {
-        const int64_t base = begin + (int64_t)p * kPass;
-        if (base >= n) return;
-        const int64_t i = base + threadIdx.x * kEach;
-        const int64_t live = n - i;  // may be <= 0: the lane still joins the reductions
-        float x[8], gr[8], m[8], v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = gr[j] = m[j] = v[j] = 0.0f;
-        if (live > 0) {
-            if constexpr (kMaster) load_upto8(master + i, live, x);
-            else load_upto8(w + i, live, x);
-            load_upto8(g + i, live, gr);
-            if constexpr (kEight) {
-                const uint8_t *mq = static_cast<const uint8_t *>(b.m[k]) + i;
-                const uint8_t *vq = static_cast<const uint8_t *>(b.v[k]) + i;
-                const float ms = b.ms[k][i / kMomentBlock], vs = b.vs[k][i / kMomentBlock];
-                uint32_t mw[2] = {0u, 0u}, vw[2] = {0u, 0u};
-                if (live >= 8) {
-                    const uint2 a = *reinterpret_cast<const uint2 *>(mq);
-                    const uint2 d = *reinterpret_cast<const uint2 *>(vq);
-                    mw[0] = a.x, mw[1] = a.y, vw[0] = d.x, vw[1] = d.y;
-                } else {
-                    for (int j = 0; j < (int)live; ++j) {
-                        mw[j / 4] |= (uint32_t)mq[j] << (8 * (j % 4));
-                        vw[j / 4] |= (uint32_t)vq[j] << (8 * (j % 4));
-                    }
-                }
-                unpack_e4m3(mw[0], ms, m), unpack_e4m3(mw[1], ms, m + 4);
-                unpack_e4m3(vw[0], vs, v), unpack_e4m3(vw[1], vs, v + 4);
-            } else {
-                load_upto8(static_cast<const float *>(b.m[k]) + i, live, m);
-                load_upto8(static_cast<const float *>(b.v[k]) + i, live, v);
-            }
+    const uint32_t wg = gridDim.x - 1 - blockIdx.x;
+    const AdamwItem e = kTable ? c.table[find_in_table(c.firsts, c.count, wg)] : b.item[find_in_batch(b.item, wg)];
+    const int64_t i = (int64_t)(wg - e.first) * kPass + threadIdx.x * kEach;
+    const int64_t live = e.n - i;  // may be <= 0: the lane still joins the reductions
+    W *w = static_cast<W *>(e.w) + i;
+    const G *g = static_cast<const G *>(e.g) + i;
+    float x[8], gr[8], m[8], v[8];
+    if (live >= 8) {  // the loads first, all in flight
+        const auto rg = load_raw(g);
+        if constexpr (kEight) {
+            const uint64_t mq = __builtin_nontemporal_load(reinterpret_cast<const uint64_t *>(static_cast<const uint8_t *>(e.m) + i));
+            const uint64_t vq = __builtin_nontemporal_load(reinterpret_cast<const uint64_t *>(static_cast<const uint8_t *>(e.v) + i));
+            const float ms = e.ms[i / kMomentBlock], vs = e.vs[i / kMomentBlock];
+            if constexpr (kMaster) values(load_stream(e.master + i), x);
+            else values(load_stream(w), x);
+            unpack_e4m3((uint32_t)mq, ms, m), unpack_e4m3((uint32_t)(mq >> 32), ms, m + 4);
+            unpack_e4m3((uint32_t)vq, vs, v), unpack_e4m3((uint32_t)(vq >> 32), vs, v + 4);
+        } else {
+            const auto rm = load_stream(static_cast<const float *>(e.m) + i);
+            const auto rv = load_stream(static_cast<const float *>(e.v) + i);
+            if constexpr (kMaster) values(load_stream(e.master + i), x);
+            else values(load_stream(w), x);
+            values(rm, m), values(rv, v);
         }
-        float ma = 0.0f, va = 0.0f;
+        values(rg, gr);
+    } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float gj = gr[j] * clip;
-            // product by product, without contraction: the stored codes follow
-            // from these fp32 values to the bit
-            m[j] = c.beta1 * m[j] + c.one_beta1 * gj;
-            v[j] = c.beta2 * v[j] + c.one_beta2 * (gj * gj);
-            // the hardware's reciprocal and root are within 1 ulp: the step is
-            // a small part of the weight it is added to
-            const float d = __builtin_amdgcn_sqrtf(v[j] * c.rbias2) + c.eps;
-            x[j] = fmaf(-step * m[j], __builtin_amdgcn_rcpf(d), x[j] * keep);
-            ma = fmaxf(ma, fabsf(m[j])), va = fmaxf(va, v[j]);
+            x[j] = gr[j] = m[j] = v[j] = 0.0f;
+            if (j >= live) continue;
+            x[j] = kMaster ? e.master[i + j] : load1(w + j);
+            gr[j] = load1(g + j);
+            if constexpr (kEight) {
+                m[j] = decode_e4m3(static_cast<const uint8_t *>(e.m)[i + j]) * e.ms[i / kMomentBlock];
+                v[j] = decode_e4m3(static_cast<const uint8_t *>(e.v)[i + j]) * e.vs[i / kMomentBlock];
+            } else {
+                m[j] = static_cast<const float *>(e.m)[i + j];
+                v[j] = static_cast<const float *>(e.v)[i + j];
+            }
         }
-        if (live > 0) {
-            if constexpr (kMaster) store_upto8(master + i, live, x);
-            store_upto8(w + i, live, x);
-        }
-        if constexpr (kEight) {
-            float rm, rv;
-            const float ms = storage_scale(max32(ma), &rm);
-            const float vs = storage_scale(max32(va), &rv);
-            uint32_t rndm[8], rndv[8];
+    }
+    float ma = 0.0f, va = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t r = mix((uint32_t)i * kWeyl + key + (uint32_t)j * kWeyl);
-                rndm[j] = r & 0xFFFF0000u, rndv[j] = r << 16;
-                m[j] = fminf(fmaxf(m[j] * rm, -kE4m3Max), kE4m3Max);
-                v[j] = fminf(fmaxf(v[j] * rv, kE4m3Min), kE4m3Max);
-            }
-            if (live > 0) {
-                uint8_t *mq = static_cast<uint8_t *>(b.m[k]) + i;
-                uint8_t *vq = static_cast<uint8_t *>(b.v[k]) + i;
-                const uint32_t mw[2] = {pack_e4m3_sr(m, rndm), pack_e4m3_sr(m + 4, rndm + 4)};
-                const uint32_t vw[2] = {pack_e4m3_sr(v, rndv), pack_e4m3_sr(v + 4, rndv + 4)};
-                if (live >= 8) {
-                    *reinterpret_cast<uint2 *>(mq) = make_uint2(mw[0], mw[1]);
-                    *reinterpret_cast<uint2 *>(vq) = make_uint2(vw[0], vw[1]);
-                } else {
-                    for (int j = 0; j < (int)live; ++j) {
-                        mq[j] = (uint8_t)(mw[j / 4] >> (8 * (j % 4)));
-                        vq[j] = (uint8_t)(vw[j / 4] >> (8 * (j % 4)));
-                    }
-                }
-                if (threadIdx.x % 32 == 0) {
-                    b.ms[k][i / kMomentBlock] = ms;
-                    b.vs[k][i / kMomentBlock] = vs;
-                }
-            }
+    for (int j = 0; j < 8; ++j) {
+        const float gj = gr[j] * clip;
+        // product by product, without contraction: the stored codes follow
+        // from these fp32 values to the bit
+        m[j] = c.beta1 * m[j] + c.one_beta1 * gj;
+        v[j] = c.beta2 * v[j] + c.one_beta2 * (gj * gj);
+        // the hardware's reciprocal and root are within 1 ulp: the step is
+        // a small part of the weight it is added to
+        const float d = __builtin_amdgcn_sqrtf(v[j] * c.rbias2) + c.eps;
+        x[j] = fmaf(-e.step * m[j], __builtin_amdgcn_rcpf(d), x[j] * e.keep);
+        ma = fmaxf(ma, fabsf(m[j])), va = fmaxf(va, v[j]);
+    }
+    if (live >= 8) {
+        if constexpr (kMaster) store_stream(e.master + i, x);
+        store_stream(w, x);
+    } else if (live > 0) {
+        if constexpr (kMaster) store_upto8(e.master + i, live, x);
+        store_upto8(w, live, x);
+    }
+    if constexpr (!kEight) {
+        if (live >= 8) {
+            store_stream(static_cast<float *>(e.m) + i, m);
+            store_stream(static_cast<float *>(e.v) + i, v);
         } else if (live > 0) {
-            store_upto8(static_cast<float *>(b.m[k]) + i, live, m);
-            store_upto8(static_cast<float *>(b.v[k]) + i, live, v);
+            store_upto8(static_cast<float *>(e.m) + i, live, m);
+            store_upto8(static_cast<float *>(e.v) + i, live, v);
+        }
+    } else {
+        float rm, rv;
+        const float ms = storage_scale(max32(ma), &rm);
+        const float vs = storage_scale(max32(va), &rv);
+        uint32_t rndm[8], rndv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t r = mix((uint32_t)i * kWeyl + e.key + (uint32_t)j * kWeyl);
+            rndm[j] = r & 0xFFFF0000u, rndv[j] = r << 16;
+            m[j] = __builtin_amdgcn_fmed3f(m[j] * rm, -kE4m3Max, kE4m3Max);
+            v[j] = __builtin_amdgcn_fmed3f(v[j] * rv, kE4m3Min, kE4m3Max);
+        }
+        if (live <= 0) return;
+        uint8_t *mq = static_cast<uint8_t *>(e.m) + i, *vq = static_cast<uint8_t *>(e.v) + i;
+        const uint32_t mw[2] = {pack_e4m3_sr(m, rndm), pack_e4m3_sr(m + 4, rndm + 4)};
+        const uint32_t vw[2] = {pack_e4m3_sr(v, rndv), pack_e4m3_sr(v + 4, rndv + 4)};
+        if (live >= 8) {
+            __builtin_nontemporal_store(mw[0] | (uint64_t)mw[1] << 32, reinterpret_cast<uint64_t *>(mq));
+            __builtin_nontemporal_store(vw[0] | (uint64_t)vw[1] << 32, reinterpret_cast<uint64_t *>(vq));
+        } else {
+            for (int j = 0; j < (int)live; ++j) {
+                mq[j] = (uint8_t)(mw[j / 4] >> (8 * (j % 4)));
+                vq[j] = (uint8_t)(vw[j / 4] >> (8 * (j % 4)));
+            }
+        }
+        if (threadIdx.x % 32 == 0) {
+            e.ms[i / kMomentBlock] = ms;
+            e.vs[i / kMomentBlock] = vs;
         }
     }
 }
 
 // ---- the gradients' norm ----
 
-constexpr int kNormBatch = 128;
-constexpr int64_t kNormChunk = 16384;  // elements of one partial sum
+constexpr int kNormBatch = 160;
+constexpr int kNormVecs = 8;                              // of a thread, in flight together
+constexpr int64_t kNormChunk = (int64_t)kPass * kNormVecs;  // elements of one partial sum
 
-struct NormBatch {
-    const void *g[kNormBatch];
-    int64_t n[kNormBatch];
-    uint32_t first[kNormBatch];
+struct NormItem {
+    const void *g;
+    int64_t n;
+    uint32_t first, pad;
 };
-static_assert(sizeof(NormBatch) <= 4000, "kernel arguments");
+struct NormBatch {
+    NormItem item[kNormBatch];
+};
+static_assert(sizeof(NormBatch) + 16 <= 4096, "kernel arguments");
 
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
@@ -233,17 +276,28 @@ __device__ __forceinline__ double block_sum(double x) {
 // Squares of 16384 consecutive gradients, each exact in fp64.
 template <typename G>
 __global__ __launch_bounds__(kThreads) void grad_square_kernel(NormBatch b, double *partial) {
-    const int k = find_entry(b.first, blockIdx.x);
-    const int64_t n = b.n[k];
-    const G *g = static_cast<const G *>(b.g[k]);
-    const int64_t begin = (int64_t)(blockIdx.x - b.first[k]) * kNormChunk;
-    const int64_t end = begin + kNormChunk < n ? begin + kNormChunk : n;
+    const NormItem e = b.item[find_in_batch(b.item, blockIdx.x)];
+    const int64_t begin = (int64_t)(blockIdx.x - e.first) * kNormChunk;
+    const G *g = static_cast<const G *>(e.g) + begin;
     double sum = 0.0;
-    for (int64_t i = begin + threadIdx.x * kEach; i < end; i += kPass) {
-        float x[8];
-        load_upto8(g + i, end - i, x);
+    if (e.n - begin >= kNormChunk) {
+        Raw8<G> raw[kNormVecs];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += (double)x[j] * (double)x[j];
+        for (int u = 0; u < kNormVecs; ++u) raw[u] = load_raw(g + u * kPass + threadIdx.x * kEach);
+#pragma unroll
+        for (int u = 0; u < kNormVecs; ++u) {
+            float x[8];
+            values(raw[u], x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fma((double)x[j], (double)x[j], sum);
+        }
+    } else {
+        for (int64_t i = threadIdx.x * kEach; i < e.n - begin; i += kPass) {
+            float x[8];
+            load_upto8(g + i, e.n - begin - i, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fma((double)x[j], (double)x[j], sum);
+        }
     }
     sum = block_sum<kThreads>(sum);
     if (threadIdx.x == 0) partial[blockIdx.x] = sum;
@@ -262,9 +316,14 @@ int64_t norm_partials(const nf4_adamw_entry *e, int32_t count) {
     return p;
 }
 
+// Entries of one kind (with or without a master weight). Up to kBatch of them
+// travel in the kernel arguments; more are first copied into a table in the
+// workspace, 48 a launch, so that one launch runs over all of them: the 448
+// adapters of a 32-layer stack took 10 launches of 17 million elements, each
+// with its own ramp and drain.
 template <typename W, typename G, bool kMaster, bool kEight>
 hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_adamw_config &cfg,
-                          const float *norm, hipStream_t s) {
+                          const float *norm, void *workspace, hipStream_t s) {
     const double bias1 = 1.0 - pow(cfg.beta1, (double)cfg.step);
     const double bias2 = 1.0 - pow(cfg.beta2, (double)cfg.step);
     AdamwScalars c{};
@@ -272,55 +331,80 @@ hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_ada
     c.beta2 = (float)cfg.beta2, c.one_beta2 = (float)(1.0 - cfg.beta2);
     c.eps = cfg.eps, c.rbias2 = (float)(1.0 / bias2);
     c.max_norm = cfg.max_norm, c.norm = norm;
-    int64_t total = 0;
-    for (int32_t i = 0; i < count; ++i) total += (e[i].n + kPass - 1) / kPass;
-    c.passes = 1;
+    auto mine = [&](int32_t i) { return e[i].n > 0 && (e[i].master != nullptr) == kMaster; };
+    int32_t total = 0;
+    for (int32_t i = 0; i < count; ++i) total += mine(i) ? 1 : 0;
+    if (total == 0) return hipSuccess;
+    const bool table = total > kBatch;
+    AdamwItem *items = static_cast<AdamwItem *>(workspace);
+    uint32_t *firsts = reinterpret_cast<uint32_t *>(items + count);
     AdamwBatch b{};
-    int used = 0;
+    int used = 0;       // entries of the batch
+    int32_t done = 0, from = 0;  // entries in the table; its first entry of the next launch
     int64_t wgs = 0;
     hipError_t err = hipSuccess;
-    auto flush = [&] {
-        if (used == 0) return;
-        for (int j = used; j < kBatch; ++j) b.first[j] = UINT32_MAX;
-        adamw_kernel<W, G, kMaster, kEight><<<dim3((uint32_t)wgs), dim3(kThreads), 0, s>>>(b, c);
+    auto note = [&] {
         const hipError_t r = hipGetLastError();
         if (err == hipSuccess) err = r;
-        used = 0, wgs = 0;
+    };
+    auto copy = [&] {  // the batch into the table
+        if (used == 0) return;
+        adamw_table_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(b, used, items + done, firsts + done);
+        note();
+        done += used, used = 0;
+    };
+    auto run = [&] {
+        if (wgs == 0) return;
+        if (table) {
+            copy();
+            c.table = items + from, c.firsts = firsts + from, c.count = done - from;
+            adamw_kernel<W, G, kMaster, kEight, true><<<dim3((uint32_t)wgs), dim3(kThreads), 0, s>>>(b, c);
+            from = done;
+        } else {
+            for (int j = used; j < kBatch; ++j) b.item[j].first = UINT32_MAX;
+            adamw_kernel<W, G, kMaster, kEight, false><<<dim3((uint32_t)wgs), dim3(kThreads), 0, s>>>(b, c);
+            used = 0;
+        }
+        note();
+        wgs = 0;
     };
     constexpr int64_t kMaxWgs = (int64_t(1) << 31) / kThreads;
     for (int32_t i = 0; i < count; ++i) {
-        if (e[i].n == 0) continue;
-        if ((e[i].master != nullptr) != kMaster) continue;
-        const int64_t need = (e[i].n + (int64_t)c.passes * kPass - 1) / ((int64_t)c.passes * kPass);
-        if (used == kBatch || wgs + need > kMaxWgs) flush();
-        b.w[used] = e[i].w, b.master[used] = e[i].master, b.g[used] = e[i].grad;
-        b.m[used] = e[i].m, b.v[used] = e[i].v, b.ms[used] = e[i].m_scale, b.vs[used] = e[i].v_scale;
-        b.n[used] = e[i].n;
-        b.step[used] = (float)((double)e[i].lr / bias1);
-        b.keep[used] = (float)(1.0 - (double)e[i].lr * (double)e[i].weight_decay);
-        b.key[used] = mix(mix((uint32_t)i * kWeyl + (uint32_t)(cfg.seed >> 32)) + (uint32_t)cfg.seed);
-        b.first[used] = (uint32_t)wgs;
+        if (!mine(i)) continue;
+        const int64_t need = (e[i].n + kPass - 1) / kPass;
+        if (wgs + need > kMaxWgs) run();
+        if (used == kBatch) copy();  // only with a table: otherwise all entries fit
+        AdamwItem &t = b.item[used++];
+        t.w = e[i].w, t.master = e[i].master, t.g = e[i].grad, t.m = e[i].m, t.v = e[i].v;
+        t.ms = e[i].m_scale, t.vs = e[i].v_scale, t.n = e[i].n;
+        t.step = (float)((double)e[i].lr / bias1);
+        t.keep = (float)(1.0 - (double)e[i].lr * (double)e[i].weight_decay);
+        t.key = mix(mix((uint32_t)i * kWeyl + (uint32_t)(cfg.seed >> 32)) + (uint32_t)cfg.seed);
+        t.first = (uint32_t)wgs;
         wgs += need;
-        ++used;
     }
-    flush();
+    run();
     return err;
 }
 
 template <typename W, typename G>
 hipError_t adamw_typed(const nf4_adamw_entry *e, int32_t count, bool eight, const nf4_adamw_config &c,
-                       const float *norm, hipStream_t s) {
-    hipError_t err = eight ? adamw_launches<W, G, false, true>(e, count, c, norm, s)
-                           : adamw_launches<W, G, false, false>(e, count, c, norm, s);
+                       const float *norm, void *ws, hipStream_t s) {
+    hipError_t err = eight ? adamw_launches<W, G, false, true>(e, count, c, norm, ws, s)
+                           : adamw_launches<W, G, false, false>(e, count, c, norm, ws, s);
     if constexpr (sizeof(W) == 2) {
-        const hipError_t r = eight ? adamw_launches<W, G, true, true>(e, count, c, norm, s)
-                                   : adamw_launches<W, G, true, false>(e, count, c, norm, s);
+        const hipError_t r = eight ? adamw_launches<W, G, true, true>(e, count, c, norm, ws, s)
+                                   : adamw_launches<W, G, true, false>(e, count, c, norm, ws, s);
         if (err == hipSuccess) err = r;
     }
     return err;
 }
 
 }  // namespace
+
+size_t adamw_workspace(int32_t count) {
+    return count > kBatch ? (size_t)count * (sizeof(AdamwItem) + sizeof(uint32_t)) : 0;
+}
 
 size_t grad_norm_workspace(const nf4_adamw_entry *e, int32_t count) {
     return (size_t)norm_partials(e, count) * sizeof(double);
@@ -335,7 +419,7 @@ hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype g
     hipError_t err = hipSuccess;
     auto flush = [&] {
         if (used == 0) return;
-        for (int j = used; j < kNormBatch; ++j) b.first[j] = UINT32_MAX;
+        for (int j = used; j < kNormBatch; ++j) b.item[j].first = UINT32_MAX;
         if (gt == NF4_BF16)
             grad_square_kernel<Bf16><<<dim3((uint32_t)wgs), dim3(kThreads), 0, s>>>(b, partial + done);
         else
@@ -349,7 +433,7 @@ hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype g
         if (e[i].n == 0) continue;
         const int64_t need = (e[i].n + kNormChunk - 1) / kNormChunk;
         if (used == kNormBatch || wgs + need > kMaxWgs) flush();
-        b.g[used] = e[i].grad, b.n[used] = e[i].n, b.first[used] = (uint32_t)wgs;
+        b.item[used] = NormItem{e[i].grad, e[i].n, (uint32_t)wgs, 0u};
         wgs += need;
         ++used;
     }
@@ -360,12 +444,13 @@ hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype g
 }
 
 hipError_t launch_adamw(const nf4_adamw_entry *e, int32_t count, nf4_dtype wt, nf4_dtype gt,
-                        bool eight, const nf4_adamw_config &c, const float *norm, hipStream_t s) {
+                        bool eight, const nf4_adamw_config &c, const float *norm, void *workspace,
+                        hipStream_t s) {
     if (wt == NF4_BF16)
-        return gt == NF4_BF16 ? adamw_typed<Bf16, Bf16>(e, count, eight, c, norm, s)
-                              : adamw_typed<Bf16, float>(e, count, eight, c, norm, s);
-    return gt == NF4_BF16 ? adamw_typed<float, Bf16>(e, count, eight, c, norm, s)
-                          : adamw_typed<float, float>(e, count, eight, c, norm, s);
+        return gt == NF4_BF16 ? adamw_typed<Bf16, Bf16>(e, count, eight, c, norm, workspace, s)
+                              : adamw_typed<Bf16, float>(e, count, eight, c, norm, workspace, s);
+    return gt == NF4_BF16 ? adamw_typed<float, Bf16>(e, count, eight, c, norm, workspace, s)
+                          : adamw_typed<float, float>(e, count, eight, c, norm, workspace, s);
 }
 
 }  // namespace nf4

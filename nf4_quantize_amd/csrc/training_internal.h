@@ -15,7 +15,8 @@ hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype g
                             void *workspace, hipStream_t s);
 hipError_t launch_adamw(const nf4_adamw_entry *e, int32_t count, nf4_dtype wt, nf4_dtype gt,
                         bool eight, const nf4_adamw_config &c, const float *grad_norm,
-                        hipStream_t s);
+                        void *workspace, hipStream_t s);
+size_t adamw_workspace(int32_t count);
 
 struct ResidualNormIn {
     const void *dx, *dh_out;  // backward only
@@ -118,14 +119,24 @@ __device__ __forceinline__ Raw8<Bf16> load_raw(const Bf16 *p) {
 __device__ __forceinline__ Raw8<float> load_raw(const float *p) {
     return {reinterpret_cast<const f32x4_any4 *>(p)->v, reinterpret_cast<const f32x4_any4 *>(p + 4)->v};
 }
-// The same from 16-byte aligned addresses, past the caches' usual order: for
-// data that no one reads again.
+// The same at 16-byte aligned addresses, past the caches' usual order: for
+// data that is not read again soon.
 __device__ __forceinline__ Raw8<Bf16> load_stream(const Bf16 *p) {
     return {__builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p))};
 }
 __device__ __forceinline__ Raw8<float> load_stream(const float *p) {
     return {__builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p)),
             __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p + 4))};
+}
+__device__ __forceinline__ void store_stream(Bf16 *p, const float (&x)[8]) {
+    u32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+    __builtin_nontemporal_store(r, reinterpret_cast<u32x4 *>(p));
+}
+__device__ __forceinline__ void store_stream(float *p, const float (&x)[8]) {
+    __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4 *>(p));
+    __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4 *>(p + 4));
 }
 __device__ __forceinline__ void values(const Raw8<Bf16> &r, float (&x)[8]) {
 #pragma unroll

@@ -36,7 +36,8 @@ def declare(L):
     for name, restype, args in (
             ("nf4_grad_norm_workspace_size", sz, [p, i32]),
             ("nf4_grad_norm", i32, [p, i32, i32, p, p, sz, p]),
-            ("nf4_adamw_step", i32, [p, i32, i32, i32, i32, ctypes.POINTER(nf4_adamw_config), p, p]),
+            ("nf4_adamw_step", i32, [p, i32, i32, i32, i32, ctypes.POINTER(nf4_adamw_config), p, p, sz, p]),
+            ("nf4_adamw_workspace_size", sz, [i32]),
             ("nf4_residual_norm_forward", i32, [shape] + [p] * 10),
             ("nf4_residual_norm_backward_workspace_size", sz, [shape]),
             ("nf4_residual_norm_backward", i32, [shape] + [p] * 15 + [sz, p]),
@@ -130,12 +131,11 @@ class NF4AdamW:
         e["w"] = [p.data_ptr() for p in self.params]
         e["master"] = [0 if mw is None else mw.data_ptr() for mw in self.masters]
         e["n"] = self._numels
-        self._norm_ws = torch.empty(max(1, self._norm_bytes()), dtype=torch.uint8, device=self.device)
+        L = _nq.lib()
+        size = max(_size(L.nf4_grad_norm_workspace_size(e.ctypes.data, len(e)), "nf4_grad_norm_workspace_size"),
+                   _size(L.nf4_adamw_workspace_size(len(e)), "nf4_adamw_workspace_size"))
+        self._workspace = torch.empty(max(1, size), dtype=torch.uint8, device=self.device)
         self._new_state()
-
-    def _norm_bytes(self):
-        return _size(_nq.lib().nf4_grad_norm_workspace_size(self._entries.ctypes.data, len(self._entries)),
-                     "nf4_grad_norm_workspace_size")
 
     def _new_state(self):
         import torch
@@ -213,14 +213,15 @@ class NF4AdamW:
         number = self.steps + 1 if step is None else int(step)
         stream = _nq._stream(dev)
         clip = self.max_grad_norm > 0
+        ws, ws_bytes = self._workspace.data_ptr(), self._workspace.numel()
         with torch.cuda.device(dev):
             if clip:
-                _nq._check(L.nf4_grad_norm(at, count, grad_dtype, self.grad_norm.data_ptr(), self._norm_ws.data_ptr(),
-                                           self._norm_ws.numel(), stream), "nf4_grad_norm")
+                _nq._check(L.nf4_grad_norm(at, count, grad_dtype, self.grad_norm.data_ptr(), ws, ws_bytes,
+                                           stream), "nf4_grad_norm")
             config = nf4_adamw_config(*self.betas, self.eps, self.max_grad_norm, number,
                                       (self.seed + number if seed is None else int(seed)) & 0xFFFFFFFFFFFFFFFF)
             _nq._check(L.nf4_adamw_step(at, count, _nq._dtype_code(self.dtype), grad_dtype, self.state_bits,
-                                        ctypes.byref(config), self.grad_norm.data_ptr() if clip else None, stream),
+                                        ctypes.byref(config), self.grad_norm.data_ptr() if clip else None, ws, ws_bytes, stream),
                        "nf4_adamw_step")
         self.steps = number
 

@@ -33,12 +33,12 @@ def entries(*changes):
     return e
 
 
-def adamw(L, e, count=None, wt=1, gt=1, moments=8, norm=None, cfg=True, **c):
+def adamw(L, e, count=None, wt=1, gt=1, moments=8, norm=None, cfg=True, ws=None, wsb=0, **c):
     f = dict(beta1=0.9, beta2=0.999, eps=1e-8, max_norm=0.0, step=1, seed=0)
     f.update(c)
     config = training.nf4_adamw_config(**f)
     return L.nf4_adamw_step(e.ctypes.data, len(e) if count is None else count, wt, gt, moments,
-                            ctypes.byref(config) if cfg else None, norm, None)
+                            ctypes.byref(config) if cfg else None, norm, ws, wsb, None)
 
 
 def test_adamw_refusals(L):
@@ -47,7 +47,7 @@ def test_adamw_refusals(L):
     assert adamw(L, entries({}), count=0) == OK
     assert adamw(L, entries({"n": 0, "w": 0, "grad": 0})) == OK
     assert adamw(L, entries({}), count=-1) == SIZE
-    assert L.nf4_adamw_step(None, 2, 1, 1, 8, None, None, None) == NULL
+    assert L.nf4_adamw_step(None, 2, 1, 1, 8, None, None, None, 0, None) == NULL
     assert adamw(L, entries(bad), cfg=False) == NULL
     assert adamw(L, entries(bad), wt=2) == UNSUPPORTED
     assert adamw(L, entries(bad), gt=-1) == UNSUPPORTED
@@ -67,6 +67,13 @@ def test_adamw_refusals(L):
         assert adamw(L, entries(bad), **c) == SIZE, c
     assert adamw(L, entries(bad), max_norm=1.0) == NULL       # clipping without a norm
     assert adamw(L, entries(bad), norm=FAKE + 2) == ALIGN
+    # more entries than the kernel arguments hold go through the workspace
+    size = L.nf4_adamw_workspace_size
+    assert size(48) == 0 and size(49) == 49 * 84 and size(-1) == ctypes.c_size_t(-1).value
+    many = entries(*[{}] * 49)
+    assert adamw(L, many) == WORKSPACE
+    assert adamw(L, many, ws=FAKE, wsb=size(49) - 1) == WORKSPACE
+    assert adamw(L, many, ws=FAKE + 128, wsb=size(49)) == ALIGN
     # 32-bit moments have no scales: the refusal of the entry after shows that this one passed
     assert adamw(L, entries({"m_scale": 0, "v_scale": 0}, {"w": 0}), moments=32) == NULL
 
