@@ -21,91 +21,154 @@ struct NormParams {
     int64_t rows;
     int32_t dim;
     float inv_dim, eps, alpha, off;
-    int32_t lanes;       // lanes of a row: a power of two, 8 .. 1024
+    int32_t lanes;       // lanes of a row: 8 .. 64, a power of two, or the whole workgroup
     int32_t gate_kind;
     bool w_bf16;
     float *partial;      // backward: [workgroups][3][dim]
 };
 
-// Eight weights from column `col` (fp32 or bf16).
-__device__ __forceinline__ void load_weight(const void *w, bool bf16, int col, int live, float (&x)[8]) {
-    if (bf16) load_upto8(static_cast<const Bf16 *>(w) + col, live, x);
-    else load_upto8(static_cast<const float *>(w) + col, live, x);
-}
+// How a row lies in memory: fewer than eight elements; any number; or whole
+// cache lines (dim a multiple of 64), which are moved past the caches' usual
+// order, as nothing here is read twice.
+enum RowKind { kRowNarrow, kRowAny, kRowLines };
 
-// Sums of kK values over each row's group of lanes, the same bits in every
-// lane. Groups of more than a wave meet in `part`, one slot a wave; the caller
-// alternates two buffers, so that one barrier a call is enough.
-template <int kK>
-__device__ __forceinline__ void row_sums(float (&x)[kK], int lanes, float (*part)[kK]) {
+template <RowKind kKind, typename T>
+__device__ __forceinline__ Raw8<T> load_row(const T *row, const Cols<kKind == kRowNarrow> &c) {
+    if constexpr (kKind == kRowLines) return load_stream(row + (uint32_t)c.base);
+    else return load_cols(row, c);
+}
+template <RowKind kKind, typename T>
+__device__ __forceinline__ void row_values(const Raw8<T> &r, const Cols<kKind == kRowNarrow> &c, float (&x)[8]) {
+    if constexpr (kKind == kRowLines) {
+        values(r, x);
 #pragma unroll
-    for (int k = 0; k < kK; ++k) x[k] = group_sum(x[k], lanes < 64 ? lanes : 64);
-    if (lanes <= 64) return;
-    const int wave = threadIdx.x / 64, waves = lanes / 64, first = wave / waves * waves;
-    if (threadIdx.x % 64 == 0)
-#pragma unroll
-        for (int k = 0; k < kK; ++k) part[wave][k] = x[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kK; ++k) {
-        float t = 0.0f;
-        for (int j = 0; j < waves; ++j) t += part[first + j][k];
-        x[k] = t;
+        for (int j = 0; j < 8; ++j) x[j] = c.live > 0 ? x[j] : 0.0f;
+    } else {
+        cols_values(r, c, x);
+    }
+}
+template <RowKind kKind, typename T>
+__device__ __forceinline__ void store_row(T *row, const Cols<kKind == kRowNarrow> &c, const float (&x)[8]) {
+    if constexpr (kKind == kRowLines) {
+        if (c.live > 0) store_stream(row + (uint32_t)c.col, x);
+    } else {
+        store_cols(row, c, x);
     }
 }
 
-template <typename T, typename R, int kVec>
+// Eight weights of the columns (fp32 or bf16).
+template <bool kNarrow>
+__device__ __forceinline__ void load_weight(const void *w, bool bf16, const Cols<kNarrow> &c, float (&x)[8]) {
+    if (bf16) cols_values(load_cols(static_cast<const Bf16 *>(w), c), c, x);
+    else cols_values(load_cols(static_cast<const float *>(w), c), c, x);
+}
+
+// Sums of kK values over each row's lanes, the same bits in every lane. A row of
+// more than a wave (kWide) is the whole workgroup's, and its waves meet in `part`; the
+// caller alternates two buffers, so that one barrier a call is enough.
+template <bool kWide, int kK>
+__device__ __forceinline__ void row_sums(float (&x)[kK], int lanes, float (*part)[16]) {
+#pragma unroll
+    for (int k = 0; k < kK; ++k) x[k] = group_sum(x[k], kWide ? 64 : lanes);
+    if constexpr (!kWide) return;
+    const int lane = threadIdx.x % 64, waves = blockDim.x / 64;
+    if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < kK; ++k) part[k][threadIdx.x / 64] = x[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kK; ++k) x[k] = group_sum(lane % 16 < waves ? part[k][lane % 16] : 0.0f, 16);
+}
+
+// The columns' weights: kept by workgroups of one vector a lane, which take many
+// rows, and loaded for each row by the others.
+template <bool kNarrow>
+struct Weights {
+    float pre[8], post[8], gate[8];
+    __device__ __forceinline__ void load(const NormParams &p, bool channel, const Cols<kNarrow> &c) {
+        load_weight(p.in.w_pre, p.w_bf16, c, pre);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) pre[j] += p.off, post[j] = 1.0f, gate[j] = 1.0f;
+        if (p.in.w_post) {
+            load_weight(p.in.w_post, p.w_bf16, c, post);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) post[j] += p.off;
+        }
+        if (channel) load_weight(p.in.gate, p.w_bf16, c, gate);
+    }
+};
+
+// A workgroup takes every gridDim.x-th set of rows. With one vector a lane it
+// loads the next set while it works on one.
+template <typename T, typename R, int kVec, RowKind kKind, bool kWide>
 __global__ __launch_bounds__(1024) void residual_norm_forward_kernel(NormParams p) {
-    __shared__ float part[2][16][1];
-    const int lane = threadIdx.x & (p.lanes - 1), groups = blockDim.x / p.lanes;
+    __shared__ float part[2][1][16];
+    constexpr bool kNarrow = kKind == kRowNarrow, kOne = kVec == 1;
+    typedef Cols<kNarrow> C;
+    const int lanes = kWide ? blockDim.x : p.lanes;
+    const int groups = kWide ? 1 : blockDim.x / lanes, group = kWide ? 0 : threadIdx.x / lanes;
+    const int lane = kWide ? threadIdx.x : threadIdx.x % lanes;
     const T *y = static_cast<const T *>(p.in.y);
+    const R *h_in = static_cast<const R *>(p.in.h);
+    const bool post = p.in.w_post != nullptr, channel = y && p.gate_kind == NF4_GATE_CHANNEL;
+    auto col = [&](int v) { return C((v * lanes + lane) * 8, p.dim); };
+    Weights<kNarrow> w;
+    Raw8<T> raw_y[kVec];
+    Raw8<R> raw_h[kVec];
+    auto load = [&](int64_t r0) {
+        const int64_t row = r0 + group < p.rows ? r0 + group : p.rows - 1;
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+            raw_h[v] = load_row<kKind>(h_in + row * p.dim, col(v));
+            if (y) raw_y[v] = load_row<kKind>(y + row * p.dim, col(v));
+        }
+    };
+    const int64_t first = (int64_t)blockIdx.x * groups, stride = (int64_t)gridDim.x * groups;
+    if constexpr (kOne) {
+        load(first);
+        w.load(p, channel, col(0));
+    }
     int turn = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += (int64_t)gridDim.x * groups) {
-        const int64_t row = r0 + threadIdx.x / p.lanes, at = row * p.dim;
+    for (int64_t r0 = first; r0 < p.rows; r0 += stride) {
+        const int64_t row = r0 + group, at = row * p.dim;
         const bool live_row = row < p.rows;
+        if constexpr (!kOne) load(r0);
         float h[kVec][8], z[kVec][8];
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
-            const int col = (v * p.lanes + lane) * 8, live = live_row ? p.dim - col : 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[v][j] = z[v][j] = 0.0f;
-            if (live > 0) {
-                load_upto8(static_cast<const R *>(p.in.h) + at + col, live, h[v]);
-                if (y) load_upto8(y + at + col, live, z[v]);
-            }
+            row_values<kKind>(raw_h[v], col(v), h[v]);
+            if (y) row_values<kKind>(raw_y[v], col(v), z[v]);
         }
+        if constexpr (kOne)
+            if (r0 + stride < p.rows) load(r0 + stride);
         if (y) {
             float r2 = 1.0f;
-            if (p.in.w_post) {
+            if (post) {
                 float s[1] = {0.0f};
 #pragma unroll
                 for (int v = 0; v < kVec; ++v)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) s[0] += z[v][j] * z[v][j];
-                row_sums<1>(s, p.lanes, part[turn]);
+                row_sums<kWide>(s, lanes, part[turn]);
                 turn ^= 1;
                 r2 = 1.0f / sqrtf(s[0] * p.inv_dim + p.eps);
                 if (live_row && lane == 0 && p.out.rstd_post) p.out.rstd_post[row] = r2;
             }
 #pragma unroll
             for (int v = 0; v < kVec; ++v) {
-                const int col = (v * p.lanes + lane) * 8, live = live_row ? p.dim - col : 0;
-                if (live <= 0) continue;
-                float w[8];
-                if (p.in.w_post) {
-                    load_weight(p.in.w_post, p.w_bf16, col, live, w);
+                if constexpr (!kOne) w.load(p, channel, col(v));
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) z[v][j] *= r2 * (w[j] + p.off);
-                }
-                if (p.gate_kind != NF4_GATE_NONE) {
-                    if (p.gate_kind == NF4_GATE_CHANNEL) load_weight(p.in.gate, p.w_bf16, col, live, w);
-                    else load_upto8(static_cast<const T *>(p.in.gate) + at + col, live, w);
+                for (int j = 0; j < 8; ++j) z[v][j] *= r2 * w.post[j];
+                if (p.gate_kind == NF4_GATE_TOKEN) {
+                    const int64_t there = (live_row ? row : p.rows - 1) * p.dim;
+                    float g[8];
+                    row_values<kKind>(load_row<kKind>(static_cast<const T *>(p.in.gate) + there, col(v)), col(v), g);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) z[v][j] *= w[j];
+                    for (int j = 0; j < 8; ++j) z[v][j] *= g[j];
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) h[v][j] += p.alpha * z[v][j];
-                store_upto8(static_cast<R *>(p.out.h) + at + col, live, h[v]);
+                for (int j = 0; j < 8; ++j) h[v][j] += p.alpha * (z[v][j] * w.gate[j]);
+                if (live_row) store_row<kKind>(static_cast<R *>(p.out.h) + at, col(v), h[v]);
             }
         }
         float s[1] = {0.0f};
@@ -113,39 +176,59 @@ __global__ __launch_bounds__(1024) void residual_norm_forward_kernel(NormParams 
         for (int v = 0; v < kVec; ++v)
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[0] += h[v][j] * h[v][j];
-        row_sums<1>(s, p.lanes, part[turn]);
+        row_sums<kWide>(s, lanes, part[turn]);
         turn ^= 1;
         const float r1 = 1.0f / sqrtf(s[0] * p.inv_dim + p.eps);
         if (live_row && lane == 0 && p.out.rstd_pre) p.out.rstd_pre[row] = r1;
+        if (!live_row) continue;
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
-            const int col = (v * p.lanes + lane) * 8, live = live_row ? p.dim - col : 0;
-            if (live <= 0) continue;
-            float w[8];
-            load_weight(p.in.w_pre, p.w_bf16, col, live, w);
+            if constexpr (!kOne) w.load(p, false, col(v));
+            float x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = h[v][j] * (r1 * (w[j] + p.off));
-            store_upto8(static_cast<T *>(p.out.x) + at + col, live, w);
+            for (int j = 0; j < 8; ++j) x[j] = h[v][j] * (r1 * w.pre[j]);
+            store_row<kKind>(static_cast<T *>(p.out.x) + at, col(v), x);
         }
     }
 }
 
-// Each workgroup takes every gridDim.x-th set of rows and keeps its columns'
-// share of the weights' gradients in registers until its last row.
+// One vector of a row's inputs in the backward pass; kToken: the gate is one.
+template <typename T, typename R, RowKind kKind, bool kToken>
+struct BackwardRow {
+    Raw8<T> dx, y, gate[kToken ? 1 : 0];
+    Raw8<R> h, dh;
+    typedef Cols<kKind == kRowNarrow> C;
+    __device__ __forceinline__ void load(const NormParams &p, int64_t at, const C &c) {
+        h = load_row<kKind>(static_cast<const R *>(p.in.h) + at, c);
+        if (p.in.dx) dx = load_row<kKind>(static_cast<const T *>(p.in.dx) + at, c);
+        if (p.in.dh_out) dh = load_row<kKind>(static_cast<const R *>(p.in.dh_out) + at, c);
+        if (p.in.y) y = load_row<kKind>(static_cast<const T *>(p.in.y) + at, c);
+        if constexpr (kToken) gate[0] = load_row<kKind>(static_cast<const T *>(p.in.gate) + at, c);
+    }
+};
+
+// As the forward: every gridDim.x-th set of rows, the next one's loads in
+// flight. A workgroup keeps its columns' share of the weights' gradients in
+// registers until its last row. With more than one vector a lane there is no room
+// for a row beside them, and the second half of the work loads it again from the
+// caches.
 //
 // One round of sums serves both norms: with e = alpha gate w_post' n2 the inner
 // product of the second, mean(dz w_post' n2), is mean(e dh), and dh is known up
 // to the first one's mean c1 = mean(dx w_pre' n1):
 //   sum e dh = sum e (dh_out + rstd_pre dx w_pre') - rstd_pre c1 sum e n1.
-template <typename T, typename R, int kVec>
+template <typename T, typename R, int kVec, RowKind kKind, bool kToken, bool kWide>
 __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormParams p) {
-    __shared__ float part[2][16][3];
+    __shared__ float part[2][3][16];
     extern __shared__ float s_cols[];
-    const int lanes = p.lanes, groups = blockDim.x / lanes;
-    const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes;
-    const T *y = static_cast<const T *>(p.in.y);
-    const T *dx = static_cast<const T *>(p.in.dx);
-    const R *dho = static_cast<const R *>(p.in.dh_out);
+    constexpr bool kNarrow = kKind == kRowNarrow, kOne = kVec == 1;
+    typedef Cols<kNarrow> C;
+    const int lanes = kWide ? blockDim.x : p.lanes;
+    const int groups = kWide ? 1 : blockDim.x / lanes, group = kWide ? 0 : threadIdx.x / lanes;
+    const int lane = kWide ? threadIdx.x : threadIdx.x % lanes;
+    const bool has_y = p.in.y != nullptr, post = p.in.w_post != nullptr;
+    const bool channel = has_y && p.gate_kind == NF4_GATE_CHANNEL;
+    auto col = [&](int v) { return C((v * lanes + lane) * 8, p.dim); };
     float acc[3][kVec][8];
 #pragma unroll
     for (int k = 0; k < 3; ++k)
@@ -153,71 +236,90 @@ __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormParams
         for (int v = 0; v < kVec; ++v)
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[k][v][j] = 0.0f;
-
+    Weights<kNarrow> w;
+    BackwardRow<T, R, kKind, kToken> raw;
+    float dx[8], n1[8], n2[8], dh[8], g[8];  // g: the gate with alpha
+    auto unpack = [&](const C &c, float r1, float r2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dx[j] = dh[j] = n2[j] = 0.0f;
+        row_values<kKind>(raw.h, c, n1);
+        if (p.in.dx) row_values<kKind>(raw.dx, c, dx);
+        if (p.in.dh_out) row_values<kKind>(raw.dh, c, dh);
+        if (has_y) row_values<kKind>(raw.y, c, n2);
+        if constexpr (kToken) row_values<kKind>(raw.gate[0], c, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) n1[j] *= r1, n2[j] *= r2, g[j] = p.alpha * (kToken ? g[j] : w.gate[j]);
+    };
+    auto row_at = [&](int64_t r0) { return r0 + group < p.rows ? r0 + group : p.rows - 1; };
+    const int64_t first = (int64_t)blockIdx.x * groups, stride = (int64_t)gridDim.x * groups;
+    float next_r1 = 0.0f, next_r2 = 1.0f;
+    auto load_stats = [&](int64_t row) {
+        next_r1 = p.in.rstd_pre[row];
+        if (post) next_r2 = p.in.rstd_post[row];
+    };
+    load_stats(row_at(first));
+    if constexpr (kOne) {
+        raw.load(p, row_at(first) * p.dim, col(0));
+        w.load(p, channel, col(0));
+    }
     int turn = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += (int64_t)gridDim.x * groups, turn ^= 1) {
-        const int64_t row = r0 + group, at = row * p.dim;
-        const bool live_row = row < p.rows;
-        const float r1 = live_row ? p.in.rstd_pre[row] : 0.0f;
-        const float r2 = live_row && y && p.in.w_post ? p.in.rstd_post[row] : 1.0f;
-        float vdx[kVec][8], vh[kVec][8], vdh[kVec][8], vy[kVec][8], w1[kVec][8], w2[kVec][8], g[kVec][8];
+    for (int64_t r0 = first; r0 < p.rows; r0 += stride, turn ^= 1) {
+        const int64_t row = row_at(r0), at = row * p.dim;
+        const bool live_row = r0 + group < p.rows;
+        const float r1 = next_r1, r2 = next_r2;
         float s[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-            const int col = (v * lanes + lane) * 8, live = live_row ? p.dim - col : 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                vdx[v][j] = vh[v][j] = vdh[v][j] = vy[v][j] = w1[v][j] = w2[v][j] = g[v][j] = 0.0f;
-            if (live > 0) {
-                load_upto8(static_cast<const R *>(p.in.h) + at + col, live, vh[v]);
-                if (dx) load_upto8(dx + at + col, live, vdx[v]);
-                if (dho) load_upto8(dho + at + col, live, vdh[v]);
-                load_weight(p.in.w_pre, p.w_bf16, col, live, w1[v]);
-                if (y) {
-                    load_upto8(y + at + col, live, vy[v]);
-                    if (p.in.w_post) load_weight(p.in.w_post, p.w_bf16, col, live, w2[v]);
-                    if (p.gate_kind == NF4_GATE_CHANNEL) load_weight(p.in.gate, p.w_bf16, col, live, g[v]);
-                    if (p.gate_kind == NF4_GATE_TOKEN)
-                        load_upto8(static_cast<const T *>(p.in.gate) + at + col, live, g[v]);
-                }
-            }
+        auto add = [&] {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                w1[v][j] += p.off;
-                w2[v][j] = p.in.w_post ? w2[v][j] + p.off : 1.0f;
-                g[v][j] = p.gate_kind == NF4_GATE_NONE ? p.alpha : g[v][j] * p.alpha;
-                vh[v][j] *= r1;   // n1
-                vy[v][j] *= r2;   // n2
-                const float q = vdx[v][j] * w1[v][j], e = g[v][j] * w2[v][j] * vy[v][j];
-                s[0] += q * vh[v][j];
-                s[1] += e * (vdh[v][j] + r1 * q);
-                s[2] += e * vh[v][j];
+                const float q = dx[j] * w.pre[j], e = g[j] * w.post[j] * n2[j];
+                s[0] += q * n1[j];
+                s[1] += e * (dh[j] + r1 * q);
+                s[2] += e * n1[j];
             }
+        };
+        if constexpr (kOne) {
+            unpack(col(0), r1, r2);
+            if (r0 + stride < p.rows) {
+                raw.load(p, row_at(r0 + stride) * p.dim, col(0));
+                load_stats(row_at(r0 + stride));
+            }
+            add();
+        } else {
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) {
+                raw.load(p, at, col(v));
+                w.load(p, channel, col(v));
+                unpack(col(v), r1, r2);
+                add();
+                asm volatile("" ::: "memory");  // one vector's loads at a time: the registers are for the sums
+            }
+            if (r0 + stride < p.rows) load_stats(row_at(r0 + stride));
         }
-        row_sums<3>(s, lanes, part[turn]);
-        const float c1 = s[0] * p.inv_dim;
-        const float c2 = (s[1] - r1 * c1 * s[2]) * p.inv_dim;
+        row_sums<kWide>(s, lanes, part[turn]);
+        const float c1 = s[0] * p.inv_dim, c2 = (s[1] - r1 * c1 * s[2]) * p.inv_dim;
+        if (!live_row) continue;
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
-            const int col = (v * lanes + lane) * 8, live = live_row ? p.dim - col : 0;
-            if (live <= 0) continue;
-            float dh[8], dy[8], dg[8];
+            if constexpr (!kOne) {
+                raw.load(p, at, col(v));
+                w.load(p, channel, col(v));
+                unpack(col(v), r1, r2);
+            }
+            float dg[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                dh[j] = vdh[v][j] + r1 * (vdx[v][j] * w1[v][j] - vh[v][j] * c1);
-                const float dz = g[v][j] * dh[j];
-                dy[j] = p.in.w_post ? r2 * (dz * w2[v][j] - vy[v][j] * c2) : dz;
-                dg[j] = p.alpha * dh[j] * (vy[v][j] * w2[v][j]);
-                acc[0][v][j] += vdx[v][j] * vh[v][j];
-                acc[1][v][j] += dz * vy[v][j];
+                acc[0][v][j] += dx[j] * n1[j];
+                dh[j] += r1 * (dx[j] * w.pre[j] - n1[j] * c1);
+                const float dz = g[j] * dh[j];
+                dg[j] = p.alpha * dh[j] * (n2[j] * w.post[j]);
+                acc[1][v][j] += dz * n2[j];
                 acc[2][v][j] += dg[j];
+                n2[j] = post ? r2 * (dz * w.post[j] - n2[j] * c2) : dz;  // dy
             }
-            if (p.out.dh) store_upto8(static_cast<R *>(p.out.dh) + at + col, live, dh);
-            if (y) {
-                if (p.out.dy) store_upto8(static_cast<T *>(p.out.dy) + at + col, live, dy);
-                if (p.out.dgate && p.gate_kind == NF4_GATE_TOKEN)
-                    store_upto8(static_cast<T *>(p.out.dgate) + at + col, live, dg);
-            }
+            if (p.out.dh) store_row<kKind>(static_cast<R *>(p.out.dh) + at, col(v), dh);
+            if (has_y && p.out.dy) store_row<kKind>(static_cast<T *>(p.out.dy) + at, col(v), n2);
+            if (kToken && p.out.dgate) store_row<kKind>(static_cast<T *>(p.out.dgate) + at, col(v), dg);
+            if constexpr (!kOne) asm volatile("" ::: "memory");
         }
     }
     if (p.partial == nullptr) return;
@@ -234,66 +336,79 @@ __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormParams
             __syncthreads();
             for (int c = threadIdx.x; c < p.dim; c += blockDim.x) {
                 float t = 0.0f;
-                for (int q = 0; q < groups; ++q) t += s_cols[q * width + c];
+                for (int i = 0; i < groups; ++i) t += s_cols[i * width + c];
                 mine[k * p.dim + c] = t;
             }
         } else {
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                const int col = (v * lanes + lane) * 8;
-                if (p.dim - col > 0) store_upto8(mine + k * p.dim + col, p.dim - col, acc[k][v]);
-            }
+            for (int v = 0; v < kVec; ++v)
+                store_cols(mine + k * p.dim, Cols<kNarrow>((v * lanes + lane) * 8, p.dim), acc[k][v]);
         }
     }
 }
 
-// Column sums over the workgroups' partial sums: 16 columns x 16 shares of the
-// rows a workgroup; blockIdx.y is the gradient.
+// Column sums over the workgroups' partial sums: 64 columns a workgroup, four a
+// lane, and 64 shares of the rows; blockIdx.y is the gradient.
 struct ColumnOut {
     void *out[3];
 };
-__global__ __launch_bounds__(256) void column_sum_kernel(const float *partial, int32_t parts, int32_t dim,
-                                                         ColumnOut o, bool bf16) {
-    __shared__ float s[16][16];
-    const int k = blockIdx.y, c = threadIdx.x % 16, share = threadIdx.x / 16;
-    const int col = blockIdx.x * 16 + c;
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float *partial, int32_t parts, int32_t dim,
+                                                          ColumnOut o, bool bf16) {
+    __shared__ float s[64][65];
+    const int k = blockIdx.y, c = threadIdx.x % 16 * 4, share = threadIdx.x / 16;
+    const int col = blockIdx.x * 64 + c;
     if (o.out[k] == nullptr) return;
-    float t = 0.0f;
-    if (col < dim)
-        for (int i = share; i < parts; i += 16) t += partial[((int64_t)i * 3 + k) * dim + col];
-    s[share][c] = t;
+    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const float *src = partial + (int64_t)k * dim + col;
+    if (col + 4 <= dim) {
+#pragma unroll 4
+        for (int i = share; i < parts; i += 64) {
+            const f32x4 x = reinterpret_cast<const f32x4_any4 *>(src + (int64_t)i * 3 * dim)->v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t[j] += x[j];
+        }
+    } else {
+        for (int i = share; i < parts; i += 64)
+            for (int j = 0; j < 4; ++j) t[j] += col + j < dim ? src[(int64_t)i * 3 * dim + j] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[share][c + j] = t[j];
     __syncthreads();
-    if (share == 0 && col < dim) {
-        t = 0.0f;
-        for (int i = 0; i < 16; ++i) t += s[i][c];
-        if (bf16) store1(static_cast<Bf16 *>(o.out[k]) + col, t);
-        else static_cast<float *>(o.out[k])[col] = t;
+    if (threadIdx.x < 64 && blockIdx.x * 64 + (int)threadIdx.x < dim) {
+        const int out = blockIdx.x * 64 + threadIdx.x;
+        float sum = 0.0f;
+        for (int i = 0; i < 64; ++i) sum += s[i][threadIdx.x];
+        if (bf16) store1(static_cast<Bf16 *>(o.out[k]) + out, sum);
+        else static_cast<float *>(o.out[k])[out] = sum;
     }
 }
 
-constexpr int64_t kMostWgs = int64_t(1) << 20;  // of a launch; more rows go round
-
-// Lanes of a row and vectors of a lane.
+// Lanes of a row, vectors of a lane, threads of a workgroup: up to 512 columns a
+// row is part of a wave and a workgroup takes several; above, a workgroup takes
+// one row with as many waves as it needs, one vector a lane up to 8192 columns.
 struct Split {
-    int lanes, vec;
+    int lanes, vec, block;
 };
 Split split_of(int64_t dim) {
     const int64_t vecs = (dim + 7) / 8;
-    int lanes = 8;
-    while (lanes < 1024 && lanes < vecs) lanes *= 2;
-    int vec = 1;
-    while ((int64_t)lanes * vec < vecs) vec *= 2;
-    return {lanes, vec};
+    if (vecs <= 64) {
+        int lanes = 8;
+        while (lanes < vecs) lanes *= 2;
+        return {lanes, 1, 256};
+    }
+    const int vec = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
+    const int lanes = (int)((vecs + 64 * vec - 1) / (64 * vec)) * 64;
+    return {lanes, vec, lanes};
 }
-int block_of(const Split &sp) { return sp.lanes < 256 ? 256 : sp.lanes; }
 
-// Workgroups of the backward pass: as many as fill the chip's 256 CUs with
-// 1024 threads each.
-int64_t backward_workgroups(int64_t rows, const Split &sp) {
-    const int64_t groups = block_of(sp) / sp.lanes, most = 256 * (1024 / block_of(sp));
-    const int64_t need = (rows + groups - 1) / groups;
+// Workgroups that fill the chip's 256 CUs with `threads` threads each, as far as
+// there are rows.
+int64_t workgroups(int64_t rows, const Split &sp, int threads) {
+    const int64_t groups = sp.block / sp.lanes, need = (rows + groups - 1) / groups;
+    const int64_t most = 256 * (threads / sp.block > 0 ? threads / sp.block : 1);
     return need < most ? need : most;
 }
+int64_t backward_workgroups(int64_t rows, const Split &sp) { return workgroups(rows, sp, 1024); }
 
 NormParams params_of(const nf4_residual_norm_shape &sh, const ResidualNormIn &in, const ResidualNormOut &out,
                      const Split &sp) {
@@ -305,30 +420,40 @@ NormParams params_of(const nf4_residual_norm_shape &sh, const ResidualNormIn &in
     return p;
 }
 
-template <typename T, typename R>
-hipError_t forward_typed(const NormParams &p, const Split &sp, hipStream_t s) {
-    const int block = block_of(sp), groups = block / sp.lanes;
-    const int64_t need = (p.rows + groups - 1) / groups;
-    const dim3 grid((uint32_t)(need < kMostWgs ? need : kMostWgs));
-    switch (sp.vec) {
-        case 1: residual_norm_forward_kernel<T, R, 1><<<grid, dim3(block), 0, s>>>(p); break;
-        case 2: residual_norm_forward_kernel<T, R, 2><<<grid, dim3(block), 0, s>>>(p); break;
-        default: residual_norm_forward_kernel<T, R, 4><<<grid, dim3(block), 0, s>>>(p); break;
-    }
+template <typename T, typename R, RowKind kKind>
+hipError_t forward_kind(const NormParams &p, const Split &sp, hipStream_t s) {
+    constexpr bool kBig = kKind != kRowNarrow;  // a row of less than eight is one vector of a lane
+    auto kernel = sp.vec == 4   ? residual_norm_forward_kernel<T, R, kBig ? 4 : 1, kKind, kBig>
+                  : sp.vec == 2 ? residual_norm_forward_kernel<T, R, kBig ? 2 : 1, kKind, kBig>
+                  : sp.lanes > 64 ? residual_norm_forward_kernel<T, R, 1, kKind, kBig>
+                                  : residual_norm_forward_kernel<T, R, 1, kKind, false>;
+    kernel<<<dim3((uint32_t)workgroups(p.rows, sp, 2048)), dim3(sp.block), 0, s>>>(p);
     return hipGetLastError();
 }
-
-template <typename T, typename R>
-hipError_t backward_typed(const NormParams &p, const Split &sp, int64_t wgs, hipStream_t s) {
-    const int block = block_of(sp);
-    const size_t lds = p.partial && block > sp.lanes ? (size_t)block * sp.vec * 8 * sizeof(float) : 0;
-    const dim3 grid((uint32_t)wgs);
-    switch (sp.vec) {
-        case 1: residual_norm_backward_kernel<T, R, 1><<<grid, dim3(block), lds, s>>>(p); break;
-        case 2: residual_norm_backward_kernel<T, R, 2><<<grid, dim3(block), lds, s>>>(p); break;
-        default: residual_norm_backward_kernel<T, R, 4><<<grid, dim3(block), lds, s>>>(p); break;
-    }
+template <typename T, typename R, RowKind kKind, bool kToken>
+hipError_t backward_kind(const NormParams &p, const Split &sp, hipStream_t s) {
+    constexpr bool kBig = kKind != kRowNarrow;
+    auto kernel = sp.vec == 4   ? residual_norm_backward_kernel<T, R, kBig ? 4 : 1, kKind, kToken, kBig>
+                  : sp.vec == 2 ? residual_norm_backward_kernel<T, R, kBig ? 2 : 1, kKind, kToken, kBig>
+                  : sp.lanes > 64 ? residual_norm_backward_kernel<T, R, 1, kKind, kToken, kBig>
+                                  : residual_norm_backward_kernel<T, R, 1, kKind, kToken, false>;
+    const size_t lds = p.partial && sp.block > sp.lanes ? (size_t)sp.block * 8 * sizeof(float) : 0;
+    kernel<<<dim3((uint32_t)backward_workgroups(p.rows, sp)), dim3(sp.block), lds, s>>>(p);
     return hipGetLastError();
+}
+template <typename T, typename R>
+hipError_t forward_typed(const NormParams &p, const Split &sp, hipStream_t s) {
+    if (p.dim < 8) return forward_kind<T, R, kRowNarrow>(p, sp, s);
+    return p.dim % 64 ? forward_kind<T, R, kRowAny>(p, sp, s) : forward_kind<T, R, kRowLines>(p, sp, s);
+}
+template <typename T, typename R, bool kToken>
+hipError_t backward_gate(const NormParams &p, const Split &sp, hipStream_t s) {
+    if (p.dim < 8) return backward_kind<T, R, kRowNarrow, kToken>(p, sp, s);
+    return p.dim % 64 ? backward_kind<T, R, kRowAny, kToken>(p, sp, s) : backward_kind<T, R, kRowLines, kToken>(p, sp, s);
+}
+template <typename T, typename R>
+hipError_t backward_typed(const NormParams &p, const Split &sp, hipStream_t s) {
+    return p.in.y && p.gate_kind == NF4_GATE_TOKEN ? backward_gate<T, R, true>(p, sp, s) : backward_gate<T, R, false>(p, sp, s);
 }
 
 }  // namespace
@@ -356,13 +481,13 @@ hipError_t launch_residual_norm_backward(const nf4_residual_norm_shape &sh, cons
     p.partial = sums ? static_cast<float *>(workspace) : nullptr;
     if (wgs > 0) {
         hipError_t e;
-        if (sh.dtype == NF4_F32) e = backward_typed<float, float>(p, sp, wgs, s);
-        else if (sh.res_dtype == NF4_F32) e = backward_typed<Bf16, float>(p, sp, wgs, s);
-        else e = backward_typed<Bf16, Bf16>(p, sp, wgs, s);
+        if (sh.dtype == NF4_F32) e = backward_typed<float, float>(p, sp, s);
+        else if (sh.res_dtype == NF4_F32) e = backward_typed<Bf16, float>(p, sp, s);
+        else e = backward_typed<Bf16, Bf16>(p, sp, s);
         if (e != hipSuccess) return e;
     }
     if (!sums) return hipSuccess;
-    column_sum_kernel<<<dim3((uint32_t)((sh.dim + 15) / 16), 3), dim3(256), 0, s>>>(
+    column_sum_kernel<<<dim3((uint32_t)((sh.dim + 63) / 64), 3), dim3(1024), 0, s>>>(
         static_cast<const float *>(workspace), (int32_t)wgs, (int32_t)sh.dim, cols, p.w_bf16);
     return hipGetLastError();
 }

@@ -172,7 +172,7 @@ __device__ __forceinline__ Raw8<float> raw_of(const float (&x)[8], const float *
 template <typename T, bool kNarrow>
 __device__ __forceinline__ Raw8<T> load_cols(const T *row, const Cols<kNarrow> &c) {
     if constexpr (!kNarrow) {
-        return load_raw(row + c.base);
+        return load_raw(row + (uint32_t)c.base);
     } else {
         float x[8];
 #pragma unroll
@@ -183,7 +183,7 @@ __device__ __forceinline__ Raw8<T> load_cols(const T *row, const Cols<kNarrow> &
 template <typename T, bool kNarrow>
 __device__ __forceinline__ void cols_values(const Raw8<T> &r, const Cols<kNarrow> &c, float (&x)[8]) {
     values(r, x);
-    if ((c.dim & 7) == 0 && c.live > 0) return;
+    if (c.live >= 8) return;  // all lanes of most waves
     const int shift = c.col - c.base;
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1)
@@ -194,8 +194,8 @@ __device__ __forceinline__ void cols_values(const Raw8<T> &r, const Cols<kNarrow
 }
 template <typename T, bool kNarrow>
 __device__ __forceinline__ void store_cols(T *row, const Cols<kNarrow> &c, const float (&x)[8]) {
-    if (c.live >= 8) return store8(row + c.col, x);
-    if (c.live > 0) store_upto8(row + c.col, c.live, x);
+    if (c.live >= 8) return store8(row + (uint32_t)c.col, x);
+    if (c.live > 0) store_upto8(row + (uint32_t)c.col, c.live, x);
 }
 
 // Sum and maximum over aligned groups of `lanes` lanes of a wave (a power of
