@@ -536,8 +536,8 @@ nf4_status nf4_residual_norm_forward(const nf4_residual_norm_shape *shape, const
                                      float *rstd_post, float *rstd_pre, void *stream);
 
 /* Bytes of device workspace of the backward pass (fp32 partial sums of the
- * weights' gradients, one row for each workgroup); (size_t)-1 for invalid
- * arguments. */
+ * weights' gradients, one row for each workgroup, and two floats a row where dim
+ * is above 8192); (size_t)-1 for invalid arguments. */
 size_t nf4_residual_norm_backward_workspace_size(const nf4_residual_norm_shape *shape);
 
 /* Backward: given dx and dh_out, the gradients of x and h',
@@ -552,7 +552,8 @@ size_t nf4_residual_norm_backward_workspace_size(const nf4_residual_norm_shape *
  *   h_out the forward's h' (h where y is NULL)
  *   dy, dh, dgate, dw_pre, dw_post  device out, each may be NULL to skip it;
  *         dw_pre, dw_post and a channel dgate have w_dtype and `dim` elements
- *   workspace  256-byte aligned; needed where a summed gradient is asked for
+ *   workspace  256-byte aligned; with dim <= 8192 it may be NULL where no summed
+ *         gradient is asked for
  * With rows == 0 the summed gradients that are given are zero. */
 nf4_status nf4_residual_norm_backward(const nf4_residual_norm_shape *shape, const void *dx,
                                       const void *dh_out, const void *y, const void *h_out,

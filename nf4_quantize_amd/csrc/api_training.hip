@@ -130,7 +130,7 @@ NF4_API nf4_status nf4_residual_norm_forward(const nf4_residual_norm_shape *shap
 }
 
 NF4_API size_t nf4_residual_norm_backward_workspace_size(const nf4_residual_norm_shape *shape) {
-    return check_norm_shape(shape) == NF4_OK ? residual_norm_workspace(*shape) : (size_t)-1;
+    return check_norm_shape(shape) == NF4_OK ? residual_norm_workspace(*shape, true) : (size_t)-1;
 }
 
 NF4_API nf4_status nf4_residual_norm_backward(const nf4_residual_norm_shape *shape, const void *dx, const void *dh_out,
@@ -154,7 +154,7 @@ NF4_API nf4_status nf4_residual_norm_backward(const nf4_residual_norm_shape *sha
                           static_cast<const void *>(dw_pre), static_cast<const void *>(dw_post)})
         if (!aligned(p, 16)) return NF4_ERR_ALIGN;
     if (!aligned(rstd_post, 4) || !aligned(rstd_pre, 4)) return NF4_ERR_ALIGN;
-    if (sums && (st = check_workspace(residual_norm_workspace(*shape), workspace, workspace_bytes)) != NF4_OK) return st;
+    if ((st = check_workspace(residual_norm_workspace(*shape, sums), workspace, workspace_bytes)) != NF4_OK) return st;
     if (shape->rows == 0 && !sums) return NF4_OK;
     ResidualNormIn in{};
     in.dx = dx, in.dh_out = dh_out, in.y = y, in.h = h_out, in.w_post = y ? w_post : nullptr, in.gate = gate;

@@ -25,21 +25,23 @@ struct NormParams {
     int32_t gate_kind;
     bool w_bf16;
     float *partial;      // backward: [workgroups][3][dim]
+    float2 *means;       // backward, rows of several tiles: [rows]
 };
 
 // How a row lies in memory: fewer than eight elements; any number; or whole
-// cache lines (dim a multiple of 64), which are moved past the caches' usual
-// order, as nothing here is read twice.
-enum RowKind { kRowNarrow, kRowAny, kRowLines };
+// vectors (dim a multiple of 8), which are moved past the caches' usual order, as
+// nothing here is read twice. The same rows as kRowAny take 67 us instead of 57
+// forward and 96 instead of 83 backward (16384 x 2048 bf16).
+enum RowKind { kRowNarrow, kRowAny, kRowVecs };
 
 template <RowKind kKind, typename T>
 __device__ __forceinline__ Raw8<T> load_row(const T *row, const Cols<kKind == kRowNarrow> &c) {
-    if constexpr (kKind == kRowLines) return load_stream(row + (uint32_t)c.base);
+    if constexpr (kKind == kRowVecs) return load_stream(row + (uint32_t)c.base);
     else return load_cols(row, c);
 }
 template <RowKind kKind, typename T>
 __device__ __forceinline__ void row_values(const Raw8<T> &r, const Cols<kKind == kRowNarrow> &c, float (&x)[8]) {
-    if constexpr (kKind == kRowLines) {
+    if constexpr (kKind == kRowVecs) {
         values(r, x);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = c.live > 0 ? x[j] : 0.0f;
@@ -49,7 +51,7 @@ __device__ __forceinline__ void row_values(const Raw8<T> &r, const Cols<kKind ==
 }
 template <RowKind kKind, typename T>
 __device__ __forceinline__ void store_row(T *row, const Cols<kKind == kRowNarrow> &c, const float (&x)[8]) {
-    if constexpr (kKind == kRowLines) {
+    if constexpr (kKind == kRowVecs) {
         if (c.live > 0) store_stream(row + (uint32_t)c.col, x);
     } else {
         store_cols(row, c, x);
@@ -133,43 +135,47 @@ __global__ __launch_bounds__(1024) void residual_norm_forward_kernel(NormParams 
         const int64_t row = r0 + group, at = row * p.dim;
         const bool live_row = row < p.rows;
         if constexpr (!kOne) load(r0);
-        float h[kVec][8], z[kVec][8];
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-            row_values<kKind>(raw_h[v], col(v), h[v]);
-            if (y) row_values<kKind>(raw_y[v], col(v), z[v]);
-        }
-        if constexpr (kOne)
+        float h[kVec][8], z[8];
+        if constexpr (kOne) {
+            row_values<kKind>(raw_h[0], col(0), h[0]);
+            if (y) row_values<kKind>(raw_y[0], col(0), z);
             if (r0 + stride < p.rows) load(r0 + stride);
-        if (y) {
-            float r2 = 1.0f;
-            if (post) {
-                float s[1] = {0.0f};
-#pragma unroll
-                for (int v = 0; v < kVec; ++v)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) s[0] += z[v][j] * z[v][j];
-                row_sums<kWide>(s, lanes, part[turn]);
-                turn ^= 1;
-                r2 = 1.0f / sqrtf(s[0] * p.inv_dim + p.eps);
-                if (live_row && lane == 0 && p.out.rstd_post) p.out.rstd_post[row] = r2;
-            }
+        }
+        float r2 = 1.0f;
+        if (post) {
+            float s[1] = {0.0f};
 #pragma unroll
             for (int v = 0; v < kVec; ++v) {
-                if constexpr (!kOne) w.load(p, channel, col(v));
+                if constexpr (!kOne) row_values<kKind>(raw_y[v], col(v), z);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) z[v][j] *= r2 * w.post[j];
-                if (p.gate_kind == NF4_GATE_TOKEN) {
-                    const int64_t there = (live_row ? row : p.rows - 1) * p.dim;
-                    float g[8];
-                    row_values<kKind>(load_row<kKind>(static_cast<const T *>(p.in.gate) + there, col(v)), col(v), g);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) z[v][j] *= g[j];
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) h[v][j] += p.alpha * (z[v][j] * w.gate[j]);
-                if (live_row) store_row<kKind>(static_cast<R *>(p.out.h) + at, col(v), h[v]);
+                for (int j = 0; j < 8; ++j) s[0] += z[j] * z[j];
             }
+            row_sums<kWide>(s, lanes, part[turn]);
+            turn ^= 1;
+            r2 = 1.0f / sqrtf(s[0] * p.inv_dim + p.eps);
+            if (live_row && lane == 0 && p.out.rstd_post) p.out.rstd_post[row] = r2;
+        }
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+            if constexpr (!kOne) row_values<kKind>(raw_h[v], col(v), h[v]);
+            if (!y) continue;
+            if constexpr (!kOne) {
+                row_values<kKind>(raw_y[v], col(v), z);
+                w.load(p, channel, col(v));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] *= r2 * w.post[j];
+            if (p.gate_kind == NF4_GATE_TOKEN) {
+                const int64_t there = (live_row ? row : p.rows - 1) * p.dim;
+                float g[8];
+                row_values<kKind>(load_row<kKind>(static_cast<const T *>(p.in.gate) + there, col(v)), col(v), g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[j] *= g[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[v][j] += p.alpha * (z[j] * w.gate[j]);
+            if (live_row) store_row<kKind>(static_cast<R *>(p.out.h) + at, col(v), h[v]);
+            if constexpr (!kOne) asm volatile("" ::: "memory");  // one vector's weights at a time
         }
         float s[1] = {0.0f};
 #pragma unroll
@@ -188,6 +194,7 @@ __global__ __launch_bounds__(1024) void residual_norm_forward_kernel(NormParams 
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = h[v][j] * (r1 * w.pre[j]);
             store_row<kKind>(static_cast<T *>(p.out.x) + at, col(v), x);
+            if constexpr (!kOne) asm volatile("" ::: "memory");
         }
     }
 }
@@ -207,142 +214,151 @@ struct BackwardRow {
     }
 };
 
-// As the forward: every gridDim.x-th set of rows, the next one's loads in
-// flight. A workgroup keeps its columns' share of the weights' gradients in
-// registers until its last row. With more than one vector a lane there is no room
-// for a row beside them, and the second half of the work loads it again from the
-// caches.
-//
-// One round of sums serves both norms: with e = alpha gate w_post' n2 the inner
-// product of the second, mean(dz w_post' n2), is mean(e dh), and dh is known up
-// to the first one's mean c1 = mean(dx w_pre' n1):
-//   sum e dh = sum e (dh_out + rstd_pre dx w_pre') - rstd_pre c1 sum e n1.
-template <typename T, typename R, int kVec, RowKind kKind, bool kToken, bool kWide>
-__global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormParams p) {
-    __shared__ float part[2][3][16];
-    extern __shared__ float s_cols[];
-    constexpr bool kNarrow = kKind == kRowNarrow, kOne = kVec == 1;
-    typedef Cols<kNarrow> C;
-    const int lanes = kWide ? blockDim.x : p.lanes;
-    const int groups = kWide ? 1 : blockDim.x / lanes, group = kWide ? 0 : threadIdx.x / lanes;
-    const int lane = kWide ? threadIdx.x : threadIdx.x % lanes;
-    const bool has_y = p.in.y != nullptr, post = p.in.w_post != nullptr;
-    const bool channel = has_y && p.gate_kind == NF4_GATE_CHANNEL;
-    auto col = [&](int v) { return C((v * lanes + lane) * 8, p.dim); };
-    float acc[3][kVec][8];
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-#pragma unroll
-        for (int v = 0; v < kVec; ++v)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[k][v][j] = 0.0f;
-    Weights<kNarrow> w;
-    BackwardRow<T, R, kKind, kToken> raw;
+// The values of one vector of a row in the backward pass.
+template <typename T, typename R, RowKind kKind, bool kToken>
+struct BackwardValues {
+    typedef Cols<kKind == kRowNarrow> C;
     float dx[8], n1[8], n2[8], dh[8], g[8];  // g: the gate with alpha
-    auto unpack = [&](const C &c, float r1, float r2) {
+    __device__ __forceinline__ void unpack(const NormParams &p, const BackwardRow<T, R, kKind, kToken> &raw,
+                                           const Weights<kKind == kRowNarrow> &w, const C &c, float r1, float r2) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) dx[j] = dh[j] = n2[j] = 0.0f;
         row_values<kKind>(raw.h, c, n1);
         if (p.in.dx) row_values<kKind>(raw.dx, c, dx);
         if (p.in.dh_out) row_values<kKind>(raw.dh, c, dh);
-        if (has_y) row_values<kKind>(raw.y, c, n2);
+        if (p.in.y) row_values<kKind>(raw.y, c, n2);
         if constexpr (kToken) row_values<kKind>(raw.gate[0], c, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) n1[j] *= r1, n2[j] *= r2, g[j] = p.alpha * (kToken ? g[j] : w.gate[j]);
-    };
+    }
+    // One round of sums serves both norms: with e = alpha gate w_post' n2 the
+    // inner product of the second, mean(dz w_post' n2), is mean(e dh), and dh is
+    // known up to the first one's mean c1 = mean(dx w_pre' n1):
+    //   sum e dh = sum e (dh_out + rstd_pre dx w_pre') - rstd_pre c1 sum e n1.
+    __device__ __forceinline__ void add(const Weights<kKind == kRowNarrow> &w, float r1, float (&s)[3]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float q = dx[j] * w.pre[j], e = g[j] * w.post[j] * n2[j];
+            s[0] += q * n1[j];
+            s[1] += e * (dh[j] + r1 * q);
+            s[2] += e * n1[j];
+        }
+    }
+};
+__device__ __forceinline__ void row_means(const float (&s)[3], float r1, float inv_dim, float &c1, float &c2) {
+    c1 = s[0] * inv_dim;
+    c2 = (s[1] - r1 * c1 * s[2]) * inv_dim;
+}
+
+// The two means of each row of more than 8192 columns: one workgroup a row, one
+// vector after the other.
+template <typename T, typename R, RowKind kKind, bool kToken>
+__global__ __launch_bounds__(1024) void residual_norm_means_kernel(NormParams p) {
+    __shared__ float part[2][3][16];
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+        const float r1 = p.in.rstd_pre[row], r2 = p.in.w_post ? p.in.rstd_post[row] : 1.0f;
+        float s[3] = {0.0f, 0.0f, 0.0f};
+        for (int c0 = threadIdx.x * 8; c0 < p.dim; c0 += 8192) {
+            const Cols<false> c(c0, p.dim);
+            BackwardRow<T, R, kKind, kToken> raw;
+            Weights<false> w;
+            BackwardValues<T, R, kKind, kToken> x;
+            raw.load(p, row * p.dim, c);
+            w.load(p, p.in.y && p.gate_kind == NF4_GATE_CHANNEL, c);
+            x.unpack(p, raw, w, c, r1, r2);
+            x.add(w, r1, s);
+        }
+        row_sums<true>(s, 1024, part[turn]);
+        float c1, c2;
+        row_means(s, r1, p.inv_dim, c1, c2);
+        if (threadIdx.x == 0) p.means[row] = make_float2(c1, c2);
+    }
+}
+
+// As the forward: every gridDim.x-th set of rows, the next one's loads in
+// flight. A workgroup keeps its columns' share of the weights' gradients in
+// registers until its last row. A row of more than 8192 columns is cut into
+// tiles (kTiled, blockIdx.y), whose means come from residual_norm_means_kernel:
+// the row is read twice, but a lane's sums stay in registers (in one kernel, two
+// vectors a lane spilled: 442 us for 2048 x 16384 bf16).
+template <typename T, typename R, RowKind kKind, bool kToken, bool kWide, bool kTiled>
+__global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormParams p) {
+    __shared__ float part[2][3][16];
+    extern __shared__ float s_cols[];
+    constexpr bool kNarrow = kKind == kRowNarrow;
+    const int lanes = kWide ? blockDim.x : p.lanes;
+    const int groups = kWide ? 1 : blockDim.x / lanes, group = kWide ? 0 : threadIdx.x / lanes;
+    const int lane = kWide ? threadIdx.x : threadIdx.x % lanes;
+    const bool post = p.in.w_post != nullptr;
+    const Cols<kNarrow> c((lane + (kTiled ? blockIdx.y * lanes : 0)) * 8, p.dim);
+    float acc[3][8];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[k][j] = 0.0f;
     auto row_at = [&](int64_t r0) { return r0 + group < p.rows ? r0 + group : p.rows - 1; };
     const int64_t first = (int64_t)blockIdx.x * groups, stride = (int64_t)gridDim.x * groups;
-    float next_r1 = 0.0f, next_r2 = 1.0f;
-    auto load_stats = [&](int64_t row) {
+    BackwardRow<T, R, kKind, kToken> raw;
+    Weights<kNarrow> w;
+    float next_r1, next_r2 = 1.0f;
+    float2 next_means = make_float2(0.0f, 0.0f);
+    auto load = [&](int64_t row) {
+        raw.load(p, row * p.dim, c);
         next_r1 = p.in.rstd_pre[row];
         if (post) next_r2 = p.in.rstd_post[row];
+        if constexpr (kTiled) next_means = p.means[row];
     };
-    load_stats(row_at(first));
-    if constexpr (kOne) {
-        raw.load(p, row_at(first) * p.dim, col(0));
-        w.load(p, channel, col(0));
-    }
+    load(row_at(first));
+    w.load(p, p.in.y && p.gate_kind == NF4_GATE_CHANNEL, c);
     int turn = 0;
     for (int64_t r0 = first; r0 < p.rows; r0 += stride, turn ^= 1) {
-        const int64_t row = row_at(r0), at = row * p.dim;
+        const int64_t at = row_at(r0) * p.dim;
         const bool live_row = r0 + group < p.rows;
         const float r1 = next_r1, r2 = next_r2;
-        float s[3] = {0.0f, 0.0f, 0.0f};
-        auto add = [&] {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float q = dx[j] * w.pre[j], e = g[j] * w.post[j] * n2[j];
-                s[0] += q * n1[j];
-                s[1] += e * (dh[j] + r1 * q);
-                s[2] += e * n1[j];
-            }
-        };
-        if constexpr (kOne) {
-            unpack(col(0), r1, r2);
-            if (r0 + stride < p.rows) {
-                raw.load(p, row_at(r0 + stride) * p.dim, col(0));
-                load_stats(row_at(r0 + stride));
-            }
-            add();
-        } else {
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                raw.load(p, at, col(v));
-                w.load(p, channel, col(v));
-                unpack(col(v), r1, r2);
-                add();
-                asm volatile("" ::: "memory");  // one vector's loads at a time: the registers are for the sums
-            }
-            if (r0 + stride < p.rows) load_stats(row_at(r0 + stride));
+        float c1 = next_means.x, c2 = next_means.y;
+        BackwardValues<T, R, kKind, kToken> x;
+        x.unpack(p, raw, w, c, r1, r2);
+        if (r0 + stride < p.rows) load(row_at(r0 + stride));
+        if constexpr (!kTiled) {
+            float s[3] = {0.0f, 0.0f, 0.0f};
+            x.add(w, r1, s);
+            row_sums<kWide>(s, lanes, part[turn]);
+            row_means(s, r1, p.inv_dim, c1, c2);
         }
-        row_sums<kWide>(s, lanes, part[turn]);
-        const float c1 = s[0] * p.inv_dim, c2 = (s[1] - r1 * c1 * s[2]) * p.inv_dim;
         if (!live_row) continue;
+        float dg[8];
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-            if constexpr (!kOne) {
-                raw.load(p, at, col(v));
-                w.load(p, channel, col(v));
-                unpack(col(v), r1, r2);
-            }
-            float dg[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                acc[0][v][j] += dx[j] * n1[j];
-                dh[j] += r1 * (dx[j] * w.pre[j] - n1[j] * c1);
-                const float dz = g[j] * dh[j];
-                dg[j] = p.alpha * dh[j] * (n2[j] * w.post[j]);
-                acc[1][v][j] += dz * n2[j];
-                acc[2][v][j] += dg[j];
-                n2[j] = post ? r2 * (dz * w.post[j] - n2[j] * c2) : dz;  // dy
-            }
-            if (p.out.dh) store_row<kKind>(static_cast<R *>(p.out.dh) + at, col(v), dh);
-            if (has_y && p.out.dy) store_row<kKind>(static_cast<T *>(p.out.dy) + at, col(v), n2);
-            if (kToken && p.out.dgate) store_row<kKind>(static_cast<T *>(p.out.dgate) + at, col(v), dg);
-            if constexpr (!kOne) asm volatile("" ::: "memory");
+        for (int j = 0; j < 8; ++j) {
+            acc[0][j] += x.dx[j] * x.n1[j];
+            x.dh[j] += r1 * (x.dx[j] * w.pre[j] - x.n1[j] * c1);
+            const float dz = x.g[j] * x.dh[j];
+            dg[j] = p.alpha * x.dh[j] * (x.n2[j] * w.post[j]);
+            acc[1][j] += dz * x.n2[j];
+            acc[2][j] += dg[j];
+            x.n2[j] = post ? r2 * (dz * w.post[j] - x.n2[j] * c2) : dz;  // dy
         }
+        if (p.out.dh) store_row<kKind>(static_cast<R *>(p.out.dh) + at, c, x.dh);
+        if (p.in.y && p.out.dy) store_row<kKind>(static_cast<T *>(p.out.dy) + at, c, x.n2);
+        if (kToken && p.out.dgate) store_row<kKind>(static_cast<T *>(p.out.dgate) + at, c, dg);
     }
     if (p.partial == nullptr) return;
     float *mine = p.partial + (int64_t)blockIdx.x * 3 * p.dim;
-    const int width = lanes * kVec * 8;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
         if (groups > 1) {
+            const int width = lanes * 8;
             __syncthreads();
 #pragma unroll
-            for (int v = 0; v < kVec; ++v)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s_cols[group * width + (v * lanes + lane) * 8 + j] = acc[k][v][j];
+            for (int j = 0; j < 8; ++j) s_cols[group * width + lane * 8 + j] = acc[k][j];
             __syncthreads();
-            for (int c = threadIdx.x; c < p.dim; c += blockDim.x) {
+            for (int i = threadIdx.x; i < p.dim; i += blockDim.x) {
                 float t = 0.0f;
-                for (int i = 0; i < groups; ++i) t += s_cols[i * width + c];
-                mine[k * p.dim + c] = t;
+                for (int q = 0; q < groups; ++q) t += s_cols[q * width + i];
+                mine[k * p.dim + i] = t;
             }
         } else {
-#pragma unroll
-            for (int v = 0; v < kVec; ++v)
-                store_cols(mine + k * p.dim, Cols<kNarrow>((v * lanes + lane) * 8, p.dim), acc[k][v]);
+            store_cols(mine + k * p.dim, c, acc[k]);
         }
     }
 }
@@ -400,6 +416,19 @@ Split split_of(int64_t dim) {
     const int lanes = (int)((vecs + 64 * vec - 1) / (64 * vec)) * 64;
     return {lanes, vec, lanes};
 }
+// The backward pass holds 128 registers a lane, so its workgroups have a power of
+// two of waves that the four SIMDs can share evenly: five waves of 2304 columns
+// (14000 rows) take 116 us, eight 96. vec: tiles of a row here.
+Split backward_split_of(int64_t dim) {
+    Split sp = split_of(dim);
+    if (sp.lanes <= 64) return sp;
+    const int64_t vecs = (dim + 7) / 8;
+    sp.vec = (int)((vecs + 1023) / 1024);
+    sp.lanes = 128;
+    while ((int64_t)sp.lanes * sp.vec < vecs) sp.lanes *= 2;
+    sp.block = sp.lanes;
+    return sp;
+}
 
 // Workgroups that fill the chip's 256 CUs with `threads` threads each, as far as
 // there are rows.
@@ -408,7 +437,10 @@ int64_t workgroups(int64_t rows, const Split &sp, int threads) {
     const int64_t most = 256 * (threads / sp.block > 0 ? threads / sp.block : 1);
     return need < most ? need : most;
 }
-int64_t backward_workgroups(int64_t rows, const Split &sp) { return workgroups(rows, sp, 1024); }
+int64_t backward_workgroups(int64_t rows, const Split &sp) {
+    const int64_t all = workgroups(rows, sp, 1024);
+    return sp.vec > 1 && all > 256 / sp.vec ? 256 / sp.vec : all;  // tiles of a row fill the chip together
+}
 
 NormParams params_of(const nf4_residual_norm_shape &sh, const ResidualNormIn &in, const ResidualNormOut &out,
                      const Split &sp) {
@@ -433,23 +465,28 @@ hipError_t forward_kind(const NormParams &p, const Split &sp, hipStream_t s) {
 template <typename T, typename R, RowKind kKind, bool kToken>
 hipError_t backward_kind(const NormParams &p, const Split &sp, hipStream_t s) {
     constexpr bool kBig = kKind != kRowNarrow;
-    auto kernel = sp.vec == 4   ? residual_norm_backward_kernel<T, R, kBig ? 4 : 1, kKind, kToken, kBig>
-                  : sp.vec == 2 ? residual_norm_backward_kernel<T, R, kBig ? 2 : 1, kKind, kToken, kBig>
-                  : sp.lanes > 64 ? residual_norm_backward_kernel<T, R, 1, kKind, kToken, kBig>
-                                  : residual_norm_backward_kernel<T, R, 1, kKind, kToken, false>;
+    auto kernel = sp.vec > 1      ? residual_norm_backward_kernel<T, R, kKind, kToken, kBig, kBig>
+                  : sp.lanes > 64 ? residual_norm_backward_kernel<T, R, kKind, kToken, kBig, false>
+                                  : residual_norm_backward_kernel<T, R, kKind, kToken, false, false>;
+    if constexpr (kBig)
+        if (sp.vec > 1) {
+            const int64_t wgs = p.rows < 512 ? p.rows : 512;
+            residual_norm_means_kernel<T, R, kKind, kToken><<<dim3((uint32_t)wgs), dim3(1024), 0, s>>>(p);
+        }
     const size_t lds = p.partial && sp.block > sp.lanes ? (size_t)sp.block * 8 * sizeof(float) : 0;
-    kernel<<<dim3((uint32_t)backward_workgroups(p.rows, sp)), dim3(sp.block), lds, s>>>(p);
+    const dim3 grid((uint32_t)backward_workgroups(p.rows, sp), sp.vec);
+    kernel<<<grid, dim3(sp.block), lds, s>>>(p);
     return hipGetLastError();
 }
 template <typename T, typename R>
 hipError_t forward_typed(const NormParams &p, const Split &sp, hipStream_t s) {
     if (p.dim < 8) return forward_kind<T, R, kRowNarrow>(p, sp, s);
-    return p.dim % 64 ? forward_kind<T, R, kRowAny>(p, sp, s) : forward_kind<T, R, kRowLines>(p, sp, s);
+    return p.dim % 8 ? forward_kind<T, R, kRowAny>(p, sp, s) : forward_kind<T, R, kRowVecs>(p, sp, s);
 }
 template <typename T, typename R, bool kToken>
 hipError_t backward_gate(const NormParams &p, const Split &sp, hipStream_t s) {
     if (p.dim < 8) return backward_kind<T, R, kRowNarrow, kToken>(p, sp, s);
-    return p.dim % 64 ? backward_kind<T, R, kRowAny, kToken>(p, sp, s) : backward_kind<T, R, kRowLines, kToken>(p, sp, s);
+    return p.dim % 8 ? backward_kind<T, R, kRowAny, kToken>(p, sp, s) : backward_kind<T, R, kRowVecs, kToken>(p, sp, s);
 }
 template <typename T, typename R>
 hipError_t backward_typed(const NormParams &p, const Split &sp, hipStream_t s) {
@@ -467,18 +504,26 @@ hipError_t launch_residual_norm_forward(const nf4_residual_norm_shape &sh, const
     return forward_typed<Bf16, Bf16>(p, sp, s);
 }
 
-size_t residual_norm_workspace(const nf4_residual_norm_shape &sh) {
-    return (size_t)(backward_workgroups(sh.rows, split_of(sh.dim)) * 3 * sh.dim) * sizeof(float);
+// The means of rows of several tiles, then the partial sums.
+size_t means_bytes(const nf4_residual_norm_shape &sh, const Split &sp) {
+    return sp.vec > 1 ? ((size_t)sh.rows * sizeof(float2) + 255) / 256 * 256 : 0;
+}
+size_t residual_norm_workspace(const nf4_residual_norm_shape &sh, bool sums) {
+    const Split sp = backward_split_of(sh.dim);
+    const size_t partial = (size_t)(backward_workgroups(sh.rows, sp) * 3 * sh.dim) * sizeof(float);
+    return means_bytes(sh, sp) + (sums ? partial : 0);
 }
 
 hipError_t launch_residual_norm_backward(const nf4_residual_norm_shape &sh, const ResidualNormIn &in,
                                          const ResidualNormOut &out, void *workspace, hipStream_t s) {
-    const Split sp = split_of(sh.dim);
+    const Split sp = backward_split_of(sh.dim);
     NormParams p = params_of(sh, in, out, sp);
     const int64_t wgs = backward_workgroups(sh.rows, sp);
     const ColumnOut cols{{out.dw_pre, out.dw_post, sh.gate_kind == NF4_GATE_CHANNEL ? out.dgate : nullptr}};
     const bool sums = cols.out[0] || cols.out[1] || cols.out[2];
-    p.partial = sums ? static_cast<float *>(workspace) : nullptr;
+    float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + means_bytes(sh, sp));
+    p.partial = sums ? partial : nullptr;
+    p.means = static_cast<float2 *>(workspace);
     if (wgs > 0) {
         hipError_t e;
         if (sh.dtype == NF4_F32) e = backward_typed<float, float>(p, sp, s);
@@ -487,8 +532,8 @@ hipError_t launch_residual_norm_backward(const nf4_residual_norm_shape &sh, cons
         if (e != hipSuccess) return e;
     }
     if (!sums) return hipSuccess;
-    column_sum_kernel<<<dim3((uint32_t)((sh.dim + 63) / 64), 3), dim3(1024), 0, s>>>(
-        static_cast<const float *>(workspace), (int32_t)wgs, (int32_t)sh.dim, cols, p.w_bf16);
+    column_sum_kernel<<<dim3((uint32_t)((sh.dim + 63) / 64), 3), dim3(1024), 0, s>>>(partial, (int32_t)wgs,
+                                                                                     (int32_t)sh.dim, cols, p.w_bf16);
     return hipGetLastError();
 }
 

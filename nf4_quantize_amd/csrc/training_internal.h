@@ -31,7 +31,8 @@ struct ResidualNormOut {
 };
 hipError_t launch_residual_norm_forward(const nf4_residual_norm_shape &sh, const ResidualNormIn &in,
                                         const ResidualNormOut &out, hipStream_t s);
-size_t residual_norm_workspace(const nf4_residual_norm_shape &sh);
+// `sums`: whether a gradient that is summed over the rows is asked for.
+size_t residual_norm_workspace(const nf4_residual_norm_shape &sh, bool sums);
 hipError_t launch_residual_norm_backward(const nf4_residual_norm_shape &sh, const ResidualNormIn &in,
                                          const ResidualNormOut &out, void *workspace, hipStream_t s);
 

@@ -335,7 +335,7 @@ def residual_norm_backward(dx, dh_out, y, h_out, rstd_pre, w_pre, rstd_post=None
     dgate = torch.empty_like(gate) if want[4] and gated else None
     L = _nq.lib()
     ws = None
-    if dw_pre is not None or dw_post is not None or (dgate is not None and shape.gate_kind == 1):
+    if shape.dim > 8192 or dw_pre is not None or dw_post is not None or (dgate is not None and shape.gate_kind == 1):
         size = _size(L.nf4_residual_norm_backward_workspace_size(ctypes.byref(shape)),
                      "nf4_residual_norm_backward_workspace_size")
         ws = torch.empty(max(size, 1), dtype=torch.uint8, device=h_out.device)
