@@ -25,6 +25,7 @@ struct NormParams {
     int32_t gate_kind;
     bool w_bf16;
     float *partial;      // backward: [workgroups][3][dim]
+    bool want[3];        // the rows of `partial` that are asked for
     float2 *means;       // backward, rows of several tiles: [rows]
 };
 
@@ -317,6 +318,12 @@ __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormParams
         const bool live_row = r0 + group < p.rows;
         const float r1 = next_r1, r2 = next_r2;
         float c1 = next_means.x, c2 = next_means.y;
+        if constexpr (sizeof(T) == 4) {
+            // no room for the weights beside fp32 rows in flight (kept, they spilled:
+            // 205 us for 8192 x 4096 instead of 178); the others gain by keeping them
+            asm volatile("" ::: "memory");
+            w.load(p, p.in.y && p.gate_kind == NF4_GATE_CHANNEL, c);
+        }
         BackwardValues<T, R, kKind, kToken> x;
         x.unpack(p, raw, w, c, r1, r2);
         if (r0 + stride < p.rows) load(row_at(r0 + stride));
@@ -346,6 +353,7 @@ __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormParams
     float *mine = p.partial + (int64_t)blockIdx.x * 3 * p.dim;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
+        if (!p.want[k]) continue;
         if (groups > 1) {
             const int width = lanes * 8;
             __syncthreads();
@@ -523,6 +531,7 @@ hipError_t launch_residual_norm_backward(const nf4_residual_norm_shape &sh, cons
     const bool sums = cols.out[0] || cols.out[1] || cols.out[2];
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + means_bytes(sh, sp));
     p.partial = sums ? partial : nullptr;
+    for (int k = 0; k < 3; ++k) p.want[k] = cols.out[k] != nullptr;
     p.means = static_cast<float2 *>(workspace);
     if (wgs > 0) {
         hipError_t e;

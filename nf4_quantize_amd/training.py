@@ -59,10 +59,39 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _same_device(dev, *ts):
+def _check_tensors(first, *ts):
+    """Contiguous tensors of the first one's device (None: absent). Returns the
+    device's index. These checks run before every call: they ask each tensor two
+    plain questions and build no objects."""
+    index = first.get_device()
+    if index < 0 or not first.is_contiguous():
+        raise ValueError("tensors must be contiguous device tensors")
     for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors of one call are on one device, got {dev} and {t.device}")
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous device tensors"
+                             if t.get_device() < 0 or not t.is_contiguous() else
+                             f"tensors of one call are on one device, got {first.device} and {t.device}")
+    return index
+
+
+def _stream(index):
+    """The current stream of a device, as _nq._stream without its objects."""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+_CODES = {}
+
+
+def _code(dtype):
+    """_nq._dtype_code, looked up."""
+    if not _CODES:
+        import torch
+
+        _CODES.update({torch.float32: _nq.NF4_F32, torch.bfloat16: _nq.NF4_BF16})
+    code = _CODES.get(dtype)
+    return _nq._dtype_code(dtype) if code is None else code
 
 
 # ------------------------------------------------------------------ AdamW
@@ -118,14 +147,14 @@ class NF4AdamW:
         for p, mw in zip(self.params, self.masters):
             if p.dtype != self.dtype:
                 raise TypeError(f"parameters of one dtype, got {self.dtype} and {p.dtype}")
-            _nq._need_cuda(p, mw)
-            _same_device(self.device, p, mw)
+            _check_tensors(self.params[0], p, mw)
             if mw is not None and (mw.dtype != torch.float32 or self.dtype != torch.bfloat16 or mw.numel() != p.numel()):
                 raise TypeError("a master weight is float32, of a bfloat16 parameter of its size")
         self.betas, self.eps, self.state_bits = (float(betas[0]), float(betas[1])), float(eps), state_bits
         self.max_grad_norm, self.seed, self.steps = float(max_grad_norm), int(seed), 0
         self.grad_norm = torch.zeros(1, dtype=torch.float32, device=self.device)
         self._entries = np.zeros(len(self.params), _ENTRY)
+        self._at = self._entries.ctypes.data
         self._numels = [p.numel() for p in self.params]
         e = self._entries
         e["w"] = [p.data_ptr() for p in self.params]
@@ -172,8 +201,7 @@ class NF4AdamW:
             scale = name.endswith("scale")
             want = torch.float32 if scale else dt
             for t, n in zip(ts, self._numels):
-                _nq._need_cuda(t)
-                _same_device(self.device, t)
+                _check_tensors(self.params[0], t)
                 if t.dtype != want or t.numel() != (-(-n // MOMENT_BLOCK) if scale else n):
                     raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} for a parameter of {n} elements")
             setattr(self, name, ts)
@@ -190,39 +218,35 @@ class NF4AdamW:
         """One step with the parameters' ``.grad``, or with ``grads`` (a tensor for
         each parameter, all bfloat16 or all float32). ``step`` and ``seed``
         override the step number (the count of calls) and the random seed."""
-        import torch
-
         L = _nq.lib()
         grads = [p.grad for p in self.params] if grads is None else grads
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
         if any(g is None for g in grads):
             raise ValueError("a parameter has no gradient")
-        dt, dev = grads[0].dtype, self.device
-        for g, n in zip(grads, self._numels):
-            if g.dtype is not dt or g.numel() != n or not g.is_contiguous() or g.device != dev:
-                raise ValueError(f"a gradient {tuple(g.shape)} {g.dtype} on {g.device}: contiguous, {n} elements of {dt} "
-                                 f"on {dev} are wanted")
-        grad_dtype = _nq._dtype_code(dt)
+        dt, index = grads[0].dtype, self.params[0].get_device()
+        if ({g.dtype for g in grads} != {dt} or {g.get_device() for g in grads} != {index}
+                or [g.numel() for g in grads] != self._numels or not all([g.is_contiguous() for g in grads])):
+            raise ValueError(f"gradients: contiguous, of the parameters' sizes, one dtype, on {self.device}; got "
+                             + ", ".join(f"{tuple(g.shape)} {g.dtype} {g.device}" for g in grads[:4]) + " ...")
+        grad_dtype = _code(dt)
         e, count = self._entries, len(grads)
         e["grad"] = [g.data_ptr() for g in grads]
         for g in self.groups:
             part = slice(g["first"], g["first"] + g["count"])
             e["lr"][part], e["weight_decay"][part] = g["lr"], g["weight_decay"]
-        at = e.ctypes.data
+        at = self._at
         number = self.steps + 1 if step is None else int(step)
-        stream = _nq._stream(dev)
+        stream = _stream(index)
         clip = self.max_grad_norm > 0
+        norm = self.grad_norm.data_ptr() if clip else None
         ws, ws_bytes = self._workspace.data_ptr(), self._workspace.numel()
-        with torch.cuda.device(dev):
-            if clip:
-                _nq._check(L.nf4_grad_norm(at, count, grad_dtype, self.grad_norm.data_ptr(), ws, ws_bytes,
-                                           stream), "nf4_grad_norm")
-            config = nf4_adamw_config(*self.betas, self.eps, self.max_grad_norm, number,
-                                      (self.seed + number if seed is None else int(seed)) & 0xFFFFFFFFFFFFFFFF)
-            _nq._check(L.nf4_adamw_step(at, count, _nq._dtype_code(self.dtype), grad_dtype, self.state_bits,
-                                        ctypes.byref(config), self.grad_norm.data_ptr() if clip else None, ws, ws_bytes, stream),
-                       "nf4_adamw_step")
+        if clip:
+            _nq._check(L.nf4_grad_norm(at, count, grad_dtype, norm, ws, ws_bytes, stream), "nf4_grad_norm")
+        config = nf4_adamw_config(*self.betas, self.eps, self.max_grad_norm, number,
+                                  (self.seed + number if seed is None else int(seed)) & 0xFFFFFFFFFFFFFFFF)
+        _nq._check(L.nf4_adamw_step(at, count, _code(self.dtype), grad_dtype, self.state_bits, ctypes.byref(config), norm,
+                                    ws, ws_bytes, stream), "nf4_adamw_step")
         self.steps = number
 
     def state_dict(self):
@@ -260,23 +284,21 @@ class NF4AdamW:
 def _norm_shape(y, h, w_pre, w_post, gate, alpha, eps, w_offset):
     """The call's shape: y None leaves only the norm of h."""
     act = h if y is None else y
-    if h.dim() < 1 or act.shape != h.shape:
-        raise ValueError(f"y {tuple(act.shape)} and h {tuple(h.shape)} have one shape")
-    dim = h.shape[-1]
-    rows = h.numel() // max(dim, 1)
-    kind = "none"
+    shape = h.shape
+    if not shape or act.shape != shape:
+        raise ValueError(f"y {tuple(act.shape)} and h {tuple(shape)} have one shape")
+    dim, wt = shape[-1], w_pre.dtype
+    kind = 0
     if gate is not None and y is not None:
-        kind = "token" if gate.dim() == act.dim() and act.dim() > 1 and gate.shape == act.shape else "channel"
-        if kind == "channel" and tuple(gate.shape) != (dim,):
+        kind = GATE_KINDS["token" if len(shape) > 1 and gate.shape == shape else "channel"]
+        if kind == 1 and gate.shape != (dim,):
             raise ValueError(f"gate {tuple(gate.shape)}: ({dim},) or the shape of y")
-        if gate.dtype != (act.dtype if kind == "token" else w_pre.dtype):
+        if gate.dtype != (act.dtype if kind == 2 else wt):
             raise TypeError("a token gate has the dtype of y, a channel gate that of the norms' weights")
-    for w in (w_pre, w_post):
-        if w is not None and (tuple(w.shape) != (dim,) or w.dtype != w_pre.dtype):
-            raise ValueError(f"norm weights are ({dim},) of one dtype, got {tuple(w.shape)} {w.dtype}")
-    return nf4_residual_norm_shape(rows, dim, _nq._dtype_code(act.dtype), _nq._dtype_code(h.dtype),
-                                   _nq._dtype_code(w_pre.dtype), GATE_KINDS[kind], float(eps), float(alpha),
-                                   float(w_offset))
+    if w_pre.shape != (dim,) or (w_post is not None and (w_post.shape != (dim,) or w_post.dtype != wt)):
+        raise ValueError(f"norm weights are ({dim},) of one dtype")
+    return nf4_residual_norm_shape(h.numel() // max(dim, 1), dim, _code(act.dtype), _code(h.dtype), _code(wt), kind, eps,
+                                   alpha, w_offset)
 
 
 def residual_norm_forward(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6, w_offset=0.0, h_out=None, x_out=None):
@@ -288,23 +310,22 @@ def residual_norm_forward(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e
     in place."""
     import torch
 
-    _nq._need_cuda(y, h, w_pre, w_post, gate, h_out, x_out)
-    _same_device(h.device, y, w_pre, w_post, gate, h_out, x_out)
+    index = _check_tensors(h, y, w_pre, w_post, gate, h_out, x_out)
     shape = _norm_shape(y, h, w_pre, w_post, gate, alpha, eps, w_offset)
     act = h if y is None else y
+    for t, like in ((h_out, h), (x_out, act)):
+        if t is not None and (t.shape != like.shape or t.dtype != like.dtype):
+            raise ValueError("outputs have the shape and dtype of h and y")
     if h_out is None and y is not None:
         h_out = torch.empty_like(h)
     if x_out is None:
         x_out = torch.empty_like(act)
-    for t, like in ((h_out, h), (x_out, act)):
-        if t is not None and (t.shape != like.shape or t.dtype != like.dtype):
-            raise ValueError("outputs have the shape and dtype of h and y")
-    post = w_post is not None and y is not None
-    stats = torch.empty((2 if post else 1, shape.rows), dtype=torch.float32, device=h.device)
-    rstd_pre, rstd_post = stats[0], stats[1] if post else None
-    st = _nq.lib().nf4_residual_norm_forward(ctypes.byref(shape), _addr(y), _addr(h), _addr(w_post), _addr(gate),
-                                             _addr(w_pre), _addr(h_out), _addr(x_out), _addr(rstd_post),
-                                             _addr(rstd_pre), _nq._stream(h.device))
+    rows = shape.rows
+    rstd_pre = torch.empty(rows, dtype=torch.float32, device=h.device)
+    rstd_post = torch.empty_like(rstd_pre) if w_post is not None and y is not None else None
+    st = _nq.lib().nf4_residual_norm_forward(ctypes.byref(shape), _addr(y), h.data_ptr(), _addr(w_post), _addr(gate),
+                                             w_pre.data_ptr(), _addr(h_out), x_out.data_ptr(), _addr(rstd_post),
+                                             rstd_pre.data_ptr(), _stream(index))
     _nq._check(st, "nf4_residual_norm_forward")
     return (h if y is None else h_out), x_out, rstd_pre, rstd_post
 
@@ -316,47 +337,45 @@ def residual_norm_backward(dx, dh_out, y, h_out, rstd_pre, w_pre, rstd_post=None
     None where ``want`` is false or the input is absent."""
     import torch
 
-    _nq._need_cuda(dx, dh_out, y, h_out, rstd_pre, w_pre, rstd_post, w_post, gate)
-    _same_device(h_out.device, dx, dh_out, y, rstd_pre, w_pre, rstd_post, w_post, gate)
+    index = _check_tensors(h_out, dx, dh_out, y, rstd_pre, w_pre, rstd_post, w_post, gate)
     shape = _norm_shape(y, h_out, w_pre, w_post, gate, alpha, 0.0, w_offset)
     act = h_out if y is None else y
     for t, like in ((dx, act), (dh_out, h_out)):
         if t is not None and (t.shape != like.shape or t.dtype != like.dtype):
             raise ValueError("dx has the shape and dtype of y, dh_out those of h")
-    post = w_post is not None and y is not None
+    post, kind, rows = w_post is not None and y is not None, shape.gate_kind, shape.rows
     for r, need in ((rstd_pre, True), (rstd_post, post)):
-        if need and (r is None or r.dtype != torch.float32 or r.numel() != shape.rows):
+        if need and (r is None or r.dtype != torch.float32 or r.numel() != rows):
             raise ValueError("rstd_pre and, with w_post, rstd_post hold one float32 a row")
-    gated = shape.gate_kind != 0
     dy = torch.empty_like(y) if want[0] and y is not None else None
     dh = torch.empty_like(h_out) if want[1] else None
     dw_pre = torch.empty_like(w_pre) if want[2] else None
     dw_post = torch.empty_like(w_post) if want[3] and post else None
-    dgate = torch.empty_like(gate) if want[4] and gated else None
-    L = _nq.lib()
-    ws = None
-    if shape.dim > 8192 or dw_pre is not None or dw_post is not None or (dgate is not None and shape.gate_kind == 1):
-        size = _size(L.nf4_residual_norm_backward_workspace_size(ctypes.byref(shape)),
-                     "nf4_residual_norm_backward_workspace_size")
-        ws = torch.empty(max(size, 1), dtype=torch.uint8, device=h_out.device)
-    st = L.nf4_residual_norm_backward(ctypes.byref(shape), _addr(dx), _addr(dh_out), _addr(y), _addr(h_out),
-                                      _addr(w_post), _addr(gate), _addr(w_pre), _addr(rstd_post), _addr(rstd_pre),
-                                      _addr(dy), _addr(dh), _addr(dgate), _addr(dw_pre), _addr(dw_post), _addr(ws),
-                                      0 if ws is None else ws.numel(), _nq._stream(h_out.device))
+    dgate = torch.empty_like(gate) if want[4] and kind else None
+    L, shape_p = _nq.lib(), ctypes.byref(shape)
+    ws, size = None, 0
+    if shape.dim > 8192 or dw_pre is not None or dw_post is not None or (dgate is not None and kind == 1):
+        size = max(_size(L.nf4_residual_norm_backward_workspace_size(shape_p),
+                         "nf4_residual_norm_backward_workspace_size"), 1)
+        ws = torch.empty(size, dtype=torch.uint8, device=h_out.device)
+    st = L.nf4_residual_norm_backward(shape_p, _addr(dx), _addr(dh_out), _addr(y), h_out.data_ptr(), _addr(w_post),
+                                      _addr(gate), w_pre.data_ptr(), _addr(rstd_post), rstd_pre.data_ptr(), _addr(dy),
+                                      _addr(dh), _addr(dgate), _addr(dw_pre), _addr(dw_post), _addr(ws), size,
+                                      _stream(index))
     _nq._check(st, "nf4_residual_norm_backward")
     return dy, dh, dw_pre, dw_post, dgate
 
 
 # ------------------------------------------------------------------ token embedding
 
-_INDEX = {"torch.int32": 0, "torch.int64": 1}
-
-
 def _index_code(ids):
-    code = _INDEX.get(str(ids.dtype))
-    if code is None:
-        raise TypeError(f"token numbers are int32 or int64, got {ids.dtype}")
-    return code
+    import torch
+
+    if ids.dtype == torch.int64:
+        return 1
+    if ids.dtype == torch.int32:
+        return 0
+    raise TypeError(f"token numbers are int32 or int64, got {ids.dtype}")
 
 
 def embedding_forward(ids, table, scale=1.0, out_dtype=None, out=None):
@@ -369,21 +388,22 @@ def embedding_forward(ids, table, scale=1.0, out_dtype=None, out=None):
     packed = isinstance(table, _nq.NF4Tensor)
     if len(table.shape) != 2:
         raise ValueError("a table is 2-D [vocab x dim]")
+    if ids.get_device() < 0:
+        raise ValueError("tensors must be contiguous device tensors")
     vocab, dim = table.shape
     if out is None:
         out_dtype = out_dtype or (torch.bfloat16 if packed else table.dtype)
         out = torch.empty((*ids.shape, dim), dtype=out_dtype, device=ids.device)
-    elif tuple(out.shape) != (*ids.shape, dim) or (out_dtype is not None and out.dtype != out_dtype):
+    elif out.shape != (*ids.shape, dim) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError(f"out: {(*ids.shape, dim)} is wanted")
-    _nq._need_cuda(ids, out, *((table.codes, table.absmax, table.absmax_q, table.absmax_scale) if packed else (table,)))
-    _same_device(ids.device, out, table.codes if packed else table)
-    L, args = _nq.lib(), (ids.data_ptr(), _index_code(ids), ids.numel())
-    od, stream = _nq._dtype_code(out.dtype), _nq._stream(ids.device)
+    L, code, count, od = _nq.lib(), _index_code(ids), ids.numel(), _code(out.dtype)
     if packed:
+        stream = _stream(_check_tensors(ids, out, table.codes, table.absmax, table.absmax_q, table.absmax_scale))
         w = table.weight_struct()
-        st = L.nf4_embedding_forward_packed(*args, ctypes.byref(w), float(scale), out.data_ptr(), od, stream)
+        st = L.nf4_embedding_forward_packed(ids.data_ptr(), code, count, ctypes.byref(w), scale, out.data_ptr(), od, stream)
     else:
-        st = L.nf4_embedding_forward(*args, table.data_ptr(), _nq._dtype_code(table.dtype), vocab, dim, float(scale),
+        stream = _stream(_check_tensors(ids, out, table))
+        st = L.nf4_embedding_forward(ids.data_ptr(), code, count, table.data_ptr(), _code(table.dtype), vocab, dim, scale,
                                      out.data_ptr(), od, stream)
     _nq._check(st, "nf4_embedding_forward")
     return out
@@ -396,25 +416,26 @@ def embedding_backward(ids, dy, vocab, scale=1.0, padding_id=None, grad=None, gr
     import torch
 
     dim = dy.shape[-1]
-    if tuple(dy.shape) != (*ids.shape, dim):
+    if dy.get_device() < 0:
+        raise ValueError("tensors must be contiguous device tensors")
+    if dy.shape != (*ids.shape, dim):
         raise ValueError(f"dy {tuple(dy.shape)} for ids {tuple(ids.shape)}")
     accumulate = grad is not None
     if not accumulate:
         grad = torch.empty((vocab, dim), dtype=grad_dtype or dy.dtype, device=dy.device)
     elif tuple(grad.shape) != (vocab, dim) or (grad_dtype is not None and grad.dtype != grad_dtype):
         raise ValueError(f"grad {tuple(grad.shape)} {grad.dtype}: ({vocab}, {dim}) is wanted")
-    _nq._need_cuda(ids, dy, grad, workspace)
-    _same_device(dy.device, ids, grad, workspace)
-    L = _nq.lib()
+    index = _check_tensors(dy, ids, grad, workspace)
+    L, count, code = _nq.lib(), ids.numel(), _index_code(ids)
     if workspace is None:
-        size = _size(L.nf4_embedding_backward_workspace_size(ids.numel(), vocab, dim),
-                     "nf4_embedding_backward_workspace_size")
-        workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=dy.device)
-    st = L.nf4_embedding_backward(ids.data_ptr(), _index_code(ids), ids.numel(), dy.data_ptr(),
-                                  _nq._dtype_code(dy.dtype), vocab, dim, float(scale),
-                                  -1 if padding_id is None else int(padding_id), grad.data_ptr(),
-                                  _nq._dtype_code(grad.dtype), 1 if accumulate else 0, workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _nq._stream(dy.device))
+        size = max(_size(L.nf4_embedding_backward_workspace_size(count, vocab, dim),
+                         "nf4_embedding_backward_workspace_size"), 1)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dy.device)
+    else:
+        size = workspace.numel() * workspace.element_size()
+    st = L.nf4_embedding_backward(ids.data_ptr(), code, count, dy.data_ptr(), _code(dy.dtype), vocab, dim, scale,
+                                  -1 if padding_id is None else int(padding_id), grad.data_ptr(), _code(grad.dtype),
+                                  1 if accumulate else 0, workspace.data_ptr(), size, _stream(index))
     _nq._check(st, "nf4_embedding_backward")
     return grad
 
