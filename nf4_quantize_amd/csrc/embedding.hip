@@ -13,7 +13,6 @@ namespace nf4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kInFlight = 4;
 
 // The row of token t, or `vocab` where it has none.
 __device__ __forceinline__ uint32_t token_key(const void *ids, bool i64, int64_t t, int64_t vocab, int64_t skip) {
@@ -23,8 +22,10 @@ __device__ __forceinline__ uint32_t token_key(const void *ids, bool i64, int64_t
 
 // ---- forward ----
 
-// A group of `lanes` lanes moves one row, four vectors of a lane in flight.
-template <typename T, typename O, bool kNarrow>
+// A group of `lanes` lanes moves one row, kInFlight vectors of a lane at a time.
+// The rows go out past the caches (16384 x 8192 bf16: 70 us instead of 80); the
+// table's stay in them, as text asks for a few rows often (98 us without).
+template <typename T, typename O, int kInFlight, bool kNarrow>
 __global__ __launch_bounds__(kThreads) void lookup_kernel(const void *ids, bool i64, int64_t tokens, const T *table,
                                                           int64_t vocab, int32_t dim, float scale, O *out, int lanes) {
     const int each = kThreads / lanes;
@@ -44,7 +45,7 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(const void *ids, bool 
                 cols_values(raw[u], c, x);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = row < vocab ? x[j] * scale : 0.0f;
-                store_cols(dst, c, x);
+                stream_cols(dst, c, x);
             }
         }
     }
@@ -596,7 +597,13 @@ template <typename T, typename O>
 hipError_t lookup(const void *ids, bool i64, int64_t tokens, const void *table, int64_t vocab, int64_t dim,
                   float scale, void *out, hipStream_t s) {
     const int lanes = lanes_for(dim);
-    auto kernel = dim < 8 ? lookup_kernel<T, O, true> : lookup_kernel<T, O, false>;
+    // as many vectors in flight as a lane has, up to four: with more, a lane
+    // works on columns past the row (16384 x 1000 bf16: 19 us instead of 12)
+    const int64_t vecs = (dim + lanes * 8 - 1) / (lanes * 8);
+    auto kernel = dim < 8     ? lookup_kernel<T, O, 1, true>
+                  : vecs == 1 ? lookup_kernel<T, O, 1, false>
+                  : vecs == 2 ? lookup_kernel<T, O, 2, false>
+                              : lookup_kernel<T, O, 4, false>;
     kernel<<<lookup_grid(tokens, lanes), dim3(kThreads), 0, s>>>(
         ids, i64, tokens, static_cast<const T *>(table), vocab, (int32_t)dim, scale, static_cast<O *>(out), lanes);
     return hipGetLastError();

@@ -55,7 +55,7 @@ __device__ __forceinline__ void store_row(T *row, const Cols<kKind == kRowNarrow
     if constexpr (kKind == kRowVecs) {
         if (c.live > 0) store_stream(row + (uint32_t)c.col, x);
     } else {
-        store_cols(row, c, x);
+        stream_cols(row, c, x);
     }
 }
 

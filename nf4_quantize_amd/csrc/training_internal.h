@@ -120,8 +120,10 @@ __device__ __forceinline__ Raw8<Bf16> load_raw(const Bf16 *p) {
 __device__ __forceinline__ Raw8<float> load_raw(const float *p) {
     return {reinterpret_cast<const f32x4_any4 *>(p)->v, reinterpret_cast<const f32x4_any4 *>(p + 4)->v};
 }
-// The same at 16-byte aligned addresses, past the caches' usual order: for
-// data that is not read again soon.
+// The same past the caches' usual order: for data that is not read again soon.
+// Loads are of 16-byte aligned addresses; stores take any element's.
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
 __device__ __forceinline__ Raw8<Bf16> load_stream(const Bf16 *p) {
     return {__builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p))};
 }
@@ -133,11 +135,11 @@ __device__ __forceinline__ void store_stream(Bf16 *p, const float (&x)[8]) {
     u32x4 r;
 #pragma unroll
     for (int j = 0; j < 4; ++j) r[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
-    __builtin_nontemporal_store(r, reinterpret_cast<u32x4 *>(p));
+    __builtin_nontemporal_store(r, reinterpret_cast<u32x4_at2 *>(p));
 }
 __device__ __forceinline__ void store_stream(float *p, const float (&x)[8]) {
-    __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4 *>(p));
-    __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4 *>(p + 4));
+    __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4_at4 *>(p));
+    __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4_at4 *>(p + 4));
 }
 __device__ __forceinline__ void values(const Raw8<Bf16> &r, float (&x)[8]) {
 #pragma unroll
@@ -196,6 +198,13 @@ __device__ __forceinline__ void cols_values(const Raw8<T> &r, const Cols<kNarrow
 template <typename T, bool kNarrow>
 __device__ __forceinline__ void store_cols(T *row, const Cols<kNarrow> &c, const float (&x)[8]) {
     if (c.live >= 8) return store8(row + (uint32_t)c.col, x);
+    if (c.live > 0) store_upto8(row + (uint32_t)c.col, c.live, x);
+}
+
+// store_cols past the caches' usual order.
+template <typename T, bool kNarrow>
+__device__ __forceinline__ void stream_cols(T *row, const Cols<kNarrow> &c, const float (&x)[8]) {
+    if (c.live >= 8) return store_stream(row + (uint32_t)c.col, x);
     if (c.live > 0) store_upto8(row + (uint32_t)c.col, c.live, x);
 }
 
