@@ -94,7 +94,7 @@ dim3 lookup_grid(int64_t tokens, int lanes) {
 
 // ---- sorting the tokens ----
 
-constexpr int kOneTile = 4096;      // up to here each token counts its place among all
+constexpr int kOneTile = 6144;      // up to here each token counts its place among all
 constexpr int kTile = 2048;         // up to kRankTokens: in its tile, and searches the others
 constexpr int kRankTokens = 32768;
 constexpr int kTiles = 64;          // workgroups of a digit pass above
@@ -542,7 +542,7 @@ hipError_t sort_tokens(const Sort &q, hipStream_t s) {
         p.ids = q.ids, p.i64 = q.i64, p.tokens = (int32_t)q.tokens, p.vocab = q.vocab, p.skip = q.skip;
         p.tile = one ? kOneTile : kTile;
         // as many workgroups as there are CUs, where there are tokens for them
-        p.each = p.tokens > 8192 ? 64 : p.tokens > 4096 ? 32 : 16;
+        p.each = p.tokens > 16384 ? 64 : p.tokens > 6144 ? 32 : 16;
         p.wgs = (p.tokens + p.each - 1) / p.each;
         p.key_out = one ? q.key : q.key2, p.idx_out = one ? q.idx : q.idx2, p.grad = q.clear, p.n = q.n;
         rank_tokens_kernel<G><<<dim3(p.wgs + clear), dim3(1024), 0, s>>>(p);

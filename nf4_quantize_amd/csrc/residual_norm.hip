@@ -283,8 +283,12 @@ __global__ __launch_bounds__(1024) void residual_norm_means_kernel(NormParams p)
 // tiles (kTiled, blockIdx.y), whose means come from residual_norm_means_kernel:
 // the row is read twice, but a lane's sums stay in registers (in one kernel, two
 // vectors a lane spilled: 442 us for 2048 x 16384 bf16).
-template <typename T, typename R, RowKind kKind, bool kToken, bool kWide, bool kTiled>
-__global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormParams p) {
+// kMost: threads of the workgroup at most. Up to 512 (4096 columns) a lane may have
+// the 133 to 167 registers that it wants, on three waves a SIMD; with 128 on four
+// it spills (4096 x 4096 with an fp32 stream and token gates: 95 us instead of 69;
+// 14000 x 2304 bf16: 99 instead of 82).
+template <typename T, typename R, RowKind kKind, bool kToken, bool kWide, bool kTiled, int kMost>
+__global__ __launch_bounds__(kMost) void residual_norm_backward_kernel(NormParams p) {
     __shared__ float part[2][3][16];
     extern __shared__ float s_cols[];
     constexpr bool kNarrow = kKind == kRowNarrow;
@@ -318,9 +322,9 @@ __global__ __launch_bounds__(1024) void residual_norm_backward_kernel(NormParams
         const bool live_row = r0 + group < p.rows;
         const float r1 = next_r1, r2 = next_r2;
         float c1 = next_means.x, c2 = next_means.y;
-        if constexpr (sizeof(T) == 4) {
+        if constexpr (sizeof(T) == 4 && kMost > 512) {
             // no room for the weights beside fp32 rows in flight (kept, they spilled:
-            // 205 us for 8192 x 4096 instead of 178); the others gain by keeping them
+            // 325 us for 4096 x 8192 with token gates instead of 307)
             asm volatile("" ::: "memory");
             w.load(p, p.in.y && p.gate_kind == NF4_GATE_CHANNEL, c);
         }
@@ -407,47 +411,54 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float *partial, 
     }
 }
 
-// Lanes of a row, vectors of a lane, threads of a workgroup: up to 512 columns a
+// Lanes of a row, vectors of a lane, threads of a workgroup, and threads that a CU
+// holds of the kernel: up to 512 columns a
 // row is part of a wave and a workgroup takes several; above, a workgroup takes
 // one row with as many waves as it needs, one vector a lane up to 8192 columns.
 struct Split {
-    int lanes, vec, block;
+    int lanes, vec, block, resident;
 };
 Split split_of(int64_t dim) {
     const int64_t vecs = (dim + 7) / 8;
     if (vecs <= 64) {
         int lanes = 8;
         while (lanes < vecs) lanes *= 2;
-        return {lanes, 1, 256};
+        return {lanes, 1, 256, 2048};
     }
     const int vec = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
     const int lanes = (int)((vecs + 64 * vec - 1) / (64 * vec)) * 64;
-    return {lanes, vec, lanes};
+    return {lanes, vec, lanes, 2048};
 }
-// The backward pass holds 128 registers a lane, so its workgroups have a power of
-// two of waves that the four SIMDs can share evenly: five waves of 2304 columns
+// The backward pass needs many registers, so its workgroups have a power of two of
+// waves that the four SIMDs can share evenly: five waves of 2304 columns
 // (14000 rows) take 116 us, eight 96. vec: tiles of a row here.
 Split backward_split_of(int64_t dim) {
     Split sp = split_of(dim);
-    if (sp.lanes <= 64) return sp;
-    const int64_t vecs = (dim + 7) / 8;
-    sp.vec = (int)((vecs + 1023) / 1024);
-    sp.lanes = 128;
-    while ((int64_t)sp.lanes * sp.vec < vecs) sp.lanes *= 2;
-    sp.block = sp.lanes;
+    if (sp.lanes > 64) {
+        const int64_t vecs = (dim + 7) / 8;
+        sp.vec = (int)((vecs + 1023) / 1024);
+        sp.lanes = 128;
+        while ((int64_t)sp.lanes * sp.vec < vecs) sp.lanes *= 2;
+        sp.block = sp.lanes;
+    }
+    sp.resident = sp.block > 512 ? 1024 : 768;  // three waves a SIMD with up to 167 registers
     return sp;
 }
 
-// Workgroups that fill the chip's 256 CUs with `threads` threads each, as far as
-// there are rows.
-int64_t workgroups(int64_t rows, const Split &sp, int threads) {
+// Workgroups that fill the chip's 256 CUs, as far as there are rows.
+int64_t workgroups(int64_t rows, const Split &sp) {
     const int64_t groups = sp.block / sp.lanes, need = (rows + groups - 1) / groups;
-    const int64_t most = 256 * (threads / sp.block > 0 ? threads / sp.block : 1);
+    const int64_t most = 256 * (sp.resident / sp.block);
     return need < most ? need : most;
 }
+// Each workgroup of the backward pass leaves a row of partial sums, so beyond one
+// for each CU none takes fewer than two sets of rows (1024 x 2048 bf16: 14 us
+// instead of 18). Tiles of a row fill the chip together.
 int64_t backward_workgroups(int64_t rows, const Split &sp) {
-    const int64_t all = workgroups(rows, sp, 1024);
-    return sp.vec > 1 && all > 256 / sp.vec ? 256 / sp.vec : all;  // tiles of a row fill the chip together
+    const int64_t groups = sp.block / sp.lanes, pairs = (rows + 2 * groups - 1) / (2 * groups);
+    const int64_t all = workgroups(rows, sp), one = all < 256 ? all : 256;
+    if (sp.vec > 1) return all < 256 / sp.vec ? all : 256 / sp.vec;
+    return all < pairs ? all : pairs < one ? one : pairs;
 }
 
 NormParams params_of(const nf4_residual_norm_shape &sh, const ResidualNormIn &in, const ResidualNormOut &out,
@@ -467,15 +478,17 @@ hipError_t forward_kind(const NormParams &p, const Split &sp, hipStream_t s) {
                   : sp.vec == 2 ? residual_norm_forward_kernel<T, R, kBig ? 2 : 1, kKind, kBig>
                   : sp.lanes > 64 ? residual_norm_forward_kernel<T, R, 1, kKind, kBig>
                                   : residual_norm_forward_kernel<T, R, 1, kKind, false>;
-    kernel<<<dim3((uint32_t)workgroups(p.rows, sp, 2048)), dim3(sp.block), 0, s>>>(p);
+    kernel<<<dim3((uint32_t)workgroups(p.rows, sp)), dim3(sp.block), 0, s>>>(p);
     return hipGetLastError();
 }
 template <typename T, typename R, RowKind kKind, bool kToken>
 hipError_t backward_kind(const NormParams &p, const Split &sp, hipStream_t s) {
     constexpr bool kBig = kKind != kRowNarrow;
-    auto kernel = sp.vec > 1      ? residual_norm_backward_kernel<T, R, kKind, kToken, kBig, kBig>
-                  : sp.lanes > 64 ? residual_norm_backward_kernel<T, R, kKind, kToken, kBig, false>
-                                  : residual_norm_backward_kernel<T, R, kKind, kToken, false, false>;
+    constexpr int kMost = kBig ? 1024 : 512;
+    auto kernel = sp.vec > 1       ? residual_norm_backward_kernel<T, R, kKind, kToken, kBig, kBig, kMost>
+                  : sp.lanes > 512 ? residual_norm_backward_kernel<T, R, kKind, kToken, kBig, false, kMost>
+                  : sp.lanes > 64  ? residual_norm_backward_kernel<T, R, kKind, kToken, kBig, false, 512>
+                                   : residual_norm_backward_kernel<T, R, kKind, kToken, false, false, 512>;
     if constexpr (kBig)
         if (sp.vec > 1) {
             const int64_t wgs = p.rows < 512 ? p.rows : 512;
