@@ -10,14 +10,16 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "training_internal.h"
 
 namespace nf4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kEach = 8;                   // elements of a thread in one pass
-constexpr int kPass = kThreads * kEach;    // 2048 elements: 8 moment blocks
+constexpr int kPass = 2048;                // elements of a workgroup: 8 moment blocks
+constexpr int kEach = kPass / kThreads;    // the norm's elements of a thread in one pass
 constexpr int kBatch = 48;                 // entries per launch: 3.9 KB of kernel arguments
 constexpr float kScaleMin = 0x1p-126f;     // the smallest scale whose reciprocal is finite
 constexpr float kE4m3Max = 448.0f;
@@ -122,14 +124,76 @@ __device__ __forceinline__ float storage_scale(float amax, float *inv) {
     return s;
 }
 
-// One workgroup: 2048 consecutive elements of one entry. A half-wave holds one block of 256, eight elements a lane, so the block's maximum is a
-// reduction over 32 lanes in registers and every byte is moved once. Weights and
-// moments go past the caches' usual order (they are not read again before the
-// next step), gradients do not, and the workgroups run from the end of the list:
-// what the norm's pass read last is still in the memory-side cache. The 448
-// tensors take 365 us with both, 424 without.
-template <typename W, typename G, bool kMaster, bool kEight, bool kTable>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b, AdamwScalars c) {
+// A lane's four elements, as eight are loaded and stored by load_raw, load_stream
+// and store_stream.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+template <typename T> struct Raw4;
+template <> struct Raw4<Bf16> { u32x2 v; };
+template <> struct Raw4<float> { f32x4 v; };
+__device__ __forceinline__ void values(const Raw4<Bf16> &r, float (&x)[4]) {
+    x[0] = bf16_lo(r.v[0]), x[1] = bf16_hi(r.v[0]), x[2] = bf16_lo(r.v[1]), x[3] = bf16_hi(r.v[1]);
+}
+__device__ __forceinline__ void values(const Raw4<float> &r, float (&x)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = r.v[j];
+}
+template <int N, typename T>
+__device__ __forceinline__ auto load_each(const T *p) {
+    if constexpr (N == 8) return load_raw(p);
+    else return *reinterpret_cast<const Raw4<T> *>(p);
+}
+template <int N, typename T>
+__device__ __forceinline__ auto stream_each(const T *p) {
+    if constexpr (N == 8) return load_stream(p);
+    else return Raw4<T>{__builtin_nontemporal_load(&reinterpret_cast<const Raw4<T> *>(p)->v)};
+}
+__device__ __forceinline__ void store_stream(float *p, const float (&x)[4]) {
+    __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4 *>(p));
+}
+__device__ __forceinline__ void store_stream(Bf16 *p, const float (&x)[4]) {
+    __builtin_nontemporal_store(u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, reinterpret_cast<u32x2 *>(p));
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_upto(T *p, int64_t live, const float (&x)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (j < live) store1(p + j, x[j]);
+}
+template <typename Code, int N>
+__device__ __forceinline__ void decode_each(Code q, float scale, float (&x)[N]) {
+    unpack_e4m3((uint32_t)q, scale, x);
+    if constexpr (N == 8) unpack_e4m3((uint32_t)(q >> 32), scale, x + 4);
+}
+template <typename Code, int N>
+__device__ __forceinline__ Code encode_each(const float (&x)[N], const uint32_t (&r)[N]) {
+    Code q = pack_e4m3_sr(x, r);
+    if constexpr (N == 8) q |= (Code)pack_e4m3_sr(x + 4, r + 4) << 32;
+    return q;
+}
+
+// One workgroup: 2048 consecutive elements of one entry, eight a lane, or four:
+// then 16 bytes of an fp32 array, and a load covers whole cache lines. Four where
+// weights are kept in fp32 or moments in 32 bits, eight where the bf16 weights and
+// the codes are all there is: 60 million elements (8 | 4 a lane)
+//   bf16 weights and gradients, 8-bit moments                    112 | 128 us
+//   the same and a master weight                                 196 | 161
+//   fp32 weights and gradients, 8-bit moments                    170 | 158
+//   bf16 weights and gradients, 32-bit moments                   242 | 217
+//   the same, fp32 gradients and a master weight                 370 | 306
+// A block of 256 is 32 lanes or the wave, so the block's maximum is a reduction in
+// registers and every byte is moved once. Weights and moments go past the caches'
+// usual order (they are not read again before the next step), gradients do not,
+// and the workgroups run from the end of the list: what the norm's pass read last
+// is still in the memory-side cache. The 448 tensors take 365 us with both, 424
+// without.
+template <typename W, bool kMaster, bool kEight>
+constexpr int kStepEach = (kEight && !kMaster && sizeof(W) == 2) ? 8 : 4;
+
+template <typename W, typename G, bool kMaster, bool kEight, bool kTable, int N = kStepEach<W, kMaster, kEight>>
+__global__ __launch_bounds__(kPass / N) void adamw_kernel(AdamwBatch b, AdamwScalars c) {
+    constexpr int kBlockLanes = kMomentBlock / N;
+    using Code = std::conditional_t<N == 8, uint64_t, uint32_t>;  // a lane's codes
     float clip = 1.0f;
     if (c.norm != nullptr) {
         const float norm = *c.norm;
@@ -138,32 +202,38 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b, AdamwScal
     }
     const uint32_t wg = gridDim.x - 1 - blockIdx.x;
     const AdamwItem e = kTable ? c.table[find_in_table(c.firsts, c.count, wg)] : b.item[find_in_batch(b.item, wg)];
-    const int64_t i = (int64_t)(wg - e.first) * kPass + threadIdx.x * kEach;
+    const int64_t i = (int64_t)(wg - e.first) * kPass + threadIdx.x * N;
     const int64_t live = e.n - i;  // may be <= 0: the lane still joins the reductions
     W *w = static_cast<W *>(e.w) + i;
     const G *g = static_cast<const G *>(e.g) + i;
-    float x[8], gr[8], m[8], v[8];
-    if (live >= 8) {  // the loads first, all in flight
-        const auto rg = load_raw(g);
+    float x[N], gr[N], m[N], v[N];
+    if (live >= N) {  // the loads first, all in flight and in this order (the weight before the codes: 4% more)
+        const auto weight = [&] {
+            if constexpr (kMaster) return stream_each<N>(e.master + i);
+            else return stream_each<N>(w);
+        };
+        const auto rg = load_each<N>(g);
         if constexpr (kEight) {
-            const uint64_t mq = __builtin_nontemporal_load(reinterpret_cast<const uint64_t *>(static_cast<const uint8_t *>(e.m) + i));
-            const uint64_t vq = __builtin_nontemporal_load(reinterpret_cast<const uint64_t *>(static_cast<const uint8_t *>(e.v) + i));
+            const Code mq = __builtin_nontemporal_load(reinterpret_cast<const Code *>(static_cast<const uint8_t *>(e.m) + i));
+            const Code vq = __builtin_nontemporal_load(reinterpret_cast<const Code *>(static_cast<const uint8_t *>(e.v) + i));
             const float ms = e.ms[i / kMomentBlock], vs = e.vs[i / kMomentBlock];
-            if constexpr (kMaster) values(load_stream(e.master + i), x);
-            else values(load_stream(w), x);
-            unpack_e4m3((uint32_t)mq, ms, m), unpack_e4m3((uint32_t)(mq >> 32), ms, m + 4);
-            unpack_e4m3((uint32_t)vq, vs, v), unpack_e4m3((uint32_t)(vq >> 32), vs, v + 4);
+            const auto rx = weight();
+            __builtin_amdgcn_sched_barrier(0);
+            values(rx, x);
+            decode_each(mq, ms, m);
+            decode_each(vq, vs, v);
         } else {
-            const auto rm = load_stream(static_cast<const float *>(e.m) + i);
-            const auto rv = load_stream(static_cast<const float *>(e.v) + i);
-            if constexpr (kMaster) values(load_stream(e.master + i), x);
-            else values(load_stream(w), x);
+            const auto rm = stream_each<N>(static_cast<const float *>(e.m) + i);
+            const auto rv = stream_each<N>(static_cast<const float *>(e.v) + i);
+            const auto rx = weight();
+            __builtin_amdgcn_sched_barrier(0);
+            values(rx, x);
             values(rm, m), values(rv, v);
         }
         values(rg, gr);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < N; ++j) {
             x[j] = gr[j] = m[j] = v[j] = 0.0f;
             if (j >= live) continue;
             x[j] = kMaster ? e.master[i + j] : load1(w + j);
@@ -179,7 +249,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b, AdamwScal
     }
     float ma = 0.0f, va = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < N; ++j) {
         const float gj = gr[j] * clip;
         // product by product, without contraction: the stored codes follow
         // from these fp32 values to the bit
@@ -191,28 +261,28 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b, AdamwScal
         x[j] = fmaf(-e.step * m[j], __builtin_amdgcn_rcpf(d), x[j] * e.keep);
         ma = fmaxf(ma, fabsf(m[j])), va = fmaxf(va, v[j]);
     }
-    if (live >= 8) {
+    if (live >= N) {
         if constexpr (kMaster) store_stream(e.master + i, x);
         store_stream(w, x);
     } else if (live > 0) {
-        if constexpr (kMaster) store_upto8(e.master + i, live, x);
-        store_upto8(w, live, x);
+        if constexpr (kMaster) store_upto(e.master + i, live, x);
+        store_upto(w, live, x);
     }
     if constexpr (!kEight) {
-        if (live >= 8) {
+        if (live >= N) {
             store_stream(static_cast<float *>(e.m) + i, m);
             store_stream(static_cast<float *>(e.v) + i, v);
         } else if (live > 0) {
-            store_upto8(static_cast<float *>(e.m) + i, live, m);
-            store_upto8(static_cast<float *>(e.v) + i, live, v);
+            store_upto(static_cast<float *>(e.m) + i, live, m);
+            store_upto(static_cast<float *>(e.v) + i, live, v);
         }
     } else {
         float rm, rv;
-        const float ms = storage_scale(max32(ma), &rm);
-        const float vs = storage_scale(max32(va), &rv);
-        uint32_t rndm[8], rndv[8];
+        const float ms = storage_scale(group_max<kBlockLanes>(ma), &rm);
+        const float vs = storage_scale(group_max<kBlockLanes>(va), &rv);
+        uint32_t rndm[N], rndv[N];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < N; ++j) {
             const uint32_t r = mix((uint32_t)i * kWeyl + e.key + (uint32_t)j * kWeyl);
             rndm[j] = r & 0xFFFF0000u, rndv[j] = r << 16;
             m[j] = __builtin_amdgcn_fmed3f(m[j] * rm, -kE4m3Max, kE4m3Max);
@@ -220,18 +290,18 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwBatch b, AdamwScal
         }
         if (live <= 0) return;
         uint8_t *mq = static_cast<uint8_t *>(e.m) + i, *vq = static_cast<uint8_t *>(e.v) + i;
-        const uint32_t mw[2] = {pack_e4m3_sr(m, rndm), pack_e4m3_sr(m + 4, rndm + 4)};
-        const uint32_t vw[2] = {pack_e4m3_sr(v, rndv), pack_e4m3_sr(v + 4, rndv + 4)};
-        if (live >= 8) {
-            __builtin_nontemporal_store(mw[0] | (uint64_t)mw[1] << 32, reinterpret_cast<uint64_t *>(mq));
-            __builtin_nontemporal_store(vw[0] | (uint64_t)vw[1] << 32, reinterpret_cast<uint64_t *>(vq));
+        const Code mw = encode_each<Code>(m, rndm);
+        const Code vw = encode_each<Code>(v, rndv);
+        if (live >= N) {
+            __builtin_nontemporal_store(mw, reinterpret_cast<Code *>(mq));
+            __builtin_nontemporal_store(vw, reinterpret_cast<Code *>(vq));
         } else {
             for (int j = 0; j < (int)live; ++j) {
-                mq[j] = (uint8_t)(mw[j / 4] >> (8 * (j % 4)));
-                vq[j] = (uint8_t)(vw[j / 4] >> (8 * (j % 4)));
+                mq[j] = (uint8_t)(mw >> (8 * j));
+                vq[j] = (uint8_t)(vw >> (8 * j));
             }
         }
-        if (threadIdx.x % 32 == 0) {
+        if (threadIdx.x % kBlockLanes == 0) {
             e.ms[i / kMomentBlock] = ms;
             e.vs[i / kMomentBlock] = vs;
         }
@@ -382,6 +452,7 @@ hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_ada
         const hipError_t r = hipGetLastError();
         if (err == hipSuccess) err = r;
     };
+    const dim3 threads(kPass / kStepEach<W, kMaster, kEight>);
     auto copy = [&] {  // the batch into the table
         if (used == 0) return;
         adamw_table_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(b, used, items + done, firsts + done);
@@ -393,11 +464,11 @@ hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_ada
         if (table) {
             copy();
             c.table = items + from, c.firsts = firsts + from, c.count = done - from;
-            adamw_kernel<W, G, kMaster, kEight, true><<<dim3((uint32_t)wgs), dim3(kThreads), 0, s>>>(b, c);
+            adamw_kernel<W, G, kMaster, kEight, true><<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
             from = done;
         } else {
             for (int j = used; j < kBatch; ++j) b.item[j].first = UINT32_MAX;
-            adamw_kernel<W, G, kMaster, kEight, false><<<dim3((uint32_t)wgs), dim3(kThreads), 0, s>>>(b, c);
+            adamw_kernel<W, G, kMaster, kEight, false><<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
             used = 0;
         }
         note();

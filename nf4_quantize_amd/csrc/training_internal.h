@@ -235,15 +235,19 @@ __device__ __forceinline__ float group_sum(float x, int lanes) {
     if (lanes > 32) rows32(x, a, b), x = a + b;
     return x;
 }
-// Maximum of non-negative values over aligned groups of 32 lanes.
-__device__ __forceinline__ float max32(float x) {
+// Maximum of non-negative values over aligned groups of 32 lanes, or the wave.
+template <int kLanes>
+__device__ __forceinline__ float group_max(float x) {
+    static_assert(kLanes == 32 || kLanes == 64, "lanes");
     float a, b;
     x = fmaxf(x, dpp<kXor1>(x));
     x = fmaxf(x, dpp<kXor2>(x));
     x = fmaxf(x, dpp<kHalfMirror>(x));
     x = fmaxf(x, dpp<kMirror>(x));
     rows16(x, a, b);
-    return fmaxf(a, b);
+    x = fmaxf(a, b);
+    if constexpr (kLanes == 64) rows32(x, a, b), x = fmaxf(a, b);
+    return x;
 }
 
 }  // namespace nf4
