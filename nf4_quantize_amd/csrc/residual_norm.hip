@@ -10,6 +10,8 @@
 // a group of lanes, eight consecutive elements a lane and vector.
 #include <math.h>
 
+#include <type_traits>
+
 #include "training_internal.h"
 
 namespace nf4 {
@@ -32,16 +34,70 @@ struct NormParams {
 // How a row lies in memory: fewer than eight elements; any number; or whole
 // vectors (dim a multiple of 8), which are moved past the caches' usual order, as
 // nothing here is read twice. The same rows as kRowAny take 67 us instead of 57
-// forward and 96 instead of 83 backward (16384 x 2048 bf16).
-enum RowKind { kRowNarrow, kRowAny, kRowVecs };
+// forward and 96 instead of 83 backward (16384 x 2048 bf16). With an fp32 stream and
+// more than 512 columns a lane takes two fours instead of an eight (kRowFours):
+// 8192 x 8192 fp32 take 186 us instead of 203 forward and 286 instead of 366
+// backward, bf16 blocks on an fp32 stream 137 (as before) and 217 instead of 259.
+enum RowKind { kRowNarrow, kRowAny, kRowVecs, kRowFours };
+
+// A lane's columns with kRowFours: four, and four 256 further on, so that a wave's
+// load of fp32 covers whole cache lines. `c` counts eights as the other kinds do; a
+// wave's 64 cover the same 512 columns, so a row's last wave is whole.
+struct Fours {
+    int lo, hi, from_lo, from_hi;
+    bool live_lo, live_hi;
+    __device__ __forceinline__ Fours(int c, int dim)
+        : lo((c & ~511) + (c & 511) / 2), hi(lo + 256), from_lo(lo < dim ? lo : dim - 4),
+          from_hi(hi < dim ? hi : dim - 4), live_lo(lo < dim), live_hi(hi < dim) {}
+};
+template <RowKind kKind>
+using ColsOf = std::conditional_t<kKind == kRowFours, Fours, Cols<kKind == kRowNarrow>>;
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ Raw8<float> load_cols(const float *row, const Fours &c) {
+    return {*reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_lo), *reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_hi)};
+}
+__device__ __forceinline__ Raw8<Bf16> load_cols(const Bf16 *row, const Fours &c) {
+    const u32x2 a = *reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_lo), b = *reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_hi);
+    return {u32x4{a[0], a[1], b[0], b[1]}};
+}
+__device__ __forceinline__ Raw8<float> stream_fours(const float *row, const Fours &c) {
+    return {__builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_lo)),
+            __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_hi))};
+}
+__device__ __forceinline__ Raw8<Bf16> stream_fours(const Bf16 *row, const Fours &c) {
+    const u32x2 a = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_lo));
+    const u32x2 b = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_hi));
+    return {u32x4{a[0], a[1], b[0], b[1]}};
+}
+template <typename T>
+__device__ __forceinline__ void cols_values(const Raw8<T> &r, const Fours &c, float (&x)[8]) {
+    values(r, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = (j < 4 ? c.live_lo : c.live_hi) ? x[j] : 0.0f;
+}
+__device__ __forceinline__ void store_cols(float *row, const Fours &c, const float (&x)[8]) {
+    if (c.live_lo) *reinterpret_cast<f32x4 *>(row + c.lo) = f32x4{x[0], x[1], x[2], x[3]};
+    if (c.live_hi) *reinterpret_cast<f32x4 *>(row + c.hi) = f32x4{x[4], x[5], x[6], x[7]};
+}
+__device__ __forceinline__ void store_fours(float *row, const Fours &c, const float (&x)[8]) {
+    if (c.live_lo) __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4 *>(row + c.lo));
+    if (c.live_hi) __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4 *>(row + c.hi));
+}
+__device__ __forceinline__ void store_fours(Bf16 *row, const Fours &c, const float (&x)[8]) {
+    const u32x2 a = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, b = {pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+    if (c.live_lo) __builtin_nontemporal_store(a, reinterpret_cast<u32x2 *>(row + c.lo));
+    if (c.live_hi) __builtin_nontemporal_store(b, reinterpret_cast<u32x2 *>(row + c.hi));
+}
 
 template <RowKind kKind, typename T>
-__device__ __forceinline__ Raw8<T> load_row(const T *row, const Cols<kKind == kRowNarrow> &c) {
-    if constexpr (kKind == kRowVecs) return load_stream(row + (uint32_t)c.base);
+__device__ __forceinline__ Raw8<T> load_row(const T *row, const ColsOf<kKind> &c) {
+    if constexpr (kKind == kRowFours) return stream_fours(row, c);
+    else if constexpr (kKind == kRowVecs) return load_stream(row + (uint32_t)c.base);
     else return load_cols(row, c);
 }
 template <RowKind kKind, typename T>
-__device__ __forceinline__ void row_values(const Raw8<T> &r, const Cols<kKind == kRowNarrow> &c, float (&x)[8]) {
+__device__ __forceinline__ void row_values(const Raw8<T> &r, const ColsOf<kKind> &c, float (&x)[8]) {
     if constexpr (kKind == kRowVecs) {
         values(r, x);
 #pragma unroll
@@ -51,8 +107,10 @@ __device__ __forceinline__ void row_values(const Raw8<T> &r, const Cols<kKind ==
     }
 }
 template <RowKind kKind, typename T>
-__device__ __forceinline__ void store_row(T *row, const Cols<kKind == kRowNarrow> &c, const float (&x)[8]) {
-    if constexpr (kKind == kRowVecs) {
+__device__ __forceinline__ void store_row(T *row, const ColsOf<kKind> &c, const float (&x)[8]) {
+    if constexpr (kKind == kRowFours) {
+        store_fours(row, c, x);
+    } else if constexpr (kKind == kRowVecs) {
         if (c.live > 0) store_stream(row + (uint32_t)c.col, x);
     } else {
         stream_cols(row, c, x);
@@ -60,8 +118,8 @@ __device__ __forceinline__ void store_row(T *row, const Cols<kKind == kRowNarrow
 }
 
 // Eight weights of the columns (fp32 or bf16).
-template <bool kNarrow>
-__device__ __forceinline__ void load_weight(const void *w, bool bf16, const Cols<kNarrow> &c, float (&x)[8]) {
+template <typename C>
+__device__ __forceinline__ void load_weight(const void *w, bool bf16, const C &c, float (&x)[8]) {
     if (bf16) cols_values(load_cols(static_cast<const Bf16 *>(w), c), c, x);
     else cols_values(load_cols(static_cast<const float *>(w), c), c, x);
 }
@@ -85,10 +143,10 @@ __device__ __forceinline__ void row_sums(float (&x)[kK], int lanes, float (*part
 
 // The columns' weights: kept by workgroups of one vector a lane, which take many
 // rows, and loaded for each row by the others.
-template <bool kNarrow>
+template <typename C>
 struct Weights {
     float pre[8], post[8], gate[8];
-    __device__ __forceinline__ void load(const NormParams &p, bool channel, const Cols<kNarrow> &c) {
+    __device__ __forceinline__ void load(const NormParams &p, bool channel, const C &c) {
         load_weight(p.in.w_pre, p.w_bf16, c, pre);
 #pragma unroll
         for (int j = 0; j < 8; ++j) pre[j] += p.off, post[j] = 1.0f, gate[j] = 1.0f;
@@ -99,6 +157,27 @@ struct Weights {
         }
         if (channel) load_weight(p.in.gate, p.w_bf16, c, gate);
     }
+    // A lane's own weights in LDS.
+    template <int kLanes>
+    __device__ __forceinline__ void save(f32x4 (*s)[kLanes]) const {
+        const float *const all[3] = {pre, post, gate};
+#pragma unroll
+        for (int k = 0; k < 6; ++k) {
+            const float *x = all[k / 2] + k % 2 * 4;
+            s[k][threadIdx.x] = f32x4{x[0], x[1], x[2], x[3]};
+        }
+    }
+    template <bool kToken, int kLanes>
+    __device__ __forceinline__ void restore(const f32x4 (*s)[kLanes]) {
+        asm volatile("" ::: "memory");
+        float *const all[3] = {pre, post, gate};
+#pragma unroll
+        for (int k = 0; k < (kToken ? 4 : 6); ++k) {
+            const f32x4 x = s[k][threadIdx.x];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) all[k / 2][k % 2 * 4 + j] = x[j];
+        }
+    }
 };
 
 // A workgroup takes every gridDim.x-th set of rows. With one vector a lane it
@@ -106,8 +185,8 @@ struct Weights {
 template <typename T, typename R, int kVec, RowKind kKind, bool kWide>
 __global__ __launch_bounds__(1024) void residual_norm_forward_kernel(NormParams p) {
     __shared__ float part[2][1][16];
-    constexpr bool kNarrow = kKind == kRowNarrow, kOne = kVec == 1;
-    typedef Cols<kNarrow> C;
+    constexpr bool kOne = kVec == 1;
+    typedef ColsOf<kKind> C;
     const int lanes = kWide ? blockDim.x : p.lanes;
     const int groups = kWide ? 1 : blockDim.x / lanes, group = kWide ? 0 : threadIdx.x / lanes;
     const int lane = kWide ? threadIdx.x : threadIdx.x % lanes;
@@ -115,7 +194,7 @@ __global__ __launch_bounds__(1024) void residual_norm_forward_kernel(NormParams 
     const R *h_in = static_cast<const R *>(p.in.h);
     const bool post = p.in.w_post != nullptr, channel = y && p.gate_kind == NF4_GATE_CHANNEL;
     auto col = [&](int v) { return C((v * lanes + lane) * 8, p.dim); };
-    Weights<kNarrow> w;
+    Weights<C> w;
     Raw8<T> raw_y[kVec];
     Raw8<R> raw_h[kVec];
     auto load = [&](int64_t r0) {
@@ -205,7 +284,7 @@ template <typename T, typename R, RowKind kKind, bool kToken>
 struct BackwardRow {
     Raw8<T> dx, y, gate[kToken ? 1 : 0];
     Raw8<R> h, dh;
-    typedef Cols<kKind == kRowNarrow> C;
+    typedef ColsOf<kKind> C;
     __device__ __forceinline__ void load(const NormParams &p, int64_t at, const C &c) {
         h = load_row<kKind>(static_cast<const R *>(p.in.h) + at, c);
         if (p.in.dx) dx = load_row<kKind>(static_cast<const T *>(p.in.dx) + at, c);
@@ -218,10 +297,10 @@ struct BackwardRow {
 // The values of one vector of a row in the backward pass.
 template <typename T, typename R, RowKind kKind, bool kToken>
 struct BackwardValues {
-    typedef Cols<kKind == kRowNarrow> C;
+    typedef ColsOf<kKind> C;
     float dx[8], n1[8], n2[8], dh[8], g[8];  // g: the gate with alpha
     __device__ __forceinline__ void unpack(const NormParams &p, const BackwardRow<T, R, kKind, kToken> &raw,
-                                           const Weights<kKind == kRowNarrow> &w, const C &c, float r1, float r2) {
+                                           const Weights<ColsOf<kKind>> &w, const C &c, float r1, float r2) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) dx[j] = dh[j] = n2[j] = 0.0f;
         row_values<kKind>(raw.h, c, n1);
@@ -236,7 +315,7 @@ struct BackwardValues {
     // inner product of the second, mean(dz w_post' n2), is mean(e dh), and dh is
     // known up to the first one's mean c1 = mean(dx w_pre' n1):
     //   sum e dh = sum e (dh_out + rstd_pre dx w_pre') - rstd_pre c1 sum e n1.
-    __device__ __forceinline__ void add(const Weights<kKind == kRowNarrow> &w, float r1, float (&s)[3]) const {
+    __device__ __forceinline__ void add(const Weights<ColsOf<kKind>> &w, float r1, float (&s)[3]) const {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float q = dx[j] * w.pre[j], e = g[j] * w.post[j] * n2[j];
@@ -260,10 +339,11 @@ __global__ __launch_bounds__(1024) void residual_norm_means_kernel(NormParams p)
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
         const float r1 = p.in.rstd_pre[row], r2 = p.in.w_post ? p.in.rstd_post[row] : 1.0f;
         float s[3] = {0.0f, 0.0f, 0.0f};
-        for (int c0 = threadIdx.x * 8; c0 < p.dim; c0 += 8192) {
-            const Cols<false> c(c0, p.dim);
+        const int end = kKind == kRowFours ? (p.dim + 511) / 512 * 512 : p.dim;  // whole waves of fours
+        for (int c0 = threadIdx.x * 8; c0 < end; c0 += 8192) {
+            const ColsOf<kKind> c(c0, p.dim);
             BackwardRow<T, R, kKind, kToken> raw;
-            Weights<false> w;
+            Weights<ColsOf<kKind>> w;
             BackwardValues<T, R, kKind, kToken> x;
             raw.load(p, row * p.dim, c);
             w.load(p, p.in.y && p.gate_kind == NF4_GATE_CHANNEL, c);
@@ -285,18 +365,24 @@ __global__ __launch_bounds__(1024) void residual_norm_means_kernel(NormParams p)
 // vectors a lane spilled: 442 us for 2048 x 16384 bf16).
 // kMost: threads of the workgroup at most. Up to 512 (4096 columns) a lane may have
 // the 133 to 167 registers that it wants, on three waves a SIMD; with 128 on four
-// it spills (4096 x 4096 with an fp32 stream and token gates: 95 us instead of 69;
-// 14000 x 2304 bf16: 99 instead of 82).
+// it spills (4096 x 4096 with an fp32 stream and token gates: 74 us instead of 68;
+// 16384 x 2304 bf16: 117 instead of 99).
 template <typename T, typename R, RowKind kKind, bool kToken, bool kWide, bool kTiled, int kMost>
 __global__ __launch_bounds__(kMost) void residual_norm_backward_kernel(NormParams p) {
     __shared__ float part[2][3][16];
     extern __shared__ float s_cols[];
-    constexpr bool kNarrow = kKind == kRowNarrow;
+    // Above 512 threads a CU holds one workgroup, and a lane's weights are in LDS: with
+    // them in registers too it spilled (8192 x 8192 bf16 162 us instead of 148, 8192 x
+    // 5120 124 instead of 96). Tiles of bf16 blocks on an fp32 stream do not spill
+    // (5461 x 12288: 374 us with LDS, 355 without).
+    constexpr bool kKeep = kMost <= 512 || (kTiled && sizeof(T) == 2 && kKind == kRowFours);
+    __shared__ f32x4 s_w[kKeep ? 1 : 6][kKeep ? 1 : kMost];
+    typedef ColsOf<kKind> C;
     const int lanes = kWide ? blockDim.x : p.lanes;
     const int groups = kWide ? 1 : blockDim.x / lanes, group = kWide ? 0 : threadIdx.x / lanes;
     const int lane = kWide ? threadIdx.x : threadIdx.x % lanes;
     const bool post = p.in.w_post != nullptr;
-    const Cols<kNarrow> c((lane + (kTiled ? blockIdx.y * lanes : 0)) * 8, p.dim);
+    const C c((lane + (kTiled ? blockIdx.y * lanes : 0)) * 8, p.dim);
     float acc[3][8];
 #pragma unroll
     for (int k = 0; k < 3; ++k)
@@ -305,7 +391,7 @@ __global__ __launch_bounds__(kMost) void residual_norm_backward_kernel(NormParam
     auto row_at = [&](int64_t r0) { return r0 + group < p.rows ? r0 + group : p.rows - 1; };
     const int64_t first = (int64_t)blockIdx.x * groups, stride = (int64_t)gridDim.x * groups;
     BackwardRow<T, R, kKind, kToken> raw;
-    Weights<kNarrow> w;
+    Weights<C> w;
     float next_r1, next_r2 = 1.0f;
     float2 next_means = make_float2(0.0f, 0.0f);
     auto load = [&](int64_t row) {
@@ -316,18 +402,14 @@ __global__ __launch_bounds__(kMost) void residual_norm_backward_kernel(NormParam
     };
     load(row_at(first));
     w.load(p, p.in.y && p.gate_kind == NF4_GATE_CHANNEL, c);
+    if constexpr (!kKeep) w.save(s_w);
     int turn = 0;
     for (int64_t r0 = first; r0 < p.rows; r0 += stride, turn ^= 1) {
         const int64_t at = row_at(r0) * p.dim;
         const bool live_row = r0 + group < p.rows;
         const float r1 = next_r1, r2 = next_r2;
         float c1 = next_means.x, c2 = next_means.y;
-        if constexpr (sizeof(T) == 4 && kMost > 512) {
-            // no room for the weights beside fp32 rows in flight (kept, they spilled:
-            // 325 us for 4096 x 8192 with token gates instead of 307)
-            asm volatile("" ::: "memory");
-            w.load(p, p.in.y && p.gate_kind == NF4_GATE_CHANNEL, c);
-        }
+        if constexpr (!kKeep) w.template restore<kToken>(s_w);
         BackwardValues<T, R, kKind, kToken> x;
         x.unpack(p, raw, w, c, r1, r2);
         if (r0 + stride < p.rows) load(row_at(r0 + stride));
@@ -429,16 +511,18 @@ Split split_of(int64_t dim) {
     const int lanes = (int)((vecs + 64 * vec - 1) / (64 * vec)) * 64;
     return {lanes, vec, lanes, 2048};
 }
-// The backward pass needs many registers, so its workgroups have a power of two of
-// waves that the four SIMDs can share evenly: five waves of 2304 columns
-// (14000 rows) take 116 us, eight 96. vec: tiles of a row here.
+// The backward pass needs many registers, so its workgroups of up to 512 threads
+// have a power of two of waves that the four SIMDs can share evenly (8192 x 2304
+// bf16: 53 us with eight waves, 57 with five); above, a CU holds one workgroup and
+// idle waves only cost (8192 x 5120 with an fp32 stream: 268 us with sixteen, 230
+// with ten). vec: tiles of a row here.
 Split backward_split_of(int64_t dim) {
     Split sp = split_of(dim);
     if (sp.lanes > 64) {
         const int64_t vecs = (dim + 7) / 8;
         sp.vec = (int)((vecs + 1023) / 1024);
-        sp.lanes = 128;
-        while ((int64_t)sp.lanes * sp.vec < vecs) sp.lanes *= 2;
+        sp.lanes = (int)((vecs + 64 * sp.vec - 1) / (64 * sp.vec)) * 64;
+        if (sp.lanes < 512) sp.lanes = sp.lanes <= 128 ? 128 : sp.lanes <= 256 ? 256 : 512;
         sp.block = sp.lanes;
     }
     sp.resident = sp.block > 512 ? 1024 : 768;  // three waves a SIMD with up to 167 registers
@@ -473,23 +557,27 @@ NormParams params_of(const nf4_residual_norm_shape &sh, const ResidualNormIn &in
 
 template <typename T, typename R, RowKind kKind>
 hipError_t forward_kind(const NormParams &p, const Split &sp, hipStream_t s) {
-    constexpr bool kBig = kKind != kRowNarrow;  // a row of less than eight is one vector of a lane
-    auto kernel = sp.vec == 4   ? residual_norm_forward_kernel<T, R, kBig ? 4 : 1, kKind, kBig>
-                  : sp.vec == 2 ? residual_norm_forward_kernel<T, R, kBig ? 2 : 1, kKind, kBig>
-                  : sp.lanes > 64 ? residual_norm_forward_kernel<T, R, 1, kKind, kBig>
-                                  : residual_norm_forward_kernel<T, R, 1, kKind, false>;
+    // What a kind comes with: fewer than eight columns are part of a wave, fours one
+    // vector of a whole workgroup, fp32 vectors a part of a wave or several vectors.
+    constexpr bool kMany = kKind == kRowAny || kKind == kRowVecs, kPart = kKind != kRowFours;
+    constexpr bool kWhole = kKind == kRowFours || kKind == kRowAny || (kKind == kRowVecs && sizeof(R) == 2);
+    auto kernel = sp.vec == 4   ? residual_norm_forward_kernel<T, R, kMany ? 4 : 1, kKind, !kPart || kMany>
+                  : sp.vec == 2 ? residual_norm_forward_kernel<T, R, kMany ? 2 : 1, kKind, !kPart || kMany>
+                  : sp.lanes > 64 ? residual_norm_forward_kernel<T, R, 1, kKind, kWhole>
+                                  : residual_norm_forward_kernel<T, R, 1, kKind, !kPart>;
     kernel<<<dim3((uint32_t)workgroups(p.rows, sp)), dim3(sp.block), 0, s>>>(p);
     return hipGetLastError();
 }
 template <typename T, typename R, RowKind kKind, bool kToken>
 hipError_t backward_kind(const NormParams &p, const Split &sp, hipStream_t s) {
-    constexpr bool kBig = kKind != kRowNarrow;
-    constexpr int kMost = kBig ? 1024 : 512;
-    auto kernel = sp.vec > 1       ? residual_norm_backward_kernel<T, R, kKind, kToken, kBig, kBig, kMost>
-                  : sp.lanes > 512 ? residual_norm_backward_kernel<T, R, kKind, kToken, kBig, false, kMost>
-                  : sp.lanes > 64  ? residual_norm_backward_kernel<T, R, kKind, kToken, kBig, false, 512>
-                                   : residual_norm_backward_kernel<T, R, kKind, kToken, false, false, 512>;
-    if constexpr (kBig)
+    constexpr bool kPart = kKind != kRowFours;
+    constexpr bool kWhole = kKind == kRowFours || kKind == kRowAny || (kKind == kRowVecs && sizeof(R) == 2);
+    constexpr int kMost = kWhole ? 1024 : 512;
+    auto kernel = sp.vec > 1       ? residual_norm_backward_kernel<T, R, kKind, kToken, kWhole, kWhole, kMost>
+                  : sp.lanes > 512 ? residual_norm_backward_kernel<T, R, kKind, kToken, kWhole, false, kMost>
+                  : sp.lanes > 64  ? residual_norm_backward_kernel<T, R, kKind, kToken, kWhole, false, 512>
+                                   : residual_norm_backward_kernel<T, R, kKind, kToken, !kPart, false, 512>;
+    if constexpr (kWhole)
         if (sp.vec > 1) {
             const int64_t wgs = p.rows < 512 ? p.rows : 512;
             residual_norm_means_kernel<T, R, kKind, kToken><<<dim3((uint32_t)wgs), dim3(1024), 0, s>>>(p);
@@ -502,12 +590,19 @@ hipError_t backward_kind(const NormParams &p, const Split &sp, hipStream_t s) {
 template <typename T, typename R>
 hipError_t forward_typed(const NormParams &p, const Split &sp, hipStream_t s) {
     if (p.dim < 8) return forward_kind<T, R, kRowNarrow>(p, sp, s);
-    return p.dim % 8 ? forward_kind<T, R, kRowAny>(p, sp, s) : forward_kind<T, R, kRowVecs>(p, sp, s);
+    if (p.dim % 8) return forward_kind<T, R, kRowAny>(p, sp, s);
+    // not with several vectors of a lane, which spill (1024 x 12288: 45 us instead of 36)
+    if constexpr (sizeof(R) == 4)
+        if (sp.lanes > 64 && sp.vec == 1) return forward_kind<T, R, kRowFours>(p, sp, s);
+    return forward_kind<T, R, kRowVecs>(p, sp, s);
 }
 template <typename T, typename R, bool kToken>
 hipError_t backward_gate(const NormParams &p, const Split &sp, hipStream_t s) {
     if (p.dim < 8) return backward_kind<T, R, kRowNarrow, kToken>(p, sp, s);
-    return p.dim % 8 ? backward_kind<T, R, kRowAny, kToken>(p, sp, s) : backward_kind<T, R, kRowVecs, kToken>(p, sp, s);
+    if (p.dim % 8) return backward_kind<T, R, kRowAny, kToken>(p, sp, s);
+    if constexpr (sizeof(R) == 4)
+        if (sp.lanes > 64) return backward_kind<T, R, kRowFours, kToken>(p, sp, s);
+    return backward_kind<T, R, kRowVecs, kToken>(p, sp, s);
 }
 template <typename T, typename R>
 hipError_t backward_typed(const NormParams &p, const Split &sp, hipStream_t s) {
