@@ -6,6 +6,8 @@
 // sorts the tokens by their id (stable, so that a row's gradient is summed in
 // the order of the tokens), sums runs of equal ids chunk by chunk and joins the
 // runs that cross chunks; a dense gradient is cleared beside the sort. It is bound by reading dy and writing the table's gradient.
+#include <type_traits>
+
 #include "linear_common.h"
 #include "training_internal.h"
 
@@ -25,22 +27,22 @@ __device__ __forceinline__ uint32_t token_key(const void *ids, bool i64, int64_t
 // A group of `lanes` lanes moves one row, kInFlight vectors of a lane at a time.
 // The rows go out past the caches (16384 x 8192 bf16: 70 us instead of 80); the
 // table's stay in them, as text asks for a few rows often (98 us without).
-template <typename T, typename O, int kInFlight, bool kNarrow>
+template <typename T, typename O, int kInFlight, typename C>
 __global__ __launch_bounds__(kThreads) void lookup_kernel(const void *ids, bool i64, int64_t tokens, const T *table,
                                                           int64_t vocab, int32_t dim, float scale, O *out, int lanes) {
-    const int each = kThreads / lanes;
+    const int each = kThreads / lanes, end = std::is_same_v<C, Fours> ? (dim + 511) / 512 * 512 : dim;
     for (int64_t t = (int64_t)blockIdx.x * each + threadIdx.x / lanes; t < tokens; t += (int64_t)gridDim.x * each) {
         const uint32_t row = token_key(ids, i64, t, vocab, -1);
         const T *src = table + (int64_t)row * dim;
         O *dst = out + t * dim;
-        for (int c0 = (threadIdx.x & (lanes - 1)) * 8; c0 < dim; c0 += lanes * 8 * kInFlight) {
+        for (int c0 = (threadIdx.x & (lanes - 1)) * 8; c0 < end; c0 += lanes * 8 * kInFlight) {
             Raw8<T> raw[kInFlight];
 #pragma unroll
             for (int u = 0; u < kInFlight; ++u)
-                if (row < vocab) raw[u] = load_cols(src, Cols<kNarrow>(c0 + u * lanes * 8, dim));
+                if (row < vocab) raw[u] = load_cols(src, C(c0 + u * lanes * 8, dim));
 #pragma unroll
             for (int u = 0; u < kInFlight; ++u) {
-                const Cols<kNarrow> c(c0 + u * lanes * 8, dim);
+                const C c(c0 + u * lanes * 8, dim);
                 float x[8];
                 cols_values(raw[u], c, x);
 #pragma unroll
@@ -361,13 +363,13 @@ __device__ __forceinline__ G *grad_row(const GradParams &p, uint32_t key) {
 // caches: beside a gradient that the sort's launch has just cleared, 16384 x 4096
 // bf16 into 32000 rows take 86 us in all instead of 109. With lines that two
 // waves share it costs instead (5003 x 1601: 38 us for 36).
-template <typename T, typename G, bool kNarrow, bool kStream, bool kAdd>
+template <typename T, typename G, typename C, bool kStream, bool kAdd>
 __global__ __launch_bounds__(kThreads) void run_sum_kernel(GradParams p) {
     const int lane = threadIdx.x % 64;
     const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
     const int64_t c = unit / p.slices;
     if (c >= p.chunks) return;
-    const Cols<kNarrow> cols((int)(unit % p.slices) * kCols + lane * 8, p.dim);
+    const C cols((int)(unit % p.slices) * kCols + lane * 8, p.dim);
     const int64_t start = c * p.chunk;
     const int len = (int)(p.tokens - start < p.chunk ? p.tokens - start : p.chunk);
     // lane j holds place start - 1 + j
@@ -388,7 +390,7 @@ __global__ __launch_bounds__(kThreads) void run_sum_kernel(GradParams p) {
             const uint32_t at = (uint32_t)__builtin_amdgcn_readlane((int)vidx, i0 + u + 1);
             const uint32_t idx = key < p.vocab ? at : 0u;
             const T *row = static_cast<const T *>(p.dy) + (int64_t)idx * p.dim;
-            if constexpr (kStream) raw[u] = load_stream(row + cols.base);
+            if constexpr (kStream) raw[u] = load_stream(row, cols);
             else raw[u] = load_cols(row, cols);
             // the row that a run ending here is added to; no other wave writes it
             const uint32_t after = (uint32_t)__builtin_amdgcn_readlane((int)vkey, i0 + u + 2);
@@ -447,11 +449,18 @@ __global__ __launch_bounds__(kThreads) void run_join_kernel(GradParams p) {
     if (c + 1 >= p.chunks) return;
     const Cols<kNarrow> cols((int)(unit % p.slices) * kCols + lane * 8, p.dim);
     const int64_t start = c * p.chunk, end = start + p.chunk;
-    const uint32_t key = p.key[end - 1];
-    if (p.key[end] != key || key >= p.vocab) return;
-    if (p.key[start] == key && start > 0 && p.key[start - 1] == key) return;  // begins before
-    const int64_t stop = end + lower_bound(p.key + end, p.tokens - end, key + 1);
-    const int64_t last = (stop - 1) / p.chunk;
+    // One round of loads tells most of it: the chunks that the run enters are those
+    // after this one that begin with its key.
+    const int64_t ahead = end + lane * p.chunk;
+    const uint32_t next = p.key[ahead < p.tokens ? ahead : p.tokens - 1];
+    const uint32_t key = p.key[end - 1], begins = p.key[start], before = start > 0 ? p.key[start - 1] : 0xFFFFFFFFu;
+    const uint64_t same = __ballot(ahead < p.tokens && next == key);
+    if (!(same & 1) || key >= p.vocab) return;
+    if (begins == key && before == key) return;  // begins before
+    const int entered = (int)__popcll(same);
+    const int64_t last = entered < 64 ? c + entered : (end + lower_bound(p.key + end, p.tokens - end, key + 1) - 1) / p.chunk;
+    Raw8<G> old;
+    if (p.accumulate) old = load_cols(grad_row<G>(p, key), cols);
     float acc[8];
     cols_values(load_cols(p.partial + (c * 2 + 1) * p.dim, cols), cols, acc);
     for (int64_t d = c + 1; d <= last; d += kRows) {
@@ -469,7 +478,7 @@ __global__ __launch_bounds__(kThreads) void run_join_kernel(GradParams p) {
         }
     }
     float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (p.accumulate) cols_values(load_cols(grad_row<G>(p, key), cols), cols, x);
+    if (p.accumulate) cols_values(old, cols, x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] += acc[j] * p.scale;
     store_cols(grad_row<G>(p, key), cols, x);
@@ -582,9 +591,14 @@ hipError_t gradient(const Sort &q, const GradParams &p, hipStream_t s) {
     const uint32_t wgs = (uint32_t)((p.chunks * p.slices + 3) / 4);
     const bool narrow = p.dim < 8, lines = p.dim * sizeof(T) % 128 == 0;
     const bool add = p.accumulate;
-    auto sum = narrow ? (add ? run_sum_kernel<T, G, true, false, true> : run_sum_kernel<T, G, true, false, false>)
-               : lines ? (add ? run_sum_kernel<T, G, false, true, true> : run_sum_kernel<T, G, false, true, false>)
-                       : (add ? run_sum_kernel<T, G, false, false, true> : run_sum_kernel<T, G, false, false, false>);
+    typedef std::conditional_t<sizeof(T) == 2 && sizeof(G) == 2, Cols<false>, Fours> Lines;
+    auto pick = [&](auto c, auto stream) {
+        typedef typename decltype(c)::type C;
+        return add ? run_sum_kernel<T, G, C, stream.value, true> : run_sum_kernel<T, G, C, stream.value, false>;
+    };
+    auto sum = narrow  ? pick(ColsTag<Cols<true>>{}, std::false_type{})
+               : lines ? pick(ColsTag<Lines>{}, std::true_type{})
+                       : pick(ColsTag<Cols<false>>{}, std::false_type{});
     sum<<<dim3(wgs), dim3(kThreads), 0, s>>>(p);
     if (p.chunks > 1) {
         auto join = narrow ? run_join_kernel<G, true> : run_join_kernel<G, false>;
@@ -600,10 +614,13 @@ hipError_t lookup(const void *ids, bool i64, int64_t tokens, const void *table, 
     // as many vectors in flight as a lane has, up to four: with more, a lane
     // works on columns past the row (16384 x 1000 bf16: 19 us instead of 12)
     const int64_t vecs = (dim + lanes * 8 - 1) / (lanes * 8);
-    auto kernel = dim < 8     ? lookup_kernel<T, O, 1, true>
-                  : vecs == 1 ? lookup_kernel<T, O, 1, false>
-                  : vecs == 2 ? lookup_kernel<T, O, 2, false>
-                              : lookup_kernel<T, O, 4, false>;
+    auto pick = [&](auto c) {
+        typedef typename decltype(c)::type C;
+        return vecs == 1 ? lookup_kernel<T, O, 1, C> : vecs == 2 ? lookup_kernel<T, O, 2, C> : lookup_kernel<T, O, 4, C>;
+    };
+    auto kernel = dim < 8 ? lookup_kernel<T, O, 1, Cols<true>> : pick(ColsTag<Cols<false>>{});
+    if constexpr (sizeof(O) == 4)  // 16384 x 2048 bf16 to fp32: 30 us instead of 44
+        if (dim % 8 == 0 && lanes >= 64) kernel = pick(ColsTag<Fours>{});
     kernel<<<lookup_grid(tokens, lanes), dim3(kThreads), 0, s>>>(
         ids, i64, tokens, static_cast<const T *>(table), vocab, (int32_t)dim, scale, static_cast<O *>(out), lanes);
     return hipGetLastError();

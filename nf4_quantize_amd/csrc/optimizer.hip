@@ -126,7 +126,6 @@ __device__ __forceinline__ float storage_scale(float amax, float *inv) {
 
 // A lane's four elements, as eight are loaded and stored by load_raw, load_stream
 // and store_stream.
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 template <typename T> struct Raw4;
 template <> struct Raw4<Bf16> { u32x2 v; };
 template <> struct Raw4<float> { f32x4 v; };

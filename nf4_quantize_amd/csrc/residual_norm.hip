@@ -40,59 +40,12 @@ struct NormParams {
 // backward, bf16 blocks on an fp32 stream 137 (as before) and 217 instead of 259.
 enum RowKind { kRowNarrow, kRowAny, kRowVecs, kRowFours };
 
-// A lane's columns with kRowFours: four, and four 256 further on, so that a wave's
-// load of fp32 covers whole cache lines. `c` counts eights as the other kinds do; a
-// wave's 64 cover the same 512 columns, so a row's last wave is whole.
-struct Fours {
-    int lo, hi, from_lo, from_hi;
-    bool live_lo, live_hi;
-    __device__ __forceinline__ Fours(int c, int dim)
-        : lo((c & ~511) + (c & 511) / 2), hi(lo + 256), from_lo(lo < dim ? lo : dim - 4),
-          from_hi(hi < dim ? hi : dim - 4), live_lo(lo < dim), live_hi(hi < dim) {}
-};
 template <RowKind kKind>
 using ColsOf = std::conditional_t<kKind == kRowFours, Fours, Cols<kKind == kRowNarrow>>;
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ Raw8<float> load_cols(const float *row, const Fours &c) {
-    return {*reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_lo), *reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_hi)};
-}
-__device__ __forceinline__ Raw8<Bf16> load_cols(const Bf16 *row, const Fours &c) {
-    const u32x2 a = *reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_lo), b = *reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_hi);
-    return {u32x4{a[0], a[1], b[0], b[1]}};
-}
-__device__ __forceinline__ Raw8<float> stream_fours(const float *row, const Fours &c) {
-    return {__builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_lo)),
-            __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_hi))};
-}
-__device__ __forceinline__ Raw8<Bf16> stream_fours(const Bf16 *row, const Fours &c) {
-    const u32x2 a = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_lo));
-    const u32x2 b = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_hi));
-    return {u32x4{a[0], a[1], b[0], b[1]}};
-}
-template <typename T>
-__device__ __forceinline__ void cols_values(const Raw8<T> &r, const Fours &c, float (&x)[8]) {
-    values(r, x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = (j < 4 ? c.live_lo : c.live_hi) ? x[j] : 0.0f;
-}
-__device__ __forceinline__ void store_cols(float *row, const Fours &c, const float (&x)[8]) {
-    if (c.live_lo) *reinterpret_cast<f32x4 *>(row + c.lo) = f32x4{x[0], x[1], x[2], x[3]};
-    if (c.live_hi) *reinterpret_cast<f32x4 *>(row + c.hi) = f32x4{x[4], x[5], x[6], x[7]};
-}
-__device__ __forceinline__ void store_fours(float *row, const Fours &c, const float (&x)[8]) {
-    if (c.live_lo) __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4 *>(row + c.lo));
-    if (c.live_hi) __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4 *>(row + c.hi));
-}
-__device__ __forceinline__ void store_fours(Bf16 *row, const Fours &c, const float (&x)[8]) {
-    const u32x2 a = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, b = {pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
-    if (c.live_lo) __builtin_nontemporal_store(a, reinterpret_cast<u32x2 *>(row + c.lo));
-    if (c.live_hi) __builtin_nontemporal_store(b, reinterpret_cast<u32x2 *>(row + c.hi));
-}
-
 template <RowKind kKind, typename T>
 __device__ __forceinline__ Raw8<T> load_row(const T *row, const ColsOf<kKind> &c) {
-    if constexpr (kKind == kRowFours) return stream_fours(row, c);
+    if constexpr (kKind == kRowFours) return load_stream(row, c);
     else if constexpr (kKind == kRowVecs) return load_stream(row + (uint32_t)c.base);
     else return load_cols(row, c);
 }
@@ -108,9 +61,7 @@ __device__ __forceinline__ void row_values(const Raw8<T> &r, const ColsOf<kKind>
 }
 template <RowKind kKind, typename T>
 __device__ __forceinline__ void store_row(T *row, const ColsOf<kKind> &c, const float (&x)[8]) {
-    if constexpr (kKind == kRowFours) {
-        store_fours(row, c, x);
-    } else if constexpr (kKind == kRowVecs) {
+    if constexpr (kKind == kRowVecs) {
         if (c.live > 0) store_stream(row + (uint32_t)c.col, x);
     } else {
         stream_cols(row, c, x);

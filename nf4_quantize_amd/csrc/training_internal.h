@@ -52,6 +52,7 @@ hipError_t launch_embedding_backward(const void *ids, bool i64, int64_t tokens, 
 // Eight consecutive elements of a row that may start at any element: bf16 rows
 // of odd width put 16-byte groups at 2-byte boundaries, which the global
 // memory path of gfx950 takes in one instruction.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 struct __attribute__((packed, aligned(2))) u32x4_any2 { u32x4 v; };
 struct __attribute__((packed, aligned(4))) f32x4_any4 { f32x4 v; };
 
@@ -201,11 +202,71 @@ __device__ __forceinline__ void store_cols(T *row, const Cols<kNarrow> &c, const
     if (c.live > 0) store_upto8(row + (uint32_t)c.col, c.live, x);
 }
 
-// store_cols past the caches' usual order.
+// load_cols and store_cols past the caches' usual order; the load is for rows of
+// whole vectors.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_stream(const T *row, const Cols<false> &c) {
+    return load_stream(row + (uint32_t)c.base);
+}
 template <typename T, bool kNarrow>
 __device__ __forceinline__ void stream_cols(T *row, const Cols<kNarrow> &c, const float (&x)[8]) {
     if (c.live >= 8) return store_stream(row + (uint32_t)c.col, x);
     if (c.live > 0) store_upto8(row + (uint32_t)c.col, c.live, x);
+}
+
+// Another eight columns of a lane, for rows of whole vectors with fp32 among them:
+// four, and four 256 further on, so that a wave's load covers whole cache lines.
+// `c` counts as in Cols; a wave's 64 lanes cover the same 512 columns, so a row's
+// last wave is whole.
+template <typename C> struct ColsTag {
+    typedef C type;
+};
+struct Fours {
+    int lo, hi, from_lo, from_hi;
+    bool live_lo, live_hi;
+    __device__ __forceinline__ Fours(int c, int dim)
+        : lo((c & ~511) + (c & 511) / 2), hi(lo + 256), from_lo(lo < dim ? lo : dim - 4),
+          from_hi(hi < dim ? hi : dim - 4), live_lo(lo < dim), live_hi(hi < dim) {}
+};
+__device__ __forceinline__ Raw8<float> load_cols(const float *row, const Fours &c) {
+    return {*reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_lo), *reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_hi)};
+}
+__device__ __forceinline__ Raw8<Bf16> load_cols(const Bf16 *row, const Fours &c) {
+    const u32x2 a = *reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_lo), b = *reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_hi);
+    return {u32x4{a[0], a[1], b[0], b[1]}};
+}
+__device__ __forceinline__ Raw8<float> load_stream(const float *row, const Fours &c) {
+    return {__builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_lo)),
+            __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_hi))};
+}
+__device__ __forceinline__ Raw8<Bf16> load_stream(const Bf16 *row, const Fours &c) {
+    const u32x2 a = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_lo));
+    const u32x2 b = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_hi));
+    return {u32x4{a[0], a[1], b[0], b[1]}};
+}
+template <typename T>
+__device__ __forceinline__ void cols_values(const Raw8<T> &r, const Fours &c, float (&x)[8]) {
+    values(r, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = (j < 4 ? c.live_lo : c.live_hi) ? x[j] : 0.0f;
+}
+__device__ __forceinline__ void store_cols(float *row, const Fours &c, const float (&x)[8]) {
+    if (c.live_lo) *reinterpret_cast<f32x4 *>(row + c.lo) = f32x4{x[0], x[1], x[2], x[3]};
+    if (c.live_hi) *reinterpret_cast<f32x4 *>(row + c.hi) = f32x4{x[4], x[5], x[6], x[7]};
+}
+__device__ __forceinline__ void store_cols(Bf16 *row, const Fours &c, const float (&x)[8]) {
+    const u32x2 a = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, b = {pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+    if (c.live_lo) *reinterpret_cast<u32x2 *>(row + c.lo) = a;
+    if (c.live_hi) *reinterpret_cast<u32x2 *>(row + c.hi) = b;
+}
+__device__ __forceinline__ void stream_cols(float *row, const Fours &c, const float (&x)[8]) {
+    if (c.live_lo) __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4 *>(row + c.lo));
+    if (c.live_hi) __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4 *>(row + c.hi));
+}
+__device__ __forceinline__ void stream_cols(Bf16 *row, const Fours &c, const float (&x)[8]) {
+    const u32x2 a = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, b = {pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+    if (c.live_lo) __builtin_nontemporal_store(a, reinterpret_cast<u32x2 *>(row + c.lo));
+    if (c.live_hi) __builtin_nontemporal_store(b, reinterpret_cast<u32x2 *>(row + c.hi));
 }
 
 // Sum and maximum over aligned groups of `lanes` lanes of a wave (a power of
