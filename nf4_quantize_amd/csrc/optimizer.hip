@@ -61,13 +61,15 @@ struct AdamwScalars {
 };
 static_assert(sizeof(AdamwBatch) + sizeof(AdamwScalars) <= 4096, "kernel arguments");
 
-// Copies a batch of entries from the kernel arguments into the table.
+// Copies a batch of entries from the kernel arguments into the table: 16 bytes a
+// thread, as the arguments lie in host memory.
 __global__ __launch_bounds__(kThreads) void adamw_table_kernel(AdamwBatch b, int32_t count, AdamwItem *table,
                                                                uint32_t *firsts) {
-    for (int i = threadIdx.x; i < count; i += kThreads) {
-        table[i] = b.item[i];
-        firsts[i] = b.item[i].first;
-    }
+    constexpr int kParts = sizeof(AdamwItem) / 16;
+    static_assert(kBatch * kParts <= kThreads, "one pass");
+    const int i = threadIdx.x;
+    if (i < count * kParts) reinterpret_cast<u32x4 *>(table)[i] = reinterpret_cast<const u32x4 *>(b.item)[i];
+    if (i < count) firsts[i] = b.item[i].first;
 }
 
 // The entry of workgroup wg: the last one whose first workgroup is not above it.

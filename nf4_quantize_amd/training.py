@@ -4,6 +4,7 @@ and the token embedding (``nf4_embedding``). Formulas, storage and limits are
 in ``include/nf4.h``; every step of the computation runs in the library's HIP
 kernels, torch supplies device memory and the current stream.
 """
+import array
 import ctypes
 
 import numpy as np
@@ -144,21 +145,16 @@ class NF4AdamW:
             raise ValueError("no parameters")
         self.dtype, self.device = self.params[0].dtype, self.params[0].device
         _nq._dtype_code(self.dtype)
-        for p, mw in zip(self.params, self.masters):
-            if p.dtype != self.dtype:
-                raise TypeError(f"parameters of one dtype, got {self.dtype} and {p.dtype}")
-            _check_tensors(self.params[0], p, mw)
-            if mw is not None and (mw.dtype != torch.float32 or self.dtype != torch.bfloat16 or mw.numel() != p.numel()):
-                raise TypeError("a master weight is float32, of a bfloat16 parameter of its size")
-        self.betas, self.eps, self.state_bits = (float(betas[0]), float(betas[1])), float(eps), state_bits
-        self.max_grad_norm, self.seed, self.steps = float(max_grad_norm), int(seed), 0
-        self.grad_norm = torch.zeros(1, dtype=torch.float32, device=self.device)
+        self._tensor = torch.Tensor
         self._entries = np.zeros(len(self.params), _ENTRY)
         self._at = self._entries.ctypes.data
         self._numels = [p.numel() for p in self.params]
+        self._weights = self.params + [mw for mw in self.masters if mw is not None]
+        self._bind()
+        self.betas, self.eps, self.state_bits = (float(betas[0]), float(betas[1])), float(eps), state_bits
+        self.max_grad_norm, self.seed, self.steps = float(max_grad_norm), int(seed), 0
+        self.grad_norm = torch.zeros(1, dtype=torch.float32, device=self.device)
         e = self._entries
-        e["w"] = [p.data_ptr() for p in self.params]
-        e["master"] = [0 if mw is None else mw.data_ptr() for mw in self.masters]
         e["n"] = self._numels
         L = _nq.lib()
         size = max(_size(L.nf4_grad_norm_workspace_size(e.ctypes.data, len(e)), "nf4_grad_norm_workspace_size"),
@@ -214,6 +210,24 @@ class NF4AdamW:
             elif p.grad is not None:
                 p.grad.zero_()
 
+    def _bind(self):
+        """Takes the weights' addresses, once they are what the step can update."""
+        import torch
+
+        for p, n, mw in zip(self.params, self._numels, self.masters):
+            if p.dtype != self.dtype:
+                raise TypeError(f"parameters of one dtype, got {self.dtype} and {p.dtype}")
+            _check_tensors(self.params[0], p, mw)
+            if p.numel() != n or p.device != self.device:
+                raise ValueError("a parameter's size or device has changed")
+            if mw is not None and (mw.dtype != torch.float32 or self.dtype != torch.bfloat16 or mw.numel() != n):
+                raise TypeError("a master weight is float32, of a bfloat16 parameter of its size")
+        self._entries["w"] = [p.data_ptr() for p in self.params]
+        self._entries["master"] = [0 if mw is None else mw.data_ptr() for mw in self.masters]
+        # held, so that no other memory can have their addresses
+        self._held = [t.detach() for t in self._weights]
+        self._bound = [t.data_ptr() for t in self._held]
+
     def step(self, grads=None, step=None, seed=None):
         """One step with the parameters' ``.grad``, or with ``grads`` (a tensor for
         each parameter, all bfloat16 or all float32). ``step`` and ``seed``
@@ -222,22 +236,27 @@ class NF4AdamW:
         grads = [p.grad for p in self.params] if grads is None else grads
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
-        if any(g is None for g in grads):
-            raise ValueError("a parameter has no gradient")
-        dt, index = grads[0].dtype, self.params[0].get_device()
-        if ({g.dtype for g in grads} != {dt} or {g.get_device() for g in grads} != {index}
-                or [g.numel() for g in grads] != self._numels or not all([g.is_contiguous() for g in grads])):
+        T = self._tensor  # the methods over the list: a third less time than a loop, for hundreds of tensors
+        try:
+            devices, sizes = set(map(T.get_device, grads)), list(map(T.numel, grads))
+        except TypeError:
+            raise ValueError("a parameter has no gradient") from None
+        dt = grads[0].dtype
+        if (devices != {self.params[0].get_device()} or sizes != self._numels or not all(map(T.is_contiguous, grads))
+                or {g.dtype for g in grads} != {dt}):
             raise ValueError(f"gradients: contiguous, of the parameters' sizes, one dtype, on {self.device}; got "
                              + ", ".join(f"{tuple(g.shape)} {g.dtype} {g.device}" for g in grads[:4]) + " ...")
+        if list(map(T.data_ptr, self._weights)) != self._bound:  # a parameter has new memory
+            self._bind()
         grad_dtype = _code(dt)
         e, count = self._entries, len(grads)
-        e["grad"] = [g.data_ptr() for g in grads]
+        e["grad"] = array.array("Q", map(T.data_ptr, grads))
         for g in self.groups:
             part = slice(g["first"], g["first"] + g["count"])
             e["lr"][part], e["weight_decay"][part] = g["lr"], g["weight_decay"]
         at = self._at
         number = self.steps + 1 if step is None else int(step)
-        stream = _stream(index)
+        stream = _stream(devices.pop())
         clip = self.max_grad_norm > 0
         norm = self.grad_norm.data_ptr() if clip else None
         ws, ws_bytes = self._workspace.data_ptr(), self._workspace.numel()

@@ -359,3 +359,28 @@ def test_refuses_gradients_that_do_not_fit(dev):
         opt.step([good, torch.zeros(257, device=dev)[1:].view(16, 16)])  # not 16-byte aligned
     with pytest.raises(ValueError):
         opt.step()  # no .grad
+
+
+def test_parameters_with_new_memory(dev):
+    """A parameter whose data has been replaced is updated where it now lies; one
+    of another type or size is refused."""
+    import torch
+
+    p = torch.nn.Parameter(torch.ones(700, device=dev))
+    opt = nq.NF4AdamW([p], lr=0.5, weight_decay=0.0, state_bits=32)
+    old = p.data
+    p.data = torch.full((700,), 2.0, device=dev)
+    opt.step([torch.ones(700, device=dev)])
+    assert torch.equal(old, torch.ones_like(old))
+    # first step with g = 1: m / (1 - beta1) = 1 and sqrt(v / (1 - beta2)) = 1, each
+    # within a few roundings, so the weight moves by lr
+    assert float((p.data - 1.5).abs().max()) < 1e-5
+    kept = p.data.clone()
+    p.data = kept.bfloat16()
+    with pytest.raises(TypeError):
+        opt.step([torch.ones(700, device=dev)])
+    p.data = kept[:600].clone()
+    with pytest.raises(ValueError):
+        opt.step([torch.ones(600, device=dev)])
+    with pytest.raises(ValueError):
+        opt.step([torch.ones(700, device=dev)])
