@@ -475,7 +475,7 @@ hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_ada
         note();
         wgs = 0;
     };
-    constexpr int64_t kMaxWgs = (int64_t(1) << 31) / kThreads;
+    constexpr int64_t kMaxWgs = (int64_t(1) << 31) / (kPass / kStepEach<W, kMaster, kEight>);  // threads of a grid
     for (int32_t i = 0; i < count; ++i) {
         if (!mine(i)) continue;
         const int64_t need = (e[i].n + kPass - 1) / kPass;
