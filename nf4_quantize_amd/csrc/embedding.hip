@@ -163,6 +163,19 @@ __device__ __forceinline__ int count_below(const uint4 *s_key, uint32_t key) {
     }
     return count;
 }
+// Those of a group that holds the key's own place: equal ones count up to there.
+__device__ __forceinline__ int count_before(const uint4 *s_key, uint32_t key, int place) {
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 k = s_key[j];
+        count += k.x < key || (k.x == key && 4 * j < place);
+        count += k.y < key || (k.y == key && 4 * j + 1 < place);
+        count += k.z < key || (k.z == key && 4 * j + 2 < place);
+        count += k.w < key || (k.w == key && 4 * j + 3 < place);
+    }
+    return count;
+}
 
 // The place of each token in its tile's stable order, by counting the tokens
 // before it: those with a smaller key, and earlier ones with its own. A
@@ -203,16 +216,15 @@ __global__ __launch_bounds__(1024) void rank_tokens_kernel(RankParams p) {
     for (int t = share; t < padded / 16; t += shares) {
         if (t < first) count += count_below<true>(s_key4 + t * 4, key);
         else if (t >= last) count += count_below<false>(s_key4 + t * 4, key);
-        else
-#pragma unroll 1
-            for (int j = t * 16; j < t * 16 + 16; ++j) count += s_key[j] < key || (s_key[j] == key && j < me);
+        else count += count_before(s_key4 + t * 4, key, me - t * 16);
     }
+    for (int o = p.each; o < 64; o <<= 1) count += __shfl_xor(count, o);  // a token's lanes
     s_count[wave][lane] = count;
     __syncthreads();
     if ((int)threadIdx.x < p.each && me < tokens) {
         int r = tile0;
-        for (int w = 0; w < 16; ++w)
-            for (int q = 0; q < parts; ++q) r += s_count[w][q * p.each + lane];
+#pragma unroll
+        for (int w = 0; w < 16; ++w) r += s_count[w][lane];
         p.key_out[r] = key;
         p.idx_out[r] = (uint32_t)(tile0 + me);
     }
