@@ -505,6 +505,15 @@ nf4_status nf4_adamw_step(const nf4_adamw_entry *entries, int32_t count, int32_t
                           const float *grad_norm, void *workspace, size_t workspace_bytes,
                           void *stream);
 
+/* nf4_grad_norm, then nf4_adamw_step with that norm; a list of few elements takes
+ * one launch for both.
+ *   grad_norm  device out, one float
+ *   workspace  as of both, the larger size */
+nf4_status nf4_adamw_clip_step(const nf4_adamw_entry *entries, int32_t count, int32_t w_dtype,
+                               int32_t grad_dtype, int32_t moments, const nf4_adamw_config *config,
+                               float *grad_norm, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
 /* The residual step between two blocks, one row of `dim` at a time:
  *   z  = w_post' y rsqrt(mean y^2 + eps)     (z = y where w_post is NULL)
  *   h' = h + alpha gate z                    (gate 1 where gate_kind is NONE)

@@ -63,6 +63,7 @@ EXPORTS = (
     "nf4_grad_norm",
     "nf4_adamw_workspace_size",
     "nf4_adamw_step",
+    "nf4_adamw_clip_step",
     "nf4_residual_norm_forward",
     "nf4_residual_norm_backward_workspace_size",
     "nf4_residual_norm_backward",

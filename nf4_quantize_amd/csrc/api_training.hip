@@ -66,9 +66,11 @@ NF4_API nf4_status nf4_grad_norm(const nf4_adamw_entry *entries, int32_t count, 
 
 NF4_API size_t nf4_adamw_workspace_size(int32_t count) { return count < 0 ? (size_t)-1 : adamw_workspace(count); }
 
-NF4_API nf4_status nf4_adamw_step(const nf4_adamw_entry *entries, int32_t count, int32_t w_dtype, int32_t grad_dtype,
-                                  int32_t moments, const nf4_adamw_config *config, const float *grad_norm,
-                                  void *workspace, size_t workspace_bytes, void *stream) {
+namespace {
+
+nf4_status adamw(const nf4_adamw_entry *entries, int32_t count, int32_t w_dtype, int32_t grad_dtype, int32_t moments,
+                 const nf4_adamw_config *config, float *norm, bool own_norm, void *workspace, size_t workspace_bytes,
+                 void *stream) {
     nf4_status st = check_grads(entries, count);
     if (st != NF4_OK) return st;
     if (!config) return NF4_ERR_NULL;
@@ -78,8 +80,8 @@ NF4_API nf4_status nf4_adamw_step(const nf4_adamw_entry *entries, int32_t count,
     if (!(c.beta1 >= 0.0 && c.beta1 < 1.0) || !(c.beta2 >= 0.0 && c.beta2 < 1.0) || !(c.eps >= 0.0f) ||
         c.step < 1 || isnan(c.max_norm))
         return NF4_ERR_SIZE;
-    if (c.max_norm > 0.0f && !grad_norm) return NF4_ERR_NULL;
-    if (grad_norm && !aligned(grad_norm, 4)) return NF4_ERR_ALIGN;
+    if ((c.max_norm > 0.0f || own_norm) && !norm) return NF4_ERR_NULL;
+    if (norm && !aligned(norm, 4)) return NF4_ERR_ALIGN;
     const bool eight = moments == NF4_MOMENTS_8;
     for (int32_t i = 0; i < count; ++i) {
         const nf4_adamw_entry &e = entries[i];
@@ -91,10 +93,28 @@ NF4_API nf4_status nf4_adamw_step(const nf4_adamw_entry *entries, int32_t count,
             return NF4_ERR_ALIGN;
         if (eight && (!aligned(e.m_scale, 4) || !aligned(e.v_scale, 4))) return NF4_ERR_ALIGN;
     }
-    if ((st = check_workspace(adamw_workspace(count), workspace, workspace_bytes)) != NF4_OK) return st;
+    size_t need = adamw_workspace(count);
+    if (own_norm && grad_norm_workspace(entries, count) > need) need = grad_norm_workspace(entries, count);
+    if ((st = check_workspace(need, workspace, workspace_bytes)) != NF4_OK) return st;
     return launch_status(launch_adamw(entries, count, static_cast<nf4_dtype>(w_dtype),
-                                      static_cast<nf4_dtype>(grad_dtype), eight, c, grad_norm, workspace,
+                                      static_cast<nf4_dtype>(grad_dtype), eight, c, norm, own_norm, workspace,
                                       stream_of(stream)));
+}
+
+}  // namespace
+
+NF4_API nf4_status nf4_adamw_step(const nf4_adamw_entry *entries, int32_t count, int32_t w_dtype, int32_t grad_dtype,
+                                  int32_t moments, const nf4_adamw_config *config, const float *grad_norm,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    return adamw(entries, count, w_dtype, grad_dtype, moments, config, const_cast<float *>(grad_norm), false, workspace,
+                 workspace_bytes, stream);  // read only
+}
+
+NF4_API nf4_status nf4_adamw_clip_step(const nf4_adamw_entry *entries, int32_t count, int32_t w_dtype,
+                                       int32_t grad_dtype, int32_t moments, const nf4_adamw_config *config,
+                                       float *grad_norm, void *workspace, size_t workspace_bytes, void *stream) {
+    return adamw(entries, count, w_dtype, grad_dtype, moments, config, grad_norm, true, workspace, workspace_bytes,
+                 stream);
 }
 
 namespace {

@@ -54,8 +54,8 @@ struct AdamwBatch {
 };
 struct AdamwScalars {
     float beta1, one_beta1, beta2, one_beta2, eps, rbias2, max_norm;
-    int32_t count;  // entries of the table
-    const float *norm;
+    int32_t count;  // entries of the table, or of the list whose norm is taken here
+    float *norm;
     const AdamwItem *table;   // in the workspace, where there are more than kBatch entries
     const uint32_t *firsts;   // their `first`, one after the other
 };
@@ -126,6 +126,73 @@ __device__ __forceinline__ float storage_scale(float amax, float *inv) {
     return s;
 }
 
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
+    return x;
+}
+
+// Sum over the workgroup, in thread 0.
+template <int kN>
+__device__ __forceinline__ double block_sum(double x) {
+    __shared__ double part[kN / 64];
+    x = wave_sum(x);
+    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = x;
+    __syncthreads();
+    double t = 0.0;
+    if (threadIdx.x == 0)
+        for (int j = 0; j < kN / 64; ++j) t += part[j];
+    return t;
+}
+
+// A thread's share of the squares of a list's gradients (up to kN / 8 entries): the
+// waves take pieces of 512 elements in turn, each wave kVecs pieces in flight.
+template <typename G, int kN, int kVecs, typename Item>
+__device__ __forceinline__ double list_squares(const Item *item, int32_t count) {
+    double sum = 0.0;
+    // the elements past an entry's last eight, eight threads an entry
+    const int at = threadIdx.x % 8;
+    if ((int)threadIdx.x / 8 < count) {
+        const Item &e = item[threadIdx.x / 8];
+        if (at < (int)(e.n % 8)) {
+            const double x = load1(static_cast<const G *>(e.g) + e.n / 8 * 8 + at);
+            sum = fma(x, x, sum);
+        }
+    }
+    const int lane = threadIdx.x % 64;
+    int k = -1;  // the piece that is next, of entry k; uniform over the wave
+    int32_t piece = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), eights = 0, pieces = 0;
+    const G *g = nullptr;
+    auto find = [&] {
+        while (piece >= pieces && k < count) {
+            piece -= pieces;
+            if (++k == count) break;
+            g = static_cast<const G *>(item[k].g);
+            eights = (int32_t)(item[k].n / 8), pieces = (eights + 63) / 64;
+        }
+    };
+    for (find(); k < count;) {
+        Raw8<G> raw[kVecs];
+        bool live[kVecs];
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+            live[u] = k < count && piece * 64 + lane < eights;
+            if (k < count) raw[u] = load_raw(g + (live[u] ? piece * 64 + lane : piece * 64) * 8);
+            piece += kN / 64;
+            find();
+        }
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+            float x[8];
+            values(raw[u], x);
+            if (live[u])
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum = fma((double)x[j], (double)x[j], sum);
+        }
+    }
+    return sum;
+}
+
 // A lane's four elements, as eight are loaded and stored by load_raw, load_stream
 // and store_stream.
 template <typename T> struct Raw4;
@@ -191,18 +258,33 @@ __device__ __forceinline__ Code encode_each(const float (&x)[N], const uint32_t 
 template <typename W, bool kMaster, bool kEight>
 constexpr int kStepEach = (kEight && !kMaster && sizeof(W) == 2) ? 8 : 4;
 
-template <typename W, typename G, bool kMaster, bool kEight, bool kTable, int N = kStepEach<W, kMaster, kEight>>
+// Where a workgroup finds its entry, and the norm that the step clips by: the
+// kernel arguments hold the list, or the workspace, or (kOwnNorm) the arguments hold
+// one of so few elements that every workgroup reads all gradients for the norm.
+enum ListKind { kInArgs, kInTable, kOwnNorm };
+
+template <typename W, typename G, bool kMaster, bool kEight, ListKind kList, int N = kStepEach<W, kMaster, kEight>>
 __global__ __launch_bounds__(kPass / N) void adamw_kernel(AdamwBatch b, AdamwScalars c) {
     constexpr int kBlockLanes = kMomentBlock / N;
     using Code = std::conditional_t<N == 8, uint64_t, uint32_t>;  // a lane's codes
     float clip = 1.0f;
-    if (c.norm != nullptr) {
-        const float norm = *c.norm;
+    if (kList == kOwnNorm || c.norm != nullptr) {
+        float norm;
+        if constexpr (kList == kOwnNorm) {
+            __shared__ float s_norm;
+            const double sum = block_sum<kPass / N>(list_squares<G, kPass / N, 8>(b.item, c.count));
+            if (threadIdx.x == 0) s_norm = (float)sqrt(sum);
+            __syncthreads();
+            norm = s_norm;
+            if (blockIdx.x == 0 && threadIdx.x == 0) *c.norm = norm;
+        } else {
+            norm = *c.norm;
+        }
         if (!(fabsf(norm) < INFINITY)) return;
         if (c.max_norm > 0.0f && norm > c.max_norm) clip = c.max_norm * (1.0f / norm);
     }
     const uint32_t wg = gridDim.x - 1 - blockIdx.x;
-    const AdamwItem e = kTable ? c.table[find_in_table(c.firsts, c.count, wg)] : b.item[find_in_batch(b.item, wg)];
+    const AdamwItem e = kList == kInTable ? c.table[find_in_table(c.firsts, c.count, wg)] : b.item[find_in_batch(b.item, wg)];
     const int64_t i = (int64_t)(wg - e.first) * kPass + threadIdx.x * N;
     const int64_t live = e.n - i;  // may be <= 0: the lane still joins the reductions
     W *w = static_cast<W *>(e.w) + i;
@@ -313,7 +395,7 @@ __global__ __launch_bounds__(kPass / N) void adamw_kernel(AdamwBatch b, AdamwSca
 
 constexpr int kNormBatch = 160;
 constexpr int64_t kSmallNorm = 1 << 17;  // elements, and
-constexpr int32_t kSmallEntries = 16;    // entries that one workgroup takes alone
+constexpr int32_t kSmallEntries = 16;    // entries: lists whose norm a single workgroup takes
 constexpr int kNormVecs = 8;                              // of a thread, in flight together
 constexpr int64_t kNormChunk = (int64_t)kPass * kNormVecs;  // elements of one partial sum
 
@@ -326,25 +408,6 @@ struct NormBatch {
     NormItem item[kNormBatch];
 };
 static_assert(sizeof(NormBatch) + 16 <= 4096, "kernel arguments");
-
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
-    return x;
-}
-
-// Sum over the workgroup, in thread 0.
-template <int kN>
-__device__ __forceinline__ double block_sum(double x) {
-    __shared__ double part[kN / 64];
-    x = wave_sum(x);
-    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = x;
-    __syncthreads();
-    double t = 0.0;
-    if (threadIdx.x == 0)
-        for (int j = 0; j < kN / 64; ++j) t += part[j];
-    return t;
-}
 
 // Squares of 16384 consecutive gradients, each exact in fp64.
 template <typename G>
@@ -380,32 +443,7 @@ __global__ __launch_bounds__(kThreads) void grad_square_kernel(NormBatch b, doub
 // of two.
 template <typename G>
 __global__ __launch_bounds__(1024) void grad_norm_small_kernel(NormBatch b, int32_t count, float *norm) {
-    double sum = 0.0;
-    for (int k = 0; k < count; ++k) {
-        const G *g = static_cast<const G *>(b.item[k].g);
-        const int64_t n = b.item[k].n, whole = n / kEach * kEach;
-        for (int64_t i0 = threadIdx.x * kEach; i0 < whole; i0 += 4 * 1024 * kEach) {
-            Raw8<G> raw[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int64_t i = i0 + u * 1024 * kEach;
-                raw[u] = load_raw(g + (i < whole ? i : i0));
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                float x[8];
-                values(raw[u], x);
-                if (i0 + u * 1024 * kEach < whole)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum = fma((double)x[j], (double)x[j], sum);
-            }
-        }
-        if (whole + threadIdx.x < n) {
-            const double x = load1(g + whole + threadIdx.x);
-            sum = fma(x, x, sum);
-        }
-    }
-    sum = block_sum<1024>(sum);
+    const double sum = block_sum<1024>(list_squares<G, 1024, 8>(b.item, count));
     if (threadIdx.x == 0) *norm = (float)sqrt(sum);
 }
 
@@ -429,7 +467,7 @@ int64_t norm_partials(const nf4_adamw_entry *e, int32_t count) {
 // with its own ramp and drain.
 template <typename W, typename G, bool kMaster, bool kEight>
 hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_adamw_config &cfg,
-                          const float *norm, void *workspace, hipStream_t s) {
+                          float *norm, bool own, void *workspace, hipStream_t s) {
     const double bias1 = 1.0 - pow(cfg.beta1, (double)cfg.step);
     const double bias2 = 1.0 - pow(cfg.beta2, (double)cfg.step);
     AdamwScalars c{};
@@ -465,11 +503,13 @@ hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_ada
         if (table) {
             copy();
             c.table = items + from, c.firsts = firsts + from, c.count = done - from;
-            adamw_kernel<W, G, kMaster, kEight, true><<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
+            adamw_kernel<W, G, kMaster, kEight, kInTable><<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
             from = done;
         } else {
             for (int j = used; j < kBatch; ++j) b.item[j].first = UINT32_MAX;
-            adamw_kernel<W, G, kMaster, kEight, false><<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
+            c.count = used;
+            if (own) adamw_kernel<W, G, kMaster, kEight, kOwnNorm, 4><<<dim3((uint32_t)wgs), dim3(kPass / 4), 0, s>>>(b, c);
+            else adamw_kernel<W, G, kMaster, kEight, kInArgs><<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
             used = 0;
         }
         note();
@@ -496,15 +536,27 @@ hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_ada
 
 template <typename W, typename G>
 hipError_t adamw_typed(const nf4_adamw_entry *e, int32_t count, bool eight, const nf4_adamw_config &c,
-                       const float *norm, void *ws, hipStream_t s) {
-    hipError_t err = eight ? adamw_launches<W, G, false, true>(e, count, c, norm, ws, s)
-                           : adamw_launches<W, G, false, false>(e, count, c, norm, ws, s);
+                       float *norm, bool own, void *ws, hipStream_t s) {
+    hipError_t err = eight ? adamw_launches<W, G, false, true>(e, count, c, norm, own, ws, s)
+                           : adamw_launches<W, G, false, false>(e, count, c, norm, own, ws, s);
     if constexpr (sizeof(W) == 2) {
-        const hipError_t r = eight ? adamw_launches<W, G, true, true>(e, count, c, norm, ws, s)
-                                   : adamw_launches<W, G, true, false>(e, count, c, norm, ws, s);
+        const hipError_t r = eight ? adamw_launches<W, G, true, true>(e, count, c, norm, own, ws, s)
+                                   : adamw_launches<W, G, true, false>(e, count, c, norm, own, ws, s);
         if (err == hipSuccess) err = r;
     }
     return err;
+}
+
+// Elements and entries with any.
+struct Extent {
+    int64_t elements;
+    int32_t live, masters;
+};
+Extent extent_of(const nf4_adamw_entry *e, int32_t count) {
+    Extent x{};
+    for (int32_t i = 0; i < count; ++i)
+        if (e[i].n > 0) x.elements += e[i].n, ++x.live, x.masters += e[i].master ? 1 : 0;
+    return x;
 }
 
 }  // namespace
@@ -535,13 +587,11 @@ hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype g
         if (err == hipSuccess) err = r;
         done += wgs, used = 0, wgs = 0;
     };
-    // One launch less, but one workgroup's bandwidth: a step with its norm takes
-    // 12.6 us instead of 16.1 for 131072 elements (bf16) in two tensors; with twice
-    // as many it is 15.1 against 15.8 among other calls, 28 against 25 alone.
-    int64_t total = 0;
-    int32_t live = 0;
-    for (int32_t i = 0; i < count; ++i) total += e[i].n, live += e[i].n > 0 ? 1 : 0;
-    if (total <= kSmallNorm && live <= kSmallEntries) {
+    // One launch less, but one workgroup's bandwidth: 4.8 us instead of 8.1 for two
+    // tensors of 1000 elements (bf16), 7.0 and 7.1 for two of 65536, 11.2 and 7.0 for
+    // two of 131072.
+    const Extent x = extent_of(e, count);
+    if (x.elements <= kSmallNorm && x.live <= kSmallEntries) {
         for (int32_t i = 0; i < count; ++i)
             if (e[i].n > 0) b.item[used++] = NormItem{e[i].grad, e[i].n, 0u, 0u};
         if (gt == NF4_BF16) grad_norm_small_kernel<Bf16><<<dim3(1), dim3(1024), 0, s>>>(b, used, norm);
@@ -564,13 +614,26 @@ hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype g
 }
 
 hipError_t launch_adamw(const nf4_adamw_entry *e, int32_t count, nf4_dtype wt, nf4_dtype gt,
-                        bool eight, const nf4_adamw_config &c, const float *norm, void *workspace,
+                        bool eight, const nf4_adamw_config &c, float *norm, bool own_norm, void *workspace,
                         hipStream_t s) {
+    bool own = false;
+    if (own_norm) {
+        const Extent x = extent_of(e, count);
+        // Every workgroup reads all gradients, but there is one launch: 7.4 us instead
+        // of 10.8 for two tensors of 8192 elements (bf16, 8-bit moments), 11.2 instead of
+        // 14.0 for 14 of them, 10.4 instead of 11.3 for two of 65536; 16.5 against 13.6
+        // for two of 131072.
+        own = x.live > 0 && x.elements <= kSmallNorm && x.live <= kSmallEntries && (x.masters == 0 || x.masters == x.live);
+        if (!own) {
+            const hipError_t r = launch_grad_norm(e, count, gt, norm, workspace, s);
+            if (r != hipSuccess) return r;
+        }
+    }
     if (wt == NF4_BF16)
-        return gt == NF4_BF16 ? adamw_typed<Bf16, Bf16>(e, count, eight, c, norm, workspace, s)
-                              : adamw_typed<Bf16, float>(e, count, eight, c, norm, workspace, s);
-    return gt == NF4_BF16 ? adamw_typed<float, Bf16>(e, count, eight, c, norm, workspace, s)
-                          : adamw_typed<float, float>(e, count, eight, c, norm, workspace, s);
+        return gt == NF4_BF16 ? adamw_typed<Bf16, Bf16>(e, count, eight, c, norm, own, workspace, s)
+                              : adamw_typed<Bf16, float>(e, count, eight, c, norm, own, workspace, s);
+    return gt == NF4_BF16 ? adamw_typed<float, Bf16>(e, count, eight, c, norm, own, workspace, s)
+                          : adamw_typed<float, float>(e, count, eight, c, norm, own, workspace, s);
 }
 
 }  // namespace nf4

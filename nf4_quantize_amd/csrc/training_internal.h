@@ -13,8 +13,9 @@ constexpr int kMomentBlock = 256;  // elements per scale of the 8-bit moments
 size_t grad_norm_workspace(const nf4_adamw_entry *e, int32_t count);
 hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype gt, float *norm,
                             void *workspace, hipStream_t s);
+// own_norm: takes the gradients' norm first, into `norm`.
 hipError_t launch_adamw(const nf4_adamw_entry *e, int32_t count, nf4_dtype wt, nf4_dtype gt,
-                        bool eight, const nf4_adamw_config &c, const float *grad_norm,
+                        bool eight, const nf4_adamw_config &c, float *norm, bool own_norm,
                         void *workspace, hipStream_t s);
 size_t adamw_workspace(int32_t count);
 

@@ -38,6 +38,7 @@ def declare(L):
             ("nf4_grad_norm_workspace_size", sz, [p, i32]),
             ("nf4_grad_norm", i32, [p, i32, i32, p, p, sz, p]),
             ("nf4_adamw_step", i32, [p, i32, i32, i32, i32, ctypes.POINTER(nf4_adamw_config), p, p, sz, p]),
+            ("nf4_adamw_clip_step", i32, [p, i32, i32, i32, i32, ctypes.POINTER(nf4_adamw_config), p, p, sz, p]),
             ("nf4_adamw_workspace_size", sz, [i32]),
             ("nf4_residual_norm_forward", i32, [shape] + [p] * 10),
             ("nf4_residual_norm_backward_workspace_size", sz, [shape]),
@@ -249,23 +250,19 @@ class NF4AdamW:
         if list(map(T.data_ptr, self._weights)) != self._bound:  # a parameter has new memory
             self._bind()
         grad_dtype = _code(dt)
-        e, count = self._entries, len(grads)
+        e = self._entries
         e["grad"] = array.array("Q", map(T.data_ptr, grads))
         for g in self.groups:
             part = slice(g["first"], g["first"] + g["count"])
             e["lr"][part], e["weight_decay"][part] = g["lr"], g["weight_decay"]
-        at = self._at
         number = self.steps + 1 if step is None else int(step)
         stream = _stream(devices.pop())
-        clip = self.max_grad_norm > 0
-        norm = self.grad_norm.data_ptr() if clip else None
-        ws, ws_bytes = self._workspace.data_ptr(), self._workspace.numel()
-        if clip:
-            _nq._check(L.nf4_grad_norm(at, count, grad_dtype, norm, ws, ws_bytes, stream), "nf4_grad_norm")
         config = nf4_adamw_config(*self.betas, self.eps, self.max_grad_norm, number,
                                   (self.seed + number if seed is None else int(seed)) & 0xFFFFFFFFFFFFFFFF)
-        _nq._check(L.nf4_adamw_step(at, count, _code(self.dtype), grad_dtype, self.state_bits, ctypes.byref(config), norm,
-                                    ws, ws_bytes, stream), "nf4_adamw_step")
+        call, norm = ((L.nf4_adamw_clip_step, self.grad_norm.data_ptr()) if self.max_grad_norm > 0
+                      else (L.nf4_adamw_step, None))
+        _nq._check(call(self._at, len(grads), _code(self.dtype), grad_dtype, self.state_bits, ctypes.byref(config), norm,
+                        self._workspace.data_ptr(), self._workspace.numel(), stream), call.__name__)
         self.steps = number
 
     def state_dict(self):

@@ -384,3 +384,49 @@ def test_parameters_with_new_memory(dev):
         opt.step([torch.ones(600, device=dev)])
     with pytest.raises(ValueError):
         opt.step([torch.ones(700, device=dev)])
+
+
+@pytest.mark.parametrize("bits,wt,gt", [(8, "bfloat16", "bfloat16"), (8, "float32", "float32"),
+                                        (32, "bfloat16", "float32"), (32, "float32", "bfloat16")])
+@pytest.mark.parametrize("case", ["one", "ragged", "sixteen", "seventeen", "large", "masters", "some masters", "empty"])
+def test_clip_step_is_norm_then_step(dev, bits, wt, gt, case):
+    """One call against the two that it stands for, bit for bit. The gradients are
+    small multiples of 2^-6, so their squares add up without rounding in any order
+    and the norms are equal."""
+    import ctypes
+
+    import torch
+    from nf4_quantize_amd import training
+
+    sizes = {"one": [1], "ragged": [7, 513, 2049, 1, 8191], "sixteen": [1030] * 16, "seventeen": [1030] * 17,
+             "large": [131072, 9], "masters": [700, 3000], "some masters": [700, 3000, 5], "empty": [0, 600, 0]}[case]
+    master = case.endswith("masters")
+    if master and wt != "bfloat16":
+        pytest.skip("masters are of bfloat16 weights")
+    log(f"clip step {case} {bits} bits {wt} {gt}")
+    rng = np.random.default_rng(len(sizes) + bits)
+    start = [torch.from_numpy(rng.standard_normal(n).astype(np.float32)).to(dev) for n in sizes]
+    grads = [torch.from_numpy(rng.integers(-16, 17, n).astype(np.float32) / 64).to(dev).to(getattr(torch, gt)) for n in sizes]
+    got = []
+    for one_call in (True, False):
+        ps = [s.clone().to(getattr(torch, wt)) for s in start]
+        ms = [s.clone() if master and not (case == "some masters" and i == 1) else None for i, s in enumerate(start)]
+        opt = nq.NF4AdamW(ps, lr=1e-2, state_bits=bits, masters=ms if master else None, max_grad_norm=0.25, seed=3)
+        for number in (1, 2):
+            if one_call:
+                opt.step(grads)
+                continue
+            L, e = nq.lib(), opt._entries
+            e["grad"], e["lr"], e["weight_decay"] = [g.data_ptr() for g in grads], 1e-2, 0.01
+            cfg = training.nf4_adamw_config(0.9, 0.999, 1e-8, 0.25, number, 3 + number)
+            ws, stream = opt._workspace, torch.cuda.current_stream().cuda_stream
+            code = {"float32": 0, "bfloat16": 1}
+            assert L.nf4_grad_norm(e.ctypes.data, len(e), code[gt], opt.grad_norm.data_ptr(), ws.data_ptr(), ws.numel(),
+                                   stream) == 0
+            assert L.nf4_adamw_step(e.ctypes.data, len(e), code[wt], code[gt], bits, ctypes.byref(cfg),
+                                    opt.grad_norm.data_ptr(), ws.data_ptr(), ws.numel(), stream) == 0
+        parts = ps + [t for t in ms if t is not None] + opt.m + opt.v + ([] if bits == 32 else opt.m_scale + opt.v_scale)
+        got.append([opt.grad_norm.clone()] + [t.clone() for t in parts])
+    want = np.float32(np.sqrt(sum((f64(g) ** 2).sum() for g in grads)))
+    assert float(got[0][0]) == want
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*got) if a.numel())

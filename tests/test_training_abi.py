@@ -230,3 +230,25 @@ def test_binding_refusals():
         nq.embedding_backward(torch.zeros(3, dtype=torch.int64), torch.zeros(2, 4), 10)
     with pytest.raises(TypeError):
         training._index_code(torch.zeros(3, dtype=torch.int16))
+
+
+def test_adamw_clip_refusals(L):
+    """What the norm's call and the step refuse; the norm is written, so it has to be there."""
+    def clip(e, norm=FAKE, ws=FAKE, b=1 << 20, wt=1, gt=1, **c):
+        f = dict(beta1=0.9, beta2=0.999, eps=1e-8, max_norm=1.0, step=1, seed=0)
+        f.update(c)
+        return L.nf4_adamw_clip_step(e.ctypes.data, len(e), wt, gt, 8, ctypes.byref(training.nf4_adamw_config(**f)),
+                                     norm, ws, b, None)
+
+    assert L.nf4_adamw_clip_step(None, 2, 1, 1, 8, None, None, None, 0, None) == NULL
+    assert clip(entries({}), norm=None) == NULL
+    assert clip(entries({}), norm=None, max_norm=0.0) == NULL
+    assert clip(entries({}), norm=FAKE + 2) == ALIGN
+    assert clip(entries({}), ws=None) == WORKSPACE
+    assert clip(entries({}, {"n": 16385}), b=23) == WORKSPACE
+    assert clip(entries(*[{}] * 49), b=49 * 84 - 1) == WORKSPACE
+    assert clip(entries({}), ws=FAKE + 64) == ALIGN
+    assert clip(entries({}), gt=2) == UNSUPPORTED
+    assert clip(entries({}), beta1=1.0) == SIZE
+    for k in ("w", "grad", "m", "v", "m_scale", "v_scale"):
+        assert clip(entries({}, {k: 0})) == NULL, k
