@@ -151,6 +151,7 @@ class NF4AdamW:
         self._at = self._entries.ctypes.data
         self._numels = [p.numel() for p in self.params]
         self._weights = self.params + [mw for mw in self.masters if mw is not None]
+        self._rates = None
         self._bind()
         self.betas, self.eps, self.state_bits = (float(betas[0]), float(betas[1])), float(eps), state_bits
         self.max_grad_norm, self.seed, self.steps = float(max_grad_norm), int(seed), 0
@@ -252,9 +253,12 @@ class NF4AdamW:
         grad_dtype = _code(dt)
         e = self._entries
         e["grad"] = array.array("Q", map(T.data_ptr, grads))
-        for g in self.groups:
-            part = slice(g["first"], g["first"] + g["count"])
-            e["lr"][part], e["weight_decay"][part] = g["lr"], g["weight_decay"]
+        rates = [(g["lr"], g["weight_decay"]) for g in self.groups]
+        if rates != self._rates:
+            for g in self.groups:
+                part = slice(g["first"], g["first"] + g["count"])
+                e["lr"][part], e["weight_decay"][part] = g["lr"], g["weight_decay"]
+            self._rates = rates
         number = self.steps + 1 if step is None else int(step)
         stream = _stream(devices.pop())
         config = nf4_adamw_config(*self.betas, self.eps, self.max_grad_norm, number,

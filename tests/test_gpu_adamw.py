@@ -430,3 +430,21 @@ def test_clip_step_is_norm_then_step(dev, bits, wt, gt, case):
     want = np.float32(np.sqrt(sum((f64(g) ** 2).sum() for g in grads)))
     assert float(got[0][0]) == want
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*got) if a.numel())
+
+
+def test_rates_change_between_steps(dev):
+    """lr and weight_decay of a group are those of the step's time."""
+    import torch
+
+    p = torch.zeros(300, device=dev)
+    opt = nq.NF4AdamW([dict(params=[p], lr=0.25, weight_decay=0.0)], state_bits=32)
+    g = torch.ones(300, device=dev)
+    want = 0.0
+    for lr in (0.25, 0.25, 0.5, 0.125):
+        opt.groups[0]["lr"] = lr
+        opt.step([g])
+        want -= lr  # constant gradients: m / (1 - beta1^t) = g and v / (1 - beta2^t) = g^2 up to rounding
+        assert float((p - want).abs().max()) < 1e-5
+    opt.groups[0].update(lr=0.5, weight_decay=0.5)
+    opt.step([g])
+    assert float((p - (want * 0.75 - 0.5)).abs().max()) < 1e-5
