@@ -350,6 +350,7 @@ __global__ __launch_bounds__(1024) void digit_scatter_kernel(DigitPass p) {
 
 // ---- the gradient ----
 
+constexpr int kFewTokens = 128;  // up to here one launch
 constexpr int kMostChunk = 16;  // sorted places of a wave
 constexpr int kCols = 512;  // columns of a wave
 constexpr int kRows = 8;    // rows of dy, or shares of a run, in flight
@@ -496,6 +497,99 @@ __global__ __launch_bounds__(kThreads) void run_join_kernel(GradParams p) {
     store_cols(grad_row<G>(p, key), cols, x);
 }
 
+// The whole gradient of few tokens in one launch. A lane knows the ids of two
+// tokens, so a wave finds all tokens of an id by ballots: the first one's wave adds
+// their rows, in the order of the tokens, for 512 columns. Without kAdd the
+// workgroups past those clear the rows that no token names. 128 tokens added to a
+// gradient of 32000 x 4096 take 8.4 us a call instead of 13 with the sort, written
+// 35 instead of 40; 128 times the same token 14.9 instead of 13, so no more than that.
+struct FewParams {
+    const void *ids;
+    bool i64;
+    int32_t tokens, dim, slices, wgs;
+    int64_t vocab, skip;
+    float scale;
+    const void *dy;
+    void *grad;
+};
+template <typename T, typename G, bool kNarrow, bool kAdd>
+__global__ __launch_bounds__(kThreads) void few_tokens_kernel(FewParams p) {
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    uint32_t key[kFewTokens / 64];
+#pragma unroll
+    for (int k = 0; k < kFewTokens / 64; ++k) {
+        const int t = lane + 64 * k;
+        key[k] = token_key(p.ids, p.i64, t < p.tokens ? t : 0, p.vocab, p.skip);
+        key[k] = t < p.tokens ? key[k] : 0xFFFFFFFFu;
+    }
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if ((int)blockIdx.x >= p.wgs) {
+        // a row is a wave's, or the workgroup's where it is longer than a wave's store
+        const bool wide = p.dim > 512;
+        const int each = wide ? 1 : kThreads / 64, step = wide ? kThreads * 8 : 512;
+        const int64_t stride = (int64_t)(gridDim.x - p.wgs) * each;
+        for (int64_t row = (int64_t)(blockIdx.x - p.wgs) * each + (wide ? 0 : wave); row < p.vocab; row += stride) {
+            bool named = false;
+#pragma unroll
+            for (int k = 0; k < kFewTokens / 64; ++k) named |= key[k] == (uint32_t)row;
+            if (__any(named)) continue;
+            G *dst = static_cast<G *>(p.grad) + row * p.dim;
+            for (int c = (wide ? (int)threadIdx.x : lane) * 8; c < p.dim; c += step) store_cols(dst, Cols<kNarrow>(c, p.dim), acc);
+        }
+        return;
+    }
+    const int unit = (int)blockIdx.x * (kThreads / 64) + wave, t = unit / p.slices;
+    if (t >= p.tokens) return;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int k = 0; k < kFewTokens / 64; ++k)
+        if (t / 64 == k) mine = (uint32_t)__builtin_amdgcn_readlane((int)key[k], t % 64);
+    if (mine >= p.vocab) return;
+    uint64_t same[kFewTokens / 64];
+#pragma unroll
+    for (int k = 0; k < kFewTokens / 64; ++k) {
+        same[k] = __ballot(key[k] == mine);
+        const uint64_t before = t / 64 > k ? ~uint64_t(0) : t / 64 == k ? (uint64_t(1) << (t % 64)) - 1 : 0;
+        if (same[k] & before) return;  // not the first one
+    }
+    const Cols<kNarrow> cols((unit % p.slices) * kCols + lane * 8, p.dim);
+    G *dst = static_cast<G *>(p.grad) + (int64_t)mine * p.dim;
+    Raw8<G> old;
+    if constexpr (kAdd) old = load_cols(dst, cols);
+    int base = 0, left = 0;
+#pragma unroll
+    for (int k = 0; k < kFewTokens / 64; ++k) left += (int)__popcll(same[k]);
+    for (; left > 0; left -= kRows) {
+        Raw8<T> raw[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            if (u >= left) break;  // a bit is left in some word as long as this does not hold
+            while (same[0] == 0) {
+#pragma unroll
+                for (int k = 0; k + 1 < kFewTokens / 64; ++k) same[k] = same[k + 1];
+                same[kFewTokens / 64 - 1] = 0;
+                base += 64;
+            }
+            const int at = base + __builtin_ctzll(same[0]);
+            same[0] &= same[0] - 1;
+            raw[u] = load_cols(static_cast<const T *>(p.dy) + (int64_t)at * p.dim, cols);
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            if (u >= left) break;
+            float x[8];
+            cols_values(raw[u], cols, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] += x[j];
+        }
+    }
+    float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (kAdd) cols_values(old, cols, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = kAdd ? x[j] + acc[j] * p.scale : acc[j] * p.scale;
+    store_cols(dst, cols, x);
+}
+
 // ---- host side ----
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
@@ -619,6 +713,17 @@ hipError_t gradient(const Sort &q, const GradParams &p, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <typename T, typename G>
+hipError_t few_tokens(FewParams p, bool add, hipStream_t s) {
+    p.wgs = (p.tokens * p.slices + 3) / 4;
+    const int64_t rows = p.dim > 512 ? p.vocab : (p.vocab + 3) / 4;
+    const int64_t clear = add ? 0 : rows < 2048 ? rows : 2048;  // eight for each CU
+    auto kernel = p.dim < 8 ? (add ? few_tokens_kernel<T, G, true, true> : few_tokens_kernel<T, G, true, false>)
+                            : (add ? few_tokens_kernel<T, G, false, true> : few_tokens_kernel<T, G, false, false>);
+    kernel<<<dim3((uint32_t)(p.wgs + clear)), dim3(kThreads), 0, s>>>(p);
+    return hipGetLastError();
+}
+
 template <typename T, typename O>
 hipError_t lookup(const void *ids, bool i64, int64_t tokens, const void *table, int64_t vocab, int64_t dim,
                   float scale, void *out, hipStream_t s) {
@@ -668,6 +773,11 @@ hipError_t launch_embedding_backward(const void *ids, bool i64, int64_t tokens, 
                                      int64_t vocab, int64_t dim, float scale, int64_t padding_id, void *grad,
                                      nf4_dtype gt, bool accumulate, void *workspace, hipStream_t s) {
     const Layout l = layout_of(tokens, dim);
+    if (tokens > 0 && tokens <= kFewTokens) {
+        const FewParams p{ids, i64, (int32_t)tokens, (int32_t)dim, l.slices, 0, vocab, padding_id, scale, dy, grad};
+        if (dt == NF4_BF16) return gt == NF4_BF16 ? few_tokens<Bf16, Bf16>(p, accumulate, s) : few_tokens<Bf16, float>(p, accumulate, s);
+        return gt == NF4_BF16 ? few_tokens<float, Bf16>(p, accumulate, s) : few_tokens<float, float>(p, accumulate, s);
+    }
     char *ws = static_cast<char *>(workspace);
     auto words = [ws](size_t at) { return reinterpret_cast<uint32_t *>(ws + at); };
     Sort q{};

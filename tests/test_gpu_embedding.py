@@ -203,3 +203,30 @@ def test_refusals_on_device(dev):
         nq.embedding_backward(ids, torch.zeros(3, 8, device=dev), 5, grad=torch.zeros(4, 8, device=dev))
     with pytest.raises(nq.NF4Error):
         nq.embedding_backward(ids, torch.zeros(3, 8, device=dev), 5, workspace=torch.zeros(8, dtype=torch.uint8, device=dev))
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 63, 64, 65, 127, 128, 129, 130])
+@pytest.mark.parametrize("vocab,dim", [(1, 1), (3, 7), (40, 8), (300, 511), (2100, 513), (37, 4100)])
+@pytest.mark.parametrize("kind", ["few", "one", "descending", "none"])
+def test_gradient_of_few_tokens(dev, tokens, vocab, dim, kind):
+    """Around the sizes that one launch takes, into memory that holds NaN where the
+    call writes every row, with padding, and with bytes around the gradient."""
+    import torch
+    from nf4_quantize_amd import training
+
+    log(f"embedding gradient of few tokens {tokens} {vocab}x{dim} {kind}")
+    ids = draw(dev, kind, tokens, vocab, seed=tokens)
+    L, pad = nq.lib(), 64
+    for dt, gd, acc in ((torch.bfloat16, torch.float32, 0), (torch.float32, torch.bfloat16, 1), (torch.bfloat16, torch.bfloat16, 0)):
+        dy = torch.randn(tokens, dim, device=dev).to(dt)
+        buf = torch.full((pad + vocab * dim + pad,), 7.0, device=dev, dtype=gd)
+        grad = buf[pad:pad + vocab * dim].view(vocab, dim)
+        grad0 = torch.randn(vocab, dim, device=dev).to(gd) if acc else None
+        grad.copy_(grad0) if acc else grad.fill_(float("nan"))
+        padding = int(ids[0]) if 0 <= int(ids[0]) < vocab and tokens > 1 else -1
+        ws = torch.empty(L.nf4_embedding_backward_workspace_size(tokens, vocab, dim), dtype=torch.uint8, device=dev)
+        assert L.nf4_embedding_backward(ids.data_ptr(), 1, tokens, dy.data_ptr(), training._code(dt), vocab, dim, 0.75,
+                                        padding, grad.data_ptr(), training._code(gd), acc, ws.data_ptr(), ws.numel(),
+                                        torch.cuda.current_stream().cuda_stream) == 0
+        check_gradient(ids, dy, vocab, 0.75, grad0, grad, padding if padding >= 0 else None)
+        assert bool((buf[:pad] == 7.0).all()) and bool((buf[pad + vocab * dim:] == 7.0).all())
