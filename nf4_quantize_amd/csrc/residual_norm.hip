@@ -17,6 +17,10 @@
 namespace nf4 {
 namespace {
 
+struct ColumnOut {
+    void *out[3];
+};
+
 struct NormParams {
     ResidualNormIn in;
     ResidualNormOut out;
@@ -26,8 +30,8 @@ struct NormParams {
     int32_t lanes;       // lanes of a row: 8 .. 64, a power of two, or the whole workgroup
     int32_t gate_kind;
     bool w_bf16;
-    float *partial;      // backward: [workgroups][3][dim]
-    bool want[3];        // the rows of `partial` that are asked for
+    float *partial;      // backward: [workgroups][3][dim], unless there is one workgroup
+    ColumnOut sums;      // the gradients summed over rows that are asked for
     float2 *means;       // backward, rows of several tiles: [rows]
 };
 
@@ -386,11 +390,13 @@ __global__ __launch_bounds__(kMost) void residual_norm_backward_kernel(NormParam
         if (p.in.y && p.out.dy) store_row<kKind>(static_cast<T *>(p.out.dy) + at, c, x.n2);
         if (kToken && p.out.dgate) store_row<kKind>(static_cast<T *>(p.out.dgate) + at, c, dg);
     }
-    if (p.partial == nullptr) return;
+    const bool last = gridDim.x == 1;  // all rows are here
     float *mine = p.partial + (int64_t)blockIdx.x * 3 * p.dim;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        if (!p.want[k]) continue;
+        if (p.sums.out[k] == nullptr) continue;
+        float *sums = last ? static_cast<float *>(p.sums.out[k]) : mine + k * p.dim;
+        Bf16 *rounded = static_cast<Bf16 *>(p.sums.out[k]);
         if (groups > 1) {
             const int width = lanes * 8;
             __syncthreads();
@@ -400,19 +406,19 @@ __global__ __launch_bounds__(kMost) void residual_norm_backward_kernel(NormParam
             for (int i = threadIdx.x; i < p.dim; i += blockDim.x) {
                 float t = 0.0f;
                 for (int q = 0; q < groups; ++q) t += s_cols[q * width + i];
-                mine[k * p.dim + i] = t;
+                if (last && p.w_bf16) store1(rounded + i, t);
+                else sums[i] = t;
             }
+        } else if (last && p.w_bf16) {
+            store_cols(rounded, c, acc[k]);
         } else {
-            store_cols(mine + k * p.dim, c, acc[k]);
+            store_cols(sums, c, acc[k]);
         }
     }
 }
 
 // Column sums over the workgroups' partial sums: 64 columns a workgroup, four a
 // lane, and 64 shares of the rows; blockIdx.y is the gradient.
-struct ColumnOut {
-    void *out[3];
-};
 __global__ __launch_bounds__(1024) void column_sum_kernel(const float *partial, int32_t parts, int32_t dim,
                                                           ColumnOut o, bool bf16) {
     __shared__ float s[64][65];
@@ -488,7 +494,10 @@ int64_t workgroups(int64_t rows, const Split &sp) {
 }
 // Each workgroup of the backward pass leaves a row of partial sums, so beyond one
 // for each CU none takes fewer than two sets of rows (1024 x 2048 bf16: 14 us
-// instead of 18). Tiles of a row fill the chip together.
+// instead of 18). A single one writes the sums itself, and there is no second launch
+// (one row of 2048: 16.4 us a call instead of 18.6; with four rows in one workgroup
+// a call alone takes longer, 4 x 8192 36 us instead of 31). Tiles of a row fill the
+// chip together.
 int64_t backward_workgroups(int64_t rows, const Split &sp) {
     const int64_t groups = sp.block / sp.lanes, pairs = (rows + 2 * groups - 1) / (2 * groups);
     const int64_t all = workgroups(rows, sp), one = all < 256 ? all : 256;
@@ -590,7 +599,7 @@ hipError_t launch_residual_norm_backward(const nf4_residual_norm_shape &sh, cons
     const bool sums = cols.out[0] || cols.out[1] || cols.out[2];
     float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + means_bytes(sh, sp));
     p.partial = sums ? partial : nullptr;
-    for (int k = 0; k < 3; ++k) p.want[k] = cols.out[k] != nullptr;
+    p.sums = cols;
     p.means = static_cast<float2 *>(workspace);
     if (wgs > 0) {
         hipError_t e;
@@ -599,7 +608,7 @@ hipError_t launch_residual_norm_backward(const nf4_residual_norm_shape &sh, cons
         else e = backward_typed<Bf16, Bf16>(p, sp, s);
         if (e != hipSuccess) return e;
     }
-    if (!sums) return hipSuccess;
+    if (!sums || wgs == 1) return hipSuccess;
     column_sum_kernel<<<dim3((uint32_t)((sh.dim + 63) / 64), 3), dim3(1024), 0, s>>>(partial, (int32_t)wgs,
                                                                                      (int32_t)sh.dim, cols, p.w_bf16);
     return hipGetLastError();
