@@ -505,8 +505,8 @@ nf4_status nf4_adamw_step(const nf4_adamw_entry *entries, int32_t count, int32_t
                           const float *grad_norm, void *workspace, size_t workspace_bytes,
                           void *stream);
 
-/* nf4_grad_norm, then nf4_adamw_step with that norm; a list of few elements takes
- * one launch for both.
+/* nf4_grad_norm, then nf4_adamw_step with that norm, in one or two launches less
+ * where the list has few elements.
  *   grad_norm  device out, one float
  *   workspace  as of both, the larger size */
 nf4_status nf4_adamw_clip_step(const nf4_adamw_entry *entries, int32_t count, int32_t w_dtype,

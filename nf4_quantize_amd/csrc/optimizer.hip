@@ -56,6 +56,8 @@ struct AdamwScalars {
     float beta1, one_beta1, beta2, one_beta2, eps, rbias2, max_norm;
     int32_t count;  // entries of the table, or of the list whose norm is taken here
     float *norm;
+    const double *partial;    // sums of squares that the norm is still to be taken from
+    int32_t parts;
     const AdamwItem *table;   // in the workspace, where there are more than kBatch entries
     const uint32_t *firsts;   // their `first`, one after the other
 };
@@ -259,20 +261,26 @@ template <typename W, bool kMaster, bool kEight>
 constexpr int kStepEach = (kEight && !kMaster && sizeof(W) == 2) ? 8 : 4;
 
 // Where a workgroup finds its entry, and the norm that the step clips by: the
-// kernel arguments hold the list, or the workspace, or (kOwnNorm) the arguments hold
-// one of so few elements that every workgroup reads all gradients for the norm.
-enum ListKind { kInArgs, kInTable, kOwnNorm };
+// kernel arguments hold the list, or the workspace; or the arguments hold one of so
+// few elements that every workgroup reads all gradients for the norm (kOwnNorm), or
+// all of the norm's partial sums (kPartNorm).
+enum ListKind { kInArgs, kInTable, kOwnNorm, kPartNorm };
 
 template <typename W, typename G, bool kMaster, bool kEight, ListKind kList, int N = kStepEach<W, kMaster, kEight>>
 __global__ __launch_bounds__(kPass / N) void adamw_kernel(AdamwBatch b, AdamwScalars c) {
     constexpr int kBlockLanes = kMomentBlock / N;
     using Code = std::conditional_t<N == 8, uint64_t, uint32_t>;  // a lane's codes
     float clip = 1.0f;
-    if (kList == kOwnNorm || c.norm != nullptr) {
+    constexpr bool kTakesNorm = kList == kOwnNorm || kList == kPartNorm;
+    if (kTakesNorm || c.norm != nullptr) {
         float norm;
-        if constexpr (kList == kOwnNorm) {
+        if constexpr (kTakesNorm) {
             __shared__ float s_norm;
-            const double sum = block_sum<kPass / N>(list_squares<G, kPass / N, 8>(b.item, c.count));
+            double sum = 0.0;
+            if constexpr (kList == kOwnNorm) sum = list_squares<G, kPass / N, 8>(b.item, c.count);
+            else
+                for (int i = threadIdx.x; i < c.parts; i += kPass / N) sum += c.partial[i];
+            sum = block_sum<kPass / N>(sum);
             if (threadIdx.x == 0) s_norm = (float)sqrt(sum);
             __syncthreads();
             norm = s_norm;
@@ -395,6 +403,7 @@ __global__ __launch_bounds__(kPass / N) void adamw_kernel(AdamwBatch b, AdamwSca
 
 constexpr int kNormBatch = 160;
 constexpr int64_t kSmallNorm = 1 << 17;  // elements, and
+constexpr int64_t kMidNorm = 1 << 23;    // elements: the step takes the norm from the partial sums
 constexpr int32_t kSmallEntries = 16;    // entries: lists whose norm a single workgroup takes
 constexpr int kNormVecs = 8;                              // of a thread, in flight together
 constexpr int64_t kNormChunk = (int64_t)kPass * kNormVecs;  // elements of one partial sum
@@ -467,7 +476,7 @@ int64_t norm_partials(const nf4_adamw_entry *e, int32_t count) {
 // with its own ramp and drain.
 template <typename W, typename G, bool kMaster, bool kEight>
 hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_adamw_config &cfg,
-                          float *norm, bool own, void *workspace, hipStream_t s) {
+                          float *norm, ListKind list, int64_t parts, void *workspace, hipStream_t s) {
     const double bias1 = 1.0 - pow(cfg.beta1, (double)cfg.step);
     const double bias2 = 1.0 - pow(cfg.beta2, (double)cfg.step);
     AdamwScalars c{};
@@ -475,6 +484,7 @@ hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_ada
     c.beta2 = (float)cfg.beta2, c.one_beta2 = (float)(1.0 - cfg.beta2);
     c.eps = cfg.eps, c.rbias2 = (float)(1.0 / bias2);
     c.max_norm = cfg.max_norm, c.norm = norm;
+    c.partial = static_cast<const double *>(workspace), c.parts = (int32_t)parts;
     auto mine = [&](int32_t i) { return e[i].n > 0 && (e[i].master != nullptr) == kMaster; };
     int32_t total = 0;
     for (int32_t i = 0; i < count; ++i) total += mine(i) ? 1 : 0;
@@ -508,7 +518,10 @@ hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_ada
         } else {
             for (int j = used; j < kBatch; ++j) b.item[j].first = UINT32_MAX;
             c.count = used;
-            if (own) adamw_kernel<W, G, kMaster, kEight, kOwnNorm, 4><<<dim3((uint32_t)wgs), dim3(kPass / 4), 0, s>>>(b, c);
+            if (list == kOwnNorm)
+                adamw_kernel<W, G, kMaster, kEight, kOwnNorm, 4><<<dim3((uint32_t)wgs), dim3(kPass / 4), 0, s>>>(b, c);
+            else if (list == kPartNorm)
+                adamw_kernel<W, G, kMaster, kEight, kPartNorm><<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
             else adamw_kernel<W, G, kMaster, kEight, kInArgs><<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
             used = 0;
         }
@@ -536,12 +549,12 @@ hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_ada
 
 template <typename W, typename G>
 hipError_t adamw_typed(const nf4_adamw_entry *e, int32_t count, bool eight, const nf4_adamw_config &c,
-                       float *norm, bool own, void *ws, hipStream_t s) {
-    hipError_t err = eight ? adamw_launches<W, G, false, true>(e, count, c, norm, own, ws, s)
-                           : adamw_launches<W, G, false, false>(e, count, c, norm, own, ws, s);
+                       float *norm, ListKind list, int64_t parts, void *ws, hipStream_t s) {
+    hipError_t err = eight ? adamw_launches<W, G, false, true>(e, count, c, norm, list, parts, ws, s)
+                           : adamw_launches<W, G, false, false>(e, count, c, norm, list, parts, ws, s);
     if constexpr (sizeof(W) == 2) {
-        const hipError_t r = eight ? adamw_launches<W, G, true, true>(e, count, c, norm, own, ws, s)
-                                   : adamw_launches<W, G, true, false>(e, count, c, norm, own, ws, s);
+        const hipError_t r = eight ? adamw_launches<W, G, true, true>(e, count, c, norm, list, parts, ws, s)
+                                   : adamw_launches<W, G, true, false>(e, count, c, norm, list, parts, ws, s);
         if (err == hipSuccess) err = r;
     }
     return err;
@@ -569,12 +582,14 @@ size_t grad_norm_workspace(const nf4_adamw_entry *e, int32_t count) {
     return (size_t)norm_partials(e, count) * sizeof(double);
 }
 
-hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype gt, float *norm,
-                            void *workspace, hipStream_t s) {
+// The sums of squares of chunks of the list; `done` of them.
+hipError_t launch_squares(const nf4_adamw_entry *e, int32_t count, nf4_dtype gt, void *workspace, int64_t &done,
+                          hipStream_t s) {
     double *partial = static_cast<double *>(workspace);
     NormBatch b{};
     int used = 0;
-    int64_t wgs = 0, done = 0;
+    int64_t wgs = 0;
+    done = 0;
     hipError_t err = hipSuccess;
     auto flush = [&] {
         if (used == 0) return;
@@ -587,17 +602,6 @@ hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype g
         if (err == hipSuccess) err = r;
         done += wgs, used = 0, wgs = 0;
     };
-    // One launch less, but one workgroup's bandwidth: 4.8 us instead of 8.1 for two
-    // tensors of 1000 elements (bf16), 7.0 and 7.1 for two of 65536, 11.2 and 7.0 for
-    // two of 131072.
-    const Extent x = extent_of(e, count);
-    if (x.elements <= kSmallNorm && x.live <= kSmallEntries) {
-        for (int32_t i = 0; i < count; ++i)
-            if (e[i].n > 0) b.item[used++] = NormItem{e[i].grad, e[i].n, 0u, 0u};
-        if (gt == NF4_BF16) grad_norm_small_kernel<Bf16><<<dim3(1), dim3(1024), 0, s>>>(b, used, norm);
-        else grad_norm_small_kernel<float><<<dim3(1), dim3(1024), 0, s>>>(b, used, norm);
-        return hipGetLastError();
-    }
     constexpr int64_t kMaxWgs = (int64_t(1) << 31) / kThreads;
     for (int32_t i = 0; i < count; ++i) {
         if (e[i].n == 0) continue;
@@ -608,7 +612,27 @@ hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype g
         ++used;
     }
     flush();
-    grad_norm_kernel<<<dim3(1), dim3(1024), 0, s>>>(partial, done, norm);
+    return err;
+}
+
+hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype gt, float *norm,
+                            void *workspace, hipStream_t s) {
+    // One launch less, but one workgroup's bandwidth: 4.8 us instead of 8.1 for two
+    // tensors of 1000 elements (bf16), 7.0 and 7.1 for two of 65536, 11.2 and 7.0 for
+    // two of 131072.
+    const Extent x = extent_of(e, count);
+    if (x.elements <= kSmallNorm && x.live <= kSmallEntries) {
+        NormBatch b{};
+        int used = 0;
+        for (int32_t i = 0; i < count; ++i)
+            if (e[i].n > 0) b.item[used++] = NormItem{e[i].grad, e[i].n, 0u, 0u};
+        if (gt == NF4_BF16) grad_norm_small_kernel<Bf16><<<dim3(1), dim3(1024), 0, s>>>(b, used, norm);
+        else grad_norm_small_kernel<float><<<dim3(1), dim3(1024), 0, s>>>(b, used, norm);
+        return hipGetLastError();
+    }
+    int64_t parts;
+    const hipError_t err = launch_squares(e, count, gt, workspace, parts, s);
+    grad_norm_kernel<<<dim3(1), dim3(1024), 0, s>>>(static_cast<const double *>(workspace), parts, norm);
     const hipError_t r = hipGetLastError();
     return err == hipSuccess ? r : err;
 }
@@ -616,24 +640,34 @@ hipError_t launch_grad_norm(const nf4_adamw_entry *e, int32_t count, nf4_dtype g
 hipError_t launch_adamw(const nf4_adamw_entry *e, int32_t count, nf4_dtype wt, nf4_dtype gt,
                         bool eight, const nf4_adamw_config &c, float *norm, bool own_norm, void *workspace,
                         hipStream_t s) {
-    bool own = false;
+    ListKind list = kInArgs;
+    int64_t parts = 0;
     if (own_norm) {
         const Extent x = extent_of(e, count);
-        // Every workgroup reads all gradients, but there is one launch: 7.4 us instead
-        // of 10.8 for two tensors of 8192 elements (bf16, 8-bit moments), 11.2 instead of
-        // 14.0 for 14 of them, 10.4 instead of 11.3 for two of 65536; 16.5 against 13.6
-        // for two of 131072.
-        own = x.live > 0 && x.elements <= kSmallNorm && x.live <= kSmallEntries && (x.masters == 0 || x.masters == x.live);
-        if (!own) {
-            const hipError_t r = launch_grad_norm(e, count, gt, norm, workspace, s);
+        if (x.live > 0 && x.elements <= kSmallNorm && x.live <= kSmallEntries && (x.masters == 0 || x.masters == x.live)) {
+            // Every workgroup reads all gradients, but there is one launch: 7.4 us
+            // instead of 10.8 for two tensors of 8192 elements (bf16, 8-bit moments),
+            // 11.2 instead of 14.0 for 14 of them, 10.4 instead of 11.3 for two of
+            // 65536; 16.5 against 13.6 for two of 131072.
+            list = kOwnNorm;
+        } else if (x.live > 0 && x.elements <= kMidNorm && x.live <= kBatch) {
+            // One launch less, and a read of up to 560 partial sums in every workgroup:
+            // 11.9 us instead of 15.2 for two tensors of 131072, 15.8 instead of 17.4 for
+            // two of 2097152, 25.0 and 25.3 for two of 4194304; 50.3 against 48.4 for 40
+            // of 524288.
+            list = kPartNorm;
+        }
+        if (list != kOwnNorm) {
+            const hipError_t r = list == kPartNorm ? launch_squares(e, count, gt, workspace, parts, s)
+                                                   : launch_grad_norm(e, count, gt, norm, workspace, s);
             if (r != hipSuccess) return r;
         }
     }
     if (wt == NF4_BF16)
-        return gt == NF4_BF16 ? adamw_typed<Bf16, Bf16>(e, count, eight, c, norm, own, workspace, s)
-                              : adamw_typed<Bf16, float>(e, count, eight, c, norm, own, workspace, s);
-    return gt == NF4_BF16 ? adamw_typed<float, Bf16>(e, count, eight, c, norm, own, workspace, s)
-                          : adamw_typed<float, float>(e, count, eight, c, norm, own, workspace, s);
+        return gt == NF4_BF16 ? adamw_typed<Bf16, Bf16>(e, count, eight, c, norm, list, parts, workspace, s)
+                              : adamw_typed<Bf16, float>(e, count, eight, c, norm, list, parts, workspace, s);
+    return gt == NF4_BF16 ? adamw_typed<float, Bf16>(e, count, eight, c, norm, list, parts, workspace, s)
+                          : adamw_typed<float, float>(e, count, eight, c, norm, list, parts, workspace, s);
 }
 
 }  // namespace nf4

@@ -388,7 +388,8 @@ def test_parameters_with_new_memory(dev):
 
 @pytest.mark.parametrize("bits,wt,gt", [(8, "bfloat16", "bfloat16"), (8, "float32", "float32"),
                                         (32, "bfloat16", "float32"), (32, "float32", "bfloat16")])
-@pytest.mark.parametrize("case", ["one", "ragged", "sixteen", "seventeen", "large", "masters", "some masters", "empty"])
+@pytest.mark.parametrize("case", ["one", "ragged", "sixteen", "seventeen", "large", "masters", "some masters", "empty", "chunks", "chunks of 48",
+                                  "chunks of 49", "chunks masters", "chunks some masters"])
 def test_clip_step_is_norm_then_step(dev, bits, wt, gt, case):
     """One call against the two that it stands for, bit for bit. The gradients are
     small multiples of 2^-6, so their squares add up without rounding in any order
@@ -399,7 +400,9 @@ def test_clip_step_is_norm_then_step(dev, bits, wt, gt, case):
     from nf4_quantize_amd import training
 
     sizes = {"one": [1], "ragged": [7, 513, 2049, 1, 8191], "sixteen": [1030] * 16, "seventeen": [1030] * 17,
-             "large": [131072, 9], "masters": [700, 3000], "some masters": [700, 3000, 5], "empty": [0, 600, 0]}[case]
+             "large": [131072, 9], "masters": [700, 3000], "some masters": [700, 3000, 5], "empty": [0, 600, 0],
+             "chunks": [200_001, 7, 16384, 16385], "chunks of 48": [5000] * 48, "chunks of 49": [5000] * 49,
+             "chunks masters": [140_000, 3], "chunks some masters": [140_000, 3000, 5]}[case]
     master = case.endswith("masters")
     if master and wt != "bfloat16":
         pytest.skip("masters are of bfloat16 weights")
@@ -410,7 +413,7 @@ def test_clip_step_is_norm_then_step(dev, bits, wt, gt, case):
     got = []
     for one_call in (True, False):
         ps = [s.clone().to(getattr(torch, wt)) for s in start]
-        ms = [s.clone() if master and not (case == "some masters" and i == 1) else None for i, s in enumerate(start)]
+        ms = [s.clone() if master and not ("some" in case and i == 1) else None for i, s in enumerate(start)]
         opt = nq.NF4AdamW(ps, lr=1e-2, state_bits=bits, masters=ms if master else None, max_grad_norm=0.25, seed=3)
         for number in (1, 2):
             if one_call:
