@@ -298,15 +298,16 @@ __global__ __launch_bounds__(kPass / N) void adamw_kernel(AdamwBatch b, AdamwSca
     W *w = static_cast<W *>(e.w) + i;
     const G *g = static_cast<const G *>(e.g) + i;
     float x[N], gr[N], m[N], v[N];
-    if (live >= N) {  // the loads first, all in flight and in this order (the weight before the codes: 4% more)
+    if (live >= N) {  // the loads first, all in flight, in this order (the weight before the codes: 4% more)
         const auto weight = [&] {
             if constexpr (kMaster) return stream_each<N>(e.master + i);
             else return stream_each<N>(w);
         };
         const auto rg = load_each<N>(g);
         if constexpr (kEight) {
-            const Code mq = __builtin_nontemporal_load(reinterpret_cast<const Code *>(static_cast<const uint8_t *>(e.m) + i));
-            const Code vq = __builtin_nontemporal_load(reinterpret_cast<const Code *>(static_cast<const uint8_t *>(e.v) + i));
+            const uint8_t *pm = static_cast<const uint8_t *>(e.m) + i, *pv = static_cast<const uint8_t *>(e.v) + i;
+            const Code mq = __builtin_nontemporal_load(reinterpret_cast<const Code *>(pm));
+            const Code vq = __builtin_nontemporal_load(reinterpret_cast<const Code *>(pv));
             const float ms = e.ms[i / kMomentBlock], vs = e.vs[i / kMomentBlock];
             const auto rx = weight();
             __builtin_amdgcn_sched_barrier(0);
@@ -644,7 +645,8 @@ hipError_t launch_adamw(const nf4_adamw_entry *e, int32_t count, nf4_dtype wt, n
     int64_t parts = 0;
     if (own_norm) {
         const Extent x = extent_of(e, count);
-        if (x.live > 0 && x.elements <= kSmallNorm && x.live <= kSmallEntries && (x.masters == 0 || x.masters == x.live)) {
+        const bool one_kind = x.masters == 0 || x.masters == x.live;
+        if (x.live > 0 && x.elements <= kSmallNorm && x.live <= kSmallEntries && one_kind) {
             // Every workgroup reads all gradients, but there is one launch: 7.4 us
             // instead of 10.8 for two tensors of 8192 elements (bf16, 8-bit moments),
             // 11.2 instead of 14.0 for 14 of them, 10.4 instead of 11.3 for two of

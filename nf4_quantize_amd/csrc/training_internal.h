@@ -230,10 +230,12 @@ struct Fours {
           from_hi(hi < dim ? hi : dim - 4), live_lo(lo < dim), live_hi(hi < dim) {}
 };
 __device__ __forceinline__ Raw8<float> load_cols(const float *row, const Fours &c) {
-    return {*reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_lo), *reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_hi)};
+    return {*reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_lo),
+            *reinterpret_cast<const f32x4 *>(row + (uint32_t)c.from_hi)};
 }
 __device__ __forceinline__ Raw8<Bf16> load_cols(const Bf16 *row, const Fours &c) {
-    const u32x2 a = *reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_lo), b = *reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_hi);
+    const u32x2 a = *reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_lo);
+    const u32x2 b = *reinterpret_cast<const u32x2 *>(row + (uint32_t)c.from_hi);
     return {u32x4{a[0], a[1], b[0], b[1]}};
 }
 __device__ __forceinline__ Raw8<float> load_stream(const float *row, const Fours &c) {
@@ -256,7 +258,8 @@ __device__ __forceinline__ void store_cols(float *row, const Fours &c, const flo
     if (c.live_hi) *reinterpret_cast<f32x4 *>(row + c.hi) = f32x4{x[4], x[5], x[6], x[7]};
 }
 __device__ __forceinline__ void store_cols(Bf16 *row, const Fours &c, const float (&x)[8]) {
-    const u32x2 a = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, b = {pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+    const u32x2 a = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+    const u32x2 b = {pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
     if (c.live_lo) *reinterpret_cast<u32x2 *>(row + c.lo) = a;
     if (c.live_hi) *reinterpret_cast<u32x2 *>(row + c.hi) = b;
 }
@@ -265,7 +268,8 @@ __device__ __forceinline__ void stream_cols(float *row, const Fours &c, const fl
     if (c.live_hi) __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4 *>(row + c.hi));
 }
 __device__ __forceinline__ void stream_cols(Bf16 *row, const Fours &c, const float (&x)[8]) {
-    const u32x2 a = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, b = {pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+    const u32x2 a = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+    const u32x2 b = {pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
     if (c.live_lo) __builtin_nontemporal_store(a, reinterpret_cast<u32x2 *>(row + c.lo));
     if (c.live_hi) __builtin_nontemporal_store(b, reinterpret_cast<u32x2 *>(row + c.hi));
 }
