@@ -532,7 +532,8 @@ __global__ __launch_bounds__(kThreads) void few_tokens_kernel(FewParams p) {
     if ((int)blockIdx.x >= p.wgs) {
         // a row is a wave's, or the workgroup's where it is longer than a wave's store
         const bool wide = p.dim > 512;
-        const int each = wide ? 1 : kThreads / 64, step = wide ? kThreads * 8 : 512;
+        constexpr int kEach = 16 / sizeof(G);
+        const int each = wide ? 1 : kThreads / 64, step = (wide ? kThreads : 64) * kEach;
         const int64_t stride = (int64_t)(gridDim.x - p.wgs) * each;
         for (int64_t row = (int64_t)(blockIdx.x - p.wgs) * each + (wide ? 0 : wave); row < p.vocab; row += stride) {
             bool named = false;
@@ -540,8 +541,11 @@ __global__ __launch_bounds__(kThreads) void few_tokens_kernel(FewParams p) {
             for (int k = 0; k < kFewTokens / 64; ++k) named |= key[k] == (uint32_t)row;
             if (__any(named)) continue;
             G *dst = static_cast<G *>(p.grad) + row * p.dim;
-            for (int c = (wide ? (int)threadIdx.x : lane) * 8; c < p.dim; c += step)
-                store_cols(dst, Cols<kNarrow>(c, p.dim), acc);
+            for (int c = (wide ? (int)threadIdx.x : lane) * kEach; c < p.dim; c += step) {
+                if (c + kEach <= p.dim) reinterpret_cast<u32x4_any2 *>(dst + c)->v = u32x4{0, 0, 0, 0};
+                else
+                    for (int j = c; j < p.dim; ++j) store1(dst + j, 0.0f);
+            }
         }
         return;
     }
