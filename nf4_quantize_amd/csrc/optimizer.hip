@@ -128,6 +128,13 @@ __device__ __forceinline__ float storage_scale(float amax, float *inv) {
     return s;
 }
 
+// v_sqrt_f32 takes subnormal numbers for zero, and second moments get there under
+// gradients of 1e-18: those are scaled by 2^48, and their root by 2^-24, both exact.
+__device__ __forceinline__ float root(float x) {
+    const bool small = x < 0x1p-126f;
+    return __builtin_amdgcn_sqrtf(x * (small ? 0x1p48f : 1.0f)) * (small ? 0x1p-24f : 1.0f);
+}
+
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
@@ -349,7 +356,7 @@ __global__ __launch_bounds__(kPass / N) void adamw_kernel(AdamwBatch b, AdamwSca
         v[j] = c.beta2 * v[j] + c.one_beta2 * (gj * gj);
         // the hardware's reciprocal and root are within 1 ulp: the step is
         // a small part of the weight it is added to
-        const float d = __builtin_amdgcn_sqrtf(v[j] * c.rbias2) + c.eps;
+        const float d = root(v[j] * c.rbias2) + c.eps;
         x[j] = fmaf(-e.step * m[j], __builtin_amdgcn_rcpf(d), x[j] * e.keep);
         ma = fmaxf(ma, fabsf(m[j])), va = fmaxf(va, v[j]);
     }
