@@ -427,12 +427,13 @@ nf4_status nf4_dequantize_ex(const uint8_t *codes, int64_t n, const nf4_format *
  * NF4_MOMENTS_8 keeps each moment as OCP FP8 E4M3FN codes and one fp32 scale
  * per block of 256 consecutive elements of a tensor (the last block may be
  * partial): x = decode(code) * scale. Storing x[block]:
- *   scale = fl32(max |x| * fl32(1 / 448)), 0 where that is below 2^-126
+ *   scale = fl32(max |x| * fl32(1 / 448)); where that is below 2^-126: 0, but 2^-126
+ *           for v where the block's scale of m is not 0
  *   t     = fl32(x * fl32(1 / scale)), 0 where the scale is 0, clamped to
  *           [-448, 448], for v to [2^-9, 448]
  *   code  = t rounded stochastically to E4M3: up in magnitude with the
  *           probability that the dropped fraction of the step has (20 bits)
- * A second moment therefore never falls to zero under a first moment that is
+ * A second moment is therefore stored as 2^-135 or more under a first moment that is
  * still stored, and neither moment stalls where a step changes it by less than
  * half a code. The random bits of element i of entry e of a call are
  *   mix(u32(i) * 0x9E3779B9 + key_e),  key_e = mix(mix(e * 0x9E3779B9 + (seed >> 32)) + u32(seed)),

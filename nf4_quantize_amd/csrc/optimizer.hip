@@ -120,10 +120,11 @@ __device__ __forceinline__ void unpack_e4m3(uint32_t c, float scale, float *x) {
 
 __device__ __forceinline__ float decode_e4m3(uint8_t c) { return __builtin_amdgcn_cvt_f32_fp8((int)c, 0); }
 
-// Scale of a block's storage and its reciprocal.
-__device__ __forceinline__ float storage_scale(float amax, float *inv) {
+// Scale of a block's storage and its reciprocal. `least`: the scale of blocks that
+// are too small for their own.
+__device__ __forceinline__ float storage_scale(float amax, float least, float *inv) {
     float s = amax * (1.0f / kE4m3Max);
-    s = s < kScaleMin ? 0.0f : s;
+    s = s < kScaleMin ? least : s;
     *inv = s > 0.0f ? 1.0f / s : 0.0f;
     return s;
 }
@@ -377,8 +378,8 @@ __global__ __launch_bounds__(kPass / N) void adamw_kernel(AdamwBatch b, AdamwSca
         }
     } else {
         float rm, rv;
-        const float ms = storage_scale(group_max<kBlockLanes>(ma), &rm);
-        const float vs = storage_scale(group_max<kBlockLanes>(va), &rv);
+        const float ms = storage_scale(group_max<kBlockLanes>(ma), 0.0f, &rm);
+        const float vs = storage_scale(group_max<kBlockLanes>(va), ms > 0.0f ? kScaleMin : 0.0f, &rv);
         uint32_t rndm[N], rndv[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {

@@ -41,3 +41,45 @@ def test_root_of_small_second_moments(dev, eps):
     tol = 2 * U * 0.26 + np.abs(step) * (24 * U + 2.0 ** -149 / v1)
     got = p.cpu().numpy().astype(np.float64)
     assert np.all(np.abs(got - (0.25 - step)) <= tol), float(np.max(np.abs(got - (0.25 - step)) / tol))
+
+
+@pytest.mark.parametrize("size", [1e-17, 1e-19, 3e-20])
+def test_second_moment_is_stored_under_a_stored_first_one(dev, size):
+    """Blocks whose second moment over 448 is below 2^-126 keep a scale as long as the
+    first moment has one: no decoded v is zero (the smallest code on the smallest scale is
+    2^-135), and without eps the steps after the last gradient are those of the stored
+    moments: 24 U and, as v may be among the subnormals, 2^-149 / v."""
+    import torch
+
+    n, lr = 600, 1e-3
+
+    def moment(opt, name):
+        return opt_values(getattr(opt, name)[0], getattr(opt, name + "_scale")[0], n)
+
+    p = torch.zeros(n, device=dev)
+    opt = nq.NF4AdamW([p], lr=lr, weight_decay=0.0, eps=0.0, state_bits=8)
+    g = torch.full((n,), size, device=dev)
+    g[256:512] = 0
+    g[256:512:7] = size  # elements without a gradient beside some with one
+    opt.step([g.clone().masked_fill_(g == 0, size)])
+    for t in range(2, 40):
+        m, v = moment(opt, "m"), moment(opt, "v")
+        assert bool((opt.m_scale[0] > 0).all()) and float(v.min()) >= 2.0 ** -135, t
+        was = p.double()
+        grad = g if t < 4 else torch.zeros_like(g)
+        opt.step([grad])
+        d = grad.double()
+        m, v = 0.9 * m + 0.1 * d, 0.999 * v + 0.001 * d * d
+        step = lr / (1 - 0.9 ** t) * m / (v / (1 - 0.999 ** t)).sqrt()
+        tol = 2 * U * (was.abs() + step.abs()) + step.abs() * (24 * U + 2.0 ** -148 / v)
+        err = (p.double() - (was - step)).abs()
+        assert bool((err <= tol).all()), (t, float((err / tol).max()))
+        assert float(step.abs().max()) <= 2 * lr, t
+    opt = nq.NF4AdamW([torch.zeros(300, device=dev)], state_bits=8)
+    opt.step([torch.zeros(300, device=dev)])
+    assert not bool(opt.v_scale[0].any()) and not bool(opt.m_scale[0].any())  # nothing to store
+
+
+def opt_values(codes, scale, n):
+    """Decoded 8-bit moments."""
+    return codes.double() * scale.double().repeat_interleave(256)[:n]
