@@ -83,6 +83,14 @@ def _stream(index):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _changed(ts):
+    """Tells autograd that these tensors were written: a graph that saved one of them
+    refuses to run backward from then on."""
+    import torch
+
+    torch.autograd.graph.increment_version(ts)
+
+
 _CODES = {}
 
 
@@ -156,6 +164,7 @@ class NF4AdamW:
         self.betas, self.eps, self.state_bits = (float(betas[0]), float(betas[1])), float(eps), state_bits
         self.max_grad_norm, self.seed, self.steps = float(max_grad_norm), int(seed), 0
         self.grad_norm = torch.zeros(1, dtype=torch.float32, device=self.device)
+        self._written = self._weights + [self.grad_norm]
         e = self._entries
         e["n"] = self._numels
         L = _nq.lib()
@@ -267,6 +276,7 @@ class NF4AdamW:
                       else (L.nf4_adamw_step, None))
         _nq._check(call(self._at, len(grads), _code(self.dtype), grad_dtype, self.state_bits, ctypes.byref(config), norm,
                         self._workspace.data_ptr(), self._workspace.numel(), stream), call.__name__)
+        _changed(self._written)
         self.steps = number
 
     def state_dict(self):

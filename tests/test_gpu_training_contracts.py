@@ -83,3 +83,24 @@ def test_second_moment_is_stored_under_a_stored_first_one(dev, size):
 def opt_values(codes, scale, n):
     """Decoded 8-bit moments."""
     return codes.double() * scale.double().repeat_interleave(256)[:n]
+
+
+# ------------------------------------------------------------------ autograd
+
+@pytest.mark.parametrize("master", [False, True])
+def test_backward_after_a_step_raises(dev, master):
+    """A graph that saved a weight is stale once the step has changed it: autograd
+    notices, as after any update in place."""
+    import torch
+
+    w = torch.nn.Parameter(torch.randn(64, 16, device=dev).to(torch.bfloat16))
+    x = torch.randn(8, 64, device=dev).to(torch.bfloat16).requires_grad_()
+    opt = nq.NF4AdamW([w], masters=[w.detach().float()] if master else None, max_grad_norm=1.0)
+    versions = [t._version for t in [w, opt.grad_norm] + ([opt.masters[0]] if master else [])]
+    y = x @ w
+    opt.step([torch.ones_like(w)])
+    assert all(t._version > v for t, v in zip([w, opt.grad_norm] + ([opt.masters[0]] if master else []), versions))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    (x @ w).sum().backward()  # and a new one is fine
+    opt.step()
