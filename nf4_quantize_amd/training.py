@@ -343,6 +343,7 @@ def residual_norm_forward(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e
     index = _check_tensors(h, y, w_pre, w_post, gate, h_out, x_out)
     shape = _norm_shape(y, h, w_pre, w_post, gate, alpha, eps, w_offset)
     act = h if y is None else y
+    given = [t for t in (None if y is None else h_out, x_out) if t is not None]
     for t, like in ((h_out, h), (x_out, act)):
         if t is not None and (t.shape != like.shape or t.dtype != like.dtype):
             raise ValueError("outputs have the shape and dtype of h and y")
@@ -357,6 +358,8 @@ def residual_norm_forward(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e
                                              w_pre.data_ptr(), _addr(h_out), x_out.data_ptr(), _addr(rstd_post),
                                              rstd_pre.data_ptr(), _stream(index))
     _nq._check(st, "nf4_residual_norm_forward")
+    if given:
+        _changed(given)
     return (h if y is None else h_out), x_out, rstd_pre, rstd_post
 
 
@@ -421,7 +424,8 @@ def embedding_forward(ids, table, scale=1.0, out_dtype=None, out=None):
     if ids.get_device() < 0:
         raise ValueError("tensors must be contiguous device tensors")
     vocab, dim = table.shape
-    if out is None:
+    given = out is not None
+    if not given:
         out_dtype = out_dtype or (torch.bfloat16 if packed else table.dtype)
         out = torch.empty((*ids.shape, dim), dtype=out_dtype, device=ids.device)
     elif out.shape != (*ids.shape, dim) or (out_dtype is not None and out.dtype != out_dtype):
@@ -436,6 +440,8 @@ def embedding_forward(ids, table, scale=1.0, out_dtype=None, out=None):
         st = L.nf4_embedding_forward(ids.data_ptr(), code, count, table.data_ptr(), _code(table.dtype), vocab, dim, scale,
                                      out.data_ptr(), od, stream)
     _nq._check(st, "nf4_embedding_forward")
+    if given:
+        _changed(out)
     return out
 
 
@@ -467,6 +473,8 @@ def embedding_backward(ids, dy, vocab, scale=1.0, padding_id=None, grad=None, gr
                                   -1 if padding_id is None else int(padding_id), grad.data_ptr(), _code(grad.dtype),
                                   1 if accumulate else 0, workspace.data_ptr(), size, _stream(index))
     _nq._check(st, "nf4_embedding_backward")
+    if accumulate:
+        _changed(grad)
     return grad
 
 

@@ -104,3 +104,31 @@ def test_backward_after_a_step_raises(dev, master):
         y.sum().backward()
     (x @ w).sum().backward()  # and a new one is fine
     opt.step()
+
+
+def test_backward_after_outputs_in_place_raises(dev):
+    """The same for outputs that the caller gives: the residual stream updated in
+    place, rows and gradients written into existing tensors."""
+    import torch
+
+    w = torch.ones(96, device=dev)
+    ids = torch.tensor([1, 3, 1], device=dev)
+    table = torch.randn(5, 96, device=dev)
+
+    def in_place(call, out):
+        p = torch.ones_like(out, requires_grad=True)
+        y = p * out  # saves out
+        call(out)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+
+    y, h = torch.randn(3, 96, device=dev), torch.randn(3, 96, device=dev)
+    in_place(lambda t: nq.residual_norm_forward(y, t, w, h_out=t), h.clone())
+    in_place(lambda t: nq.residual_norm_forward(y, h, w, x_out=t), h.clone())
+    in_place(lambda t: nq.embedding_forward(ids, table, out=t), h.clone())
+    in_place(lambda t: nq.embedding_backward(ids, y, 5, grad=t), table.clone())
+    with torch.inference_mode():  # tensors without a version
+        t = h.clone()
+        nq.residual_norm_forward(y, t, w, h_out=t, x_out=torch.empty_like(t))
+        nq.embedding_forward(ids, table, out=t)
+        nq.embedding_backward(ids, y, 5, grad=table.clone())
