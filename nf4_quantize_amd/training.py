@@ -490,6 +490,7 @@ def _functions():
     if _FUNCTIONS is not None:
         return _FUNCTIONS
     import torch
+    from torch.autograd.function import once_differentiable
 
     class ResidualNormFunction(torch.autograd.Function):
         @staticmethod
@@ -504,6 +505,7 @@ def _functions():
             return (h_out if y is not None else h.view_as(h)), x
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, dh_out, dx):
             y, h_out, rstd_pre, w_pre, rstd_post, w_post, gate = ctx.saved_tensors
             act = h_out if y is None else y
@@ -524,6 +526,7 @@ def _functions():
             return embedding_forward(ids, table.contiguous(), scale, out_dtype)
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, dy):
             grad = embedding_backward(ctx.saved_tensors[0], dy.contiguous(), ctx.vocab, ctx.scale, ctx.padding_id,
                                       grad_dtype=ctx.dtype)

@@ -132,3 +132,21 @@ def test_backward_after_outputs_in_place_raises(dev):
         nq.residual_norm_forward(y, t, w, h_out=t, x_out=torch.empty_like(t))
         nq.embedding_forward(ids, table, out=t)
         nq.embedding_backward(ids, y, 5, grad=table.clone())
+
+
+def test_second_derivatives_are_refused(dev):
+    """The backward passes are kernels without a derivative of their own: asking for
+    second derivatives raises instead of leaving terms out."""
+    import torch
+
+    def refused(out, t):
+        g, = torch.autograd.grad(out.square().sum(), t, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (g.square().sum() + t.square().sum()).backward()
+
+    y, h = (torch.randn(3, 40, device=dev, requires_grad=True) for _ in range(2))
+    w = torch.rand(40, device=dev) + 0.5
+    refused(nq.residual_norm(y, h, w)[1], y)
+    refused(nq.residual_norm(None, h, w)[1], h)
+    table = torch.randn(7, 40, device=dev, requires_grad=True)
+    refused(nq.nf4_embedding(torch.tensor([2, 2, 6], device=dev), table), table)
