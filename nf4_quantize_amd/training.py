@@ -106,6 +106,27 @@ def _code(dtype):
 
 # ------------------------------------------------------------------ AdamW
 
+class _BoundList(list):
+    """The tensors whose addresses a step takes: other moments come in through
+    bind_state, other weights through a parameter's ``data``."""
+
+    def _refuse(self, *args, **kwargs):
+        raise TypeError("a step writes at these tensors' addresses: bind_state gives it other moments, a parameter's "
+                        "data another weight")
+
+    __setitem__ = __delitem__ = __iadd__ = __imul__ = _refuse
+    append = extend = insert = pop = remove = clear = sort = reverse = _refuse
+
+
+def _moment(name):
+    def tensors(self):
+        if name not in self._moments:
+            raise AttributeError(f"32-bit moments have no {name}")
+        return self._moments[name]
+
+    return property(tensors)
+
+
 class NF4AdamW:
     """AdamW over a list of device tensors in a few launches, with the moments in
     8 bits (E4M3 codes with one fp32 scale per 256 elements, rounded
@@ -120,8 +141,11 @@ class NF4AdamW:
     step takes the next ones.
 
     ``m``, ``v`` (and ``m_scale``, ``v_scale``) are the lists of the tensors'
-    moments in the order of the parameters, ``grad_norm`` the last norm (a device
-    tensor of one float)."""
+    moments in the order of the parameters; they are read only like ``params`` and
+    ``masters``, and ``bind_state`` replaces them. ``grad_norm`` is the last norm (a
+    device tensor of one float)."""
+
+    m, v, m_scale, v_scale = (_moment(name) for name in ("m", "v", "m_scale", "v_scale"))
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=8,
                  max_grad_norm=0.0, seed=0, masters=None):
@@ -137,7 +161,7 @@ class NF4AdamW:
         elif masters is not None:
             raise ValueError("masters belong to the groups")
         self.groups = []
-        self.params, self.masters, self._master_rounds = [], [], []
+        self.params, self.masters = [], []
         for g in params:
             ps = list(g["params"])
             ms = g.get("masters")
@@ -152,6 +176,7 @@ class NF4AdamW:
             self.masters += ms
         if not self.params:
             raise ValueError("no parameters")
+        self.params, self.masters = _BoundList(self.params), _BoundList(self.masters)
         self.dtype, self.device = self.params[0].dtype, self.params[0].device
         _nq._dtype_code(self.dtype)
         self._tensor = torch.Tensor
@@ -211,7 +236,10 @@ class NF4AdamW:
                 _check_tensors(self.params[0], t)
                 if t.dtype != want or t.numel() != (-(-n // MOMENT_BLOCK) if scale else n):
                     raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} for a parameter of {n} elements")
-            setattr(self, name, ts)
+        # held as well, so that their memory stays where a tensor of the list gets other data
+        self._held_state = [t.detach() for ts in lists.values() for t in ts]
+        self._moments = {name: _BoundList(ts) for name, ts in lists.items()}
+        for name, ts in lists.items():
             self._entries[name] = [t.data_ptr() for t in ts]
 
     def zero_grad(self, set_to_none=True):

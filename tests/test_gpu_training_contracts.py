@@ -150,3 +150,51 @@ def test_second_derivatives_are_refused(dev):
     refused(nq.residual_norm(None, h, w)[1], h)
     table = torch.randn(7, 40, device=dev, requires_grad=True)
     refused(nq.nf4_embedding(torch.tensor([2, 2, 6], device=dev), table), table)
+
+
+# ------------------------------------------------------------------ the optimizer's tensors
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_moments_are_replaced_by_bind_state_alone(dev, bits):
+    """The step writes at the addresses that bind_state took, so the lists refuse
+    other tensors; the memory stays the optimizer's for as long as it uses it."""
+    import torch
+
+    opt = nq.NF4AdamW([torch.zeros(300, device=dev), torch.zeros(20, device=dev)], state_bits=bits)
+    for name in ("m", "v") + (("m_scale", "v_scale") if bits == 8 else ()):
+        ts = getattr(opt, name)
+        assert len(ts) == 2 and isinstance(ts, list)
+        with pytest.raises(AttributeError):
+            setattr(opt, name, [t.clone() for t in ts])
+
+        def item():
+            ts[0] = ts[0].clone()
+
+        def part():
+            ts[:] = [t.clone() for t in ts]
+
+        def more():
+            nonlocal ts
+            ts += [ts[0].clone()]
+
+        def gone():
+            del ts[1]
+
+        for change in (item, part, more, gone, ts.clear, ts.reverse, ts.pop, lambda: ts.append(ts[0]),
+                       lambda: ts.extend(ts), lambda: ts.insert(0, ts[0]), lambda: ts.remove(ts[0]), lambda: ts.sort(key=id)):
+            with pytest.raises(TypeError, match="bind_state"):
+                change()
+        assert len(getattr(opt, name)) == 2
+    for ts in (opt.params, opt.masters):
+        with pytest.raises(TypeError, match="data"):
+            ts[0] = torch.zeros(300, device=dev)
+    held = {t.untyped_storage().data_ptr() for t in opt._held_state}
+    assert {t.untyped_storage().data_ptr() for t in opt.m + opt.v} <= held
+    fresh = [[torch.zeros_like(t) for t in getattr(opt, n)] for n in ("m", "v")]
+    scales = [[torch.zeros_like(t) for t in getattr(opt, n)] for n in ("m_scale", "v_scale")] if bits == 8 else []
+    old = [t.view(torch.uint8).clone() for t in opt.m]
+    kept = opt.m
+    opt.bind_state(*fresh, *scales)
+    opt.step([torch.ones(300, device=dev), torch.ones(20, device=dev)])
+    assert all(bool(t.view(torch.uint8).any()) for t in fresh[0]) and opt.m[0] is fresh[0][0]
+    assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(old, kept))
