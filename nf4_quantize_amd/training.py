@@ -285,8 +285,8 @@ class NF4AdamW:
                 or {g.dtype for g in grads} != {dt}):
             raise ValueError(f"gradients: contiguous, of the parameters' sizes, one dtype, on {self.device}; got "
                              + ", ".join(f"{tuple(g.shape)} {g.dtype} {g.device}" for g in grads[:4]) + " ...")
-        if list(map(T.data_ptr, self._weights)) != self._bound:  # a parameter has new memory
-            self._bind()
+        if list(map(T.data_ptr, self._weights)) != self._bound or not all(map(T.is_contiguous, self._weights)):
+            self._bind()  # a weight has new memory, or lies in another order, which this refuses
         grad_dtype = _code(dt)
         e = self._entries
         e["grad"] = array.array("Q", map(T.data_ptr, grads))

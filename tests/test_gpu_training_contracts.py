@@ -198,3 +198,24 @@ def test_moments_are_replaced_by_bind_state_alone(dev, bits):
     opt.step([torch.ones(300, device=dev), torch.ones(20, device=dev)])
     assert all(bool(t.view(torch.uint8).any()) for t in fresh[0]) and opt.m[0] is fresh[0][0]
     assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(old, kept))
+
+
+def test_weights_with_new_strides_are_refused(dev):
+    """A weight that its own memory's transposed view replaces lies at the same
+    address in another order; the step notices before it launches anything."""
+    import torch
+
+    p = torch.nn.Parameter(torch.randn(16, 16, device=dev).to(torch.bfloat16))
+    master = torch.randn(16, 16, device=dev)
+    for what in (p, master):
+        opt = nq.NF4AdamW([p], masters=[master])
+        g = torch.ones(16, 16, device=dev)
+        opt.step([g])
+        was, kept = p.data, [t.detach().clone() for t in (p, master)]
+        what.data = what.data.t()
+        with pytest.raises(ValueError, match="contiguous"):
+            opt.step([g])
+        what.data = what.data.t()
+        assert opt.steps == 1 and all(torch.equal(a, b) for a, b in zip(kept, (p, master)))
+        opt.step([g])
+        assert not torch.equal(was, kept[0])
