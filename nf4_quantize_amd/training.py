@@ -76,6 +76,15 @@ def _check_tensors(first, *ts):
     return index
 
 
+def _check_apart(ts):
+    """No two of the tensors share memory: a launch updates them all at once."""
+    end = 0
+    for at, size in sorted((t.data_ptr(), t.numel() * t.element_size()) for t in ts):
+        if size and at < end:
+            raise ValueError("two of an optimizer's weights, masters and moments share memory")
+        end = max(end, at + size)
+
+
 def _stream(index):
     """The current stream of a device, as _nq._stream without its objects."""
     import torch
@@ -133,7 +142,8 @@ class NF4AdamW:
     stochastically) or in 32, and clipping by the gradients' global norm.
 
     ``params``: tensors, or groups ``dict(params=[...], lr=..., weight_decay=...,
-    masters=[...])``; all have one dtype (bfloat16 or float32). ``masters`` are
+    masters=[...])``; all have one dtype (bfloat16 or float32), and no two share
+    memory. ``masters`` are
     the fp32 weights of bfloat16 parameters: the step updates them and rounds
     them into the parameters (``masters=True``: made here from the parameters).
     ``max_grad_norm`` > 0 clips; the step then changes nothing when the norm is
@@ -185,6 +195,7 @@ class NF4AdamW:
         self._numels = [p.numel() for p in self.params]
         self._weights = self.params + [mw for mw in self.masters if mw is not None]
         self._rates = None
+        self._held_state = []
         self._bind()
         self.betas, self.eps, self.state_bits = (float(betas[0]), float(betas[1])), float(eps), state_bits
         self.max_grad_norm, self.seed, self.steps = float(max_grad_norm), int(seed), 0
@@ -236,6 +247,7 @@ class NF4AdamW:
                 _check_tensors(self.params[0], t)
                 if t.dtype != want or t.numel() != (-(-n // MOMENT_BLOCK) if scale else n):
                     raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} for a parameter of {n} elements")
+        _check_apart(self._weights + [t for ts in lists.values() for t in ts])
         # held as well, so that their memory stays where a tensor of the list gets other data
         self._held_state = [t.detach() for ts in lists.values() for t in ts]
         self._moments = {name: _BoundList(ts) for name, ts in lists.items()}
@@ -261,6 +273,7 @@ class NF4AdamW:
                 raise ValueError("a parameter's size or device has changed")
             if mw is not None and (mw.dtype != torch.float32 or self.dtype != torch.bfloat16 or mw.numel() != n):
                 raise TypeError("a master weight is float32, of a bfloat16 parameter of its size")
+        _check_apart(self._weights + self._held_state)
         self._entries["w"] = [p.data_ptr() for p in self.params]
         self._entries["master"] = [0 if mw is None else mw.data_ptr() for mw in self.masters]
         # held, so that no other memory can have their addresses

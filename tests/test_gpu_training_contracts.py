@@ -219,3 +219,36 @@ def test_weights_with_new_strides_are_refused(dev):
         assert opt.steps == 1 and all(torch.equal(a, b) for a, b in zip(kept, (p, master)))
         opt.step([g])
         assert not torch.equal(was, kept[0])
+
+
+def test_tensors_that_share_memory_are_refused(dev):
+    """Two workgroups may not update the same element: a tensor given twice, a tied
+    weight in two groups, slices that overlap, shared moments. Neighbours in one
+    buffer are fine."""
+    import torch
+
+    flat = torch.zeros(1024, device=dev)
+    p, q = flat[:512], flat[512:]
+    opt = nq.NF4AdamW([p, q, flat[512:512]])
+    for bad in ([p, p], [p, p.view(32, 16)], [dict(params=[p]), dict(params=[q, p])], [p, flat[256:768]], [flat, q]):
+        with pytest.raises(ValueError, match="share"):
+            nq.NF4AdamW(bad)
+    half = [torch.zeros(64, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    master = torch.zeros(64, device=dev)
+    with pytest.raises(ValueError, match="share"):
+        nq.NF4AdamW(half, masters=[master, master])
+    with pytest.raises(ValueError, match="share"):
+        nq.NF4AdamW(half[:1], masters=[master], state_bits=32).bind_state([master], [torch.zeros(64, device=dev)])
+    opt = nq.NF4AdamW([p, q], state_bits=32)
+    m, v = torch.zeros(1024, device=dev), torch.zeros(1024, device=dev)
+    opt.bind_state([m[:512], m[512:]], [v[:512], v[512:]])
+    for ms, vs in (([m[:512], m[:512]], [v[:512], v[512:]]), ([m[:512], m[512:]], [v[:512], m[512:]]),
+                   ([p, m[512:]], [v[:512], v[512:]])):
+        with pytest.raises(ValueError, match="share"):
+            opt.bind_state(ms, vs)
+        assert opt.m[0].data_ptr() == m.data_ptr() and opt.v[1].data_ptr() == v[512:].data_ptr()  # as it was
+    a, b = torch.nn.Parameter(p.clone()), torch.nn.Parameter(q.clone())
+    opt = nq.NF4AdamW([a, b])
+    b.data = a.data
+    with pytest.raises(ValueError, match="share"):
+        opt.step([flat[:512].clone(), flat[:512].clone()])
