@@ -320,6 +320,9 @@ class NF4AdamW:
         _changed(self._written)
         self.steps = number
 
+    def __reduce_ex__(self, protocol):
+        raise TypeError("an NF4AdamW holds its tensors' addresses and is not copied: state_dict carries its state")
+
     def state_dict(self):
         d = dict(steps=self.steps, seed=self.seed, state_bits=self.state_bits,
                  groups=[dict(lr=g["lr"], weight_decay=g["weight_decay"]) for g in self.groups],

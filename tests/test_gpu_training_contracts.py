@@ -252,3 +252,14 @@ def test_tensors_that_share_memory_are_refused(dev):
     b.data = a.data
     with pytest.raises(ValueError, match="share"):
         opt.step([flat[:512].clone(), flat[:512].clone()])
+
+
+def test_copies_are_refused(dev):
+    """A copy would hold the addresses of the first one's tensors; state_dict is what
+    carries a state."""
+    import torch
+
+    opt = nq.NF4AdamW([torch.zeros(64, device=dev)])
+    for copied in (copy.copy, copy.deepcopy, pickle.dumps):
+        with pytest.raises(TypeError, match="state_dict"):
+            copied(opt)
