@@ -347,7 +347,7 @@ class NF4AdamW:
             if x.dtype != y.dtype or x.numel() != y.numel():
                 raise ValueError("the state of another optimizer: sizes")
         for x, y in pairs:
-            x.view(torch.uint8).copy_(y.reshape(x.shape).to(x.device).view(torch.uint8))
+            x.reshape(-1).view(torch.uint8).copy_(y.reshape(-1).to(x.device).view(torch.uint8))
         self.steps, self.seed = int(d["steps"]), int(d["seed"])
         for g, new in zip(self.groups, d["groups"]):
             g.update(lr=float(new["lr"]), weight_decay=float(new["weight_decay"]))

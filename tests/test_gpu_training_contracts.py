@@ -263,3 +263,23 @@ def test_copies_are_refused(dev):
     for copied in (copy.copy, copy.deepcopy, pickle.dumps):
         with pytest.raises(TypeError, match="state_dict"):
             copied(opt)
+
+
+# ------------------------------------------------------------------ the optimizer's state
+
+def test_state_of_a_weight_without_dimensions(dev):
+    """A bfloat16 weight of shape () with a master weight goes through state_dict."""
+    import torch
+
+    def fresh(x):
+        return nq.NF4AdamW([torch.tensor(x, device=dev, dtype=torch.bfloat16), torch.full((3,), x, device=dev, dtype=torch.bfloat16)],
+                           masters=True, lr=0.1)
+
+    g = [torch.tensor(1.0, device=dev), torch.ones(3, device=dev)]
+    a, b = fresh(1.0), fresh(2.0)
+    a.step(g)
+    b.load_state_dict(a.state_dict())
+    a.step(g)
+    b.step(g)
+    for s, t in zip(a.masters + a.params, b.masters + b.params):
+        assert torch.equal(s, t)
