@@ -335,9 +335,10 @@ class NF4AdamW:
     def load_state_dict(self, d):
         import torch
 
-        if d["state_bits"] != self.state_bits or len(d["m"]) != len(self.params) or len(d["groups"]) != len(self.groups):
-            raise ValueError("the state of another optimizer")
         names = ["m", "v"] + (["m_scale", "v_scale"] if self.state_bits == 8 else [])
+        if (d["state_bits"] != self.state_bits or len(d["groups"]) != len(self.groups)
+                or any(len(d[k]) != len(self.params) for k in names + ["masters"])):
+            raise ValueError("the state of another optimizer")
         pairs = [(x, y) for k in names for x, y in zip(getattr(self, k), d[k])]
         for x, y in zip(self.masters, d["masters"]):
             if (x is None) != (y is None):

@@ -283,3 +283,24 @@ def test_state_of_a_weight_without_dimensions(dev):
     b.step(g)
     for s, t in zip(a.masters + a.params, b.masters + b.params):
         assert torch.equal(s, t)
+
+
+def test_states_with_parts_missing_are_refused(dev):
+    """A state that lacks tensors of one of its lists is not loaded in part."""
+    import torch
+
+    opt = nq.NF4AdamW([torch.ones(300, device=dev, dtype=torch.bfloat16), torch.ones(40, device=dev, dtype=torch.bfloat16)],
+                      masters=True)
+    other = nq.NF4AdamW([torch.ones(300, device=dev, dtype=torch.bfloat16), torch.ones(40, device=dev, dtype=torch.bfloat16)],
+                        masters=True)
+    g = [torch.ones(300, device=dev), torch.ones(40, device=dev)]
+    other.step(g)
+    for name in ("m", "v", "m_scale", "v_scale", "masters"):
+        for wrong in (lambda ts: ts[:1], lambda ts: ts + ts[:1]):
+            d = other.state_dict()
+            d[name] = wrong(d[name])
+            with pytest.raises(ValueError, match="another optimizer"):
+                opt.load_state_dict(d)
+    assert opt.steps == 0 and not any(bool(t.view(torch.uint8).any()) for t in opt.m + opt.v)
+    opt.load_state_dict(other.state_dict())
+    assert opt.steps == 1 and bool(opt.m[1].view(torch.uint8).any())
