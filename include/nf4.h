@@ -494,7 +494,8 @@ size_t nf4_adamw_workspace_size(int32_t count);
  *   entries    host array, read during the call only
  *   moments    an nf4_moments
  *   grad_norm  device, one float, or NULL (no clipping; required where
- *              max_norm > 0). Where it is not finite the step changes nothing.
+ *              max_norm > 0). Where it is not finite the step changes nothing; what
+ *              step number the next call has is the caller's choice.
  *   workspace  256-byte aligned, >= nf4_adamw_workspace_size(count) bytes (may be
  *              NULL when that is 0); calls that overlap must not share one
  * Every entry is validated before anything is launched. Buffers of different

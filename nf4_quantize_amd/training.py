@@ -143,12 +143,13 @@ class NF4AdamW:
 
     ``params``: tensors, or groups ``dict(params=[...], lr=..., weight_decay=...,
     masters=[...])``; all have one dtype (bfloat16 or float32), and no two share
-    memory. ``masters`` are
-    the fp32 weights of bfloat16 parameters: the step updates them and rounds
-    them into the parameters (``masters=True``: made here from the parameters).
-    ``max_grad_norm`` > 0 clips; the step then changes nothing when the norm is
-    not finite. ``seed`` starts the random bits of the stochastic rounding; each
-    step takes the next ones.
+    memory. ``masters`` are the fp32 weights of bfloat16 parameters: the step
+    updates them and rounds them into the parameters (``masters=True``: made here
+    from the parameters). ``max_grad_norm`` > 0 clips; a step whose norm is not
+    finite then changes none of these tensors and no moment, but it counts in
+    ``steps``, the step number of the bias corrections, like any other (``step=``
+    gives a call another number). ``seed`` starts the random bits of the stochastic
+    rounding; each step takes the next ones.
 
     ``m``, ``v`` (and ``m_scale``, ``v_scale``) are the lists of the tensors'
     moments in the order of the parameters; they are read only like ``params`` and

@@ -304,3 +304,28 @@ def test_states_with_parts_missing_are_refused(dev):
     assert opt.steps == 0 and not any(bool(t.view(torch.uint8).any()) for t in opt.m + opt.v)
     opt.load_state_dict(other.state_dict())
     assert opt.steps == 1 and bool(opt.m[1].view(torch.uint8).any())
+
+
+def test_step_number_after_a_skipped_step(dev):
+    """A step whose norm is not finite changes no tensor and still counts: the next
+    one is step 2 to the bias corrections, unless the caller gives its own number."""
+    import torch
+
+    def run(bad_first, number):
+        p = torch.zeros(300, device=dev)
+        opt = nq.NF4AdamW([p], lr=0.5, weight_decay=0.0, state_bits=32, max_grad_norm=1e6)
+        if bad_first:
+            opt.step([torch.full((300,), float("inf"), device=dev)])
+            assert opt.steps == 1 and not bool(p.any()) and not bool(opt.m[0].any())
+        opt.step([torch.ones(300, device=dev)], step=number)
+        return p, opt.steps
+
+    skipped, steps = run(True, None)
+    second, _ = run(False, 2)
+    assert steps == 2 and torch.equal(skipped, second)
+    given, steps = run(True, 1)
+    first, _ = run(False, 1)
+    assert steps == 1 and torch.equal(given, first)
+    # (1 - b1) g / (1 - b1^2) over the root of (1 - b2) g^2 / (1 - b2^2), 24 U
+    want = 0.5 * (0.1 / 0.19) / np.sqrt(0.001 / (1 - 0.999 ** 2))
+    assert float((skipped + want).abs().max()) <= 32 * U * want
