@@ -467,6 +467,9 @@ def embedding_forward(ids, table, scale=1.0, out_dtype=None, out=None):
     packed = isinstance(table, _nq.NF4Tensor)
     if len(table.shape) != 2:
         raise ValueError("a table is 2-D [vocab x dim]")
+    if packed and not table.fmt.is_default:
+        raise ValueError("the embedding takes NF4 tables in the default storage format "
+                         "(B1 = 64, B2 = 256, E4M3, no mean offset)")
     if ids.get_device() < 0:
         raise ValueError("tensors must be contiguous device tensors")
     vocab, dim = table.shape

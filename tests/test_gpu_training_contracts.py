@@ -329,3 +329,19 @@ def test_step_number_after_a_skipped_step(dev):
     # (1 - b1) g / (1 - b1^2) over the root of (1 - b2) g^2 / (1 - b2^2), 24 U
     want = 0.5 * (0.1 / 0.19) / np.sqrt(0.001 / (1 - 0.999 ** 2))
     assert float((skipped + want).abs().max()) <= 32 * U * want
+
+
+# ------------------------------------------------------------------ tables and outputs
+
+def test_table_in_another_storage_format(dev):
+    """Refused as a table: the message names the embedding and the format it takes."""
+    import torch
+
+    w = torch.randn(32, 128, device=dev).to(torch.bfloat16)
+    ids = torch.tensor([1, 2], device=dev)
+    for fmt in (nq.NF4Format(blocksize=128), nq.NF4Format(codebook="fp4"), nq.NF4Format(dq_format="e5m2")):
+        t = nq.quantize(w, fmt=fmt)
+        for call in (nq.embedding_forward, nq.nf4_embedding):
+            with pytest.raises(ValueError, match="embedding") as e:
+                call(ids, t)
+            assert "linear" not in str(e.value)
