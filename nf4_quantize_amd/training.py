@@ -381,7 +381,7 @@ def residual_norm_forward(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e
     """h' = h + alpha gate norm(y; w_post), x = norm(h'; w_pre) over the last
     dimension (nf4_residual_norm_forward). ``y`` bfloat16 or float32, ``h`` the
     same or float32; without ``w_post`` y is added as it is; ``y=None``: x =
-    norm(h) and h' = h. ``gate``: one value a channel, or one an element. Returns
+    norm(h) and h' = h, which no other ``h_out`` receives. ``gate``: one value a channel, or one an element. Returns
     (h', x, rstd_pre, rstd_post or None); ``h_out=h`` updates the residual stream
     in place."""
     import torch
@@ -389,6 +389,8 @@ def residual_norm_forward(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e
     index = _check_tensors(h, y, w_pre, w_post, gate, h_out, x_out)
     shape = _norm_shape(y, h, w_pre, w_post, gate, alpha, eps, w_offset)
     act = h if y is None else y
+    if y is None and h_out is not None and h_out.data_ptr() != h.data_ptr():
+        raise ValueError("h_out without y: h' is h, and nothing is written")
     given = [t for t in (None if y is None else h_out, x_out) if t is not None]
     for t, like in ((h_out, h), (x_out, act)):
         if t is not None and (t.shape != like.shape or t.dtype != like.dtype):

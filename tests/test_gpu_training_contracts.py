@@ -345,3 +345,17 @@ def test_table_in_another_storage_format(dev):
             with pytest.raises(ValueError, match="embedding") as e:
                 call(ids, t)
             assert "linear" not in str(e.value)
+
+
+def test_h_out_without_y_is_refused(dev):
+    """Without y the stream stays as it is and nothing would be written to h_out."""
+    import torch
+
+    h = torch.randn(3, 40, device=dev)
+    w = torch.ones(40, device=dev)
+    with pytest.raises(ValueError, match="h_out"):
+        nq.residual_norm_forward(None, h, w, h_out=torch.zeros_like(h))
+    out, x, _, _ = nq.residual_norm_forward(None, h, w, h_out=h)  # the stream itself
+    assert out is h
+    assert nq.residual_norm_forward(None, h, w, h_out=h.view(3, 40))[0] is h
+    assert nq.residual_norm_forward(None, h, w)[0] is h
