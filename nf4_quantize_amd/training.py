@@ -79,7 +79,7 @@ def _check_tensors(first, *ts):
 def _check_apart(ts):
     """No two of the tensors share memory: a launch updates them all at once."""
     end = 0
-    for at, size in sorted((t.data_ptr(), t.numel() * t.element_size()) for t in ts):
+    for at, size in sorted([(t.data_ptr(), t.nbytes) for t in ts]):
         if size and at < end:
             raise ValueError("two of an optimizer's weights, masters and moments share memory")
         end = max(end, at + size)
@@ -93,8 +93,8 @@ def _stream(index):
 
 
 def _changed(ts):
-    """Tells autograd that these tensors were written: a graph that saved one of them
-    refuses to run backward from then on."""
+    """Tells autograd that this tensor, or these, were written: a graph that saved one
+    of them refuses to run backward from then on."""
     import torch
 
     torch.autograd.graph.increment_version(ts)
@@ -274,7 +274,8 @@ class NF4AdamW:
                 raise ValueError("a parameter's size or device has changed")
             if mw is not None and (mw.dtype != torch.float32 or self.dtype != torch.bfloat16 or mw.numel() != n):
                 raise TypeError("a master weight is float32, of a bfloat16 parameter of its size")
-        _check_apart(self._weights + self._held_state)
+        if self._held_state:  # at construction bind_state asks this
+            _check_apart(self._weights + self._held_state)
         self._entries["w"] = [p.data_ptr() for p in self.params]
         self._entries["master"] = [0 if mw is None else mw.data_ptr() for mw in self.masters]
         # held, so that no other memory can have their addresses
