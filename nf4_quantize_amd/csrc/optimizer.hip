@@ -131,7 +131,11 @@ __device__ __forceinline__ float storage_scale(float amax, float least, float *i
 
 // v_sqrt_f32 takes subnormal numbers for zero, and second moments get there under
 // gradients of 1e-18: those are scaled by 2^48, and their root by 2^-24, both exact.
-__device__ __forceinline__ float root(float x) {
+// Such roots are below 2^-63, half of the last place of an eps from 2^-39 on, where
+// kernels without the scaling run: 448 tensors take 280 us in them, 298 in those with
+// it, and 289 where the kernel itself asks eps.
+constexpr float kRootEps = 0x1p-39f;
+__device__ __forceinline__ float root_of_any(float x) {
     const bool small = x < 0x1p-126f;
     return __builtin_amdgcn_sqrtf(x * (small ? 0x1p48f : 1.0f)) * (small ? 0x1p-24f : 1.0f);
 }
@@ -268,39 +272,17 @@ __device__ __forceinline__ Code encode_each(const float (&x)[N], const uint32_t 
 template <typename W, bool kMaster, bool kEight>
 constexpr int kStepEach = (kEight && !kMaster && sizeof(W) == 2) ? 8 : 4;
 
-// Where a workgroup finds its entry, and the norm that the step clips by: the
-// kernel arguments hold the list, or the workspace; or the arguments hold one of so
-// few elements that every workgroup reads all gradients for the norm (kOwnNorm), or
-// all of the norm's partial sums (kPartNorm).
-enum ListKind { kInArgs, kInTable, kOwnNorm, kPartNorm };
+// A pointer that was loaded from memory, as one to global memory; what the compiler
+// cannot tell by itself it reads as flat memory (448 tensors: 291 us instead of 283).
+template <typename T> __device__ __forceinline__ T *in_global(T *p) {
+    return (T *)(__attribute__((address_space(1))) T *)reinterpret_cast<uintptr_t>(p);
+}
 
-template <typename W, typename G, bool kMaster, bool kEight, ListKind kList, int N = kStepEach<W, kMaster, kEight>>
-__global__ __launch_bounds__(kPass / N) void adamw_kernel(AdamwBatch b, AdamwScalars c) {
+// The step of workgroup wg's elements of its entry (kAnyRoot: see root_of_any).
+template <typename W, typename G, bool kMaster, bool kEight, bool kAnyRoot, int N>
+__device__ __forceinline__ void step_elements(const AdamwScalars &c, const AdamwItem &e, float clip, uint32_t wg) {
     constexpr int kBlockLanes = kMomentBlock / N;
     using Code = std::conditional_t<N == 8, uint64_t, uint32_t>;  // a lane's codes
-    float clip = 1.0f;
-    constexpr bool kTakesNorm = kList == kOwnNorm || kList == kPartNorm;
-    if (kTakesNorm || c.norm != nullptr) {
-        float norm;
-        if constexpr (kTakesNorm) {
-            __shared__ float s_norm;
-            double sum = 0.0;
-            if constexpr (kList == kOwnNorm) sum = list_squares<G, kPass / N, 8>(b.item, c.count);
-            else
-                for (int i = threadIdx.x; i < c.parts; i += kPass / N) sum += c.partial[i];
-            sum = block_sum<kPass / N>(sum);
-            if (threadIdx.x == 0) s_norm = (float)sqrt(sum);
-            __syncthreads();
-            norm = s_norm;
-            if (blockIdx.x == 0 && threadIdx.x == 0) *c.norm = norm;
-        } else {
-            norm = *c.norm;
-        }
-        if (!(fabsf(norm) < INFINITY)) return;
-        if (c.max_norm > 0.0f && norm > c.max_norm) clip = c.max_norm * (1.0f / norm);
-    }
-    const uint32_t wg = gridDim.x - 1 - blockIdx.x;
-    const AdamwItem e = kList == kInTable ? c.table[find_in_table(c.firsts, c.count, wg)] : b.item[find_in_batch(b.item, wg)];
     const int64_t i = (int64_t)(wg - e.first) * kPass + threadIdx.x * N;
     const int64_t live = e.n - i;  // may be <= 0: the lane still joins the reductions
     W *w = static_cast<W *>(e.w) + i;
@@ -357,7 +339,7 @@ __global__ __launch_bounds__(kPass / N) void adamw_kernel(AdamwBatch b, AdamwSca
         v[j] = c.beta2 * v[j] + c.one_beta2 * (gj * gj);
         // the hardware's reciprocal and root are within 1 ulp: the step is
         // a small part of the weight it is added to
-        const float d = root(v[j] * c.rbias2) + c.eps;
+        const float t = v[j] * c.rbias2, d = (kAnyRoot ? root_of_any(t) : __builtin_amdgcn_sqrtf(t)) + c.eps;
         x[j] = fmaf(-e.step * m[j], __builtin_amdgcn_rcpf(d), x[j] * e.keep);
         ma = fmaxf(ma, fabsf(m[j])), va = fmaxf(va, v[j]);
     }
@@ -406,6 +388,43 @@ __global__ __launch_bounds__(kPass / N) void adamw_kernel(AdamwBatch b, AdamwSca
             e.vs[i / kMomentBlock] = vs;
         }
     }
+}
+
+// Where a workgroup finds its entry, and the norm that the step clips by: the
+// kernel arguments hold the list, or the workspace; or the arguments hold one of so
+// few elements that every workgroup reads all gradients for the norm (kOwnNorm), or
+// all of the norm's partial sums (kPartNorm).
+enum ListKind { kInArgs, kInTable, kOwnNorm, kPartNorm };
+
+template <typename W, typename G, bool kMaster, bool kEight, ListKind kList, int N = kStepEach<W, kMaster, kEight>,
+          bool kAnyRoot = false>
+__global__ __launch_bounds__(kPass / N) void adamw_kernel(AdamwBatch b, AdamwScalars c) {
+    float clip = 1.0f;
+    constexpr bool kTakesNorm = kList == kOwnNorm || kList == kPartNorm;
+    if (kTakesNorm || c.norm != nullptr) {
+        float norm;
+        if constexpr (kTakesNorm) {
+            __shared__ float s_norm;
+            double sum = 0.0;
+            if constexpr (kList == kOwnNorm) sum = list_squares<G, kPass / N, 8>(b.item, c.count);
+            else
+                for (int i = threadIdx.x; i < c.parts; i += kPass / N) sum += c.partial[i];
+            sum = block_sum<kPass / N>(sum);
+            if (threadIdx.x == 0) s_norm = (float)sqrt(sum);
+            __syncthreads();
+            norm = s_norm;
+            if (blockIdx.x == 0 && threadIdx.x == 0) *c.norm = norm;
+        } else {
+            norm = *c.norm;
+        }
+        if (!(fabsf(norm) < INFINITY)) return;
+        if (c.max_norm > 0.0f && norm > c.max_norm) clip = c.max_norm * (1.0f / norm);
+    }
+    const uint32_t wg = gridDim.x - 1 - blockIdx.x;
+    AdamwItem e = kList == kInTable ? c.table[find_in_table(c.firsts, c.count, wg)] : b.item[find_in_batch(b.item, wg)];
+    e.w = in_global(e.w), e.master = in_global(e.master), e.g = in_global(e.g);
+    e.m = in_global(e.m), e.v = in_global(e.v), e.ms = in_global(e.ms), e.vs = in_global(e.vs);
+    step_elements<W, G, kMaster, kEight, kAnyRoot, N>(c, e, clip, wg);
 }
 
 // ---- the gradients' norm ----
@@ -510,7 +529,9 @@ hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_ada
         const hipError_t r = hipGetLastError();
         if (err == hipSuccess) err = r;
     };
-    const dim3 threads(kPass / kStepEach<W, kMaster, kEight>);
+    constexpr int kLaneElems = kStepEach<W, kMaster, kEight>;
+    const dim3 threads(kPass / kLaneElems);
+    const bool any_root = cfg.eps < kRootEps;
     auto copy = [&] {  // the batch into the table
         if (used == 0) return;
         adamw_table_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(b, used, items + done, firsts + done);
@@ -522,7 +543,10 @@ hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_ada
         if (table) {
             copy();
             c.table = items + from, c.firsts = firsts + from, c.count = done - from;
-            adamw_kernel<W, G, kMaster, kEight, kInTable><<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
+            if (any_root)
+                adamw_kernel<W, G, kMaster, kEight, kInTable, kLaneElems, true>
+                    <<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
+            else adamw_kernel<W, G, kMaster, kEight, kInTable><<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
             from = done;
         } else {
             for (int j = used; j < kBatch; ++j) b.item[j].first = UINT32_MAX;
@@ -531,13 +555,16 @@ hipError_t adamw_launches(const nf4_adamw_entry *e, int32_t count, const nf4_ada
                 adamw_kernel<W, G, kMaster, kEight, kOwnNorm, 4><<<dim3((uint32_t)wgs), dim3(kPass / 4), 0, s>>>(b, c);
             else if (list == kPartNorm)
                 adamw_kernel<W, G, kMaster, kEight, kPartNorm><<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
+            else if (any_root)
+                adamw_kernel<W, G, kMaster, kEight, kInArgs, kLaneElems, true>
+                    <<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
             else adamw_kernel<W, G, kMaster, kEight, kInArgs><<<dim3((uint32_t)wgs), threads, 0, s>>>(b, c);
             used = 0;
         }
         note();
         wgs = 0;
     };
-    constexpr int64_t kMaxWgs = (int64_t(1) << 31) / (kPass / kStepEach<W, kMaster, kEight>);  // threads of a grid
+    constexpr int64_t kMaxWgs = (int64_t(1) << 31) / (kPass / kLaneElems);  // threads of a grid
     for (int32_t i = 0; i < count; ++i) {
         if (!mine(i)) continue;
         const int64_t need = (e[i].n + kPass - 1) / kPass;
@@ -654,7 +681,9 @@ hipError_t launch_adamw(const nf4_adamw_entry *e, int32_t count, nf4_dtype wt, n
     if (own_norm) {
         const Extent x = extent_of(e, count);
         const bool one_kind = x.masters == 0 || x.masters == x.live;
-        if (x.live > 0 && x.elements <= kSmallNorm && x.live <= kSmallEntries && one_kind) {
+        if (c.eps < kRootEps) {
+            // kernels with a root of any second moment take the norm as a number
+        } else if (x.live > 0 && x.elements <= kSmallNorm && x.live <= kSmallEntries && one_kind) {
             // Every workgroup reads all gradients, but there is one launch: 7.4 us
             // instead of 10.8 for two tensors of 8192 elements (bf16, 8-bit moments),
             // 11.2 instead of 14.0 for 14 of them, 10.4 instead of 11.3 for two of

@@ -18,7 +18,7 @@ U = 2.0 ** -24
 
 # ------------------------------------------------------------------ small moments
 
-@pytest.mark.parametrize("eps", [0.0, 1e-24, 1e-8])
+@pytest.mark.parametrize("eps", [0.0, 1e-24, 2.0 ** -60, 0.99 * 2.0 ** -39, 2.0 ** -39, 1e-8])
 def test_root_of_small_second_moments(dev, eps):
     """Second moments among fp32's subnormals (below 2^-126) and around them: the
     step is lr m / (sqrt(v) + eps), not lr m / eps. The moments before the step are
