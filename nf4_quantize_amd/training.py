@@ -85,19 +85,27 @@ def _check_apart(ts):
         end = max(end, at + size)
 
 
+_TORCH = {}
+
+
+def _torch(name):
+    """Functions of torch that every call needs (torch is imported by the first one)."""
+    if not _TORCH:
+        import torch
+
+        _TORCH.update(stream=torch._C._cuda_getCurrentRawStream, changed=torch.autograd.graph.increment_version)
+    return _TORCH[name]
+
+
 def _stream(index):
     """The current stream of a device, as _nq._stream without its objects."""
-    import torch
-
-    return torch._C._cuda_getCurrentRawStream(index)
+    return _torch("stream")(index)
 
 
 def _changed(ts):
     """Tells autograd that this tensor, or these, were written: a graph that saved one
     of them refuses to run backward from then on."""
-    import torch
-
-    torch.autograd.graph.increment_version(ts)
+    _torch("changed")(ts)
 
 
 _CODES = {}
