@@ -478,9 +478,6 @@ def embedding_forward(ids, table, scale=1.0, out_dtype=None, out=None):
     packed = isinstance(table, _nq.NF4Tensor)
     if len(table.shape) != 2:
         raise ValueError("a table is 2-D [vocab x dim]")
-    if packed and not table.fmt.is_default:
-        raise ValueError("the embedding takes NF4 tables in the default storage format "
-                         "(B1 = 64, B2 = 256, E4M3, no mean offset)")
     if ids.get_device() < 0:
         raise ValueError("tensors must be contiguous device tensors")
     vocab, dim = table.shape
@@ -493,7 +490,11 @@ def embedding_forward(ids, table, scale=1.0, out_dtype=None, out=None):
     L, code, count, od = _nq.lib(), _index_code(ids), ids.numel(), _code(out.dtype)
     if packed:
         stream = _stream(_check_tensors(ids, out, table.codes, table.absmax, table.absmax_q, table.absmax_scale))
-        w = table.weight_struct()
+        try:
+            w = table.weight_struct()
+        except ValueError:  # the table is 2-D, so its format is another one
+            raise ValueError("the embedding takes NF4 tables in the default storage format "
+                             "(B1 = 64, B2 = 256, E4M3, no mean offset)") from None
         st = L.nf4_embedding_forward_packed(ids.data_ptr(), code, count, ctypes.byref(w), scale, out.data_ptr(), od, stream)
     else:
         stream = _stream(_check_tensors(ids, out, table))
