@@ -340,7 +340,9 @@ __device__ __forceinline__ void step_elements(const AdamwScalars &c, const Adamw
         // the hardware's reciprocal and root are within 1 ulp: the step is
         // a small part of the weight it is added to
         const float t = v[j] * c.rbias2, d = (kAnyRoot ? root_of_any(t) : __builtin_amdgcn_sqrtf(t)) + c.eps;
-        x[j] = fmaf(-e.step * m[j], __builtin_amdgcn_rcpf(d), x[j] * e.keep);
+        // the reciprocal of a subnormal number is infinite there, so eps is scaled as well
+        const float up = kAnyRoot && d < 0x1p-126f ? 0x1p24f : 1.0f;
+        x[j] = fmaf(-(e.step * up) * m[j], __builtin_amdgcn_rcpf(d * up), x[j] * e.keep);
         ma = fmaxf(ma, fabsf(m[j])), va = fmaxf(va, v[j]);
     }
     if (live >= N) {

@@ -359,3 +359,28 @@ def test_h_out_without_y_is_refused(dev):
     assert out is h
     assert nq.residual_norm_forward(None, h, w, h_out=h.view(3, 40))[0] is h
     assert nq.residual_norm_forward(None, h, w)[0] is h
+
+
+def test_eps_among_the_subnormals(dev):
+    """An eps below 2^-126 divides like any other: nothing moves where both moments are
+    zero, and m / eps is m / eps where the second moment has left fp32 under the first."""
+    import torch
+
+    n = 400
+    m0 = torch.zeros(n, device=dev)
+    m0[::2] = torch.logspace(-36, -30, n // 2, device=dev)
+    for eps in (2.0 ** -149, 1e-40, 1e-38, 2.0 ** -126):
+        for bits in (8, 32):
+            p = torch.full((n,), 0.5, device=dev)
+            opt = nq.NF4AdamW([p], lr=1e-6, weight_decay=0.0, eps=eps, state_bits=bits)
+            opt.step([torch.zeros(n, device=dev)])
+            assert bool((p == 0.5).all()), (eps, bits)
+        opt.bind_state([m0.clone()], [torch.zeros(n, device=dev)])
+        opt.step([torch.zeros(n, device=dev)], step=100000)
+        step = 1e-6 * 0.9 * m0.double() / float(np.float32(eps))
+        want = 0.5 - step
+        # 24 U of the step, the weight's rounding, and 2^-150 of m' over the eps
+        tol = 26 * U * step + 2 * U * (0.5 + want.abs())
+        big = step >= 2.0 ** 127
+        assert bool((((p.double() - want).abs() <= tol) | big).all()), eps
+        assert bool((p[1::2] == 0.5).all())
