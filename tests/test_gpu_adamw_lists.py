@@ -1,5 +1,6 @@
 """AdamW over lists that go through the workspace's table (more than 48 tensors of
-a kind), with bfloat16 weights, master weights for all or some and clipping. The
+a kind), with bfloat16 weights, master weights for all or some and clipping, and
+with the kernels that a small eps takes. The
 weights are compared with the formulas in 64 bits (test_gpu_adamw.py has the
 tolerances); the moments, their scales and their codes are defined to the bit by
 fp32 operations (nf4.h) and have to be equal."""
@@ -40,23 +41,23 @@ def stored(x, least, bits16, second):
     return scale, np.sign(t) * np.floor(a / step + bits16 / 65536.0) * step
 
 
-@pytest.mark.parametrize("count", [48, 49, 97, 448])
+@pytest.mark.parametrize("count,eps", [(48, 1e-8), (49, 1e-8), (97, 1e-8), (448, 1e-8), (3, 0.0), (48, 0.0), (97, 0.0)])
 @pytest.mark.parametrize("bits", [8, 32])
 @pytest.mark.parametrize("wt,gt,master", [("bfloat16", "bfloat16", "none"), ("bfloat16", "bfloat16", "all"),
                                           ("bfloat16", "float32", "some"), ("float32", "bfloat16", "none")])
-def test_steps(dev, count, bits, wt, gt, master):
+def test_steps(dev, count, eps, bits, wt, gt, master):
     import torch
 
-    log(f"adamw list of {count}, {bits} bits, {wt} {gt}, masters {master}")
+    log(f"adamw list of {count}, eps {eps}, {bits} bits, {wt} {gt}, masters {master}")
     shapes = [(1 + (i * 157) % 900,) for i in range(count)]
     shapes[count // 2] = (5003,)  # more than a workgroup's share
     opt, params, masters, grads = make(dev, shapes, getattr(torch, wt), getattr(torch, gt), bits, master != "none", 17,
-                                       max_grad_norm=0.5)
+                                       max_grad_norm=0.5, eps=eps)
     if master == "some":
         keep = [None if i % 3 == 1 else t for i, t in enumerate(masters)]
         opt = nq.NF4AdamW([dict(params=params[:1], lr=3e-3, weight_decay=0.1, masters=keep[:1]),
                            dict(params=params[1:], lr=1e-3, weight_decay=0.0, masters=keep[1:])],
-                          state_bits=bits, seed=17 << 33, max_grad_norm=0.5)
+                          state_bits=bits, seed=17 << 33, max_grad_norm=0.5, eps=eps)
     for number in (1, 2):
         before = snapshot(opt)
         opt.step(grads)
