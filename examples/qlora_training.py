@@ -83,7 +83,8 @@ def train(steps=60, moments=8, vocab=1024, dim=512, hidden=1024, blocks=2, rank=
           noise=0.1, seed=0, report=None):
     """Trains for `steps` steps; returns the losses."""
     model = Model(vocab, dim, hidden, blocks, rank, seed)
-    # bfloat16 parameters with fp32 master weights, and the fp32 norms and gates
+    # bfloat16 parameters with fp32 master weights, and the fp32 norms and gates: a list
+    # has one dtype, and each optimizer clips by the norm of its own list
     half = [p for p in model.parameters() if p.dtype == torch.bfloat16]
     full = [p for p in model.parameters() if p.dtype == torch.float32]
     optimizers = [nq.NF4AdamW([dict(params=half, lr=lr, weight_decay=0.0, masters=True)], state_bits=moments,

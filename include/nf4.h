@@ -489,8 +489,10 @@ nf4_status nf4_grad_norm(const nf4_adamw_entry *entries, int32_t count, int32_t 
  * there are more than 48 (0 up to there); (size_t)-1 for count < 0. */
 size_t nf4_adamw_workspace_size(int32_t count);
 
-/* One AdamW step of every entry, in one launch (see above). Up to 48 entries travel
- * in the kernel arguments; more are first copied into a table in the workspace.
+/* One AdamW step of every entry (see above): one launch for the entries without a
+ * master weight and one for those with, more where those have over 2^31 threads. Up
+ * to 48 entries of a kind travel in the kernel arguments; more are first copied into
+ * a table in the workspace, 48 a launch.
  *   entries    host array, read during the call only
  *   moments    an nf4_moments
  *   grad_norm  device, one float, or NULL (no clipping; required where
@@ -500,7 +502,8 @@ size_t nf4_adamw_workspace_size(int32_t count);
  *              NULL when that is 0); calls that overlap must not share one
  * Every entry is validated before anything is launched. Buffers of different
  * entries must not overlap. Gradients that are not finite are outside the
- * contract unless grad_norm is given. The step number and the seed are
+ * contract unless grad_norm is given, and so are those whose square, after the
+ * clipping, is not in fp32 (1.8e19 and above). The step number and the seed are
  * arguments: a captured call replays the same step. */
 nf4_status nf4_adamw_step(const nf4_adamw_entry *entries, int32_t count, int32_t w_dtype,
                           int32_t grad_dtype, int32_t moments, const nf4_adamw_config *config,
@@ -508,7 +511,9 @@ nf4_status nf4_adamw_step(const nf4_adamw_entry *entries, int32_t count, int32_t
                           void *stream);
 
 /* nf4_grad_norm, then nf4_adamw_step with that norm, in one or two launches less
- * where the list has few elements.
+ * where the list has few elements. The squares are then added in another order
+ * (that too depends on the sizes alone), so the norm may differ from
+ * nf4_grad_norm's in its last bit.
  *   grad_norm  device out, one float
  *   workspace  as of both, the larger size */
 nf4_status nf4_adamw_clip_step(const nf4_adamw_entry *entries, int32_t count, int32_t w_dtype,

@@ -100,7 +100,8 @@ dim3 lookup_grid(int64_t tokens, int lanes) {
 
 // Up to kOneTile each token counts its place among all, up to kRankTokens in its
 // tile, and searches the others: a call with 7000 tokens takes 17.5 us the one way
-// and 18.5 the other, with 9000 25.0 and 20.6.
+// and 18.5 the other, with 9000 25.0 and 20.6. They cross between three tiles and
+// four; the bound is three.
 constexpr int kOneTile = 6144;
 constexpr int kTile = 2048;
 constexpr int kRankTokens = 32768;
@@ -379,8 +380,9 @@ __device__ __forceinline__ G *grad_row(const GradParams &p, uint32_t key) {
 // Each wave sums the runs of up to 16 sorted places in 512 columns. dy is read once, so
 // where a wave's columns are whole cache lines (kStream) it is read past the
 // caches: beside a gradient that the sort's launch has just cleared, 16384 x 4096
-// bf16 into 32000 rows take 86 us in all instead of 109. With lines that two
-// waves share it costs instead (5003 x 1601: 38 us for 36).
+// bf16 into 32000 rows take 106 us in all instead of 117 (90 instead of 107 where
+// every call writes the same gradient). With lines that two waves share it costs
+// instead (5003 x 1601: 38 us for 36).
 template <typename T, typename G, typename C, bool kStream, bool kAdd>
 __global__ __launch_bounds__(kThreads) void run_sum_kernel(GradParams p) {
     const int lane = threadIdx.x % 64;

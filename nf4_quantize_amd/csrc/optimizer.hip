@@ -267,8 +267,8 @@ __device__ __forceinline__ Code encode_each(const float (&x)[N], const uint32_t 
 // registers and every byte is moved once. Weights and moments go past the caches'
 // usual order (they are not read again before the next step), gradients do not,
 // and the workgroups run from the end of the list: what the norm's pass read last
-// is still in the memory-side cache. The 448 tensors take 365 us with both, 424
-// without.
+// is still in the memory-side cache. The 448 tensors take 362 us with both and 424
+// without (with the norm's launches and the table's).
 template <typename W, bool kMaster, bool kEight>
 constexpr int kStepEach = (kEight && !kMaster && sizeof(W) == 2) ? 8 : 4;
 

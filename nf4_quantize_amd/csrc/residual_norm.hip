@@ -6,8 +6,9 @@
 //
 // Both are bound by HBM: the forward reads y and h and writes h' and x (8 bytes
 // an element in bf16), the backward reads dx, dh', y and h' and writes dy and
-// dh (12 bytes), and each element is moved once. A row is held in registers by
-// a group of lanes, eight consecutive elements a lane and vector.
+// dh (12 bytes), and each element is moved once; the backward pass reads rows of more
+// than 8192 columns twice. A row is held in registers by a group of lanes, eight
+// consecutive elements a lane and vector.
 #include <math.h>
 
 #include <type_traits>
@@ -327,9 +328,11 @@ __global__ __launch_bounds__(kMost) void residual_norm_backward_kernel(NormParam
     __shared__ float part[2][3][16];
     extern __shared__ float s_cols[];
     // Above 512 threads a CU holds one workgroup, and a lane's weights are in LDS: with
-    // them in registers too it spilled (8192 x 8192 bf16 162 us instead of 148, 8192 x
-    // 5120 124 instead of 96). Tiles of bf16 blocks on an fp32 stream do not spill
-    // (5461 x 12288: 374 us with LDS, 355 without).
+    // them in registers too it spilled more (8192 x 8192 bf16 162 us instead of 148, 8192
+    // x 5120 124 instead of 96). What still spills there: fp32 rows 6 to 35 registers,
+    // token gates 2 to 35, bf16 rows of odd width on an fp32 stream 6. Tiles of bf16
+    // blocks on an fp32 stream spill 4 to 6 without LDS and are faster so (5461 x 12288:
+    // 374 us with LDS, 355 without).
     constexpr bool kKeep = kMost <= 512 || (kTiled && sizeof(T) == 2 && kKind == kRowFours);
     __shared__ f32x4 s_w[kKeep ? 1 : 6][kKeep ? 1 : kMost];
     typedef ColsOf<kKind> C;
@@ -451,9 +454,10 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float *partial, 
 }
 
 // Lanes of a row, vectors of a lane, threads of a workgroup, and threads that a CU
-// holds of the kernel: up to 512 columns a
-// row is part of a wave and a workgroup takes several; above, a workgroup takes
-// one row with as many waves as it needs, one vector a lane up to 8192 columns.
+// holds of the kernel: up to 512 columns a row is part of a wave and a workgroup takes
+// several; above, a workgroup takes one row with as many waves as it needs, one vector a lane up to 8192 columns, two up
+// to 16384 and four above, which spill 43 to 85 registers (1024 x 32768 bf16: 84 us,
+// its bytes 41; 2048 x 16384 with two, the same bytes: 55).
 struct Split {
     int lanes, vec, block, resident;
 };

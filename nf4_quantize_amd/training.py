@@ -147,7 +147,8 @@ def _moment(name):
 class NF4AdamW:
     """AdamW over a list of device tensors in a few launches, with the moments in
     8 bits (E4M3 codes with one fp32 scale per 256 elements, rounded
-    stochastically) or in 32, and clipping by the gradients' global norm.
+    stochastically) or in 32, and clipping by the norm of all its list's gradients
+    (each optimizer by its own: a list has one dtype).
 
     ``params``: tensors, or groups ``dict(params=[...], lr=..., weight_decay=...,
     masters=[...])``; all have one dtype (bfloat16 or float32), and no two share
@@ -390,9 +391,9 @@ def residual_norm_forward(y, h, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e
     """h' = h + alpha gate norm(y; w_post), x = norm(h'; w_pre) over the last
     dimension (nf4_residual_norm_forward). ``y`` bfloat16 or float32, ``h`` the
     same or float32; without ``w_post`` y is added as it is; ``y=None``: x =
-    norm(h) and h' = h, which no other ``h_out`` receives. ``gate``: one value a channel, or one an element. Returns
-    (h', x, rstd_pre, rstd_post or None); ``h_out=h`` updates the residual stream
-    in place."""
+    norm(h) and h' = h, which no other ``h_out`` receives. ``gate``: one value a
+    channel, or one an element. Returns (h', x, rstd_pre, rstd_post or None);
+    ``h_out=h`` updates the residual stream in place."""
     import torch
 
     index = _check_tensors(h, y, w_pre, w_post, gate, h_out, x_out)
