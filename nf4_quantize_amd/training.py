@@ -6,6 +6,7 @@ kernels, torch supplies device memory and the current stream.
 """
 import array
 import ctypes
+import operator
 
 import numpy as np
 
@@ -123,23 +124,14 @@ def _code(dtype):
 
 # ------------------------------------------------------------------ AdamW
 
-class _BoundList(list):
-    """The tensors whose addresses a step takes: other moments come in through
-    bind_state, other weights through a parameter's ``data``."""
+def _taken(name):
+    """The list of the tensors whose addresses a step takes, made on first use. A step
+    refuses to run where the caller has put others in."""
 
-    def _refuse(self, *args, **kwargs):
-        raise TypeError("a step writes at these tensors' addresses: bind_state gives it other moments, a parameter's "
-                        "data another weight")
-
-    __setitem__ = __delitem__ = __iadd__ = __imul__ = _refuse
-    append = extend = insert = pop = remove = clear = sort = reverse = _refuse
-
-
-def _moment(name):
     def tensors(self):
-        if name not in self._moments:
+        if name not in self._taken:
             raise AttributeError(f"32-bit moments have no {name}")
-        return self._moments[name]
+        return self._given.setdefault(name, list(self._taken[name]))
 
     return property(tensors)
 
@@ -161,11 +153,12 @@ class NF4AdamW:
     rounding; each step takes the next ones.
 
     ``m``, ``v`` (and ``m_scale``, ``v_scale``) are the lists of the tensors'
-    moments in the order of the parameters; they are read only like ``params`` and
-    ``masters``, and ``bind_state`` replaces them. ``grad_norm`` is the last norm (a
-    device tensor of one float)."""
+    moments in the order of the parameters. A step writes at these tensors' addresses,
+    so ``bind_state`` replaces them, and a step refuses lists whose tensors are others,
+    ``params`` and ``masters`` too (a parameter's ``data`` may change). ``grad_norm`` is
+    the last norm (a device tensor of one float)."""
 
-    m, v, m_scale, v_scale = (_moment(name) for name in ("m", "v", "m_scale", "v_scale"))
+    params, masters, m, v, m_scale, v_scale = map(_taken, ("params", "masters", "m", "v", "m_scale", "v_scale"))
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=8,
                  max_grad_norm=0.0, seed=0, masters=None):
@@ -181,7 +174,7 @@ class NF4AdamW:
         elif masters is not None:
             raise ValueError("masters belong to the groups")
         self.groups = []
-        self.params, self.masters = [], []
+        self._params, self._masters = [], []
         for g in params:
             ps = list(g["params"])
             ms = g.get("masters")
@@ -191,19 +184,19 @@ class NF4AdamW:
             if len(ms) != len(ps):
                 raise ValueError(f"{len(ms)} masters for {len(ps)} parameters")
             self.groups.append(dict(lr=float(g.get("lr", lr)), weight_decay=float(g.get("weight_decay", weight_decay)),
-                                    first=len(self.params), count=len(ps)))
-            self.params += ps
-            self.masters += ms
-        if not self.params:
+                                    first=len(self._params), count=len(ps)))
+            self._params += ps
+            self._masters += ms
+        if not self._params:
             raise ValueError("no parameters")
-        self.params, self.masters = _BoundList(self.params), _BoundList(self.masters)
-        self.dtype, self.device = self.params[0].dtype, self.params[0].device
+        self._taken, self._given = dict(params=tuple(self._params), masters=tuple(self._masters)), {}
+        self.dtype, self.device = self._params[0].dtype, self._params[0].device
         _nq._dtype_code(self.dtype)
         self._tensor = torch.Tensor
-        self._entries = np.zeros(len(self.params), _ENTRY)
+        self._entries = np.zeros(len(self._params), _ENTRY)
         self._at = self._entries.ctypes.data
-        self._numels = [p.numel() for p in self.params]
-        self._weights = self.params + [mw for mw in self.masters if mw is not None]
+        self._numels = [p.numel() for p in self._params]
+        self._weights = self._params + [mw for mw in self._masters if mw is not None]
         self._rates = None
         self._held_state = []
         self._bind()
@@ -249,23 +242,24 @@ class NF4AdamW:
             lists.update(m_scale=list(m_scale), v_scale=list(v_scale))
         dt = torch.float8_e4m3fn if self.state_bits == 8 else torch.float32
         for name, ts in lists.items():
-            if len(ts) != len(self.params):
-                raise ValueError(f"{name}: {len(ts)} tensors for {len(self.params)} parameters")
+            if len(ts) != len(self._params):
+                raise ValueError(f"{name}: {len(ts)} tensors for {len(self._params)} parameters")
             scale = name.endswith("scale")
             want = torch.float32 if scale else dt
             for t, n in zip(ts, self._numels):
-                _check_tensors(self.params[0], t)
+                _check_tensors(self._params[0], t)
                 if t.dtype != want or t.numel() != (-(-n // MOMENT_BLOCK) if scale else n):
                     raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} for a parameter of {n} elements")
         _check_apart(self._weights + [t for ts in lists.values() for t in ts])
         # held as well, so that their memory stays where a tensor of the list gets other data
         self._held_state = [t.detach() for ts in lists.values() for t in ts]
-        self._moments = {name: _BoundList(ts) for name, ts in lists.items()}
         for name, ts in lists.items():
+            self._taken[name] = tuple(ts)
+            self._given.pop(name, None)
             self._entries[name] = [t.data_ptr() for t in ts]
 
     def zero_grad(self, set_to_none=True):
-        for p in self.params:
+        for p in self._params:
             if set_to_none:
                 p.grad = None
             elif p.grad is not None:
@@ -275,37 +269,46 @@ class NF4AdamW:
         """Takes the weights' addresses, once they are what the step can update."""
         import torch
 
-        for p, n, mw in zip(self.params, self._numels, self.masters):
+        for p, n, mw in zip(self._params, self._numels, self._masters):
             if p.dtype != self.dtype:
                 raise TypeError(f"parameters of one dtype, got {self.dtype} and {p.dtype}")
-            _check_tensors(self.params[0], p, mw)
+            _check_tensors(self._params[0], p, mw)
             if p.numel() != n or p.device != self.device:
                 raise ValueError("a parameter's size or device has changed")
             if mw is not None and (mw.dtype != torch.float32 or self.dtype != torch.bfloat16 or mw.numel() != n):
                 raise TypeError("a master weight is float32, of a bfloat16 parameter of its size")
         if self._held_state:  # at construction bind_state asks this
             _check_apart(self._weights + self._held_state)
-        self._entries["w"] = [p.data_ptr() for p in self.params]
-        self._entries["master"] = [0 if mw is None else mw.data_ptr() for mw in self.masters]
+        self._entries["w"] = [p.data_ptr() for p in self._params]
+        self._entries["master"] = [0 if mw is None else mw.data_ptr() for mw in self._masters]
         # held, so that no other memory can have their addresses
         self._held = [t.detach() for t in self._weights]
         self._bound = [t.data_ptr() for t in self._held]
+
+    def _check_given(self):
+        for name, ts in self._given.items():
+            taken = self._taken[name]
+            if len(ts) != len(taken) or any(map(operator.is_not, ts, taken)):
+                raise ValueError(f"{name} has other tensors than the step writes: bind_state gives it other moments, a "
+                                 "parameter's data another weight")
 
     def step(self, grads=None, step=None, seed=None):
         """One step with the parameters' ``.grad``, or with ``grads`` (a tensor for
         each parameter, all bfloat16 or all float32). ``step`` and ``seed``
         override the step number (the count of calls) and the random seed."""
         L = _nq.lib()
-        grads = [p.grad for p in self.params] if grads is None else grads
-        if len(grads) != len(self.params):
-            raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        if self._given:
+            self._check_given()
+        grads = [p.grad for p in self._params] if grads is None else grads
+        if len(grads) != len(self._params):
+            raise ValueError(f"{len(grads)} gradients for {len(self._params)} parameters")
         T = self._tensor  # the methods over the list: a third less time than a loop, for hundreds of tensors
         try:
             devices, sizes = set(map(T.get_device, grads)), list(map(T.numel, grads))
         except TypeError:
             raise ValueError("a parameter has no gradient") from None
         dt = grads[0].dtype
-        if (devices != {self.params[0].get_device()} or sizes != self._numels or not all(map(T.is_contiguous, grads))
+        if (devices != {self._params[0].get_device()} or sizes != self._numels or not all(map(T.is_contiguous, grads))
                 or {g.dtype for g in grads} != {dt}):
             raise ValueError(f"gradients: contiguous, of the parameters' sizes, one dtype, on {self.device}; got "
                              + ", ".join(f"{tuple(g.shape)} {g.dtype} {g.device}" for g in grads[:4]) + " ...")
@@ -337,10 +340,10 @@ class NF4AdamW:
     def state_dict(self):
         d = dict(steps=self.steps, seed=self.seed, state_bits=self.state_bits,
                  groups=[dict(lr=g["lr"], weight_decay=g["weight_decay"]) for g in self.groups],
-                 m=[t.clone() for t in self.m], v=[t.clone() for t in self.v],
-                 masters=[None if t is None else t.clone() for t in self.masters])
+                 m=[t.clone() for t in self._taken["m"]], v=[t.clone() for t in self._taken["v"]],
+                 masters=[None if t is None else t.clone() for t in self._masters])
         if self.state_bits == 8:
-            d.update(m_scale=[t.clone() for t in self.m_scale], v_scale=[t.clone() for t in self.v_scale])
+            d.update(m_scale=[t.clone() for t in self._taken["m_scale"]], v_scale=[t.clone() for t in self._taken["v_scale"]])
         return d
 
     def load_state_dict(self, d):
@@ -348,10 +351,10 @@ class NF4AdamW:
 
         names = ["m", "v"] + (["m_scale", "v_scale"] if self.state_bits == 8 else [])
         if (d["state_bits"] != self.state_bits or len(d["groups"]) != len(self.groups)
-                or any(len(d[k]) != len(self.params) for k in names + ["masters"])):
+                or any(len(d[k]) != len(self._params) for k in names + ["masters"])):
             raise ValueError("the state of another optimizer")
-        pairs = [(x, y) for k in names for x, y in zip(getattr(self, k), d[k])]
-        for x, y in zip(self.masters, d["masters"]):
+        pairs = [(x, y) for k in names for x, y in zip(self._taken[k], d[k])]
+        for x, y in zip(self._masters, d["masters"]):
             if (x is None) != (y is None):
                 raise ValueError("the state of another optimizer: master weights")
             pairs += [] if x is None else [(x, y)]

@@ -3,6 +3,7 @@ moments, what autograd is told, which tensors an optimizer takes and keeps, and
 what it refuses. Sizes are small; the formulas' own tests are in
 test_gpu_adamw.py, test_gpu_residual_norm.py and test_gpu_embedding.py."""
 import copy
+import io
 import pickle
 
 import numpy as np
@@ -156,47 +157,60 @@ def test_second_derivatives_are_refused(dev):
 
 @pytest.mark.parametrize("bits", [8, 32])
 def test_moments_are_replaced_by_bind_state_alone(dev, bits):
-    """The step writes at the addresses that bind_state took, so the lists refuse
-    other tensors; the memory stays the optimizer's for as long as it uses it."""
+    """The step writes at the addresses that bind_state took: it refuses lists that hold
+    other tensors, before it launches anything, and their memory stays the optimizer's
+    for as long as it uses it. The lists themselves are saved like any others."""
     import torch
 
-    opt = nq.NF4AdamW([torch.zeros(300, device=dev), torch.zeros(20, device=dev)], state_bits=bits)
-    for name in ("m", "v") + (("m_scale", "v_scale") if bits == 8 else ()):
-        ts = getattr(opt, name)
-        assert len(ts) == 2 and isinstance(ts, list)
+    names = ("m", "v") + (("m_scale", "v_scale") if bits == 8 else ())
+    grads = [torch.ones(300, device=dev), torch.ones(20, device=dev)]
+
+    def fresh():
+        return nq.NF4AdamW([torch.zeros(300, device=dev), torch.zeros(20, device=dev)], state_bits=bits)
+
+    def item(ts):
+        ts[0] = ts[1] if ts[0] is None else ts[0].clone()
+
+    def part(ts):
+        ts[:] = [None if t is None else t.clone() for t in ts]
+        ts[1] = grads[1]
+
+    changes = (item, part, lambda ts: ts.append(grads[0]), lambda ts: ts.pop(), lambda ts: ts.clear(),
+               lambda ts: ts.__setitem__(1, grads[1]))
+    for name in names + ("params", "masters"):
+        for k, change in enumerate(changes):
+            if name == "masters" and k == 0:
+                continue  # there are none
+            opt = fresh()
+            kept = list(opt.params) + list(opt.m)
+            change(getattr(opt, name))
+            with pytest.raises(ValueError, match=name):
+                opt.step(grads)
+            assert opt.steps == 0 and not any(bool(t.view(torch.uint8).any()) for t in kept)
+            if name in names:
+                opt.bind_state(*([t for t in fresh()._taken[n]] for n in names))
+                opt.step(grads)
+                assert bool(getattr(opt, name)[1].view(torch.uint8).any())
         with pytest.raises(AttributeError):
-            setattr(opt, name, [t.clone() for t in ts])
-
-        def item():
-            ts[0] = ts[0].clone()
-
-        def part():
-            ts[:] = [t.clone() for t in ts]
-
-        def more():
-            nonlocal ts
-            ts += [ts[0].clone()]
-
-        def gone():
-            del ts[1]
-
-        for change in (item, part, more, gone, ts.clear, ts.reverse, ts.pop, lambda: ts.append(ts[0]),
-                       lambda: ts.extend(ts), lambda: ts.insert(0, ts[0]), lambda: ts.remove(ts[0]), lambda: ts.sort(key=id)):
-            with pytest.raises(TypeError, match="bind_state"):
-                change()
-        assert len(getattr(opt, name)) == 2
-    for ts in (opt.params, opt.masters):
-        with pytest.raises(TypeError, match="data"):
-            ts[0] = torch.zeros(300, device=dev)
+            setattr(opt, name, [])
+    assert bits == 8 or not hasattr(opt, "m_scale")
+    opt = fresh()
     held = {t.untyped_storage().data_ptr() for t in opt._held_state}
     assert {t.untyped_storage().data_ptr() for t in opt.m + opt.v} <= held
-    fresh = [[torch.zeros_like(t) for t in getattr(opt, n)] for n in ("m", "v")]
-    scales = [[torch.zeros_like(t) for t in getattr(opt, n)] for n in ("m_scale", "v_scale")] if bits == 8 else []
+    file = io.BytesIO()
+    opt.step(grads)
+    torch.save([getattr(opt, n) for n in names], file)
+    file.seek(0)
+    saved = torch.load(file, weights_only=True)
+    again = fresh()
+    again.bind_state(*saved)
+    assert all(torch.equal(s.view(torch.uint8), t.view(torch.uint8)) for s, t in zip(again.m + again.v, opt.m + opt.v))
     old = [t.view(torch.uint8).clone() for t in opt.m]
     kept = opt.m
-    opt.bind_state(*fresh, *scales)
-    opt.step([torch.ones(300, device=dev), torch.ones(20, device=dev)])
-    assert all(bool(t.view(torch.uint8).any()) for t in fresh[0]) and opt.m[0] is fresh[0][0]
+    new = [[torch.zeros_like(t) for t in getattr(opt, n)] for n in names]
+    opt.bind_state(*new)
+    opt.step(grads)
+    assert all(bool(t.view(torch.uint8).any()) for t in new[0]) and opt.m[0] is new[0][0]
     assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(old, kept))
 
 
