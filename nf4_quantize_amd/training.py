@@ -343,7 +343,8 @@ class NF4AdamW:
                  m=[t.clone() for t in self._taken["m"]], v=[t.clone() for t in self._taken["v"]],
                  masters=[None if t is None else t.clone() for t in self._masters])
         if self.state_bits == 8:
-            d.update(m_scale=[t.clone() for t in self._taken["m_scale"]], v_scale=[t.clone() for t in self._taken["v_scale"]])
+            d.update(m_scale=[t.clone() for t in self._taken["m_scale"]],
+                     v_scale=[t.clone() for t in self._taken["v_scale"]])
         return d
 
     def load_state_dict(self, d):

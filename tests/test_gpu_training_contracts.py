@@ -286,8 +286,8 @@ def test_state_of_a_weight_without_dimensions(dev):
     import torch
 
     def fresh(x):
-        return nq.NF4AdamW([torch.tensor(x, device=dev, dtype=torch.bfloat16), torch.full((3,), x, device=dev, dtype=torch.bfloat16)],
-                           masters=True, lr=0.1)
+        half = dict(device=dev, dtype=torch.bfloat16)
+        return nq.NF4AdamW([torch.tensor(x, **half), torch.full((3,), x, **half)], masters=True, lr=0.1)
 
     g = [torch.tensor(1.0, device=dev), torch.ones(3, device=dev)]
     a, b = fresh(1.0), fresh(2.0)
@@ -303,10 +303,8 @@ def test_states_with_parts_missing_are_refused(dev):
     """A state that lacks tensors of one of its lists is not loaded in part."""
     import torch
 
-    opt = nq.NF4AdamW([torch.ones(300, device=dev, dtype=torch.bfloat16), torch.ones(40, device=dev, dtype=torch.bfloat16)],
-                      masters=True)
-    other = nq.NF4AdamW([torch.ones(300, device=dev, dtype=torch.bfloat16), torch.ones(40, device=dev, dtype=torch.bfloat16)],
-                        masters=True)
+    opt, other = (nq.NF4AdamW([torch.ones(n, device=dev, dtype=torch.bfloat16) for n in (300, 40)], masters=True)
+                  for _ in range(2))
     g = [torch.ones(300, device=dev), torch.ones(40, device=dev)]
     other.step(g)
     for name in ("m", "v", "m_scale", "v_scale", "masters"):
