@@ -616,6 +616,82 @@ nf4_status nf4_embedding_backward(const void *ids, int32_t id_dtype, int64_t tok
                                   int32_t accumulate, void *workspace, size_t workspace_bytes,
                                   void *stream);
 
+/* Queries and keys between the projections and attention: the norm of each head
+ * (where there are weights) and the rotation by the token's position, in one pass.
+ * For a head x of `dim` elements, its pairs (a_i, b_i), i < rotated / 2, being
+ * (x_i, x_{i + rotated/2}) (NF4_ROTARY_HALF) or (x_{2i}, x_{2i+1})
+ * (NF4_ROTARY_INTERLEAVED):
+ *   n   = w' x rsqrt(mean x^2 + eps),  w' = w + w_offset   (n = x without weights)
+ *   y   : a_i' = scale (a_i cos - b_i sin),  b_i' = scale (b_i cos + a_i sin)  of n's pairs,
+ *         with the angle position * f_i;  elements from `rotated` on are n's
+ * in fp32, rounded once. The frequencies are given in turns: turns[i] =
+ * round(2^64 f_i / (2 pi)) modulo 2^64, so that position * turns[i] modulo 2^64 is
+ * the angle in 2^-64 turns, off by at most |position| 2^-65 turns whatever the
+ * position (|position| < 2^31: by 4e-10 radians), and cosine and sine are those of
+ * its upper 32 bits, to about 1e-7. */
+typedef enum { NF4_ROTARY_HALF = 0, NF4_ROTARY_INTERLEAVED = 1 } nf4_rotary_layout;
+
+typedef struct {
+    int64_t batch, tokens; /* >= 0; batch * tokens <= 2^30 */
+    int32_t heads_q;       /* 0 .. 65536 */
+    int32_t heads_k;       /* 0 .. 65536: 0 where there are no keys */
+    int32_t dim;           /* of a head, 1 .. 512 */
+    int32_t rotated;       /* 2 .. dim, even */
+    int32_t layout;        /* an nf4_rotary_layout */
+    int32_t dtype;         /* of queries, keys and their gradients */
+    int32_t w_dtype;       /* of the norms' weights and their gradients */
+    float eps;             /* >= 0 */
+    float w_offset;
+    float scale;           /* of cosine and sine */
+} nf4_rotary_shape;
+
+/* Heads in memory: element d of head h of token t of sequence b is at
+ * data[b * batch_stride + t * token_stride + h * head_stride + d]. Strides are in
+ * elements, 0 or more; `data` is aligned to its element. Elements that are written
+ * must lie apart: two of them at one address are outside the contract. */
+typedef struct {
+    void *data;
+    int64_t batch_stride, token_stride, head_stride;
+} nf4_heads;
+
+/* Forward.
+ *   turns      device, rotated / 2 numbers
+ *   positions  device, one for each token: that of token t of sequence b is
+ *              positions[b * position_batch_stride + t] (0: the sequences share
+ *              them), an nf4_index_dtype; NULL: t itself
+ *   w_q, w_k   device, `dim` weights (w_dtype, 16-byte aligned), or NULL: no norm
+ *   q_out, k_out  may be q, k themselves (the same memory and strides); other
+ *              memory that overlaps an input is outside the contract
+ * q (k) and its output are read only where heads_q (heads_k) > 0. */
+nf4_status nf4_rotary_forward(const nf4_rotary_shape *shape, const uint64_t *turns,
+                              const void *positions, int32_t position_dtype,
+                              int64_t position_batch_stride, const nf4_heads *q, const nf4_heads *k,
+                              const void *w_q, const void *w_k, const nf4_heads *q_out,
+                              const nf4_heads *k_out, void *stream);
+
+/* Bytes of device workspace of the backward pass where a weight's gradient is
+ * asked for (fp32 partial sums, two rows for each workgroup); (size_t)-1 for
+ * invalid arguments. */
+size_t nf4_rotary_backward_workspace_size(const nf4_rotary_shape *shape);
+
+/* Backward: given the gradients dq_out, dk_out of the outputs, with g their
+ * rotation by the negative angles (times scale where the forward has it):
+ *   without weights  dx = g
+ *   with weights     r = rsqrt(mean x^2 + eps),  dw = sum over all heads of g x r,
+ *                    dx = r (g w' - x r mean(g w' x r))
+ *   q, k       the forward's inputs, read where there are weights (else may be NULL)
+ *   dq, dk     out; may be dq_out, dk_out themselves
+ *   dw_q, dw_k device out, `dim` elements (w_dtype), or NULL; sums run in fp32 in an
+ *              order that depends on the sizes alone. Without tokens they are zero.
+ *   workspace  256-byte aligned; may be NULL where neither is asked for */
+nf4_status nf4_rotary_backward(const nf4_rotary_shape *shape, const uint64_t *turns,
+                               const void *positions, int32_t position_dtype,
+                               int64_t position_batch_stride, const nf4_heads *dq_out,
+                               const nf4_heads *dk_out, const nf4_heads *q, const nf4_heads *k,
+                               const void *w_q, const void *w_k, const nf4_heads *dq,
+                               const nf4_heads *dk, void *dw_q, void *dw_k, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

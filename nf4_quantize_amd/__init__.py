@@ -71,6 +71,9 @@ EXPORTS = (
     "nf4_embedding_forward_packed",
     "nf4_embedding_backward_workspace_size",
     "nf4_embedding_backward",
+    "nf4_rotary_forward",
+    "nf4_rotary_backward_workspace_size",
+    "nf4_rotary_backward",
 )
 
 # nf4_dq_format: the 8-bit code of double quantization.
@@ -195,6 +198,7 @@ def lib():
                                  ctypes.c_size_t, p]
     L.nf4_merge_lora.restype = ctypes.c_int
     declare(L)
+    heads.declare(L)
     _lib = L
     return L
 
@@ -962,4 +966,12 @@ from .training import (  # noqa: E402
     residual_norm,
     residual_norm_backward,
     residual_norm_forward,
+)
+from . import heads  # noqa: E402
+from .heads import (  # noqa: E402
+    NF4Rotary,
+    rotary,
+    rotary_backward,
+    rotary_forward,
+    rotary_frequencies,
 )

@@ -1,5 +1,6 @@
 // api_training.hip - the extern "C" entry points of the training-step operators
-// (AdamW, the residual norms, the token embedding): host-side validation and
+// (AdamW, the residual norms, the token embedding, the rotation of queries and
+// keys): host-side validation and
 // dispatch. Declarations and contracts are in include/nf4.h.
 //
 // Every argument is checked before any HIP call; a rejected call launches
@@ -254,4 +255,101 @@ NF4_API nf4_status nf4_embedding_backward(const void *ids, int32_t id_dtype, int
                                                    static_cast<nf4_dtype>(dtype), vocab, dim, scale, padding_id, grad,
                                                    static_cast<nf4_dtype>(grad_dtype), accumulate != 0, workspace,
                                                    stream_of(stream)));
+}
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t(1) << 30;  // tokens of a call, counted in 32 bits
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int32_t kMaxHeads = 65536, kMaxHeadDim = 512;
+
+nf4_status check_rotary_shape(const nf4_rotary_shape *sh) {
+    if (!sh) return NF4_ERR_NULL;
+    if (sh->batch < 0 || sh->tokens < 0 || sh->heads_q < 0 || sh->heads_q > kMaxHeads || sh->heads_k < 0 ||
+        sh->heads_k > kMaxHeads || sh->dim < 1 || sh->dim > kMaxHeadDim)
+        return NF4_ERR_SIZE;
+    if (sh->batch > kMaxRows || sh->tokens > kMaxRows || sh->batch * sh->tokens > kMaxRows) return NF4_ERR_SIZE;
+    if (sh->rotated < 2 || sh->rotated > sh->dim || sh->rotated % 2 != 0) return NF4_ERR_SIZE;
+    if (sh->layout != NF4_ROTARY_HALF && sh->layout != NF4_ROTARY_INTERLEAVED) return NF4_ERR_UNSUPPORTED;
+    if (!is_dtype(sh->dtype) || !is_dtype(sh->w_dtype)) return NF4_ERR_UNSUPPORTED;
+    if (!(sh->eps >= 0.0f) || !isfinite(sh->eps) || !isfinite(sh->w_offset) || !isfinite(sh->scale)) return NF4_ERR_SIZE;
+    return NF4_OK;
+}
+
+nf4_status check_heads(const nf4_heads *h, int32_t dtype) {
+    if (!h || !h->data) return NF4_ERR_NULL;
+    if (!aligned(h->data, dtype == NF4_F32 ? 4 : 2)) return NF4_ERR_ALIGN;
+    for (const int64_t stride : {h->batch_stride, h->token_stride, h->head_stride})
+        if (stride < 0 || stride > kMaxStride) return NF4_ERR_SIZE;
+    return NF4_OK;
+}
+
+nf4_status check_positions(const uint64_t *turns, const void *positions, int32_t dtype, int64_t batch_stride) {
+    if (dtype != NF4_I32 && dtype != NF4_I64) return NF4_ERR_UNSUPPORTED;
+    if (batch_stride < 0 || batch_stride > kMaxStride) return NF4_ERR_SIZE;
+    if (!turns) return NF4_ERR_NULL;
+    return aligned(turns, 8) && aligned(positions, dtype == NF4_I64 ? 8 : 4) ? NF4_OK : NF4_ERR_ALIGN;
+}
+
+}  // namespace
+
+NF4_API nf4_status nf4_rotary_forward(const nf4_rotary_shape *shape, const uint64_t *turns, const void *positions,
+                                      int32_t position_dtype, int64_t position_batch_stride, const nf4_heads *q,
+                                      const nf4_heads *k, const void *w_q, const void *w_k, const nf4_heads *q_out,
+                                      const nf4_heads *k_out, void *stream) {
+    nf4_status st = check_rotary_shape(shape);
+    if (st != NF4_OK) return st;
+    if (shape->batch * shape->tokens == 0 || (shape->heads_q == 0 && shape->heads_k == 0)) return NF4_OK;
+    if ((st = check_positions(turns, positions, position_dtype, position_batch_stride)) != NF4_OK) return st;
+    RotaryArgs a{};
+    a.turns = turns, a.positions = positions, a.i64 = position_dtype == NF4_I64;
+    a.position_batch_stride = position_batch_stride;
+    const nf4_heads *in[2] = {q, k}, *out[2] = {q_out, k_out};
+    const void *w[2] = {w_q, w_k};
+    for (int i = 0; i < 2; ++i) {
+        if ((i == 0 ? shape->heads_q : shape->heads_k) == 0) continue;
+        for (const nf4_heads *h : {in[i], out[i]})
+            if ((st = check_heads(h, shape->dtype)) != NF4_OK) return st;
+        if (!aligned(w[i], 16)) return NF4_ERR_ALIGN;
+        a.in[i] = *in[i], a.out[i] = *out[i], a.w[i] = w[i];
+    }
+    return launch_status(launch_rotary(*shape, a, false, nullptr, stream_of(stream)));
+}
+
+NF4_API size_t nf4_rotary_backward_workspace_size(const nf4_rotary_shape *shape) {
+    return check_rotary_shape(shape) == NF4_OK ? rotary_backward_workspace(*shape) : (size_t)-1;
+}
+
+NF4_API nf4_status nf4_rotary_backward(const nf4_rotary_shape *shape, const uint64_t *turns, const void *positions,
+                                       int32_t position_dtype, int64_t position_batch_stride, const nf4_heads *dq_out,
+                                       const nf4_heads *dk_out, const nf4_heads *q, const nf4_heads *k, const void *w_q,
+                                       const void *w_k, const nf4_heads *dq, const nf4_heads *dk, void *dw_q, void *dw_k,
+                                       void *workspace, size_t workspace_bytes, void *stream) {
+    nf4_status st = check_rotary_shape(shape);
+    if (st != NF4_OK) return st;
+    const bool rows = shape->batch * shape->tokens > 0;
+    if (rows && (st = check_positions(turns, positions, position_dtype, position_batch_stride)) != NF4_OK) return st;
+    RotaryArgs a{};
+    a.turns = turns, a.positions = positions, a.i64 = position_dtype == NF4_I64;
+    a.position_batch_stride = position_batch_stride;
+    const nf4_heads *in[2] = {dq_out, dk_out}, *x[2] = {q, k}, *out[2] = {dq, dk};
+    const void *w[2] = {w_q, w_k};
+    void *dw[2] = {dw_q, dw_k};
+    for (int i = 0; i < 2; ++i) {
+        if (dw[i] && !w[i]) return NF4_ERR_NULL;
+        if (!aligned(w[i], 16) || !aligned(dw[i], 16)) return NF4_ERR_ALIGN;
+        a.dw[i] = dw[i];
+        if (!rows || (i == 0 ? shape->heads_q : shape->heads_k) == 0) continue;
+        for (const nf4_heads *h : {in[i], out[i]})
+            if ((st = check_heads(h, shape->dtype)) != NF4_OK) return st;
+        if (w[i] && (st = check_heads(x[i], shape->dtype)) != NF4_OK) return st;
+        a.in[i] = *in[i], a.out[i] = *out[i], a.w[i] = w[i];
+        if (w[i]) a.x[i] = *x[i];
+    }
+    if (dw_q || dw_k) {
+        if ((st = check_workspace(rotary_backward_workspace(*shape), workspace, workspace_bytes)) != NF4_OK) return st;
+    } else if (!rows || (shape->heads_q == 0 && shape->heads_k == 0)) {
+        return NF4_OK;
+    }
+    return launch_status(launch_rotary(*shape, a, true, workspace, stream_of(stream)));
 }

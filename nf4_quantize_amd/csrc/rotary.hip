@@ -1,0 +1,412 @@
+// rotary.hip - norms of queries and keys for each head and their rotation by the
+// token's position, for gfx950: forward and backward. The formulas are in nf4.h
+// (nf4_rotary_forward, nf4_rotary_backward).
+//
+// All of it is bound by HBM: an element is read and written once (4 bytes in bf16),
+// the backward pass of a norm reads the input as well (6 bytes). A head lies in a
+// group of lanes, 2 V elements a lane: two vectors of V elements whose pairs are the
+// lane's own, so a rotation needs no other lane and a norm one sum over the group.
+#include <math.h>
+
+#include <type_traits>
+
+#include "training_internal.h"
+
+namespace nf4 {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+
+struct RotaryParams {
+    nf4_heads in[2], x[2], out[2];
+    const void *w[2];
+    const uint64_t *turns;
+    const void *positions;
+    int64_t position_batch_stride;
+    uint32_t tokens, items;    // tokens of a sequence; (token, part) pairs in all
+    uint32_t splits;           // parts of a token's heads
+    int32_t steps[2];          // rounds of heads of a token: queries, keys
+    int32_t heads[2];
+    int32_t dim, rotated;
+    int32_t lanes;             // of a head: a power of two
+    bool half, i64, w_bf16;
+    float sign;                // of the angle
+    float inv_dim, eps, off, scale;
+    float *partial;            // backward: [workgroups][2][dim], or NULL
+};
+
+// V elements as they lie in memory, at an address of their own size.
+template <typename T, int V> struct RawVec;
+template <> struct RawVec<Bf16, 8> { u32x4 v; };
+template <> struct RawVec<Bf16, 4> { u32x2 v; };
+template <> struct RawVec<Bf16, 2> { uint32_t v; };
+template <> struct RawVec<Bf16, 1> { uint16_t v; };
+template <> struct RawVec<float, 4> { f32x4 v; };
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+template <> struct RawVec<float, 2> { f32x2 v; };
+template <> struct RawVec<float, 1> { float v; };
+
+template <typename T, int V>
+__device__ __forceinline__ RawVec<T, V> load_vec(const T *p) {
+    return {*reinterpret_cast<const decltype(RawVec<T, V>::v) *>(p)};
+}
+template <int V>
+__device__ __forceinline__ void vec_values(const RawVec<Bf16, V> &r, float *x) {
+    if constexpr (V == 1) x[0] = bf16_lo(r.v);
+    else if constexpr (V == 2) x[0] = bf16_lo(r.v), x[1] = bf16_hi(r.v);
+    else
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) x[2 * j] = bf16_lo(r.v[j]), x[2 * j + 1] = bf16_hi(r.v[j]);
+}
+template <int V>
+__device__ __forceinline__ void vec_values(const RawVec<float, V> &r, float *x) {
+    if constexpr (V == 1) x[0] = r.v;
+    else
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = r.v[j];
+}
+template <int V>
+__device__ __forceinline__ void store_vec(Bf16 *p, const float *x) {
+    RawVec<Bf16, V> r;
+    if constexpr (V == 1) r.v = (uint16_t)(pack_bf16x2(x[0], 0.0f) & 0xFFFFu);
+    else if constexpr (V == 2) r.v = pack_bf16x2(x[0], x[1]);
+    else
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) r.v[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+    *reinterpret_cast<decltype(r.v) *>(p) = r.v;
+}
+template <int V>
+__device__ __forceinline__ void store_vec(float *p, const float *x) {
+    RawVec<float, V> r;
+    if constexpr (V == 1) r.v = x[0];
+    else
+#pragma unroll
+        for (int j = 0; j < V; ++j) r.v[j] = x[j];
+    *reinterpret_cast<decltype(r.v) *>(p) = r.v;
+}
+
+// Cosine and sine of phase 2^-32 turns. The phase is cut to an eighth of a turn
+// either side of a quarter, x in [-pi/4, pi/4], where sin x / x and cos x are
+// polynomials in x^2 (least largest error: 3e-9 and 5e-11).
+__device__ __forceinline__ void cos_sin(uint32_t phase, float &c, float &s) {
+    const uint32_t quarter = (phase + 0x20000000u) >> 30;
+    const float x = (float)(int32_t)(phase - (quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float t = x * x;
+    const float sx = x * fmaf(t, fmaf(t, fmaf(t, -0.00019504022202454507f, 0.008332036435604095f), -0.16666650772094727f), 1.0f);
+    const float cx =
+        fmaf(t, fmaf(t, fmaf(t, fmaf(t, 2.4379929527640343e-05f, -0.0013886619126424193f), 0.04166661575436592f), -0.5f), 1.0f);
+    const float cc = (quarter & 1) ? sx : cx, ss = (quarter & 1) ? cx : sx;
+    c = ((quarter + 1) & 2) ? -cc : cc;
+    s = (quarter & 2) ? -ss : ss;
+}
+
+// Where a lane's 2 V elements lie in a head, and which pairs they are.
+struct Unit {
+    int lo, hi, pair;         // first element of each vector; the first pair, in `rotated` / 2
+    bool live_lo, live_hi;
+};
+template <int V>
+__device__ __forceinline__ Unit unit_of(const RotaryParams &p, int u) {
+    const int rotated_units = p.half ? p.rotated / 2 / V : 0;
+    Unit r;
+    r.pair = u * V;
+    if (p.half && u < rotated_units) {
+        r.lo = u * V, r.hi = p.rotated / 2 + u * V;
+    } else {
+        r.lo = (p.half ? p.rotated : 0) + (u - rotated_units) * 2 * V, r.hi = r.lo + V;
+    }
+    r.live_lo = r.lo < p.dim, r.live_hi = r.hi < p.dim;
+    return r;
+}
+
+enum RotaryKind { kTurn, kNormTurn, kNormTurnBack };
+
+// A wave takes a token and every splits-th round of its heads: 64 / lanes heads a
+// round, queries first. Its cosines and sines serve all of them. U units a lane.
+template <typename T, int V, int U, RotaryKind kKind>
+__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p) {
+    constexpr bool kBack = kKind == kNormTurnBack, kNorm = kKind != kTurn;
+    constexpr int E = 2 * V;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int in_group = lane & (p.lanes - 1), group = lane / p.lanes, groups = 64 / p.lanes;
+    Unit unit[U];
+    float w[2][kNorm ? U : 1][E], sums[2][kBack ? U : 1][E];
+#pragma unroll
+    for (int u = 0; u < U; ++u) unit[u] = unit_of<V>(p, in_group + u * 64);
+    if constexpr (kNorm)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const int d = j < V ? unit[u].lo + j : unit[u].hi + j - V;
+                    const bool live = p.w[i] != nullptr && (j < V ? unit[u].live_lo : unit[u].live_hi);
+                    w[i][u][j] = 1.0f;
+                    if (live) w[i][u][j] = p.off + (p.w_bf16 ? load1(static_cast<const Bf16 *>(p.w[i]) + d)
+                                                             : load1(static_cast<const float *>(p.w[i]) + d));
+                    if constexpr (kBack) sums[i][u][j] = 0.0f;
+                }
+    for (uint32_t item = blockIdx.x * kWaves + wave; item < p.items; item += gridDim.x * kWaves) {
+        const uint32_t row = item / p.splits, part = item % p.splits;
+        const uint32_t b = row / p.tokens, t = row % p.tokens;
+        int64_t position = t;
+        if (p.positions) {
+            const int64_t at = (int64_t)b * p.position_batch_stride + t;
+            position = p.i64 ? static_cast<const int64_t *>(p.positions)[at] : static_cast<const int32_t *>(p.positions)[at];
+        }
+        float c[U][V], s[U][V];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                c[u][j] = 1.0f, s[u][j] = 0.0f;
+                if (unit[u].pair + j < p.rotated / 2) {
+                    const uint64_t phase = (uint64_t)position * p.turns[unit[u].pair + j] + 0x80000000u;
+                    cos_sin((uint32_t)(phase >> 32), c[u][j], s[u][j]);
+                    c[u][j] *= p.scale, s[u][j] *= p.scale * p.sign;
+                }
+            }
+        auto turn = [&](float (&x)[U][E]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (p.half || V == 1) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float a = x[u][j], d = x[u][V + j];
+                        x[u][j] = a * c[u][j] - d * s[u][j], x[u][V + j] = d * c[u][j] + a * s[u][j];
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float a = x[u][2 * j], d = x[u][2 * j + 1];
+                        x[u][2 * j] = a * c[u][j] - d * s[u][j], x[u][2 * j + 1] = d * c[u][j] + a * s[u][j];
+                    }
+                }
+            }
+        };
+        auto load = [&](const nf4_heads &h, int head, float (&x)[U][E]) {
+            const T *from = static_cast<const T *>(h.data) + (b * h.batch_stride + t * h.token_stride + head * h.head_stride);
+            RawVec<T, V> lo[U], hi[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                lo[u] = load_vec<T, V>(from + (unit[u].live_lo ? unit[u].lo : 0));
+                hi[u] = load_vec<T, V>(from + (unit[u].live_hi ? unit[u].hi : 0));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                vec_values<V>(lo[u], x[u]);
+                vec_values<V>(hi[u], x[u] + V);
+#pragma unroll
+                for (int j = 0; j < E; ++j) x[u][j] = (j < V ? unit[u].live_lo : unit[u].live_hi) ? x[u][j] : 0.0f;
+            }
+        };
+        auto heads = [&](auto which, int round) {
+            constexpr int i = decltype(which)::value;
+            const int head = round * groups + group;
+            const bool live = head < p.heads[i];
+            const int from = live ? head : p.heads[i] - 1;
+            float x[U][E];
+            load(p.in[i], from, x);
+            if constexpr (kKind == kTurn) {
+                turn(x);
+            } else if constexpr (kKind == kNormTurn) {
+                if (p.w[i]) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int j = 0; j < E; ++j) sum += x[u][j] * x[u][j];
+                    const float r = 1.0f / sqrtf(group_sum(sum, p.lanes) * p.inv_dim + p.eps);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int j = 0; j < E; ++j) x[u][j] *= r * w[i][u][j];
+                }
+                turn(x);
+            } else {
+                turn(x);  // the gradient of the normed head
+                if (p.w[i]) {
+                    float n[U][E];
+                    load(p.x[i], from, n);
+                    float sum = 0.0f, dot = 0.0f;
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int j = 0; j < E; ++j) {
+                            sum += n[u][j] * n[u][j];
+                            dot += x[u][j] * w[i][u][j] * n[u][j];
+                        }
+                    const float r = 1.0f / sqrtf(group_sum(sum, p.lanes) * p.inv_dim + p.eps);
+                    const float mean = group_sum(dot, p.lanes) * p.inv_dim * r;
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int j = 0; j < E; ++j) {
+                            const float nr = n[u][j] * r;
+                            sums[i][u][j] += live ? x[u][j] * nr : 0.0f;
+                            x[u][j] = r * (x[u][j] * w[i][u][j] - nr * mean);
+                        }
+                }
+            }
+            if (!live) return;
+            const nf4_heads &h = p.out[i];
+            T *to = static_cast<T *>(h.data) + (b * h.batch_stride + t * h.token_stride + head * h.head_stride);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (unit[u].live_lo) store_vec<V>(to + unit[u].lo, x[u]);
+                if (unit[u].live_hi) store_vec<V>(to + unit[u].hi, x[u] + V);
+            }
+        };
+        int step = part;
+        for (; step < p.steps[0]; step += p.splits) heads(std::integral_constant<int, 0>{}, step);
+        for (; step < p.steps[0] + p.steps[1]; step += p.splits) heads(std::integral_constant<int, 1>{}, step - p.steps[0]);
+    }
+    if constexpr (kBack) {
+        if (!p.partial) return;
+        // the workgroup's sums: the wave's groups, then its waves
+        __shared__ float part[kWaves][2][U * 64 * E];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    float x = sums[i][u][j];
+                    for (int o = p.lanes; o < 64; o *= 2) x += __shfl_xor(x, o, 64);
+                    const int d = j < V ? unit[u].lo + j : unit[u].hi + j - V;
+                    if (group == 0 && (j < V ? unit[u].live_lo : unit[u].live_hi)) part[wave][i][d] = x;
+                }
+        __syncthreads();
+        for (int k = threadIdx.x; k < 2 * p.dim; k += kThreads) {
+            const int i = k / p.dim, d = k % p.dim;
+            float x = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kWaves; ++v) x += part[v][i][d];
+            p.partial[(int64_t)blockIdx.x * 2 * p.dim + k] = x;
+        }
+    }
+}
+
+// The weights' gradients: columns of the workgroups' partial sums, 16 columns a
+// workgroup and 16 rows at a time.
+__global__ __launch_bounds__(kThreads) void rotary_sums_kernel(const float *partial, int32_t rows, int32_t dim, bool bf16,
+                                                               void *dw_q, void *dw_k) {
+    __shared__ float part[16][17];
+    const int col = threadIdx.x % 16, first = threadIdx.x / 16, k = blockIdx.x * 16 + col;
+    float x = 0.0f;
+    if (k < 2 * dim)
+        for (int r = first; r < rows; r += 16) x += partial[(int64_t)r * 2 * dim + k];
+    part[first][col] = x;
+    __syncthreads();
+    if (first != 0 || k >= 2 * dim) return;
+    x = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) x += part[r][col];
+    void *dw = k < dim ? dw_q : dw_k;
+    if (!dw) return;
+    const int d = k < dim ? k : k - dim;
+    if (bf16) store1(static_cast<Bf16 *>(dw) + d, x);
+    else store1(static_cast<float *>(dw) + d, x);
+}
+
+constexpr uint32_t kMostGroups = 1024;  // workgroups of a backward pass with weights: rows of partial sums
+
+// Workgroups of a call; p.steps, p.splits and p.items follow.
+uint32_t plan(RotaryParams &p, uint32_t rows, int units, bool sums) {
+    p.lanes = 1;
+    while (p.lanes < units && p.lanes < 64) p.lanes *= 2;
+    const int groups = 64 / p.lanes;
+    p.steps[0] = (p.heads[0] + groups - 1) / groups;
+    p.steps[1] = (p.heads[1] + groups - 1) / groups;
+    const uint32_t steps = p.steps[0] + p.steps[1];
+    // few tokens: a token's heads are shared by several waves
+    constexpr uint32_t kWant = 4096;
+    p.splits = rows >= kWant ? 1 : (kWant + rows - 1) / rows;
+    if (p.splits > steps) p.splits = steps;
+    p.items = rows * p.splits;
+    const uint32_t wgs = (p.items + kWaves - 1) / kWaves;
+    const uint32_t most = sums ? kMostGroups : 16384;
+    return wgs < most ? wgs : most;
+}
+
+template <typename T, int V, int U>
+void launch_units(const RotaryParams &p, RotaryKind kind, uint32_t wgs, hipStream_t s) {
+    const dim3 grid(wgs), block(kThreads);
+    if (kind == kTurn) rotary_kernel<T, V, U, kTurn><<<grid, block, 0, s>>>(p);
+    else if (kind == kNormTurn) rotary_kernel<T, V, U, kNormTurn><<<grid, block, 0, s>>>(p);
+    else rotary_kernel<T, V, U, kNormTurnBack><<<grid, block, 0, s>>>(p);
+}
+
+// Elements of a vector: the widest up to 16 bytes that divides the head, the two
+// halves of its rotated part, every stride, and the addresses.
+int vector_of(const nf4_rotary_shape &sh, const RotaryArgs &a) {
+    const int size = sh.dtype == NF4_F32 ? 4 : 2;
+    int v = 16 / size;
+    for (; v > 1; v /= 2) {
+        bool fits = sh.dim % v == 0 && (sh.layout == NF4_ROTARY_INTERLEAVED || sh.rotated / 2 % v == 0);
+        for (int i = 0; i < 2; ++i)
+            for (const nf4_heads *h : {&a.in[i], &a.x[i], &a.out[i]})
+                if (h->data)
+                    fits = fits && reinterpret_cast<uintptr_t>(h->data) % (v * size) == 0 && h->batch_stride % v == 0 &&
+                           h->token_stride % v == 0 && h->head_stride % v == 0;
+        if (fits) break;
+    }
+    return v;
+}
+
+int units_of(const nf4_rotary_shape &sh, int v) {
+    if (sh.layout == NF4_ROTARY_INTERLEAVED) return (sh.dim + 2 * v - 1) / (2 * v);
+    return sh.rotated / 2 / v + (sh.dim - sh.rotated + 2 * v - 1) / (2 * v);
+}
+
+}  // namespace
+
+size_t rotary_backward_workspace(const nf4_rotary_shape &sh) {
+    return (size_t)kMostGroups * 2 * sh.dim * sizeof(float);
+}
+
+hipError_t launch_rotary(const nf4_rotary_shape &sh, const RotaryArgs &a, bool backward, void *workspace,
+                         hipStream_t s) {
+    RotaryParams p{};
+    for (int i = 0; i < 2; ++i) p.in[i] = a.in[i], p.x[i] = a.x[i], p.out[i] = a.out[i], p.w[i] = a.w[i];
+    p.turns = a.turns, p.positions = a.positions, p.i64 = a.i64;
+    p.position_batch_stride = a.position_batch_stride;
+    p.heads[0] = sh.heads_q, p.heads[1] = sh.heads_k;
+    p.dim = sh.dim, p.rotated = sh.rotated, p.half = sh.layout == NF4_ROTARY_HALF;
+    p.w_bf16 = sh.w_dtype == NF4_BF16;
+    p.sign = backward ? -1.0f : 1.0f;
+    p.inv_dim = 1.0f / (float)sh.dim, p.eps = sh.eps, p.off = sh.w_offset, p.scale = sh.scale;
+    const bool norm = p.w[0] || p.w[1], sums = a.dw[0] || a.dw[1];
+    p.partial = sums ? static_cast<float *>(workspace) : nullptr;
+    const RotaryKind kind = !norm ? kTurn : backward ? kNormTurnBack : kNormTurn;
+    const uint32_t rows = sh.heads_q + sh.heads_k > 0 ? (uint32_t)(sh.batch * sh.tokens) : 0;
+    uint32_t wgs = 0;
+    if (rows > 0) {
+        p.tokens = (uint32_t)sh.tokens;
+        const int v = vector_of(sh, a), units = units_of(sh, v);
+        wgs = plan(p, rows, units, sums);
+        if (sh.dtype == NF4_F32) {
+            if (v == 4) launch_units<float, 4, 1>(p, kind, wgs, s);
+            else if (v == 2 && units <= 64) launch_units<float, 2, 1>(p, kind, wgs, s);
+            else if (v == 2) launch_units<float, 2, 2>(p, kind, wgs, s);
+            else if (units <= 64) launch_units<float, 1, 1>(p, kind, wgs, s);
+            else launch_units<float, 1, 4>(p, kind, wgs, s);
+        } else {
+            if (v == 8) launch_units<Bf16, 8, 1>(p, kind, wgs, s);
+            else if (v == 4) launch_units<Bf16, 4, 1>(p, kind, wgs, s);
+            else if (v == 2 && units <= 64) launch_units<Bf16, 2, 1>(p, kind, wgs, s);
+            else if (v == 2) launch_units<Bf16, 2, 2>(p, kind, wgs, s);
+            else if (units <= 64) launch_units<Bf16, 1, 1>(p, kind, wgs, s);
+            else launch_units<Bf16, 1, 4>(p, kind, wgs, s);
+        }
+        const hipError_t r = hipGetLastError();
+        if (r != hipSuccess) return r;
+    }
+    if (!sums) return hipSuccess;
+    rotary_sums_kernel<<<dim3((2 * sh.dim + 15) / 16), dim3(kThreads), 0, s>>>(p.partial, (int32_t)wgs, sh.dim, p.w_bf16,
+                                                                             a.dw[0], a.dw[1]);
+    return hipGetLastError();
+}
+
+}  // namespace nf4

@@ -1,5 +1,5 @@
 // training_internal.h - internal declarations of the training-step operators
-// (optimizer.hip, residual_norm.hip, embedding.hip); their contracts are in
+// (optimizer.hip, residual_norm.hip, embedding.hip, rotary.hip); their contracts are in
 // nf4.h. Shared by the library's own sources only.
 #pragma once
 
@@ -47,6 +47,20 @@ hipError_t launch_embedding_backward(const void *ids, bool i64, int64_t tokens, 
                                      nf4_dtype dt, int64_t vocab, int64_t dim, float scale,
                                      int64_t padding_id, void *grad, nf4_dtype gt, bool accumulate,
                                      void *workspace, hipStream_t s);
+
+// Queries and keys (index 0, 1). `x`: the forward's inputs (backward with weights only).
+struct RotaryArgs {
+    const uint64_t *turns;
+    const void *positions;
+    bool i64;
+    int64_t position_batch_stride;
+    nf4_heads in[2], x[2], out[2];
+    const void *w[2];
+    void *dw[2];
+};
+size_t rotary_backward_workspace(const nf4_rotary_shape &sh);
+hipError_t launch_rotary(const nf4_rotary_shape &sh, const RotaryArgs &a, bool backward, void *workspace,
+                         hipStream_t s);
 
 // ---- device helpers ----
 

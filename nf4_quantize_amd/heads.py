@@ -1,0 +1,376 @@
+"""Between the query and key projections and attention: the norm of each head and
+the rotation by the token's position in one pass (``NF4Rotary``, ``rotary``).
+Formulas and limits are in ``include/nf4.h`` (nf4_rotary_forward,
+nf4_rotary_backward); every step of the computation runs in the library's HIP
+kernels, torch supplies device memory and the current stream.
+"""
+import ctypes
+import math
+from fractions import Fraction
+
+import nf4_quantize_amd as _nq
+
+from .training import _addr, _changed, _code, _index_code, _size, _stream
+
+LAYOUTS = {"half": 0, "interleaved": 1}
+TWO_PI = Fraction("6.283185307179586476925286766559005768394338798750")
+
+
+class nf4_rotary_shape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("tokens", ctypes.c_int64), ("heads_q", ctypes.c_int32),
+                ("heads_k", ctypes.c_int32), ("dim", ctypes.c_int32), ("rotated", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("w_offset", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class nf4_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+def declare(L):
+    """argtypes and restypes of this module's entry points."""
+    p, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+    shape, heads = ctypes.POINTER(nf4_rotary_shape), ctypes.POINTER(nf4_heads)
+    for name, restype, args in (
+            ("nf4_rotary_forward", i32, [shape, p, p, i32, i64, heads, heads, p, p, heads, heads, p]),
+            ("nf4_rotary_backward_workspace_size", sz, [shape]),
+            ("nf4_rotary_backward", i32, [shape, p, p, i32, i64] + [heads] * 4 + [p, p, heads, heads, p, p, p, sz, p])):
+        fn = getattr(L, name)
+        fn.restype, fn.argtypes = restype, args
+
+
+# ------------------------------------------------------------------ frequencies
+
+# The keys of a scaling besides its kind, with their defaults (None: required).
+SCALINGS = {
+    "linear": dict(factor=None),
+    "ntk": dict(factor=None),
+    "yarn": dict(factor=None, length=None, slow=1.0, fast=32.0, attention=None),
+    "wavelength": dict(factor=None, length=None, low=1.0, high=4.0),
+}
+
+
+def rotary_frequencies(dim, base=10000.0, scaling=None):
+    """Radians a position for each pair of a head's ``dim`` rotated elements, f_i =
+    base^(-2i / dim), and the factor of cosine and sine: (list, float).
+
+    ``scaling`` stretches them over ``factor`` times the context, dict(kind=...):
+
+    - ``linear``: f_i / factor;
+    - ``ntk``: the base times factor^(dim / (dim - 2)): the fastest pair stays, the
+      slowest is divided by the factor;
+    - ``yarn``: pairs that turn more than ``fast`` (32) times in the first context of
+      ``length`` positions stay, those below ``slow`` (1) turns are divided by the
+      factor, those between are blended by their index; cosine and sine are scaled by
+      ``attention`` (0.1 ln factor + 1);
+    - ``wavelength``: the same with a blend by the number of turns, between ``low`` (1)
+      and ``high`` (4), and no factor of cosine and sine."""
+    if dim < 2 or dim % 2:
+        raise ValueError(f"rotated elements come in pairs, got {dim}")
+    if not (math.isfinite(base) and base > 0):
+        raise ValueError(f"base {base}")
+    plain = [base ** (-2.0 * i / dim) for i in range(dim // 2)]
+    if scaling is None:
+        return plain, 1.0
+    given = dict(scaling)
+    kind = given.pop("kind", None)
+    if kind not in SCALINGS:
+        raise ValueError(f"scaling kind {kind!r}: one of {sorted(SCALINGS)}")
+    opts = {**SCALINGS[kind], **given}
+    if set(opts) != set(SCALINGS[kind]):
+        raise ValueError(f"{kind} scaling takes {sorted(SCALINGS[kind])}, got {sorted(given)}")
+    for name, x in opts.items():
+        if x is None and name != "attention":
+            raise ValueError(f"{kind} scaling needs {name}")
+        if x is not None and not (math.isfinite(x) and x > 0):
+            raise ValueError(f"{name} {x}")
+    factor = float(opts["factor"])
+    if kind == "linear":
+        return [f / factor for f in plain], 1.0
+    if kind == "ntk":
+        wide = base * factor ** (dim / (dim - 2.0)) if dim > 2 else base
+        return [wide ** (-2.0 * i / dim) for i in range(dim // 2)], 1.0
+    length = float(opts["length"])
+    if kind == "yarn":
+        if base == 1.0 or opts["slow"] >= opts["fast"]:
+            raise ValueError("yarn scaling: base is not 1, slow is below fast")
+
+        def place(turns):  # the index of the pair that turns so often in the first context
+            return dim * math.log(length / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        low, high = max(math.floor(place(opts["fast"])), 0), min(math.ceil(place(opts["slow"])), dim - 1)
+        ramp = [min(max((i - low) / max(high - low, 1e-3), 0.0), 1.0) for i in range(dim // 2)]
+        attention = opts["attention"]
+        if attention is None:
+            attention = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+        return [f / factor * x + f * (1 - x) for f, x in zip(plain, ramp)], float(attention)
+    if opts["low"] >= opts["high"]:
+        raise ValueError("wavelength scaling: low is below high")
+    out = []
+    for f in plain:
+        turns = length * f / (2 * math.pi)
+        x = min(max((turns - opts["low"]) / (opts["high"] - opts["low"]), 0.0), 1.0)
+        out.append(f / factor * (1 - x) + f * x)
+    return out, 1.0
+
+
+class NF4Rotary:
+    """The rotation that a model keeps: ``dim`` rotated elements a head (the first
+    ones; a head may have more), their pairs' ``layout`` ("half": element i with
+    i + dim / 2, "interleaved": 2i with 2i + 1) and frequencies
+    (``rotary_frequencies``, or given as ``frequencies`` with ``scale``, the factor
+    of cosine and sine). There is no table over positions: any int32 or int64
+    position is taken, the angle's error is below 4e-10 radians up to 2^31."""
+
+    def __init__(self, dim, base=10000.0, layout="half", scaling=None, frequencies=None, scale=None, device="cuda"):
+        import torch
+
+        if layout not in LAYOUTS:
+            raise ValueError(f"layout {layout!r}: one of {sorted(LAYOUTS)}")
+        if frequencies is None:
+            frequencies, attention = rotary_frequencies(dim, base, scaling)
+            scale = attention if scale is None else scale
+        elif scaling is not None:
+            raise ValueError("frequencies are given, or scaled")
+        self.dim, self.layout = int(dim), layout
+        self.frequencies, self.scale = [float(f) for f in frequencies], 1.0 if scale is None else float(scale)
+        if self.dim < 2 or self.dim % 2 or len(self.frequencies) != self.dim // 2:
+            raise ValueError(f"{len(self.frequencies)} frequencies for {dim} rotated elements")
+        if not all(map(math.isfinite, self.frequencies + [self.scale])):
+            raise ValueError("frequencies and scale are finite")
+        # in integers: 64-bit floats would leave far positions off by 2^-53 of their angle
+        turns = [round(Fraction(f) / TWO_PI * 2 ** 64) % 2 ** 64 for f in self.frequencies]
+        self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns], dtype=torch.int64).to(device)
+
+
+# ------------------------------------------------------------------ the calls
+
+def _strides(x):
+    """(batch, token, head) strides of [tokens x heads x dim] or [batch x tokens x heads x dim]; a
+    dimension of one element has none."""
+    st = [0 if n < 2 else s for n, s in zip(x.shape, x.stride())]
+    if st[-1] not in (0, 1):
+        raise ValueError(f"a head's elements are consecutive, got strides {x.stride()}")
+    return (0, *st[:2]) if len(st) == 3 else st[:3]
+
+
+def _heads(x):
+    return None if x is None else nf4_heads(x.data_ptr(), *_strides(x))
+
+
+def _extent(x):
+    """The bytes between the addresses of a tensor's first and last element."""
+    last = sum((n - 1) * s for n, s in zip(x.shape, x.stride()))
+    return x.data_ptr(), x.data_ptr() + (last + 1) * x.element_size()
+
+
+def _apart(x, y):
+    """Whether two tensors share no element: by their addresses, or as slices of the same rows (the
+    heads of queries and of keys in one projection's output)."""
+    if x.numel() == 0 or y.numel() == 0:
+        return True
+    (a0, a1), (b0, b1) = _extent(x), _extent(y)
+    if a1 <= b0 or b1 <= a0:
+        return True
+    sx, sy = _strides(x), _strides(y)
+    if x.dtype != y.dtype or sx[:2] != sy[:2] or x.shape[:-2] != y.shape[:-2]:
+        return False
+    # every token is a block of its own: no two blocks' starts are closer than the shortest stride
+    token = min([s for s in sx[:2] if s] or [1 << 62]) * x.element_size()
+    wide = [((t.shape[-2] - 1) * s[2] + t.shape[-1]) * t.element_size() for t, s in ((x, sx), (y, sy))]
+    gap = abs(b0 - a0)
+    first = wide[0] if a0 < b0 else wide[1]
+    second = wide[1] if a0 < b0 else wide[0]
+    return gap >= first and gap + second <= token and all(not s or s % (token // x.element_size()) == 0 for s in sx[:2])
+
+
+def _check_out(out, own, others, what):
+    """An output: no element twice, its own input or apart from every input."""
+    order = sorted((s, n) for n, s in zip(out.shape, out.stride()) if n > 1)
+    reach = 1
+    for s, n in order:
+        if s < reach:
+            raise ValueError(f"{what}: elements that share memory")
+        reach += s * (n - 1)
+    if own is not None and out.data_ptr() == own.data_ptr() and _strides(out) == _strides(own):
+        others = [t for t in others if t is not own]
+    if not all(_apart(out, t) for t in others):
+        raise ValueError(f"{what} is the input itself, or memory that no input has")
+
+
+def _check(rope, positions, pairs, weights):
+    """Checks (tensor of queries, tensor of keys) pairs and weights; returns (shape without the norm's
+    numbers, positions' code, their batch stride, the device's index)."""
+    first = pairs[0][0] if pairs[0][0] is not None else pairs[0][1]
+    if first is None:
+        raise ValueError("neither queries nor keys")
+    if first.dim() not in (3, 4):
+        raise ValueError(f"[tokens x heads x dim] or [batch x tokens x heads x dim], got {tuple(first.shape)}")
+    index, lead, dim = first.get_device(), first.shape[:-2], first.shape[-1]
+    if index < 0:
+        raise ValueError("device tensors")
+    heads = [0, 0]
+    for pair in pairs:
+        for i, x in enumerate(pair):
+            if x is None:
+                continue
+            if x.shape[:-2] != lead or x.shape[-1] != dim or x.dtype != first.dtype or x.get_device() != index:
+                raise ValueError(f"queries, keys and their gradients differ in their heads alone: {tuple(first.shape)} "
+                                 f"{first.dtype} {first.device} and {tuple(x.shape)} {x.dtype} {x.device}")
+            if heads[i] and heads[i] != x.shape[-2]:
+                raise ValueError(f"{heads[i]} and {x.shape[-2]} heads")
+            heads[i] = x.shape[-2]
+    if rope.dim > dim:
+        raise ValueError(f"{rope.dim} rotated elements in heads of {dim}")
+    if rope.turns.get_device() != index:
+        raise ValueError(f"the rotation is on {rope.turns.device}, the heads on {first.device}")
+    wt = first.dtype
+    given = [w for w in weights if w is not None]
+    for w in given:
+        if w.shape != (dim,) or w.dtype != given[0].dtype or w.get_device() != index or not w.is_contiguous():
+            raise ValueError(f"norm weights are ({dim},), contiguous, of one dtype, on {first.device}")
+        wt = w.dtype
+    tokens, batch = lead[-1], (lead[0] if len(lead) == 2 else 1)
+    code, stride = 1, 0
+    if positions is not None:
+        code = _index_code(positions)
+        if positions.shape not in (lead, lead[-1:]):
+            raise ValueError(f"positions {tuple(positions.shape)} for tokens {tuple(lead)}")
+        if positions.get_device() != index or (tokens > 1 and positions.stride(-1) != 1):
+            raise ValueError("positions: consecutive, on the heads' device")
+        if positions.dim() == 2 and batch > 1:
+            stride = positions.stride(0)
+    shape = nf4_rotary_shape(batch, tokens, heads[0], heads[1], dim, rope.dim, LAYOUTS[rope.layout], _code(first.dtype),
+                             _code(wt), 0.0, 0.0, rope.scale)
+    return shape, code, stride, index
+
+
+def _like(x):
+    """An output in x's order in memory, without its gaps."""
+    import torch
+
+    return None if x is None else torch.empty_like(x)
+
+
+def rotary_forward(q, k, positions, rope, w_q=None, w_k=None, eps=1e-6, w_offset=0.0, q_out=None, k_out=None):
+    """Queries and keys, rotated by their tokens' positions, and before that normed
+    head by head where there are weights (nf4_rotary_forward). ``q``, ``k``
+    [tokens x heads x dim] or [batch x tokens x heads x dim], bfloat16 or float32,
+    with any strides but a head's own (a transposed view, a slice of one projection's
+    output); ``k`` may be None. ``positions``: int32 or int64, one for each token
+    (``[batch x tokens]``), or ``[tokens]`` that the sequences share; None: 0, 1, ...
+    in each sequence. ``rope``: an NF4Rotary. Returns (q', k'); ``q_out=q`` and
+    ``k_out=k`` rotate in place."""
+    if q is None:
+        raise ValueError("queries")
+    shape, code, stride, index = _check(rope, positions, ((q, k), (q_out, k_out)), (w_q, w_k))
+    if (k is None and (w_k is not None or k_out is not None)):
+        raise ValueError("weights and an output of keys, without keys")
+    shape.eps, shape.w_offset = eps, w_offset
+    inputs = [t for t in (q, k) if t is not None]
+    given = []
+    for out, own, what in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if out is not None:
+            _check_out(out, own, inputs, what)
+            given.append(out)
+    if len(given) == 2 and not _apart(*given):
+        raise ValueError("q_out and k_out share memory")
+    if not all(_range_apart(out, w) for out in given for w in (w_q, w_k) if w is not None):
+        raise ValueError("an output shares memory with a weight")
+    q_out = _like(q) if q_out is None else q_out
+    k_out = _like(k) if k_out is None else k_out
+    st = _nq.lib().nf4_rotary_forward(ctypes.byref(shape), rope.turns.data_ptr(), _addr(positions), code, stride, _heads(q),
+                                      _heads(k), _addr(w_q), _addr(w_k), _heads(q_out), _heads(k_out), _stream(index))
+    _nq._check(st, "nf4_rotary_forward")
+    if given:
+        _changed(given)
+    return q_out, k_out
+
+
+def _range_apart(x, y):
+    (a0, a1), (b0, b1) = _extent(x), _extent(y)
+    return x.numel() == 0 or y.numel() == 0 or a1 <= b0 or b1 <= a0
+
+
+def rotary_backward(dq_out, dk_out, positions, rope, q=None, k=None, w_q=None, w_k=None, eps=1e-6, w_offset=0.0,
+                    want=(True, True)):
+    """Gradients of rotary_forward from those of its outputs (either may be None) and,
+    where there are weights, its inputs: (dq, dk, dw_q, dw_k), None where an input is
+    absent or ``want`` (of dw_q and dw_k) is false."""
+    import torch
+
+    for d, x, w, what in ((dq_out, q, w_q, "queries"), (dk_out, k, w_k, "keys")):
+        if w is not None and d is not None and x is None:
+            raise ValueError(f"the gradient of normed {what} needs them")
+        if w is not None and d is None:
+            raise ValueError(f"weights of {what} without their gradient")
+    live = ((dq_out, dk_out), (q if w_q is not None else None, k if w_k is not None else None))
+    shape, code, stride, index = _check(rope, positions, live, (w_q, w_k))
+    shape.eps, shape.w_offset = eps, w_offset
+    dq, dk = _like(dq_out), _like(dk_out)
+    dw = [torch.empty_like(w) if w is not None and ask else None for w, ask in zip((w_q, w_k), want)]
+    L, ws, size = _nq.lib(), None, 0
+    if dw[0] is not None or dw[1] is not None:
+        size = _size(L.nf4_rotary_backward_workspace_size(ctypes.byref(shape)), "nf4_rotary_backward_workspace_size")
+        ws = torch.empty(size, dtype=torch.uint8, device=rope.turns.device)
+    st = L.nf4_rotary_backward(ctypes.byref(shape), rope.turns.data_ptr(), _addr(positions), code, stride, _heads(dq_out),
+                               _heads(dk_out), _heads(live[1][0]), _heads(live[1][1]), _addr(w_q), _addr(w_k), _heads(dq),
+                               _heads(dk), _addr(dw[0]), _addr(dw[1]), _addr(ws), size, _stream(index))
+    _nq._check(st, "nf4_rotary_backward")
+    return dq, dk, dw[0], dw[1]
+
+
+# ------------------------------------------------------------------ autograd
+
+_FUNCTION = None
+
+
+def _function():
+    """The autograd function (made on first use: importing this module does not
+    import torch)."""
+    global _FUNCTION
+    if _FUNCTION is not None:
+        return _FUNCTION
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class RotaryFunction(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, positions, rope, w_q, w_k, eps, w_offset):
+            q = _dense_heads(q)
+            k = None if k is None else _dense_heads(k)
+            ctx.save_for_backward(q if w_q is not None else None, k if w_k is not None else None, positions, w_q, w_k)
+            ctx.rope, ctx.eps, ctx.w_offset = rope, eps, w_offset
+            ctx.set_materialize_grads(False)
+            return rotary_forward(q, k, positions, rope, w_q, w_k, eps, w_offset)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dq_out, dk_out):
+            q, k, positions, w_q, w_k = ctx.saved_tensors
+            need = ctx.needs_input_grad
+            ask_q, ask_k = need[0] or need[4], need[1] or need[5]
+            dq_out = None if dq_out is None or not ask_q else _dense_heads(dq_out)
+            dk_out = None if dk_out is None or not ask_k else _dense_heads(dk_out)
+            if dq_out is None and dk_out is None:
+                return (None,) * 8
+            dq, dk, dw_q, dw_k = rotary_backward(
+                dq_out, dk_out, positions, ctx.rope, q, k, None if dq_out is None else w_q,
+                None if dk_out is None else w_k, ctx.eps, ctx.w_offset, want=(need[4], need[5]))
+            return dq if need[0] else None, dk if need[1] else None, None, None, dw_q, dw_k, None, None
+
+    _FUNCTION = RotaryFunction
+    return _FUNCTION
+
+
+def _dense_heads(x):
+    """x, or a copy where a head's elements are not consecutive (a broadcast gradient)."""
+    return x if x.shape[-1] < 2 or x.stride(-1) == 1 else x.contiguous()
+
+
+def rotary(q, k, positions, rope, w_q=None, w_k=None, eps=1e-6, w_offset=0.0):
+    """Differentiable rotation of queries and keys, with the norms of their heads where
+    there are weights: (q', k') of rotary_forward. Gradients flow to q, k and both
+    weights."""
+    return _function().apply(q, k, positions, rope, w_q, w_k, float(eps), float(w_offset))
