@@ -692,6 +692,62 @@ nf4_status nf4_rotary_backward(const nf4_rotary_shape *shape, const uint64_t *tu
                                const nf4_heads *dk, void *dw_q, void *dw_k, void *workspace,
                                size_t workspace_bytes, void *stream);
 
+/* The Muon step over a list of adapter matrices. For a matrix [rows x cols]:
+ *   m' = mu m + (1 - mu) g,  u = mu m' + (1 - mu) g with nesterov, else m'
+ *   X  = u / max(|u|, eps),  |u| the root of the sum of squares
+ *   `iterations` times  X = a X + b (X X^T) X + c (X X^T)^2 X
+ *   w' = w (1 - lr weight_decay) - lr scale X
+ * m' and w' are rounded once to their types; u is taken from the fp32 m'. With
+ * (a, b, c) = (3.4445, -4.775, 2.0315) five iterations bring the singular values
+ * of X that are not tiny near 1. The smaller of rows and cols is at most 256, the
+ * largest rank that the linears' adapters have: the iteration runs on the Gram
+ * matrix of that side, summed in fp64 from fp32 sums over 64 rows at most, in fp64;
+ * the products with the long matrices run in fp32.
+ *
+ *   w, master, grad, m  device, rows * cols elements each, as in nf4_adamw_entry
+ *                       (m: m_dtype; zeros before the first step)
+ *   scale               of the orthogonalised update in this matrix
+ * An entry with rows or cols == 0 is skipped. */
+typedef struct {
+    void *w;
+    float *master;
+    const void *grad;
+    void *m;
+    int64_t rows, cols;
+    float lr, weight_decay, scale;
+} nf4_muon_entry;
+
+typedef struct {
+    double momentum;    /* mu: 0 <= mu < 1; mu and 1 - mu are rounded to fp32 once each */
+    double eps;         /* 1e-12 and above */
+    double a, b, c;
+    int32_t nesterov;   /* 0 or 1 */
+    int32_t iterations; /* 1 .. 16 */
+} nf4_muon_config;
+
+/* Bytes of device workspace of nf4_muon_step and of nf4_orthogonalize for matrices
+ * of these rows and cols (only those are read): the list, the partial sums of the
+ * Gram matrices and the matrices of the iteration. 0 for an empty list,
+ * (size_t)-1 for invalid arguments. */
+size_t nf4_muon_workspace_size(const nf4_muon_entry *entries, int32_t count);
+
+/* One step of every entry (see above).
+ *   entries    host array, read during the call only
+ *   workspace  256-byte aligned; calls that overlap must not share one
+ * An entry whose update's norm is not finite (a gradient that is not, or elements
+ * above about 1e18) keeps its weight and momentum. Sums run in an order that
+ * depends on the sizes alone. Buffers of different entries must not overlap. */
+nf4_status nf4_muon_step(const nf4_muon_entry *entries, int32_t count, int32_t w_dtype,
+                         int32_t grad_dtype, int32_t m_dtype, const nf4_muon_config *config,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* The orthogonalising alone: w = X of u = grad (w and grad of one dtype; w may be
+ * grad). master, m, lr, weight_decay, scale, momentum and nesterov are not read. A
+ * matrix whose norm is not finite becomes NaN. */
+nf4_status nf4_orthogonalize(const nf4_muon_entry *entries, int32_t count, int32_t dtype,
+                             const nf4_muon_config *config, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -74,6 +74,9 @@ EXPORTS = (
     "nf4_rotary_forward",
     "nf4_rotary_backward_workspace_size",
     "nf4_rotary_backward",
+    "nf4_muon_workspace_size",
+    "nf4_muon_step",
+    "nf4_orthogonalize",
 )
 
 # nf4_dq_format: the 8-bit code of double quantization.
@@ -199,6 +202,7 @@ def lib():
     L.nf4_merge_lora.restype = ctypes.c_int
     declare(L)
     heads.declare(L)
+    muon.declare(L)
     _lib = L
     return L
 
@@ -975,3 +979,5 @@ from .heads import (  # noqa: E402
     rotary_forward,
     rotary_frequencies,
 )
+from . import muon  # noqa: E402
+from .muon import NF4Muon, orthogonalize  # noqa: E402

@@ -1,11 +1,14 @@
 // api_training.hip - the extern "C" entry points of the training-step operators
 // (AdamW, the residual norms, the token embedding, the rotation of queries and
-// keys): host-side validation and
+// keys, Muon): host-side validation and
 // dispatch. Declarations and contracts are in include/nf4.h.
 //
 // Every argument is checked before any HIP call; a rejected call launches
 // nothing and returns its status. The library allocates nothing.
 #include <math.h>
+
+#include <new>
+#include <vector>
 
 #include "training_internal.h"
 
@@ -352,4 +355,92 @@ NF4_API nf4_status nf4_rotary_backward(const nf4_rotary_shape *shape, const uint
         return NF4_OK;
     }
     return launch_status(launch_rotary(*shape, a, true, workspace, stream_of(stream)));
+}
+
+namespace {
+
+// Sizes of a list's matrices.
+nf4_status check_matrices(const nf4_muon_entry *e, int32_t count) {
+    if (count < 0) return NF4_ERR_SIZE;
+    if (count > 0 && !e) return NF4_ERR_NULL;
+    for (int32_t i = 0; i < count; ++i) {
+        if (e[i].rows < 0 || e[i].cols < 0) return NF4_ERR_SIZE;
+        const int64_t side = e[i].rows < e[i].cols ? e[i].rows : e[i].cols;
+        const int64_t length = e[i].rows < e[i].cols ? e[i].cols : e[i].rows;
+        if (side > kMuonSide || (side > 0 && length > kMaxEntry / side)) return NF4_ERR_SIZE;
+    }
+    return NF4_OK;
+}
+
+nf4_status check_muon(const nf4_muon_config *c) {
+    if (!c) return NF4_ERR_NULL;
+    if (!(c->eps >= 1e-12) || !isfinite(c->eps) || !isfinite(c->a) || !isfinite(c->b) || !isfinite(c->c)) return NF4_ERR_SIZE;
+    return c->iterations >= 1 && c->iterations <= 16 ? NF4_OK : NF4_ERR_SIZE;
+}
+
+nf4_status muon(const nf4_muon_entry *e, int32_t count, const nf4_muon_config &config, bool step, nf4_dtype wt, nf4_dtype gt,
+                nf4_dtype mt, void *workspace, size_t workspace_bytes, void *stream) {
+    try {
+        std::vector<MuonMatrix> list(count);
+        for (int32_t i = 0; i < count; ++i)
+            list[i] = MuonMatrix{e[i].grad, step ? e[i].m : nullptr, e[i].w, step ? e[i].master : nullptr,
+                                 e[i].rows, e[i].cols, e[i].lr, e[i].weight_decay, e[i].scale};
+        const size_t need = muon_workspace(list.data(), count);
+        if (need == (size_t)-1) return NF4_ERR_SIZE;
+        const nf4_status st = check_workspace(need, workspace, workspace_bytes);
+        if (st != NF4_OK) return st;
+        MuonCall c{config.momentum, config.eps, config.a, config.b, config.c, config.nesterov, config.iterations,
+                   step, wt, gt, mt};
+        return launch_status(launch_muon(list.data(), count, c, workspace, stream_of(stream)));
+    } catch (const std::bad_alloc &) {
+        return NF4_ERR_SIZE;
+    }
+}
+
+}  // namespace
+
+NF4_API size_t nf4_muon_workspace_size(const nf4_muon_entry *entries, int32_t count) {
+    if (check_matrices(entries, count) != NF4_OK) return (size_t)-1;
+    try {
+        std::vector<MuonMatrix> list(count);
+        for (int32_t i = 0; i < count; ++i) list[i].rows = entries[i].rows, list[i].cols = entries[i].cols;
+        return muon_workspace(list.data(), count);
+    } catch (const std::bad_alloc &) {
+        return (size_t)-1;
+    }
+}
+
+NF4_API nf4_status nf4_muon_step(const nf4_muon_entry *entries, int32_t count, int32_t w_dtype, int32_t grad_dtype,
+                                 int32_t m_dtype, const nf4_muon_config *config, void *workspace, size_t workspace_bytes,
+                                 void *stream) {
+    nf4_status st = check_matrices(entries, count);
+    if (st != NF4_OK || (st = check_muon(config)) != NF4_OK) return st;
+    if (!is_dtype(w_dtype) || !is_dtype(grad_dtype) || !is_dtype(m_dtype)) return NF4_ERR_UNSUPPORTED;
+    if (!(config->momentum >= 0.0 && config->momentum < 1.0)) return NF4_ERR_SIZE;
+    if (config->nesterov != 0 && config->nesterov != 1) return NF4_ERR_UNSUPPORTED;
+    for (int32_t i = 0; i < count; ++i) {
+        const nf4_muon_entry &e = entries[i];
+        if (e.rows == 0 || e.cols == 0) continue;
+        if (!isfinite(e.lr) || !isfinite(e.weight_decay) || !isfinite(e.scale)) return NF4_ERR_SIZE;
+        if (!e.w || !e.grad || !e.m) return NF4_ERR_NULL;
+        if (e.master && w_dtype != NF4_BF16) return NF4_ERR_UNSUPPORTED;
+        if (!aligned(e.w, 16) || !aligned(e.grad, 16) || !aligned(e.m, 16) || !aligned(e.master, 16)) return NF4_ERR_ALIGN;
+    }
+    return muon(entries, count, *config, true, static_cast<nf4_dtype>(w_dtype), static_cast<nf4_dtype>(grad_dtype),
+                static_cast<nf4_dtype>(m_dtype), workspace, workspace_bytes, stream);
+}
+
+NF4_API nf4_status nf4_orthogonalize(const nf4_muon_entry *entries, int32_t count, int32_t dtype,
+                                     const nf4_muon_config *config, void *workspace, size_t workspace_bytes, void *stream) {
+    nf4_status st = check_matrices(entries, count);
+    if (st != NF4_OK || (st = check_muon(config)) != NF4_OK) return st;
+    if (!is_dtype(dtype)) return NF4_ERR_UNSUPPORTED;
+    for (int32_t i = 0; i < count; ++i) {
+        const nf4_muon_entry &e = entries[i];
+        if (e.rows == 0 || e.cols == 0) continue;
+        if (!e.w || !e.grad) return NF4_ERR_NULL;
+        if (!aligned(e.w, 16) || !aligned(e.grad, 16)) return NF4_ERR_ALIGN;
+    }
+    const nf4_dtype dt = static_cast<nf4_dtype>(dtype);
+    return muon(entries, count, *config, false, dt, dt, NF4_F32, workspace, workspace_bytes, stream);
 }

@@ -1,5 +1,5 @@
 // training_internal.h - internal declarations of the training-step operators
-// (optimizer.hip, residual_norm.hip, embedding.hip, rotary.hip); their contracts are in
+// (optimizer.hip, residual_norm.hip, embedding.hip, rotary.hip, muon.hip); their contracts are in
 // nf4.h. Shared by the library's own sources only.
 #pragma once
 
@@ -61,6 +61,24 @@ struct RotaryArgs {
 size_t rotary_backward_workspace(const nf4_rotary_shape &sh);
 hipError_t launch_rotary(const nf4_rotary_shape &sh, const RotaryArgs &a, bool backward, void *workspace,
                          hipStream_t s);
+
+// One matrix of a call: the optimizer's step, or the orthogonalising alone (grad into w).
+struct MuonMatrix {
+    const void *grad;
+    void *m, *w;
+    float *master;
+    int64_t rows, cols;
+    float lr, weight_decay, scale;
+};
+struct MuonCall {
+    double momentum, eps, a, b, c;
+    int32_t nesterov, iterations;
+    bool step;
+    nf4_dtype w, grad, m;
+};
+constexpr int kMuonSide = 256;  // of the shorter side at most
+size_t muon_workspace(const MuonMatrix *list, int32_t count);
+hipError_t launch_muon(const MuonMatrix *list, int32_t count, const MuonCall &call, void *workspace, hipStream_t s);
 
 // ---- device helpers ----
 

@@ -1,0 +1,198 @@
+"""The Muon step over a list of adapter matrices (``NF4Muon``) and the
+orthogonalising of updates alone (``orthogonalize``). Formulas, storage and limits
+are in ``include/nf4.h`` (nf4_muon_step, nf4_orthogonalize); every step of the
+computation runs in the library's HIP kernels, torch supplies device memory and the
+current stream.
+"""
+import ctypes
+import math
+
+import numpy as np
+
+import nf4_quantize_amd as _nq
+
+from .training import ListOptimizer, _changed, _check_apart, _check_tensors, _code, _size, _stream, _taken
+
+MAX_SIDE = 256  # of the shorter of rows and columns
+
+# nf4_muon_entry, as one row of a host array.
+_ENTRY = np.dtype([("w", "u8"), ("master", "u8"), ("grad", "u8"), ("m", "u8"), ("rows", "i8"), ("cols", "i8"), ("lr", "f4"),
+                   ("weight_decay", "f4"), ("scale", "f4"), ("pad", "f4")])
+
+
+class nf4_muon_config(ctypes.Structure):
+    _fields_ = [("momentum", ctypes.c_double), ("eps", ctypes.c_double), ("a", ctypes.c_double), ("b", ctypes.c_double),
+                ("c", ctypes.c_double), ("nesterov", ctypes.c_int32), ("iterations", ctypes.c_int32)]
+
+
+def declare(L):
+    """argtypes and restypes of this module's entry points."""
+    p, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    config = ctypes.POINTER(nf4_muon_config)
+    for name, restype, args in (("nf4_muon_workspace_size", sz, [p, i32]),
+                                ("nf4_muon_step", i32, [p, i32, i32, i32, i32, config, p, sz, p]),
+                                ("nf4_orthogonalize", i32, [p, i32, i32, config, p, sz, p])):
+        fn = getattr(L, name)
+        fn.restype, fn.argtypes = restype, args
+
+
+COEFFICIENTS = (3.4445, -4.775, 2.0315)
+
+
+def _check_matrix(shape):
+    if len(shape) != 2 or min(shape) > MAX_SIDE:
+        raise ValueError(f"{tuple(shape)}: matrices with at most {MAX_SIDE} rows or columns, as adapters are (NF4AdamW takes "
+                         "any tensor)")
+
+
+def _adjusted(shape, adjust):
+    """The factor of an orthogonalised update of this shape."""
+    if not shape[0] or not shape[1] or adjust == "none":
+        return 1.0
+    if adjust == "shape":
+        return math.sqrt(max(1.0, shape[0] / shape[1]))
+    if adjust == "rms":
+        return 0.2 * math.sqrt(max(shape))
+    raise ValueError(f"adjust {adjust!r}: 'shape', 'rms' or 'none'")
+
+
+class NF4Muon(ListOptimizer):
+    """Muon over a list of adapter matrices: the momentum of each gradient,
+    orthogonalised by Newton-Schulz products, is its update (nf4_muon_step). One of a
+    matrix's sides is at most 256; norms, gates and tables are NF4AdamW's.
+
+    ``params``: tensors, or groups ``dict(params=[...], lr=..., weight_decay=...,
+    masters=[...])``; all have one dtype (bfloat16 or float32), and no two share
+    memory. ``masters`` are the fp32 weights of bfloat16 parameters (``masters=True``:
+    made here). ``momentum`` and ``nesterov``: the update is mu m' + (1 - mu) g, or m'
+    alone. ``coefficients`` (a, b, c), ``iterations`` and ``eps`` are those of the
+    orthogonalising. ``adjust`` scales it: "shape" by sqrt(max(1, rows / columns)),
+    "rms" by 0.2 sqrt(max(rows, columns)), so that its elements are as large as
+    AdamW's, "none" not at all. ``state_bits``: the momentum is float32 (32) or
+    bfloat16 (16).
+
+    ``m`` is the list of the matrices' momenta in the order of the parameters. A step
+    writes at these tensors' addresses, so ``bind_state`` replaces them, and a step
+    refuses lists whose tensors are others (a parameter's ``data`` may change, its
+    shape may not). A matrix whose update's norm is not finite keeps its weight and
+    momentum."""
+
+    m = _taken("m")
+
+    def __init__(self, params, lr=1e-3, weight_decay=0.1, momentum=0.95, nesterov=True, coefficients=COEFFICIENTS,
+                 iterations=5, eps=1e-7, state_bits=32, adjust="shape", masters=None):
+        import torch
+
+        if state_bits not in (16, 32):
+            raise ValueError("state_bits is 16 or 32")
+        a, b, c = (float(x) for x in coefficients)
+        self.momentum, self.nesterov, self.coefficients = float(momentum), bool(nesterov), (a, b, c)
+        self.iterations, self.eps, self.state_bits, self.adjust = int(iterations), float(eps), state_bits, adjust
+        if not 0.0 <= self.momentum < 1.0 or not 1 <= self.iterations <= 16 or not 1e-12 <= self.eps < math.inf:
+            raise ValueError("0 <= momentum < 1, 1 to 16 iterations, eps from 1e-12 on")
+        self._shapes = None
+        self._take(params, masters, lr, weight_decay, _ENTRY)
+        self._shapes = [p.shape for p in self._params]
+        for shape in self._shapes:
+            _check_matrix(shape)
+        e = self._entries
+        e["rows"], e["cols"] = zip(*self._shapes)
+        e["scale"] = [_adjusted(shape, adjust) for shape in self._shapes]
+        self.steps = 0
+        size = _size(_nq.lib().nf4_muon_workspace_size(self._at, len(e)), "nf4_muon_workspace_size")
+        self._workspace = torch.empty(max(1, size), dtype=torch.uint8, device=self.device)
+        dt = torch.float32 if state_bits == 32 else torch.bfloat16
+        self._state_code = _code(dt)
+        # one buffer, in which every matrix starts at a multiple of 256 elements
+        starts = np.concatenate(([0], np.cumsum([-(-n // 256) * 256 for n in self._numels])))
+        flat = torch.zeros(int(starts[-1]), dtype=dt, device=self.device)
+        self.bind_state([flat[at:at + n].view(shape) for at, n, shape in zip(starts.tolist(), self._numels, self._shapes)])
+
+    def bind_state(self, m):
+        """Uses these tensors as the momenta (a checkpoint's, or shares of a buffer of the
+        caller's): per parameter one of its shape, float32 or with 16 bits bfloat16."""
+        import torch
+
+        ts = list(m)
+        want = torch.float32 if self.state_bits == 32 else torch.bfloat16
+        if len(ts) != len(self._params):
+            raise ValueError(f"m: {len(ts)} tensors for {len(self._params)} parameters")
+        for t, shape in zip(ts, self._shapes):
+            _check_tensors(self._params[0], t)
+            if t.dtype != want or t.shape != shape:
+                raise ValueError(f"m: {tuple(t.shape)} {t.dtype} for a parameter {tuple(shape)}, {want} is wanted")
+        self._bind_lists(dict(m=ts))
+
+    def _bind(self):
+        if self._shapes is not None and [p.shape for p in self._params] != self._shapes:
+            raise ValueError("a parameter's shape has changed")
+        super()._bind()
+
+    def step(self, grads=None):
+        """One step with the parameters' ``.grad``, or with ``grads`` (a tensor for each
+        parameter, all bfloat16 or all float32)."""
+        grad_dtype, device = self._take_grads(grads, self._shapes)
+        if list(map(_shape_of, self._params)) != self._shapes:
+            self._bind()  # refuses
+        config = nf4_muon_config(self.momentum, self.eps, *self.coefficients, self.nesterov, self.iterations)
+        _nq._check(_nq.lib().nf4_muon_step(self._at, len(self._params), _code(self.dtype), grad_dtype, self._state_code,
+                                           ctypes.byref(config), self._workspace.data_ptr(), self._workspace.numel(),
+                                           _stream(device)), "nf4_muon_step")
+        _changed(self._weights)
+        self.steps += 1
+
+    def state_dict(self):
+        return dict(steps=self.steps, state_bits=self.state_bits, **self._common_state(),
+                    m=[t.clone() for t in self._taken["m"]])
+
+    def load_state_dict(self, d):
+        if (d["state_bits"] != self.state_bits or len(d["groups"]) != len(self.groups)
+                or any(len(d[k]) != len(self._params) for k in ("m", "masters"))):
+            raise ValueError("the state of another optimizer")
+        self._copy_state(list(zip(self._taken["m"], d["m"])), d)
+        self.steps = int(d["steps"])
+
+
+def _shape_of(t):
+    return t.shape
+
+
+def orthogonalize(updates, coefficients=COEFFICIENTS, iterations=5, eps=1e-7, outs=None, workspace=None):
+    """Each matrix of the list over its norm (at least ``eps``), and ``iterations`` times
+    X <- a X + b (X X^T) X + c (X X^T)^2 X (nf4_orthogonalize): its singular values
+    come near 1. All are bfloat16 or all float32, with at most 256 rows or columns.
+    Returns a list of new tensors, or ``outs`` (which may be the updates themselves).
+    A matrix whose norm is not finite becomes NaN."""
+    import torch
+
+    updates = list(updates)
+    if not updates:
+        return []
+    given = outs is not None
+    outs = list(outs) if given else [torch.empty_like(u, memory_format=torch.contiguous_format) for u in updates]
+    if len(outs) != len(updates):
+        raise ValueError(f"{len(outs)} outputs for {len(updates)} updates")
+    index, dt = _check_tensors(updates[0], *updates[1:], *outs, workspace), updates[0].dtype
+    code = _code(dt)
+    e = np.zeros(len(updates), _ENTRY)
+    for u, o in zip(updates, outs):
+        _check_matrix(u.shape)
+        if u.dtype != dt or o.dtype != dt or o.shape != u.shape:
+            raise ValueError("updates and outputs have one dtype, and each pair one shape")
+    if given:
+        # an update that is not its own output must not be one; the same update may be there twice
+        read = {(u.data_ptr(), u.nbytes): u for u, o in zip(updates, outs) if u.data_ptr() != o.data_ptr()}
+        _check_apart(outs + list(read.values()))
+    e["rows"], e["cols"] = zip(*[u.shape for u in updates])
+    e["grad"], e["w"] = [u.data_ptr() for u in updates], [o.data_ptr() for o in outs]
+    L = _nq.lib()
+    if workspace is None:
+        size = _size(L.nf4_muon_workspace_size(e.ctypes.data, len(e)), "nf4_muon_workspace_size")
+        workspace = torch.empty(max(1, size), dtype=torch.uint8, device=updates[0].device)
+    a, b, c = (float(x) for x in coefficients)
+    config = nf4_muon_config(0.0, eps, a, b, c, 0, int(iterations))
+    _nq._check(L.nf4_orthogonalize(e.ctypes.data, len(e), code, ctypes.byref(config), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream(index)), "nf4_orthogonalize")
+    if given:
+        _changed(outs)
+    return outs

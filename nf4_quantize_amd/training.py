@@ -82,7 +82,7 @@ def _check_apart(ts):
     end = 0
     for at, size in sorted([(t.data_ptr(), t.nbytes) for t in ts]):
         if size and at < end:
-            raise ValueError("two of an optimizer's weights, masters and moments share memory")
+            raise ValueError("two of the tensors that a call writes share memory (an optimizer's weights, masters and moments)")
         end = max(end, at + size)
 
 
@@ -122,7 +122,7 @@ def _code(dtype):
     return _nq._dtype_code(dtype) if code is None else code
 
 
-# ------------------------------------------------------------------ AdamW
+# ------------------------------------------------------------------ optimizers
 
 def _taken(name):
     """The list of the tensors whose addresses a step takes, made on first use. A step
@@ -136,36 +136,17 @@ def _taken(name):
     return property(tensors)
 
 
-class NF4AdamW:
-    """AdamW over a list of device tensors in a few launches, with the moments in
-    8 bits (E4M3 codes with one fp32 scale per 256 elements, rounded
-    stochastically) or in 32, and clipping by the norm of all its list's gradients
-    (each optimizer by its own: a list has one dtype).
+class ListOptimizer:
+    """What the optimizers over a list of device tensors have in common: their groups,
+    the addresses that a step writes at, and the questions of every step. A subclass
+    has ``_entries`` (with the columns w, master, grad, lr and weight_decay)."""
 
-    ``params``: tensors, or groups ``dict(params=[...], lr=..., weight_decay=...,
-    masters=[...])``; all have one dtype (bfloat16 or float32), and no two share
-    memory. ``masters`` are the fp32 weights of bfloat16 parameters: the step
-    updates them and rounds them into the parameters (``masters=True``: made here
-    from the parameters). ``max_grad_norm`` > 0 clips; a step whose norm is not
-    finite then changes none of these tensors and no moment, but it counts in
-    ``steps``, the step number of the bias corrections, like any other (``step=``
-    gives a call another number). ``seed`` starts the random bits of the stochastic
-    rounding; each step takes the next ones.
+    params, masters = map(_taken, ("params", "masters"))
 
-    ``m``, ``v`` (and ``m_scale``, ``v_scale``) are the lists of the tensors'
-    moments in the order of the parameters. A step writes at these tensors' addresses,
-    so ``bind_state`` replaces them, and a step refuses lists whose tensors are others,
-    ``params`` and ``masters`` too (a parameter's ``data`` may change). ``grad_norm`` is
-    the last norm (a device tensor of one float)."""
-
-    params, masters, m, v, m_scale, v_scale = map(_taken, ("params", "masters", "m", "v", "m_scale", "v_scale"))
-
-    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=8,
-                 max_grad_norm=0.0, seed=0, masters=None):
+    def _take(self, params, masters, lr, weight_decay, entry):
+        """Takes the parameters, or groups of them, into ``groups`` and one row of ``entry`` each."""
         import torch
 
-        if state_bits not in (8, 32):
-            raise ValueError("state_bits is 8 or 32")
         params = list(params)
         if not params:
             raise ValueError("no parameters")
@@ -193,13 +174,145 @@ class NF4AdamW:
         self.dtype, self.device = self._params[0].dtype, self._params[0].device
         _nq._dtype_code(self.dtype)
         self._tensor = torch.Tensor
-        self._entries = np.zeros(len(self._params), _ENTRY)
+        self._entries = np.zeros(len(self._params), entry)
         self._at = self._entries.ctypes.data
         self._numels = [p.numel() for p in self._params]
         self._weights = self._params + [mw for mw in self._masters if mw is not None]
         self._rates = None
         self._held_state = []
         self._bind()
+
+    def _bind_lists(self, lists):
+        """Takes these lists of tensors (name: list) as the state, once they are looked over."""
+        _check_apart(self._weights + [t for ts in lists.values() for t in ts])
+        # held as well, so that their memory stays where a tensor of the list gets other data
+        self._held_state = [t.detach() for ts in lists.values() for t in ts]
+        for name, ts in lists.items():
+            self._taken[name] = tuple(ts)
+            self._given.pop(name, None)
+            self._entries[name] = [t.data_ptr() for t in ts]
+
+    def zero_grad(self, set_to_none=True):
+        for p in self._params:
+            if set_to_none:
+                p.grad = None
+            elif p.grad is not None:
+                p.grad.zero_()
+
+    def _bind(self):
+        """Takes the weights' addresses, once they are what the step can update."""
+        import torch
+
+        for p, n, mw in zip(self._params, self._numels, self._masters):
+            if p.dtype != self.dtype:
+                raise TypeError(f"parameters of one dtype, got {self.dtype} and {p.dtype}")
+            _check_tensors(self._params[0], p, mw)
+            if p.numel() != n or p.device != self.device:
+                raise ValueError("a parameter's size or device has changed")
+            if mw is not None and (mw.dtype != torch.float32 or self.dtype != torch.bfloat16 or mw.numel() != n):
+                raise TypeError("a master weight is float32, of a bfloat16 parameter of its size")
+        if self._held_state:  # at construction bind_state asks this
+            _check_apart(self._weights + self._held_state)
+        self._entries["w"] = [p.data_ptr() for p in self._params]
+        self._entries["master"] = [0 if mw is None else mw.data_ptr() for mw in self._masters]
+        # held, so that no other memory can have their addresses
+        self._held = [t.detach() for t in self._weights]
+        self._bound = [t.data_ptr() for t in self._held]
+
+    def _check_given(self):
+        for name, ts in self._given.items():
+            taken = self._taken[name]
+            if len(ts) != len(taken) or any(map(operator.is_not, ts, taken)):
+                raise ValueError(f"{name} has other tensors than the step writes: bind_state gives it other moments, a "
+                                 "parameter's data another weight")
+
+    def _take_grads(self, grads, shapes=None):
+        """The entries' gradients and rates for a step; returns the gradients' dtype and the device's
+        index. ``shapes``: what the gradients' have to be, where their numbers of elements do not say enough."""
+        if self._given:
+            self._check_given()
+        grads = [p.grad for p in self._params] if grads is None else grads
+        if len(grads) != len(self._params):
+            raise ValueError(f"{len(grads)} gradients for {len(self._params)} parameters")
+        T = self._tensor  # the methods over the list: a third less time than a loop, for hundreds of tensors
+        try:
+            devices, sizes = set(map(T.get_device, grads)), list(map(T.numel, grads))
+        except TypeError:
+            raise ValueError("a parameter has no gradient") from None
+        dt = grads[0].dtype
+        if (devices != {self._params[0].get_device()} or sizes != self._numels or not all(map(T.is_contiguous, grads))
+                or {g.dtype for g in grads} != {dt} or (shapes is not None and [g.shape for g in grads] != shapes)):
+            raise ValueError(f"gradients: contiguous, of the parameters' sizes, one dtype, on {self.device}; got "
+                             + ", ".join(f"{tuple(g.shape)} {g.dtype} {g.device}" for g in grads[:4]) + " ...")
+        if list(map(T.data_ptr, self._weights)) != self._bound or not all(map(T.is_contiguous, self._weights)):
+            self._bind()  # a weight has new memory, or lies in another order, which this refuses
+        grad_dtype = _code(dt)
+        e = self._entries
+        e["grad"] = array.array("Q", map(T.data_ptr, grads))
+        rates = [(g["lr"], g["weight_decay"]) for g in self.groups]
+        if rates != self._rates:
+            for g in self.groups:
+                part = slice(g["first"], g["first"] + g["count"])
+                e["lr"][part], e["weight_decay"][part] = g["lr"], g["weight_decay"]
+            self._rates = rates
+        return grad_dtype, devices.pop()
+
+    def _copy_state(self, pairs, d):
+        """The masters and groups of a state, and (own, given) pairs of tensors, once all of them fit."""
+        import torch
+
+        for x, y in zip(self._masters, d["masters"]):
+            if (x is None) != (y is None):
+                raise ValueError("the state of another optimizer: master weights")
+            pairs += [] if x is None else [(x, y)]
+        for x, y in pairs:
+            if x.dtype != y.dtype or x.numel() != y.numel():
+                raise ValueError("the state of another optimizer: sizes")
+        for x, y in pairs:
+            x.reshape(-1).view(torch.uint8).copy_(y.reshape(-1).to(x.device).view(torch.uint8))
+        for g, new in zip(self.groups, d["groups"]):
+            g.update(lr=float(new["lr"]), weight_decay=float(new["weight_decay"]))
+
+    def _common_state(self):
+        return dict(groups=[dict(lr=g["lr"], weight_decay=g["weight_decay"]) for g in self.groups],
+                    masters=[None if t is None else t.clone() for t in self._masters])
+
+    def __reduce_ex__(self, protocol):
+        raise TypeError(f"an {type(self).__name__} holds its tensors' addresses and is not copied: state_dict carries "
+                        "its state")
+
+
+class NF4AdamW(ListOptimizer):
+    """AdamW over a list of device tensors in a few launches, with the moments in
+    8 bits (E4M3 codes with one fp32 scale per 256 elements, rounded
+    stochastically) or in 32, and clipping by the norm of all its list's gradients
+    (each optimizer by its own: a list has one dtype).
+
+    ``params``: tensors, or groups ``dict(params=[...], lr=..., weight_decay=...,
+    masters=[...])``; all have one dtype (bfloat16 or float32), and no two share
+    memory. ``masters`` are the fp32 weights of bfloat16 parameters: the step
+    updates them and rounds them into the parameters (``masters=True``: made here
+    from the parameters). ``max_grad_norm`` > 0 clips; a step whose norm is not
+    finite then changes none of these tensors and no moment, but it counts in
+    ``steps``, the step number of the bias corrections, like any other (``step=``
+    gives a call another number). ``seed`` starts the random bits of the stochastic
+    rounding; each step takes the next ones.
+
+    ``m``, ``v`` (and ``m_scale``, ``v_scale``) are the lists of the tensors'
+    moments in the order of the parameters. A step writes at these tensors' addresses,
+    so ``bind_state`` replaces them, and a step refuses lists whose tensors are others,
+    ``params`` and ``masters`` too (a parameter's ``data`` may change). ``grad_norm`` is
+    the last norm (a device tensor of one float)."""
+
+    m, v, m_scale, v_scale = map(_taken, ("m", "v", "m_scale", "v_scale"))
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=8,
+                 max_grad_norm=0.0, seed=0, masters=None):
+        import torch
+
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits is 8 or 32")
+        self._take(params, masters, lr, weight_decay, _ENTRY)
         self.betas, self.eps, self.state_bits = (float(betas[0]), float(betas[1])), float(eps), state_bits
         self.max_grad_norm, self.seed, self.steps = float(max_grad_norm), int(seed), 0
         self.grad_norm = torch.zeros(1, dtype=torch.float32, device=self.device)
@@ -250,123 +363,40 @@ class NF4AdamW:
                 _check_tensors(self._params[0], t)
                 if t.dtype != want or t.numel() != (-(-n // MOMENT_BLOCK) if scale else n):
                     raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} for a parameter of {n} elements")
-        _check_apart(self._weights + [t for ts in lists.values() for t in ts])
-        # held as well, so that their memory stays where a tensor of the list gets other data
-        self._held_state = [t.detach() for ts in lists.values() for t in ts]
-        for name, ts in lists.items():
-            self._taken[name] = tuple(ts)
-            self._given.pop(name, None)
-            self._entries[name] = [t.data_ptr() for t in ts]
-
-    def zero_grad(self, set_to_none=True):
-        for p in self._params:
-            if set_to_none:
-                p.grad = None
-            elif p.grad is not None:
-                p.grad.zero_()
-
-    def _bind(self):
-        """Takes the weights' addresses, once they are what the step can update."""
-        import torch
-
-        for p, n, mw in zip(self._params, self._numels, self._masters):
-            if p.dtype != self.dtype:
-                raise TypeError(f"parameters of one dtype, got {self.dtype} and {p.dtype}")
-            _check_tensors(self._params[0], p, mw)
-            if p.numel() != n or p.device != self.device:
-                raise ValueError("a parameter's size or device has changed")
-            if mw is not None and (mw.dtype != torch.float32 or self.dtype != torch.bfloat16 or mw.numel() != n):
-                raise TypeError("a master weight is float32, of a bfloat16 parameter of its size")
-        if self._held_state:  # at construction bind_state asks this
-            _check_apart(self._weights + self._held_state)
-        self._entries["w"] = [p.data_ptr() for p in self._params]
-        self._entries["master"] = [0 if mw is None else mw.data_ptr() for mw in self._masters]
-        # held, so that no other memory can have their addresses
-        self._held = [t.detach() for t in self._weights]
-        self._bound = [t.data_ptr() for t in self._held]
-
-    def _check_given(self):
-        for name, ts in self._given.items():
-            taken = self._taken[name]
-            if len(ts) != len(taken) or any(map(operator.is_not, ts, taken)):
-                raise ValueError(f"{name} has other tensors than the step writes: bind_state gives it other moments, a "
-                                 "parameter's data another weight")
+        self._bind_lists(lists)
 
     def step(self, grads=None, step=None, seed=None):
         """One step with the parameters' ``.grad``, or with ``grads`` (a tensor for
         each parameter, all bfloat16 or all float32). ``step`` and ``seed``
         override the step number (the count of calls) and the random seed."""
         L = _nq.lib()
-        if self._given:
-            self._check_given()
-        grads = [p.grad for p in self._params] if grads is None else grads
-        if len(grads) != len(self._params):
-            raise ValueError(f"{len(grads)} gradients for {len(self._params)} parameters")
-        T = self._tensor  # the methods over the list: a third less time than a loop, for hundreds of tensors
-        try:
-            devices, sizes = set(map(T.get_device, grads)), list(map(T.numel, grads))
-        except TypeError:
-            raise ValueError("a parameter has no gradient") from None
-        dt = grads[0].dtype
-        if (devices != {self._params[0].get_device()} or sizes != self._numels or not all(map(T.is_contiguous, grads))
-                or {g.dtype for g in grads} != {dt}):
-            raise ValueError(f"gradients: contiguous, of the parameters' sizes, one dtype, on {self.device}; got "
-                             + ", ".join(f"{tuple(g.shape)} {g.dtype} {g.device}" for g in grads[:4]) + " ...")
-        if list(map(T.data_ptr, self._weights)) != self._bound or not all(map(T.is_contiguous, self._weights)):
-            self._bind()  # a weight has new memory, or lies in another order, which this refuses
-        grad_dtype = _code(dt)
-        e = self._entries
-        e["grad"] = array.array("Q", map(T.data_ptr, grads))
-        rates = [(g["lr"], g["weight_decay"]) for g in self.groups]
-        if rates != self._rates:
-            for g in self.groups:
-                part = slice(g["first"], g["first"] + g["count"])
-                e["lr"][part], e["weight_decay"][part] = g["lr"], g["weight_decay"]
-            self._rates = rates
+        grad_dtype, device = self._take_grads(grads)
         number = self.steps + 1 if step is None else int(step)
-        stream = _stream(devices.pop())
+        stream = _stream(device)
         config = nf4_adamw_config(*self.betas, self.eps, self.max_grad_norm, number,
                                   (self.seed + number if seed is None else int(seed)) & 0xFFFFFFFFFFFFFFFF)
         call, norm = ((L.nf4_adamw_clip_step, self.grad_norm.data_ptr()) if self.max_grad_norm > 0
                       else (L.nf4_adamw_step, None))
-        _nq._check(call(self._at, len(grads), _code(self.dtype), grad_dtype, self.state_bits, ctypes.byref(config), norm,
+        _nq._check(call(self._at, len(self._params), _code(self.dtype), grad_dtype, self.state_bits, ctypes.byref(config), norm,
                         self._workspace.data_ptr(), self._workspace.numel(), stream), call.__name__)
         _changed(self._written)
         self.steps = number
 
-    def __reduce_ex__(self, protocol):
-        raise TypeError("an NF4AdamW holds its tensors' addresses and is not copied: state_dict carries its state")
-
     def state_dict(self):
-        d = dict(steps=self.steps, seed=self.seed, state_bits=self.state_bits,
-                 groups=[dict(lr=g["lr"], weight_decay=g["weight_decay"]) for g in self.groups],
-                 m=[t.clone() for t in self._taken["m"]], v=[t.clone() for t in self._taken["v"]],
-                 masters=[None if t is None else t.clone() for t in self._masters])
+        d = dict(steps=self.steps, seed=self.seed, state_bits=self.state_bits, **self._common_state(),
+                 m=[t.clone() for t in self._taken["m"]], v=[t.clone() for t in self._taken["v"]])
         if self.state_bits == 8:
             d.update(m_scale=[t.clone() for t in self._taken["m_scale"]],
                      v_scale=[t.clone() for t in self._taken["v_scale"]])
         return d
 
     def load_state_dict(self, d):
-        import torch
-
         names = ["m", "v"] + (["m_scale", "v_scale"] if self.state_bits == 8 else [])
         if (d["state_bits"] != self.state_bits or len(d["groups"]) != len(self.groups)
                 or any(len(d[k]) != len(self._params) for k in names + ["masters"])):
             raise ValueError("the state of another optimizer")
-        pairs = [(x, y) for k in names for x, y in zip(self._taken[k], d[k])]
-        for x, y in zip(self._masters, d["masters"]):
-            if (x is None) != (y is None):
-                raise ValueError("the state of another optimizer: master weights")
-            pairs += [] if x is None else [(x, y)]
-        for x, y in pairs:
-            if x.dtype != y.dtype or x.numel() != y.numel():
-                raise ValueError("the state of another optimizer: sizes")
-        for x, y in pairs:
-            x.reshape(-1).view(torch.uint8).copy_(y.reshape(-1).to(x.device).view(torch.uint8))
+        self._copy_state([(x, y) for k in names for x, y in zip(self._taken[k], d[k])], d)
         self.steps, self.seed = int(d["steps"]), int(d["seed"])
-        for g, new in zip(self.groups, d["groups"]):
-            g.update(lr=float(new["lr"]), weight_decay=float(new["weight_decay"]))
 
 
 # ------------------------------------------------------------------ residual norms
