@@ -701,7 +701,7 @@ nf4_status nf4_rotary_backward(const nf4_rotary_shape *shape, const uint64_t *tu
  * (a, b, c) = (3.4445, -4.775, 2.0315) five iterations bring the singular values
  * of X that are not tiny near 1. The smaller of rows and cols is at most 256, the
  * largest rank that the linears' adapters have: the iteration runs on the Gram
- * matrix of that side, summed in fp64 from fp32 sums over 64 rows at most, in fp64;
+ * matrix of that side, summed in fp64 from fp32 sums over 32 rows, in fp64;
  * the products with the long matrices run in fp32.
  *
  *   w, master, grad, m  device, rows * cols elements each, as in nf4_adamw_entry
