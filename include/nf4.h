@@ -706,6 +706,7 @@ nf4_status nf4_rotary_backward(const nf4_rotary_shape *shape, const uint64_t *tu
  *
  *   w, master, grad, m  device, rows * cols elements each, as in nf4_adamw_entry
  *                       (m: m_dtype; zeros before the first step)
+ *   rows, cols          rows * cols < 2^30, the smaller at most 256
  *   scale               of the orthogonalised update in this matrix
  * An entry with rows or cols == 0 is skipped. */
 typedef struct {

@@ -367,7 +367,7 @@ nf4_status check_matrices(const nf4_muon_entry *e, int32_t count) {
         if (e[i].rows < 0 || e[i].cols < 0) return NF4_ERR_SIZE;
         const int64_t side = e[i].rows < e[i].cols ? e[i].rows : e[i].cols;
         const int64_t length = e[i].rows < e[i].cols ? e[i].cols : e[i].rows;
-        if (side > kMuonSide || (side > 0 && length > kMaxEntry / side)) return NF4_ERR_SIZE;
+        if (side > kMuonSide || (side > 0 && length > kMuonElements / side)) return NF4_ERR_SIZE;
     }
     return NF4_OK;
 }

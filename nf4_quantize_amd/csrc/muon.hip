@@ -30,10 +30,9 @@ struct Item {
     void *m;                 // NULL: no momentum
     void *w;                 // the weight, or the output
     float *master;
-    int64_t length;          // of the longer side
     int64_t partial, mats;   // first element in the workspace's fp64 parts
-    int32_t side;            // the shorter
-    int32_t tall;
+    int32_t side, length;    // the shorter and the longer
+    int32_t total, tall;     // elements
     float keep, step;        // w' = keep w - step O
     uint32_t gram_first, gram_chunk, gram_chunks, gram_pairs;
     uint32_t apply_first, apply_chunk;
@@ -87,80 +86,142 @@ __device__ __forceinline__ int32_t find(const uint32_t *firsts, int32_t count, u
 
 struct None {};  // no momentum
 
-// N consecutive elements (4 or 8) as they lie in memory, at any element's address. Of
-// those, `live` (maybe none) are the matrix's; the others are zero.
+// N consecutive elements as they lie in memory, at any element's address.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 template <typename T, int N> struct RawN;
+template <> struct RawN<Bf16, 1> { uint16_t v; };
+template <> struct RawN<Bf16, 2> { uint32_t v; };
 template <> struct RawN<Bf16, 4> { u32x2 v; };
-template <> struct RawN<float, 4> { f32x4 v; };
 template <> struct RawN<Bf16, 8> { u32x4 v; };
+template <> struct RawN<float, 1> { float v; };
+template <> struct RawN<float, 2> { f32x2 v; };
+template <> struct RawN<float, 4> { f32x4 v; };
 template <> struct RawN<float, 8> { f32x4 v, w; };
 template <int N> struct RawN<None, N> {};
+typedef uint32_t u32_at2 __attribute__((aligned(2)));
 typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
+typedef f32x2 f32x2_at4 __attribute__((aligned(4)));
 
-template <typename T, int N, bool kStream>
-__device__ __forceinline__ RawN<T, N> load_n(const void *p, int64_t at, int live) {
-    if constexpr (std::is_same_v<T, None>) return {};
-    else {
-        const T *q = static_cast<const T *>(p) + at;
-        RawN<T, N> r{};
-        if (live >= N) {
-            if constexpr (sizeof(T) == 4) {
-                const f32x4_at4 *f = reinterpret_cast<const f32x4_at4 *>(q);
-                r.v = kStream ? __builtin_nontemporal_load(f) : *f;
-                const f32x4_at4 *f1 = reinterpret_cast<const f32x4_at4 *>(q + 4);
-                if constexpr (N == 8) r.w = kStream ? __builtin_nontemporal_load(f1) : *f1;
-            } else if constexpr (N == 8) {
-                const u32x4_at2 *f = reinterpret_cast<const u32x4_at2 *>(q);
-                r.v = kStream ? __builtin_nontemporal_load(f) : *f;
-            } else {
-                const u32x2_at2 *f = reinterpret_cast<const u32x2_at2 *>(q);
-                r.v = kStream ? __builtin_nontemporal_load(f) : *f;
-            }
-        } else if (live > 0) {
-            float x[N];
-#pragma unroll
-            for (int j = 0; j < N; ++j) x[j] = j < live ? load1(q + j) : 0.0f;
-            if constexpr (sizeof(T) == 4) {
-                r.v = f32x4{x[0], x[1], x[2], x[3]};
-                if constexpr (N == 8) r.w = f32x4{x[4], x[5], x[6], x[7]};
-            } else {
-#pragma unroll
-                for (int j = 0; j < N / 2; ++j) r.v[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
-            }
-        }
-        return r;
-    }
-}
 template <int N>
 __device__ __forceinline__ void values_n(const RawN<Bf16, N> &r, float *x) {
+    if constexpr (N == 1) x[0] = bf16_lo(r.v);
+    else if constexpr (N == 2) x[0] = bf16_lo(r.v), x[1] = bf16_hi(r.v);
+    else
 #pragma unroll
-    for (int j = 0; j < N / 2; ++j) x[2 * j] = bf16_lo(r.v[j]), x[2 * j + 1] = bf16_hi(r.v[j]);
+        for (int j = 0; j < N / 2; ++j) x[2 * j] = bf16_lo(r.v[j]), x[2 * j + 1] = bf16_hi(r.v[j]);
 }
 template <int N>
 __device__ __forceinline__ void values_n(const RawN<float, N> &r, float *x) {
+    if constexpr (N == 1) x[0] = r.v;
+    else
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = r.v[j];
+        for (int j = 0; j < (N == 2 ? 2 : 4); ++j) x[j] = r.v[j];
     if constexpr (N == 8)
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[4 + j] = r.w[j];
+}
+template <typename T, int N>
+__device__ __forceinline__ RawN<T, N> raw_from(const float *x) {
+    RawN<T, N> r;
+    if constexpr (sizeof(T) == 2) {
+        if constexpr (N == 1) r.v = (uint16_t)pack_bf16x2(x[0], 0.0f);
+        else if constexpr (N == 2) r.v = pack_bf16x2(x[0], x[1]);
+        else
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) r.v[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+    } else {
+        if constexpr (N == 1) r.v = x[0];
+        else if constexpr (N == 2) r.v = f32x2{x[0], x[1]};
+        else r.v = f32x4{x[0], x[1], x[2], x[3]};
+        if constexpr (N == 8) r.w = f32x4{x[4], x[5], x[6], x[7]};
+    }
+    return r;
+}
+
+// Elements at .. at + N - 1 of a matrix, of which the first `live` (none, some or all) are
+// wanted. Every lane loads N, without a branch, so that many loads are in flight: those
+// that would pass the matrix's end start earlier, by `shift`, and lanes with nothing to
+// load take its last elements. What is not wanted is made zero afterwards, in turns that
+// have such lanes at all.
+// Offsets are 32 bits (a matrix has less than 2^30 elements), so that an address is a
+// uniform base and one register.
+template <int N> struct Span {
+    uint32_t at;
+    int live;
+    __device__ __forceinline__ uint32_t from(const Item &e) const {
+        const int last = (int)e.total - N;
+        return last >= 0 ? min(at, (uint32_t)last) : 0u;
+    }
+    __device__ __forceinline__ void fix(const Item &e, float *x) const {
+        if (!__any(live < N)) return;
+        const int shift = (int)(at - from(e));
+#pragma unroll
+        for (int o = N / 2; o > 0; o /= 2)
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = (shift & o) ? (j + o < N ? x[j + o] : 0.0f) : x[j];
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = j < live ? x[j] : 0.0f;
+    }
+};
+// Of row `row` of the longer side in a tall matrix, columns from `col` on; of row `row` of the
+// shorter side in a wide one. Rows that are not there are taken as the last one.
+template <int N>
+__device__ __forceinline__ Span<N> tall_span(const Item &e, int row, int rows, int col) {
+    return {(uint32_t)min(row, rows - 1) * e.side + col, row < rows ? e.side - col : 0};
+}
+template <int N>
+__device__ __forceinline__ Span<N> wide_span(const Item &e, int row, int l, int live) {
+    return {(uint32_t)min(row, e.side - 1) * e.length + l, row < e.side ? live : 0};
+}
+template <typename T> __device__ __forceinline__ T *place(const void *p, uint32_t at) {
+    return reinterpret_cast<T *>(reinterpret_cast<char *>(const_cast<void *>(p)) + at * (uint32_t)sizeof(T));
+}
+template <typename T, int N, bool kStream>
+__device__ __forceinline__ RawN<T, N> load_n(const Item &e, const void *p, const Span<N> &s) {
+    if constexpr (std::is_same_v<T, None>) return {};
+    else {
+        if (e.total < N) {  // less than one vector: `from` is 0 and the shift `at`
+            float x[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = load1(static_cast<const T *>(p) + min(j, (int)e.total - 1));
+            return raw_from<T, N>(x);
+        }
+        const T *q = place<const T>(p, s.from(e));
+        RawN<T, N> r;
+        if constexpr (N == 1) {
+            r.v = *reinterpret_cast<const decltype(r.v) *>(q);
+        } else if constexpr (N == 2 && sizeof(T) == 4) {
+            const f32x2_at4 *f = reinterpret_cast<const f32x2_at4 *>(q);
+            r.v = kStream ? __builtin_nontemporal_load(f) : *f;
+        } else if constexpr (N == 2) {
+            const u32_at2 *f = reinterpret_cast<const u32_at2 *>(q);
+            r.v = kStream ? __builtin_nontemporal_load(f) : *f;
+        } else if constexpr (sizeof(T) == 4) {
+            const f32x4_at4 *f = reinterpret_cast<const f32x4_at4 *>(q);
+            r.v = kStream ? __builtin_nontemporal_load(f) : *f;
+            const f32x4_at4 *f1 = reinterpret_cast<const f32x4_at4 *>(q + 4);
+            if constexpr (N == 8) r.w = kStream ? __builtin_nontemporal_load(f1) : *f1;
+        } else if constexpr (N == 8) {
+            const u32x4_at2 *f = reinterpret_cast<const u32x4_at2 *>(q);
+            r.v = kStream ? __builtin_nontemporal_load(f) : *f;
+        } else {
+            const u32x2_at2 *f = reinterpret_cast<const u32x2_at2 *>(q);
+            r.v = kStream ? __builtin_nontemporal_load(f) : *f;
+        }
+        return r;
+    }
 }
 // Weights and momenta go past the caches: nothing here reads them again.
 template <int N, typename T>
 __device__ __forceinline__ void store_n(T *q, int live, const float *x) {
     if (live >= N) {
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int j = 0; j < N; j += 4)
-                __builtin_nontemporal_store(f32x4{x[j], x[j + 1], x[j + 2], x[j + 3]}, reinterpret_cast<f32x4_at4 *>(q + j));
-        } else if constexpr (N == 8) {
-            u32x4 r;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
-            __builtin_nontemporal_store(r, reinterpret_cast<u32x4_at2 *>(q));
-        } else {
-            __builtin_nontemporal_store(u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])},
-                                        reinterpret_cast<u32x2_at2 *>(q));
-        }
+        const RawN<T, N> r = raw_from<T, N>(x);
+        if constexpr (N == 2 && sizeof(T) == 4) __builtin_nontemporal_store(r.v, reinterpret_cast<f32x2_at4 *>(q));
+        else if constexpr (N == 2) __builtin_nontemporal_store(r.v, reinterpret_cast<u32_at2 *>(q));
+        else if constexpr (sizeof(T) == 4) __builtin_nontemporal_store(r.v, reinterpret_cast<f32x4_at4 *>(q));
+        else if constexpr (N == 8) __builtin_nontemporal_store(r.v, reinterpret_cast<u32x4_at2 *>(q));
+        else __builtin_nontemporal_store(r.v, reinterpret_cast<u32x2_at2 *>(q));
+        if constexpr (N == 8 && sizeof(T) == 4) __builtin_nontemporal_store(r.w, reinterpret_cast<f32x4_at4 *>(q + 4));
         return;
     }
 #pragma unroll
@@ -174,13 +235,14 @@ template <typename G, typename M, int N> struct Raw {
     RawN<M, N> m;
 };
 template <typename G, typename M, int N, bool kStream>
-__device__ __forceinline__ Raw<G, M, N> load_update(const Item &e, int64_t at, int live) {
-    return {load_n<G, N, kStream>(e.g, at, live), load_n<M, N, kStream>(e.m, at, live)};
+__device__ __forceinline__ Raw<G, M, N> load_update(const Item &e, const Span<N> &s) {
+    return {load_n<G, N, kStream>(e, e.g, s), load_n<M, N, kStream>(e, e.m, s)};
 }
 // Their update, and the new momentum. Each is computed by the same operations in both
 // passes, so both see the same bits.
 template <typename G, typename M, int N>
-__device__ __forceinline__ void update_of(const Raw<G, M, N> &r, const Scalars &c, float *u, float *m) {
+__device__ __forceinline__ void update_of(const Item &e, const Raw<G, M, N> &r, const Span<N> &s, const Scalars &c, float *u,
+                                          float *m) {
     values_n<N>(r.g, u);
     if constexpr (!std::is_same_v<M, None>) {
         values_n<N>(r.m, m);
@@ -190,7 +252,9 @@ __device__ __forceinline__ void update_of(const Raw<G, M, N> &r, const Scalars &
             m[j] = fmaf(c.mu, m[j], g);
             u[j] = c.nesterov ? fmaf(c.mu, m[j], g) : m[j];
         }
+        s.fix(e, m);
     }
+    s.fix(e, u);
 }
 
 // ---- fp32 products on the bf16 matrix instruction ----
@@ -245,69 +309,46 @@ constexpr int kPartsOf = std::is_same_v<G, Bf16> && std::is_same_v<M, None> ? 1 
 // and added in fp64. In a tall matrix a lane loads NI consecutive columns of rows 4 r + k,
 // so its column in operand i is NI n + i; in a wide one rows 8 k + r of column 16 i + n.
 template <typename G, typename M, int NI, int NJ, bool kDiag>
-__device__ __forceinline__ void gram_rows(const Item &e, const Scalars &c, int bi, int bj, int64_t begin, int64_t end,
+__device__ __forceinline__ void gram_rows(const Item &e, const Scalars &c, int bi, int bj, int begin, int end,
                                           f64x4 *sums) {
     constexpr int kParts = kPartsOf<G, M>;
     constexpr int kTiles = kDiag ? NI * (NI + 1) / 2 : NI * NJ;
     const int lane = threadIdx.x % 64, n = lane % 16, k = lane / 16;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) sums[t] = f64x4{0.0, 0.0, 0.0, 0.0};
-    auto load = [&](auto &ops, int block, int64_t row) {
+    auto load = [&](auto &ops, int block, int row) {
         constexpr int N = sizeof(ops) / sizeof(ops[0]);
         if (e.tall) {
             const int col = 64 * block + N * n;
-            const int64_t first = (row + k) * e.side + col, step = 4 * (int64_t)e.side;
-            const int rows = (int)min(end - row - k, (int64_t)32);  // the lane's are every fourth of them
+            auto span = [&](int r) { return tall_span<N>(e, row + 4 * r + k, end, col); };
+            Raw<G, M, N> raw[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) raw[r] = load_update<G, M, N, false>(e, span(r));
             float x[N][8];
-            if constexpr (N == 4) {
-                Raw<G, M, 4> raw[8];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) raw[r] = load_update<G, M, 4, false>(e, first + r * step, 4 * r < rows ? e.side - col : 0);
+            for (int r = 0; r < 8; ++r) {
+                float u[N], m[N];
+                update_of(e, raw[r], span(r), c, u, m);
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    float u[4], m[4];
-                    update_of(raw[r], c, u, m);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j][r] = u[j];
-                }
-            } else {
-                Raw<G, M, 4> raw[N][8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-#pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        const int live = 4 * r < rows && col + j < e.side ? 1 : 0;
-                        raw[j][r] = load_update<G, M, 4, false>(e, first + r * step + j, live);
-                    }
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-#pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        float u[4], m[4];
-                        update_of(raw[j][r], c, u, m);
-                        x[j][r] = u[0];
-                    }
+                for (int j = 0; j < N; ++j) x[j][r] = u[j];
             }
 #pragma unroll
             for (int j = 0; j < N; ++j) ops[j] = operand_of<kParts>(x[j]);
         } else {
+            const int l = row + 8 * k;
+            auto span = [&](int j) { return wide_span<8>(e, 64 * block + 16 * j + n, min(l, end - 1), end - l); };
             Raw<G, M, 8> raw[N];
-            const int64_t l = row + 8 * k;
-            const int rows = l < end ? (int)min(end - l, (int64_t)8) : 0;
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const int col = 64 * block + 16 * j + n;
-                raw[j] = load_update<G, M, 8, false>(e, (int64_t)col * e.length + l, col < e.side ? rows : 0);
-            }
+            for (int j = 0; j < N; ++j) raw[j] = load_update<G, M, 8, false>(e, span(j));
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 float u[8], m[8];
-                update_of(raw[j], c, u, m);
+                update_of(e, raw[j], span(j), c, u, m);
                 ops[j] = operand_of<kParts>(u);
             }
         }
     };
-    for (int64_t row = begin; row < end; row += 32) {
+    for (int row = begin; row < end; row += 32) {
         Operand<kParts> x[NI], y[kDiag ? 1 : NJ];
         load(x, bi, row);
         if constexpr (!kDiag) load(y, bj, row);
@@ -325,12 +366,12 @@ __device__ __forceinline__ void gram_rows(const Item &e, const Scalars &c, int b
 
 // Sums of the workgroup's waves, then out: [tile][register][lane].
 template <typename G, typename M, int NI, int NJ, bool kDiag>
-__device__ __forceinline__ void gram_part(const Item &e, const Scalars &c, int bi, int bj, int64_t begin, int64_t end,
+__device__ __forceinline__ void gram_part(const Item &e, const Scalars &c, int bi, int bj, int begin, int end,
                                           double *out, double (*part)[256]) {
     constexpr int kTiles = kDiag ? NI * (NI + 1) / 2 : NI * NJ;
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const int64_t share = ((end - begin + kWaves - 1) / kWaves + 31) / 32 * 32;
-    const int64_t b = min(begin + wave * share, end);
+    const int share = ((end - begin + kWaves - 1) / kWaves + 31) / 32 * 32;
+    const int b = min(begin + wave * share, end);
     f64x4 sums[kTiles];
     gram_rows<G, M, NI, NJ, kDiag>(e, c, bi, bj, b, min(b + share, end), sums);
     for (int v = 0; v < kWaves; ++v) {
@@ -365,7 +406,7 @@ __global__ __launch_bounds__(kThreads, 2) void muon_gram_kernel(List list, Scala
     const Item e = list.item[find(list.gram_first, list.count, wg)];
     if ((e.side > kSmall) != kLarge) return;
     const uint32_t own = wg - e.gram_first, chunk = own / e.gram_pairs, pair = own % e.gram_pairs;
-    const int64_t begin = (int64_t)chunk * e.gram_chunk, end = min(begin + e.gram_chunk, e.length);
+    const int begin = chunk * e.gram_chunk, end = min(begin + (int)e.gram_chunk, e.length);
     double *out = ws.partial + e.partial + (int64_t)own * gram_tiles(e.side) * 256;
     if constexpr (kLarge) {
         int bi, bj;
@@ -671,37 +712,39 @@ __global__ __launch_bounds__(kThreads) void muon_product_kernel(List list, Scala
 
 // ---- O = U P and the step ----
 
-// N consecutive weights before the step.
-template <int N> struct Weight {
-    RawN<Bf16, N> half;
-    RawN<float, N> full;
-};
-template <int N>
-__device__ __forceinline__ Weight<N> load_weight(const Item &e, const Scalars &c, int64_t at, int live) {
-    Weight<N> r{};
-    if (!c.step) return r;
-    if (e.master) r.full = load_n<float, N, true>(e.master, at, live);
-    else if (c.w_bf16) r.half = load_n<Bf16, N, true>(e.w, at, live);
-    else r.full = load_n<float, N, true>(e.w, at, live);
-    return r;
+// N consecutive weights before the step. W: bf16 weights without a master, or fp32 ones
+// (masters among them); in the orthogonalising alone, the output's type.
+template <typename W, int N>
+__device__ __forceinline__ RawN<W, N> load_weight(const Item &e, const Scalars &c, const Span<N> &s) {
+    if (!c.step) return {};
+    if constexpr (sizeof(W) == 4) return load_n<float, N, true>(e, e.master ? e.master : e.w, s);
+    else return load_n<Bf16, N, true>(e, e.w, s);
 }
 // Their step, or the output alone.
-template <int N>
-__device__ __forceinline__ void finish(const Item &e, const Scalars &c, const Weight<N> &before, int64_t at, int live, float *o) {
+template <typename W, int N>
+__device__ __forceinline__ void finish(const Item &e, const Scalars &c, const RawN<W, N> &before, const Span<N> &s, float *o) {
     if (c.step) {
         float w[N];
-        if (!e.master && c.w_bf16) values_n<N>(before.half, w);
-        else values_n<N>(before.full, w);
+        values_n<N>(before, w);
+        s.fix(e, w);
 #pragma unroll
         for (int j = 0; j < N; ++j) o[j] = fmaf(-e.step, o[j], e.keep * w[j]);
-        if (e.master) store_n<N>(e.master + at, live, o);
+        if constexpr (sizeof(W) == 4)
+            if (e.master) {
+                store_n<N>(place<float>(e.master, s.at), s.live, o);
+                return store_n<N>(place<Bf16>(e.w, s.at), s.live, o);
+            }
     }
-    if (c.w_bf16) store_n<N>(static_cast<Bf16 *>(e.w) + at, live, o);
-    else store_n<N>(static_cast<float *>(e.w) + at, live, o);
+    store_n<N>(place<W>(e.w, s.at), s.live, o);
+}
+// Whether a kernel of this W takes the matrix.
+template <typename W>
+__device__ __forceinline__ bool takes(const Item &e, const Scalars &c) {
+    return (sizeof(W) == 4) == (e.master != nullptr || !c.w_bf16);
 }
 template <typename M, int N>
-__device__ __forceinline__ void store_momentum(const Item &e, int64_t at, int live, const float *m) {
-    if constexpr (!std::is_same_v<M, None>) store_n<N>(static_cast<M *>(e.m) + at, live, m);
+__device__ __forceinline__ void store_momentum(const Item &e, const Span<N> &s, const float *m) {
+    if constexpr (!std::is_same_v<M, None>) store_n<N>(place<M>(e.m, s.at), s.live, m);
 }
 
 // A part of P, `blocks` operands wide: result i, operand s.
@@ -728,114 +771,125 @@ __device__ __forceinline__ f32x4 mfma_p(const Operand<3> &p, const Operand<kPart
 }
 
 // A matrix of up to 64 on its shorter side, P in LDS. In a tall matrix a wave takes 16
-// rows, a lane columns 32 s + 8 k .. + 7 of row n, of U and of O; in a wide one 64 columns, a
-// lane four of them (4 n .. + 3) in rows 32 s + 8 k .. + 7.
-template <typename G, typename M, int kBlocks>
-__device__ __forceinline__ void apply_small(const Item &e, const Scalars &c, const u32x4 *p, int64_t begin, int64_t end) {
+// rows, a lane columns 32 s + 8 k .. + 7 of row n, of U and of O; in a wide one 16 kWideCols
+// columns, a lane kWideCols of them (from kWideCols n on) in rows 32 s + 8 k .. + 7. All of
+// a turn's loads are issued before its first product. The barriers to the scheduler keep
+// the operands of P from being read all at once, which spills.
+constexpr int kWideCols = 4;
+
+template <typename G, typename M, typename W, int kBlocks>
+__device__ __forceinline__ void apply_tall(const Item &e, const Scalars &c, const u32x4 *p, int begin, int end) {
     constexpr int kParts = kPartsOf<G, M>;
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, n = lane % 16, k = lane / 16;
-    if (e.tall) {
-        for (int64_t row = begin + wave * 16; row < end; row += 16 * kWaves) {
-            const int64_t l = row + n, at = l * e.side + 8 * k;
-            const int live = l < end ? e.side - 8 * k : 0;
-            Raw<G, M, 8> raw[kBlocks];
-            Weight<8> before[kBlocks];
+    for (int row = begin + wave * 16; row < end; row += 16 * kWaves) {
+        auto span = [&](int s) { return tall_span<8>(e, row + n, end, 32 * s + 8 * k); };
+        Raw<G, M, 8> raw[kBlocks];
+        RawN<W, 8> before[kBlocks];
 #pragma unroll
-            for (int s = 0; s < kBlocks; ++s) raw[s] = load_update<G, M, 8, true>(e, at + 32 * s, live - 32 * s);
+        for (int s = 0; s < kBlocks; ++s) raw[s] = load_update<G, M, 8, true>(e, span(s));
 #pragma unroll
-            for (int s = 0; s < kBlocks; ++s) before[s] = load_weight<8>(e, c, at + 32 * s, live - 32 * s);
-            Operand<kParts> u[kBlocks];
+        for (int s = 0; s < kBlocks; ++s) before[s] = load_weight<W, 8>(e, c, span(s));
+        __builtin_amdgcn_sched_barrier(0);
+        Operand<kParts> u[kBlocks];
 #pragma unroll
-            for (int s = 0; s < kBlocks; ++s) {
-                float x[8], m[8];
-                update_of(raw[s], c, x, m);
-                store_momentum<M, 8>(e, at + 32 * s, live - 32 * s, m);
-                u[s] = operand_of<kParts>(x);
-            }
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                float o[8];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int s = 0; s < kBlocks; ++s) acc = mfma_p<kParts>(p_operand<kParts>(p, kBlocks, 2 * b + h, s), u[s], acc);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[4 * h + r] = acc[r];
-                }
-                finish<8>(e, c, before[b], at + 32 * b, live - 32 * b, o);
-            }
+        for (int s = 0; s < kBlocks; ++s) {
+            float x[8], m[8];
+            update_of(e, raw[s], span(s), c, x, m);
+            store_momentum<M, 8>(e, span(s), m);
+            u[s] = operand_of<kParts>(x);
         }
-    } else {
-        for (int64_t col = begin + wave * 64; col < end; col += 64 * kWaves) {
-            const int64_t l = col + 4 * n;
-            const int live = l < end ? (int)min(end - l, (int64_t)4) : 0;
-            f32x4 acc[2 * kBlocks][4];
 #pragma unroll
-            for (int i = 0; i < 2 * kBlocks; ++i)
+        for (int b = 0; b < kBlocks; ++b) {
+            float o[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int h = 0; h < 2; ++h) {
+                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int s = 0; s < kBlocks; ++s) {
-                Raw<G, M, 4> raw[8];
+                for (int s = 0; s < kBlocks; ++s) acc = mfma_p<kParts>(p_operand<kParts>(p, kBlocks, 2 * b + h, s), u[s], acc);
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const int row = 32 * s + 8 * k + r;
-                    raw[r] = load_update<G, M, 4, true>(e, (int64_t)row * e.length + l, row < e.side ? live : 0);
-                }
-                float x[4][8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const int row = 32 * s + 8 * k + r;
-                    float u[4], m[4];
-                    update_of(raw[r], c, u, m);
-                    store_momentum<M, 4>(e, (int64_t)row * e.length + l, row < e.side ? live : 0, m);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j][r] = u[j];
-                }
-                Operand<kParts> u[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) u[j] = operand_of<kParts>(x[j]);
-#pragma unroll
-                for (int i = 0; i < 2 * kBlocks; ++i) {
-                    const Operand<3> a = p_operand<kParts>(p, kBlocks, i, s);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = mfma_p<kParts>(a, u[j], acc[i][j]);
-                }
+                for (int r = 0; r < 4; ++r) o[4 * h + r] = acc[r];
             }
-#pragma unroll
-            for (int i = 0; i < 2 * kBlocks; ++i) {
-                Weight<4> before[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 32 * (i / 2) + 8 * k + 4 * (i % 2) + r;
-                    before[r] = load_weight<4>(e, c, (int64_t)row * e.length + l, row < e.side ? live : 0);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 32 * (i / 2) + 8 * k + 4 * (i % 2) + r;
-                    float o[4] = {acc[i][0][r], acc[i][1][r], acc[i][2][r], acc[i][3][r]};
-                    finish<4>(e, c, before[r], (int64_t)row * e.length + l, row < e.side ? live : 0, o);
-                }
-            }
+            __builtin_amdgcn_sched_barrier(0);
+            finish<W, 8>(e, c, before[b], span(b), o);
         }
     }
 }
 
-template <typename G, typename M>
+template <typename G, typename M, typename W, int kBlocks>
+__device__ __forceinline__ void apply_wide(const Item &e, const Scalars &c, const u32x4 *p, int begin, int end) {
+    constexpr int kParts = kPartsOf<G, M>, V = kWideCols;
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, n = lane % 16, k = lane / 16;
+    for (int col = begin + wave * 16 * V; col < end; col += 16 * V * kWaves) {
+        const int l = col + V * n;
+        auto span = [&](int s, int r) { return wide_span<V>(e, 32 * s + 8 * k + r, min(l, end - 1), end - l); };
+        Raw<G, M, V> raw[kBlocks][8];
+        RawN<W, V> before[kBlocks][8];
+#pragma unroll
+        for (int s = 0; s < kBlocks; ++s)
+#pragma unroll
+            for (int r = 0; r < 8; ++r) raw[s][r] = load_update<G, M, V, true>(e, span(s, r));
+#pragma unroll
+        for (int s = 0; s < kBlocks; ++s)
+#pragma unroll
+            for (int r = 0; r < 8; ++r) before[s][r] = load_weight<W, V>(e, c, span(s, r));
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 acc[2 * kBlocks][V];
+#pragma unroll
+        for (int i = 0; i < 2 * kBlocks; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < kBlocks; ++s) {
+            float x[V][8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                float u[V], m[V];
+                update_of(e, raw[s][r], span(s, r), c, u, m);
+                store_momentum<M, V>(e, span(s, r), m);
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[j][r] = u[j];
+            }
+            Operand<kParts> u[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) u[j] = operand_of<kParts>(x[j]);
+#pragma unroll
+            for (int i = 0; i < 2 * kBlocks; ++i) {
+                const Operand<3> a = p_operand<kParts>(p, kBlocks, i, s);
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[i][j] = mfma_p<kParts>(a, u[j], acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < kBlocks; ++s)
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                float o[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) o[j] = acc[2 * s + r / 4][j][r % 4];
+                finish<W, V>(e, c, before[s][r], span(s, r), o);
+            }
+    }
+}
+
+template <typename G, typename M, typename W>
 __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(List list, Scalars c, Space ws) {
     __shared__ u32x4 sp[3 * 2 * 2 * 2 * 64];
     const uint32_t wg = gridDim.x - 1 - blockIdx.x;  // the first pass's last reads may still be cached
     const int32_t index = find(list.apply_first, list.count, wg);
     const Item e = list.item[index];
-    if (e.side > kSmall || (c.step && !isfinite(ws.norm[index]))) return;
-    const int64_t begin = (int64_t)(wg - e.apply_first) * e.apply_chunk;
-    const int64_t end = min(begin + e.apply_chunk, e.length);
+    if (e.side > kSmall || !takes<W>(e, c) || (c.step && !isfinite(ws.norm[index]))) return;
+    const int begin = (wg - e.apply_first) * e.apply_chunk, end = min(begin + (int)e.apply_chunk, e.length);
     const u32x4 *p = reinterpret_cast<const u32x4 *>(ws.p + (int64_t)e.p * 512);
     for (int i = threadIdx.x; i < p_elements(e.side) / 8; i += kThreads) sp[i] = p[i];
     __syncthreads();
-    if (e.side <= 32) apply_small<G, M, 1>(e, c, sp, begin, end);
-    else apply_small<G, M, 2>(e, c, sp, begin, end);
+    if (e.tall) {
+        if (e.side <= 32) apply_tall<G, M, W, 1>(e, c, sp, begin, end);
+        else apply_tall<G, M, W, 2>(e, c, sp, begin, end);
+    } else {
+        if (e.side <= 32) apply_wide<G, M, W, 1>(e, c, sp, begin, end);
+        else apply_wide<G, M, W, 2>(e, c, sp, begin, end);
+    }
 }
 
 // A matrix of up to 256 on its shorter side, 64 places of the longer at a time: the
@@ -844,50 +898,47 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(List list, Scal
 // operand j: 16 j + n in a tall matrix, 4 n + j in a wide one.
 constexpr int kLargeThreads = 512, kLargeWaves = kLargeThreads / 64;
 
-template <typename G, typename M>
+template <typename G, typename M, typename W>
 __global__ __launch_bounds__(kLargeThreads) void muon_apply_large_kernel(List list, Scalars c, Space ws) {
     extern __shared__ u32x4 us[];  // [part][place's operand j][operand s][lane]
     constexpr int kParts = kPartsOf<G, M>;
     const uint32_t wg = gridDim.x - 1 - blockIdx.x;
     const int32_t index = find(list.apply_first, list.count, wg);
     const Item e = list.item[index];
-    if (e.side <= kSmall || (c.step && !isfinite(ws.norm[index]))) return;
-    const int64_t begin = (int64_t)(wg - e.apply_first) * e.apply_chunk;
-    const int64_t end = min(begin + e.apply_chunk, e.length);
+    if (e.side <= kSmall || !takes<W>(e, c) || (c.step && !isfinite(ws.norm[index]))) return;
+    const int begin = (wg - e.apply_first) * e.apply_chunk, end = min(begin + (int)e.apply_chunk, e.length);
     const u32x4 *p = reinterpret_cast<const u32x4 *>(ws.p + (int64_t)e.p * 512);
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, n = lane % 16, k = lane / 16;
     const int blocks = p_blocks(e.side);
-    auto place = [&](int part, int j, int s) { return us + ((part * 4 + j) * blocks + s) * 64; };
-    for (int64_t l0 = begin; l0 < end; l0 += 64) {
-        const int rows = (int)min(end - l0, (int64_t)64);
+    auto operand = [&](int part, int j, int s) { return us + ((part * 4 + j) * blocks + s) * 64; };
+    for (int l0 = begin; l0 < end; l0 += 64) {
         __syncthreads();
         if (e.tall) {
             for (int i = threadIdx.x; i < 64 * 4 * blocks; i += kLargeThreads) {
-                const int row = i / (4 * blocks), col = i % (4 * blocks) * 8, live = row < rows ? e.side - col : 0;
-                const int64_t at = (l0 + row) * e.side + col;
+                const int row = i / (4 * blocks), col = i % (4 * blocks) * 8;
+                const Span<8> span = tall_span<8>(e, l0 + row, end, col);
                 float x[8], m[8];
-                update_of(load_update<G, M, 8, true>(e, at, live), c, x, m);
-                store_momentum<M, 8>(e, at, live, m);
+                update_of(e, load_update<G, M, 8, true>(e, span), span, c, x, m);
+                store_momentum<M, 8>(e, span, m);
                 const Operand<kParts> u = operand_of<kParts>(x);
 #pragma unroll
                 for (int part = 0; part < kParts; ++part)
-                    place(part, row / 16, col / 32)[col % 32 / 8 * 16 + row % 16] = u.part[part];
+                    operand(part, row / 16, col / 32)[col % 32 / 8 * 16 + row % 16] = u.part[part];
             }
         } else {
             for (int i = threadIdx.x; i < 16 * 4 * blocks; i += kLargeThreads) {
                 const int first = i / 16 * 8, four = i % 16;
-                const int64_t l = l0 + 4 * four;
-                const int live = max(rows - 4 * four, 0);
+                const int l = l0 + 4 * four;
+                auto span = [&](int r) { return wide_span<4>(e, first + r, min(l, end - 1), end - l); };
                 Raw<G, M, 4> raw[8];
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    raw[r] = load_update<G, M, 4, true>(e, (int64_t)(first + r) * e.length + l, first + r < e.side ? live : 0);
+                for (int r = 0; r < 8; ++r) raw[r] = load_update<G, M, 4, true>(e, span(r));
                 float x[4][8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
                     float u[4], m[4];
-                    update_of(raw[r], c, u, m);
-                    store_momentum<M, 4>(e, (int64_t)(first + r) * e.length + l, first + r < e.side ? live : 0, m);
+                    update_of(e, raw[r], span(r), c, u, m);
+                    store_momentum<M, 4>(e, span(r), m);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[j][r] = u[j];
                 }
@@ -896,7 +947,7 @@ __global__ __launch_bounds__(kLargeThreads) void muon_apply_large_kernel(List li
                     const Operand<kParts> u = operand_of<kParts>(x[j]);
 #pragma unroll
                     for (int part = 0; part < kParts; ++part)
-                        place(part, j, first / 32)[first % 32 / 8 * 16 + four] = u.part[part];
+                        operand(part, j, first / 32)[first % 32 / 8 * 16 + four] = u.part[part];
                 }
             }
         }
@@ -913,7 +964,7 @@ __global__ __launch_bounds__(kLargeThreads) void muon_apply_large_kernel(List li
                 for (int j = 0; j < 4; ++j) {
                     Operand<kParts> u;
 #pragma unroll
-                    for (int part = 0; part < kParts; ++part) u.part[part] = place(part, j, s)[lane];
+                    for (int part = 0; part < kParts; ++part) u.part[part] = operand(part, j, s)[lane];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) acc[h][j] = mfma_p<kParts>(a[h], u, acc[h][j]);
                 }
@@ -922,23 +973,22 @@ __global__ __launch_bounds__(kLargeThreads) void muon_apply_large_kernel(List li
             if (e.tall) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int row = 16 * j + n, live = row < rows ? e.side - first : 0;
-                    const int64_t at = (l0 + row) * e.side + first;
-                    const Weight<8> before = load_weight<8>(e, c, at, live);
+                    const int row = 16 * j + n;
+                    const Span<8> span = tall_span<8>(e, l0 + row, end, first);
+                    const RawN<W, 8> before = load_weight<W, 8>(e, c, span);
                     float o[8];
 #pragma unroll
                     for (int r = 0; r < 8; ++r) o[r] = acc[r / 4][j][r % 4];
-                    finish<8>(e, c, before, at, live, o);
+                    finish<W, 8>(e, c, before, span, o);
                 }
             } else {
-                const int64_t l = l0 + 4 * n;
+                const int l = l0 + 4 * n;
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    const int live = first + r < e.side ? rows - 4 * n : 0;
-                    const int64_t at = (int64_t)(first + r) * e.length + l;
-                    const Weight<4> before = load_weight<4>(e, c, at, live);
+                    const Span<4> span = wide_span<4>(e, first + r, min(l, end - 1), end - l);
+                    const RawN<W, 4> before = load_weight<W, 4>(e, c, span);
                     float o[4] = {acc[r / 4][0][r % 4], acc[r / 4][1][r % 4], acc[r / 4][2][r % 4], acc[r / 4][3][r % 4]};
-                    finish<4>(e, c, before, at, live, o);
+                    finish<W, 4>(e, c, before, span, o);
                 }
             }
         }
@@ -954,7 +1004,8 @@ size_t round_up(size_t x, size_t to) { return (x + to - 1) / to * to; }
 struct Plan {
     size_t items, gram_first, apply_first, norm, partial, mats, p, bytes;  // offsets
     uint32_t gram_wgs, apply_wgs;
-    int32_t count, largest, smallest;  // matrices with elements; their largest and smallest shorter side
+    int32_t count, masters;      // matrices with elements, and with a master weight
+    int32_t largest, smallest;   // of their shorter sides
     bool fits;
 };
 constexpr int64_t kShares = 2048;
@@ -968,6 +1019,7 @@ Plan make_plan(const MuonMatrix *list, int32_t count, F &&each) {
         const int64_t length = list[i].rows < list[i].cols ? list[i].cols : list[i].rows;
         if (side == 0) continue;
         ++p.count;
+        p.masters += list[i].master != nullptr;
         const int nb = blocks_of((int)side);
         gram_rows += length * (nb * (nb + 1) / 2);
         apply_rows += length;
@@ -987,7 +1039,8 @@ Plan make_plan(const MuonMatrix *list, int32_t count, F &&each) {
         const MuonMatrix &x = list[i];
         Item e{};
         e.tall = x.rows >= x.cols;
-        e.side = (int32_t)(e.tall ? x.cols : x.rows), e.length = e.tall ? x.rows : x.cols;
+        e.side = (int32_t)(e.tall ? x.cols : x.rows), e.length = (int32_t)(e.tall ? x.rows : x.cols);
+        e.total = (int32_t)(x.rows * x.cols);
         if (e.side == 0) continue;
         const int nb = blocks_of(e.side);
         const int64_t edge = 64 * nb;
@@ -1062,15 +1115,26 @@ hipError_t run(const Plan &p, const List &list, const Scalars &c, const Space &w
         }
         if (r != hipSuccess) return r;
     }
-    if (small) {
-        muon_apply_kernel<G, M><<<dim3(p.apply_wgs), dim3(kThreads), 0, s>>>(list, c, ws);
-        if (!note()) return r;
-    }
-    if (large) {
-        const size_t lds = (size_t)kPartsOf<G, M> * 4 * p_blocks(p.largest) * 1024;
-        if ((r = allow_lds(reinterpret_cast<const void *>(&muon_apply_large_kernel<G, M>), lds)) != hipSuccess) return r;
-        muon_apply_large_kernel<G, M><<<dim3(p.apply_wgs), dim3(kLargeThreads), lds, s>>>(list, c, ws);
-        note();
+    auto apply = [&](auto w) {
+        typedef decltype(w) W;
+        if (r == hipSuccess && small) {
+            muon_apply_kernel<G, M, W><<<dim3(p.apply_wgs), dim3(kThreads), 0, s>>>(list, c, ws);
+            note();
+        }
+        if (r == hipSuccess && large) {
+            const size_t lds = (size_t)kPartsOf<G, M> * 4 * p_blocks(p.largest) * 1024;
+            r = allow_lds(reinterpret_cast<const void *>(&muon_apply_large_kernel<G, M, W>), lds);
+            if (r != hipSuccess) return;
+            muon_apply_large_kernel<G, M, W><<<dim3(p.apply_wgs), dim3(kLargeThreads), lds, s>>>(list, c, ws);
+            note();
+        }
+    };
+    // the orthogonalising alone writes what it reads
+    if constexpr (std::is_same_v<M, None>) {
+        apply(G{});
+    } else {
+        if (c.w_bf16 && p.masters < p.count) apply(Bf16{});
+        if (!c.w_bf16 || p.masters > 0) apply(float{});
     }
     return r;
 }

@@ -76,7 +76,8 @@ struct MuonCall {
     bool step;
     nf4_dtype w, grad, m;
 };
-constexpr int kMuonSide = 256;  // of the shorter side at most
+constexpr int kMuonSide = 256;                            // of the shorter side at most
+constexpr int64_t kMuonElements = (int64_t(1) << 30) - 1;  // of a matrix: 32-bit offsets in bytes
 size_t muon_workspace(const MuonMatrix *list, int32_t count);
 hipError_t launch_muon(const MuonMatrix *list, int32_t count, const MuonCall &call, void *workspace, hipStream_t s);
 

