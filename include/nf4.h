@@ -701,8 +701,10 @@ nf4_status nf4_rotary_backward(const nf4_rotary_shape *shape, const uint64_t *tu
  * (a, b, c) = (3.4445, -4.775, 2.0315) five iterations bring the singular values
  * of X that are not tiny near 1. The smaller of rows and cols is at most 256, the
  * largest rank that the linears' adapters have: the iteration runs on the Gram
- * matrix of that side, summed in fp64 from fp32 sums over 32 rows, in fp64;
- * the products with the long matrices run in fp32.
+ * matrix of that side, summed in fp64 from fp32 sums over 32 rows (in fp64 throughout
+ * by nf4_orthogonalize in fp32), its first steps in fp64 and the others in fp32 (one in fp64
+ * with bf16 weights alone, two with fp32 weights or masters, all by nf4_orthogonalize
+ * in fp32); the products with the long matrices run in fp32.
  *
  *   w, master, grad, m  device, rows * cols elements each, as in nf4_adamw_entry
  *                       (m: m_dtype; zeros before the first step)
@@ -735,8 +737,8 @@ size_t nf4_muon_workspace_size(const nf4_muon_entry *entries, int32_t count);
 /* One step of every entry (see above).
  *   entries    host array, read during the call only
  *   workspace  256-byte aligned; calls that overlap must not share one
- * An entry whose update's norm is not finite (a gradient that is not, or elements
- * above about 1e18) keeps its weight and momentum. Sums run in an order that
+ * An entry whose update's norm is not finite or is 2^60 or more keeps its weight and
+ * momentum. Sums run in an order that
  * depends on the sizes alone. Buffers of different entries must not overlap. */
 nf4_status nf4_muon_step(const nf4_muon_entry *entries, int32_t count, int32_t w_dtype,
                          int32_t grad_dtype, int32_t m_dtype, const nf4_muon_config *config,
@@ -744,7 +746,7 @@ nf4_status nf4_muon_step(const nf4_muon_entry *entries, int32_t count, int32_t w
 
 /* The orthogonalising alone: w = X of u = grad (w and grad of one dtype; w may be
  * grad). master, m, lr, weight_decay, scale, momentum and nesterov are not read. A
- * matrix whose norm is not finite becomes NaN. */
+ * matrix whose norm is not finite or is 2^60 or more becomes NaN. */
 nf4_status nf4_orthogonalize(const nf4_muon_entry *entries, int32_t count, int32_t dtype,
                              const nf4_muon_config *config, void *workspace,
                              size_t workspace_bytes, void *stream);

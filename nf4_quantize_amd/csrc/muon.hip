@@ -53,9 +53,9 @@ struct Scalars {
     float mu, one_mu;
     int32_t nesterov;
     double eps, a, b, c;
-    int32_t iterations;
+    int32_t iterations, exact;  // steps; those of them in fp64, see exact_steps
     bool step;               // the optimizer's step, or the orthogonalising alone
-    bool w_bf16;
+    bool w_bf16, precise;    // precise: S is summed in fp64 throughout, see kPartsOf
 };
 struct Space {
     double *partial, *mats, *norm;  // norm: of each matrix's update
@@ -301,6 +301,11 @@ __device__ __forceinline__ f32x4 mfma_f32(const Operand<kParts> &a, const Operan
 }
 template <typename G, typename M>
 constexpr int kPartsOf = std::is_same_v<G, Bf16> && std::is_same_v<M, None> ? 1 : 3;
+// fp32 updates that are orthogonalised for themselves: S on the fp64 instruction. Where
+// the rows are not many more than the columns, the fp32 sums of 32 rows would leave up to
+// 8 times the error of a plain fp32 iteration (64 x 64: 7e-6 and 1.2e-6).
+template <typename G, typename M>
+constexpr bool kPrecise = std::is_same_v<G, float> && std::is_same_v<M, None>;
 
 // ---- S: the Gram matrix ----
 
@@ -316,15 +321,15 @@ __device__ __forceinline__ void gram_rows(const Item &e, const Scalars &c, int b
     const int lane = threadIdx.x % 64, n = lane % 16, k = lane / 16;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) sums[t] = f64x4{0.0, 0.0, 0.0, 0.0};
-    auto load = [&](auto &ops, int block, int row) {
-        constexpr int N = sizeof(ops) / sizeof(ops[0]);
+    // x[j][r]: eight rows of operand j's column
+    auto load = [&](auto &x, int block, int row) {
+        constexpr int N = sizeof(x) / sizeof(x[0]);
         if (e.tall) {
             const int col = 64 * block + N * n;
             auto span = [&](int r) { return tall_span<N>(e, row + 4 * r + k, end, col); };
             Raw<G, M, N> raw[8];
 #pragma unroll
             for (int r = 0; r < 8; ++r) raw[r] = load_update<G, M, N, false>(e, span(r));
-            float x[N][8];
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 float u[N], m[N];
@@ -332,8 +337,6 @@ __device__ __forceinline__ void gram_rows(const Item &e, const Scalars &c, int b
 #pragma unroll
                 for (int j = 0; j < N; ++j) x[j][r] = u[j];
             }
-#pragma unroll
-            for (int j = 0; j < N; ++j) ops[j] = operand_of<kParts>(x[j]);
         } else {
             const int l = row + 8 * k;
             auto span = [&](int j) { return wide_span<8>(e, 64 * block + 16 * j + n, min(l, end - 1), end - l); };
@@ -342,25 +345,47 @@ __device__ __forceinline__ void gram_rows(const Item &e, const Scalars &c, int b
             for (int j = 0; j < N; ++j) raw[j] = load_update<G, M, 8, false>(e, span(j));
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                float u[8], m[8];
-                update_of(e, raw[j], span(j), c, u, m);
-                ops[j] = operand_of<kParts>(u);
+                float m[8];
+                update_of(e, raw[j], span(j), c, x[j], m);
             }
         }
     };
     for (int row = begin; row < end; row += 32) {
-        Operand<kParts> x[NI], y[kDiag ? 1 : NJ];
-        load(x, bi, row);
-        if constexpr (!kDiag) load(y, bj, row);
-        int t = 0;
+        if constexpr (kPrecise<G, M>) {
+            float x[NI][8], y[kDiag ? 1 : NJ][8];
+            load(x, bi, row);
+            if constexpr (!kDiag) load(y, bj, row);
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+            for (int r = 0; r < 8; ++r) {
+                int t = 0;
 #pragma unroll
-            for (int j = kDiag ? i : 0; j < NJ; ++j, ++t) {
-                const f32x4 s = mfma_f32<kParts>(x[i], kDiag ? x[j] : y[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                for (int i = 0; i < NI; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) sums[t][r] += (double)s[r];
+                    for (int j = kDiag ? i : 0; j < NJ; ++j, ++t)
+                        sums[t] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)x[i][r], (double)(kDiag ? x[j][r] : y[j][r]), sums[t],
+                                                                       0, 0, 0);
             }
+        } else {
+            Operand<kParts> x[NI], y[kDiag ? 1 : NJ];
+            auto operands = [&](auto &ops, int block) {
+                constexpr int N = sizeof(ops) / sizeof(ops[0]);
+                float v[N][8];
+                load(v, block, row);
+#pragma unroll
+                for (int j = 0; j < N; ++j) ops[j] = operand_of<kParts>(v[j]);
+            };
+            operands(x, bi);
+            if constexpr (!kDiag) operands(y, bj);
+            int t = 0;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = kDiag ? i : 0; j < NJ; ++j, ++t) {
+                    const f32x4 s = mfma_f32<kParts>(x[i], kDiag ? x[j] : y[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sums[t][r] += (double)s[r];
+                }
+        }
     }
 }
 
@@ -421,7 +446,7 @@ __global__ __launch_bounds__(kThreads, 2) void muon_gram_kernel(List list, Scala
 
 // Where sum i of a pair of blocks lies in it; false for the half of a tile on the diagonal
 // that its other half has too (rounded otherwise: one of the two is taken).
-__device__ __forceinline__ bool place_of(const Item &e, int width, bool diag, int i, int &row, int &col) {
+__device__ __forceinline__ bool place_of(const Item &e, bool precise, int width, bool diag, int i, int &row, int &col) {
     int t = i / 256;
     const int reg = i / 64 % 4, lane = i % 64;
     int ti, tj;
@@ -432,25 +457,31 @@ __device__ __forceinline__ bool place_of(const Item &e, int width, bool diag, in
     } else {
         ti = t / width, tj = t % width;
     }
-    const int r = 4 * (lane / 16) + reg, n = lane % 16;
+    // the fp64 instruction's results lie otherwise
+    const int r = precise ? 4 * reg + lane / 16 : 4 * (lane / 16) + reg, n = lane % 16;
     row = e.tall ? width * r + ti : 16 * ti + r;
     col = e.tall ? width * n + tj : 16 * tj + n;
     return ti != tj || r <= n;
 }
 
-// The sum of `count` partial sums, `stride` apart, in their order, eight loads in flight.
-__device__ __forceinline__ double chunk_total(const double *from, int64_t stride, uint32_t count) {
-    double x = 0.0;
-    uint32_t k = 0;
-    for (; k + 8 <= count; k += 8) {
-        double y[8];
+// N sums of `count` partial sums each, `stride` apart, in their order: N times four loads
+// in flight, none of them behind a branch. Number j is at from + at[j].
+template <int N>
+__device__ __forceinline__ void chunk_totals(const double *from, const int (&at)[N], int64_t stride, uint32_t count,
+                                             double (&x)[N]) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = from[(k + j) * stride];
+    for (int j = 0; j < N; ++j) x[j] = 0.0;
+    for (uint32_t k = 0; k < count; k += 4) {
+        double y[N][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x += y[j];
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) y[j][i] = from[at[j] + min(k + i, count - 1) * stride];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] += k + i < count ? y[j][i] : 0.0;
     }
-    for (; k < count; ++k) x += from[k * stride];
-    return x;
 }
 
 __device__ __forceinline__ double block_total(double x, double *part) {
@@ -483,107 +514,224 @@ __device__ __forceinline__ void put_p(uint16_t *p, int blocks, int row, int col,
     }
 }
 
+// The norm, infinite from 2^60 on, where fp32 products of two elements may be; and what
+// makes NaN of such a matrix.
+__device__ __forceinline__ double norm_of(double trace) { return trace < 0x1p120 ? sqrt(trace) : (double)INFINITY; }
+__device__ __forceinline__ double inverse(double norm, double eps) {
+    return norm < INFINITY ? 1.0 / fmax(norm, eps) : (double)NAN;
+}
+
 // ---- the iteration, shorter sides up to 64: one workgroup a matrix ----
 
 constexpr int kStride = kSmall + 2;  // doubles: 16 rows of two columns lie in different banks
 typedef double SmallMat[kSmall][kStride];
-constexpr int kSmallThreads = 1024;
 
-// A wave takes tiles of the upper triangle (all matrices are symmetric) and writes
-// both halves.
-__global__ __launch_bounds__(kSmallThreads) void muon_small_kernel(List list, Scalars c, Space ws) {
+// 16 columns of a matrix, a wave's: what the fp64 instruction leaves as a result (register
+// r of tile i: row 16 i + 4 r + k, column n) it takes as its right operand as it is, so that
+// only left factors go through LDS, and a step needs two barriers.
+template <int kEdge> struct Strip {
+    f64x4 tile[kEdge];
+};
+template <int kEdge>
+__device__ __forceinline__ Strip<kEdge> times(const SmallMat &x, const Strip<kEdge> &y) {
+    const int n = threadIdx.x % 16, k4 = threadIdx.x % 64 / 16;
+    Strip<kEdge> out;
+#pragma unroll
+    for (int i = 0; i < kEdge; ++i) out.tile[i] = f64x4{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+    for (int k = 0; k < kEdge; ++k) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < kEdge; ++i)
+                out.tile[i] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[16 * i + n][16 * k + 4 * r + k4], y.tile[k][r], out.tile[i],
+                                                                   0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);  // no more operands in registers than these: otherwise 76 spill
+    }
+    return out;
+}
+
+// The same in fp32 parts. A column's operand is what the instruction leaves as two tiles'
+// results, registers 0 .. 3 of tiles 2 b and 2 b + 1: its eight rows are 32 b + 4 k + r and
+// 32 b + 16 + 4 k + r, and the left factor's columns lie in that order in LDS.
+constexpr int kHalfStride = kSmall + 8;  // bf16: rows of 16 bytes a lane lie in different banks
+typedef uint16_t SmallParts[3][kSmall][kHalfStride];
+template <int kEdge> struct Strip32 {
+    f32x4 tile[kEdge];
+};
+template <int kEdge>
+__device__ __forceinline__ Strip32<kEdge> times(const SmallParts &x, const Strip32<kEdge> &y) {
+    const int n = threadIdx.x % 16, k = threadIdx.x % 64 / 16;
+    Strip32<kEdge> out;
+#pragma unroll
+    for (int i = 0; i < kEdge; ++i) out.tile[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int b = 0; b < (kEdge + 1) / 2; ++b) {
+        float column[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) column[r] = 2 * b + r / 4 < kEdge ? y.tile[2 * b + r / 4][r % 4] : 0.0f;
+        const Operand<3> u = operand_of<3>(column);
+#pragma unroll
+        for (int i = 0; i < kEdge; ++i) {
+            Operand<3> a;
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+                a.part[part] = *reinterpret_cast<const u32x4 *>(&x[part][16 * i + n][32 * b + 8 * k]);
+            out.tile[i] = mfma_f32<3>(a, u, out.tile[i]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    return out;
+}
+// A wave's columns as the rows that they are too.
+template <int kEdge>
+__device__ __forceinline__ void put(SmallParts &x, const Strip32<kEdge> &y) {
+    const int n = threadIdx.x % 16, k = threadIdx.x % 64 / 16, wave = threadIdx.x / 64;
+#pragma unroll
+    for (int i = 0; i < 2 * ((kEdge + 1) / 2); ++i) {
+        float rest[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) rest[r] = i < kEdge ? y.tile[i][r] : 0.0f;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+            const u32x2 w = {pack_bf16x2(rest[0], rest[1]), pack_bf16x2(rest[2], rest[3])};
+            *reinterpret_cast<u32x2 *>(&x[part][16 * wave + n][i / 2 * 32 + 8 * k + i % 2 * 4]) = w;
+            rest[0] -= bf16_lo(w[0]), rest[1] -= bf16_hi(w[0]), rest[2] -= bf16_lo(w[1]), rest[3] -= bf16_hi(w[1]);
+        }
+    }
+}
+template <int kEdge>
+__device__ __forceinline__ void put(SmallMat &x, const Strip<kEdge> &y) {
+    const int n = threadIdx.x % 16, k = threadIdx.x % 64 / 16, wave = threadIdx.x / 64;
+#pragma unroll
+    for (int i = 0; i < kEdge; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[16 * i + 4 * r + k][16 * wave + n] = y.tile[i][r];
+}
+// c x^2 + b x + a I, from x^2.
+template <int kEdge, typename S>
+__device__ __forceinline__ void polynomial(const Scalars &c, S &square, const S &x) {
+    constexpr bool kWide = std::is_same_v<S, Strip<kEdge>>;
+    typedef std::conditional_t<kWide, double, float> T;
+    const int n = threadIdx.x % 16, k = threadIdx.x % 64 / 16, wave = threadIdx.x / 64;
+#pragma unroll
+    for (int i = 0; i < kEdge; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * i + (kWide ? 4 * r + k : 4 * k + r);
+            square.tile[i][r] = (T)c.c * square.tile[i][r] + (T)c.b * x.tile[i][r] + (row == 16 * wave + n ? (T)c.a : T(0));
+        }
+}
+// Steps `from` to `to` of the iteration on a and p (P so far), every wave of the matrix its
+// own columns; `left` holds a. `go_on`: whether a step follows the last of these.
+template <int kEdge, typename S, typename L>
+__device__ __forceinline__ void steps(const Scalars &c, L &left, L &other, S &a, S &p, int from, int to, bool go_on, bool mine) {
+    for (int it = from; it < to; ++it) {
+        const bool last = it + 1 == to && !go_on;
+        S q, t;
+        if (mine) {
+            q = times<kEdge>(left, a);
+            polynomial<kEdge>(c, q, a);
+            put<kEdge>(other, q);
+            if (!last) t = times<kEdge>(left, q);
+        }
+        __syncthreads();
+        if (mine) {
+            p = it == 0 ? q : times<kEdge>(other, p);
+            if (!last) {
+                a = times<kEdge>(other, t);
+                put<kEdge>(left, a);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// The places that P's operands of 32 have beyond the tiles are zero.
+template <int kEdge>
+__device__ __forceinline__ void iterate(const Item &e, const Scalars &c, double *smem, double inv, uint16_t *out) {
+    SmallMat *wide = reinterpret_cast<SmallMat *>(smem);
+    SmallParts *narrow = reinterpret_cast<SmallParts *>(smem);
+    const int lane = threadIdx.x % 64, n = lane % 16, k = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), col = 16 * wave + n;
+    const bool mine = wave < kEdge;
+    const int exact = c.exact;
+    Strip32<kEdge> a32, p32;
+    {
+        Strip<kEdge> a, p;
+        if (mine)
+#pragma unroll
+            for (int i = 0; i < kEdge; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) a.tile[i][r] = wide[0][16 * i + 4 * r + k][col] * (inv * inv);
+        __syncthreads();
+        if (mine) put<kEdge>(wide[0], a);
+        __syncthreads();
+        steps<kEdge>(c, wide[0], wide[1], a, p, 0, exact, exact < c.iterations, mine);
+        // to fp32's layout (rows 4 k + r of a tile), through LDS
+        if (mine) put<kEdge>(wide[0], p), put<kEdge>(wide[1], a);
+        __syncthreads();
+        if (mine)
+#pragma unroll
+            for (int i = 0; i < kEdge; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    p32.tile[i][r] = (float)(wide[0][16 * i + 4 * k + r][col] * (exact < c.iterations ? 1.0 : inv));
+                    a32.tile[i][r] = (float)wide[1][16 * i + 4 * k + r][col];
+                }
+        __syncthreads();
+    }
+    if (exact < c.iterations) {
+        if (mine) put<kEdge>(narrow[0], a32);
+        __syncthreads();
+        steps<kEdge>(c, narrow[0], narrow[1], a32, p32, exact, c.iterations, false, mine);
+        if (mine)
+#pragma unroll
+            for (int i = 0; i < kEdge; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) p32.tile[i][r] = (float)(p32.tile[i][r] * inv);
+    }
+    if (!mine) return;
+    const int blocks = p_blocks(e.side);
+#pragma unroll
+    for (int i = 0; i < 2 * ((kEdge + 1) / 2); ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * i + 4 * k + r;
+            const float x = i < kEdge && row < e.side && col < e.side ? p32.tile[i < kEdge ? i : 0][r] : 0.0f;
+            put_p(out, blocks, row, col, x);
+            if (kEdge % 2 != 0 && wave == 0) put_p(out, blocks, row, 16 * kEdge + n, 0.0f);
+        }
+}
+
+__global__ __launch_bounds__(kThreads, 2) void muon_small_kernel(List list, Scalars c, Space ws) {
     extern __shared__ double smem[];
-    SmallMat &A = *reinterpret_cast<SmallMat *>(smem), &Q = (&A)[1], &P = (&A)[2];
-    double *part = smem + 3 * kSmall * kStride;
+    SmallMat &A = *reinterpret_cast<SmallMat *>(smem);
+    double *part = smem + 2 * kSmall * kStride;
     const Item e = list.item[blockIdx.x];
     if (e.side > kSmall) return;
-    const int threads = blockDim.x, waves = threads / 64;
-    const int tiles = gram_tiles(e.side), width = gram_width(e.side), edge = (e.side + 15) / 16;
+    const int tiles = gram_tiles(e.side), width = gram_width(e.side);
     const double *from = ws.partial + e.partial;
-    for (int i = threadIdx.x; i < tiles * 256; i += threads) {
-        const double x = chunk_total(from + i, (int64_t)tiles * 256, e.gram_chunks);
-        int row, col;
-        if (place_of(e, width, true, i, row, col)) A[row][col] = x, A[col][row] = x;
+    for (int tile = 0; tile < tiles; tile += 5) {
+        int at[5];
+        double x[5];
+#pragma unroll
+        for (int j = 0; j < 5; ++j) at[j] = min(tile + j, tiles - 1) * 256 + threadIdx.x;
+        chunk_totals<5>(from, at, (int64_t)tiles * 256, e.gram_chunks, x);
+#pragma unroll
+        for (int j = 0; j < 5; ++j) {
+            int row, col;
+            if (tile + j < tiles && place_of(e, c.precise, width, true, at[j], row, col)) A[row][col] = x[j], A[col][row] = x[j];
+        }
     }
     __syncthreads();
     const double trace = block_total((int)threadIdx.x < e.side ? A[threadIdx.x][threadIdx.x] : 0.0, part);
-    const double norm = sqrt(trace), inv = 1.0 / fmax(norm, c.eps);
-    for (int i = threadIdx.x; i < 16 * edge * 16 * edge; i += threads) A[i / (16 * edge)][i % (16 * edge)] *= inv * inv;
-    const int lane = threadIdx.x % 64, n = lane % 16, k4 = lane / 16;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int count = edge * (edge + 1) / 2;
-    auto tile_of = [&](int t, int &ti, int &tj) { pair_of(t, ti, tj); };
-    auto product = [&](const SmallMat &x, const SmallMat &y, int t) {
-        int ti, tj;
-        tile_of(t, ti, tj);
-        f64x4 r = {0.0, 0.0, 0.0, 0.0};
-        for (int k = 0; k < 16 * edge; k += 16)
-#pragma unroll
-            for (int j = 0; j < 16; j += 4)
-                r = __builtin_amdgcn_mfma_f64_16x16x4f64(x[16 * ti + n][k + j + k4], y[16 * tj + n][k + j + k4], r, 0, 0, 0);
-        return r;
-    };
-    auto put = [&](SmallMat &x, const f64x4 &r, int t) {
-        int ti, tj;
-        tile_of(t, ti, tj);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int row = 16 * ti + 4 * j + k4, col = 16 * tj + n;
-            x[row][col] = r[j];
-            if (ti != tj) x[col][row] = r[j];
-        }
-    };
-    for (int it = 0; it < c.iterations; ++it) {
-        const bool last = it + 1 == c.iterations;
-        __syncthreads();
-        for (int t = wave; t < count; t += waves) {
-            f64x4 q = product(A, A, t);
-            int ti, tj;
-            tile_of(t, ti, tj);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = 16 * ti + 4 * j + k4, col = 16 * tj + n;
-                q[j] = c.c * q[j] + c.b * A[row][col] + (row == col ? c.a : 0.0);
-            }
-            if (it == 0) put(P, q, t);
-            put(Q, q, t);
-        }
-        __syncthreads();
-        // A Q and P Q: at most two tiles a wave, held until all of them have been read
-        f64x4 held[2];
-        const int from_p = last ? 0 : count, all = from_p + (it > 0 ? count : 0);
-        int mine = 0;
-        for (int t = wave; t < all; t += waves, ++mine) {
-            const f64x4 r = t < from_p ? product(A, Q, t) : product(P, Q, t - from_p);
-            if (mine == 0) held[0] = r;
-            else held[1] = r;
-        }
-        __syncthreads();
-        mine = 0;
-        for (int t = wave; t < all; t += waves, ++mine) {
-            const f64x4 r = mine == 0 ? held[0] : held[1];
-            if (t < from_p) put(A, r, t);
-            else put(P, r, t - from_p);
-        }
-        if (last) break;
-        __syncthreads();
-        mine = 0;
-        for (int t = wave; t < count; t += waves, ++mine) {
-            const f64x4 r = product(A, Q, t);
-            if (mine == 0) held[0] = r;
-            else held[1] = r;
-        }
-        __syncthreads();
-        mine = 0;
-        for (int t = wave; t < count; t += waves, ++mine) put(A, mine == 0 ? held[0] : held[1], t);
-    }
-    __syncthreads();
-    const int blocks = p_blocks(e.side), full = 32 * blocks;
+    const double norm = norm_of(trace), inv = inverse(norm, c.eps);
     uint16_t *out = ws.p + (int64_t)e.p * 512;
-    for (int i = threadIdx.x; i < full * full; i += threads) {
-        const int row = i / full, col = i % full;
-        put_p(out, blocks, row, col, row < e.side && col < e.side ? (float)(P[row][col] * inv) : 0.0f);
-    }
+    if (e.side <= 16) iterate<1>(e, c, smem, inv, out);
+    else if (e.side <= 32) iterate<2>(e, c, smem, inv, out);
+    else if (e.side <= 48) iterate<3>(e, c, smem, inv, out);
+    else iterate<4>(e, c, smem, inv, out);
     if (threadIdx.x == 0) ws.norm[blockIdx.x] = norm;
 }
 
@@ -607,37 +755,44 @@ __global__ __launch_bounds__(kThreads) void muon_start_kernel(List list, Scalars
     const int64_t stride = (int64_t)e.gram_pairs * 16 * 256;
     const int edge = 64 * blocks_of(e.side);
     // the trace, by every workgroup: thread s takes element (s, s), in the pair of its block with itself
-    double x = 0.0;
+    double diagonal[1] = {0.0};
     if ((int)threadIdx.x < e.side) {
         const int b = threadIdx.x / 64, d = threadIdx.x % 64, pair = b * (b + 1) / 2 + b;
         // its tile, row and column: (4 r + i) in a tall matrix, (16 i + r) in a wide one
         const int i = e.tall ? d % 4 : d / 16, r = e.tall ? d / 4 : d % 16;
-        x = chunk_total(from + ((pair * 16) + i * 4 + i) * 256 + (r % 4) * 64 + (r / 4) * 16 + r, stride, e.gram_chunks);
+        const int reg = c.precise ? r / 4 : r % 4, group = c.precise ? r % 4 : r / 4;
+        const int at[1] = {((pair * 16) + i * 4 + i) * 256 + reg * 64 + group * 16 + r};
+        chunk_totals<1>(from, at, stride, e.gram_chunks, diagonal);
     }
-    const double trace = block_total(x, part);
-    const double norm = sqrt(trace), inv = 1.0 / fmax(norm, c.eps);
+    const double trace = block_total(diagonal[0], part);
+    const double norm = norm_of(trace), inv = inverse(norm, c.eps);
     int bi, bj;
     pair_of(blockIdx.y, bi, bj);
     double *A = mat_of(e, ws, kA);
-    constexpr int kEach = 16 * 256 / kStartParts;
-    for (int i = blockIdx.z * kEach + threadIdx.x; i < ((int)blockIdx.z + 1) * kEach; i += kThreads) {
-        const double sum = chunk_total(from + (int64_t)blockIdx.y * 16 * 256 + i, stride, e.gram_chunks) * inv * inv;
+    constexpr int kEach = 16 / kStartParts;  // tiles
+    int at[kEach];
+    double sum[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) at[j] = ((blockIdx.y * 16) + blockIdx.z * kEach + j) * 256 + threadIdx.x;
+    chunk_totals<kEach>(from, at, stride, e.gram_chunks, sum);
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
         int row, col;
-        place_of(e, 4, false, i, row, col);
+        place_of(e, c.precise, 4, false, at[j] - (int)blockIdx.y * 16 * 256, row, col);
         row += 64 * bi, col += 64 * bj;
+        const double x = sum[j] * inv * inv;
         // a block with itself holds both of each pair: the upper one is taken
-        if (bi != bj || row <= col) A[(int64_t)row * edge + col] = sum, A[(int64_t)col * edge + row] = sum;
+        if (bi != bj || row <= col) A[(int64_t)row * edge + col] = x, A[(int64_t)col * edge + row] = x;
     }
     if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) ws.norm[blockIdx.x] = norm;
 }
 
-// out = x y, with q: c out + b x + a I (x = y), which also goes to `copy`; with fin: over
-// the norm, in parts, to P. blockIdx.z chooses one of two products. All matrices are
+// out = x y, with q: c out + b x + a I (x = y); with fin: over the norm, in parts, to P. blockIdx.z chooses one of two products. All matrices are
 // polynomials of one, so x y is symmetric: a workgroup takes 32 x 32 of the upper
 // triangle, writes both halves, and reads a column of y as its row.
 struct Product {
-    int32_t x, y, out, copy;  // copy: -1 none
-    bool q, fin;
+    int32_t x, y, out;
+    bool q, fin, narrow;  // narrow: out is fp32
 };
 struct Products {
     Product of[2];
@@ -685,8 +840,8 @@ __global__ __launch_bounds__(kThreads) void muon_product_kernel(List list, Scala
                 acc[j] = __builtin_amdgcn_mfma_f64_16x16x4f64(xs[16 * ti + n][k + 4 * j + k4], ys[16 * tj + n][k + 4 * j + k4],
                                                               acc[j], 0, 0, 0);
     }
-    const double inv = 1.0 / fmax(ws.norm[blockIdx.x], c.eps);
-    double *out = mat_of(e, ws, d.out), *copy = d.copy >= 0 ? mat_of(e, ws, d.copy) : nullptr;
+    const double inv = inverse(ws.norm[blockIdx.x], c.eps);
+    double *out = mat_of(e, ws, d.out);
     const double *whole = mat_of(e, ws, d.x);
     const int blocks = p_blocks(e.side);
     uint16_t *p = ws.p + (int64_t)e.p * 512;
@@ -701,13 +856,85 @@ __global__ __launch_bounds__(kThreads) void muon_product_kernel(List list, Scala
             const float f = row < e.side && col < e.side ? (float)(v * inv) : 0.0f;
             put_p(p, blocks, row, col, f);
             if (bi != bj) put_p(p, blocks, col, row, f);
+        } else if (d.narrow) {
+            float *f = reinterpret_cast<float *>(out);
+            f[at] = (float)v;
+            if (bi != bj) f[mirror] = (float)v;
         } else {
             out[at] = v;
             if (bi != bj) out[mirror] = v;
-            if (copy) copy[at] = v;
-            if (copy && bi != bj) copy[mirror] = v;
         }
     }
+}
+
+// The same on fp32 matrices in parts: a wave takes 32 x 32 of the upper triangle and reads
+// its operands from the caches, a row's eight columns a lane.
+__global__ __launch_bounds__(64) void muon_product32_kernel(List list, Scalars c, Space ws, Products products) {
+    const Item e = list.item[blockIdx.x];
+    const int edge = 64 * blocks_of(e.side), nb = edge / kEdge;
+    if (e.side <= kSmall || (int)blockIdx.y >= nb * (nb + 1) / 2) return;
+    const Product d = products.of[blockIdx.z];
+    int bi, bj;
+    pair_of(blockIdx.y, bi, bj);
+    auto mat = [&](int which) { return reinterpret_cast<float *>(mat_of(e, ws, which)); };
+    const int n = threadIdx.x % 16, k = threadIdx.x / 16;
+    const float *x = mat(d.x) + (kEdge * bi + n) * edge + 8 * k, *y = mat(d.y) + (kEdge * bj + n) * edge + 8 * k;
+    f32x4 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // two steps of 32 columns at a time: 16 loads in flight
+    for (int k0 = 0; k0 < edge; k0 += 64) {
+        f32x4 raw[2][4][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float *from = (i < 2 ? x + 16 * i * edge : y + 16 * (i - 2) * edge) + k0 + 32 * s;
+                raw[s][i][0] = *reinterpret_cast<const f32x4 *>(from);
+                raw[s][i][1] = *reinterpret_cast<const f32x4 *>(from + 4);
+            }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            Operand<3> op[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = raw[s][i][j / 4][j % 4];
+                op[i] = operand_of<3>(v);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_f32<3>(op[i], op[2 + j], acc[i][j]);
+        }
+    }
+    const double inv = inverse(ws.norm[blockIdx.x], c.eps);
+    const int blocks = p_blocks(e.side);
+    uint16_t *p = ws.p + (int64_t)e.p * 512;
+    const float *whole = mat(d.x);
+    float *out = mat(d.out);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = kEdge * bi + 16 * i + 4 * k + r, col = kEdge * bj + 16 * j + n;
+                float v = acc[i][j][r];
+                if (d.q) v = (float)c.c * v + (float)c.b * whole[row * edge + col] + (row == col ? (float)c.a : 0.0f);
+                if (d.fin) {
+                    if (row >= 32 * blocks || col >= 32 * blocks) continue;
+                    const float f = row < e.side && col < e.side ? (float)(v * inv) : 0.0f;
+                    put_p(p, blocks, row, col, f);
+                    if (bi != bj) put_p(p, blocks, col, row, f);
+                } else {
+                    out[row * edge + col] = v;
+                    if (bi != bj) out[col * edge + row] = v;
+                }
+            }
 }
 
 // ---- O = U P and the step ----
@@ -786,7 +1013,7 @@ __device__ __forceinline__ void apply_tall(const Item &e, const Scalars &c, cons
         Raw<G, M, 8> raw[kBlocks];
         RawN<W, 8> before[kBlocks];
 #pragma unroll
-        for (int s = 0; s < kBlocks; ++s) raw[s] = load_update<G, M, 8, true>(e, span(s));
+        for (int s = 0; s < kBlocks; ++s) raw[s] = load_update<G, M, 8, false>(e, span(s));
 #pragma unroll
         for (int s = 0; s < kBlocks; ++s) before[s] = load_weight<W, 8>(e, c, span(s));
         __builtin_amdgcn_sched_barrier(0);
@@ -827,7 +1054,7 @@ __device__ __forceinline__ void apply_wide(const Item &e, const Scalars &c, cons
 #pragma unroll
         for (int s = 0; s < kBlocks; ++s)
 #pragma unroll
-            for (int r = 0; r < 8; ++r) raw[s][r] = load_update<G, M, V, true>(e, span(s, r));
+            for (int r = 0; r < 8; ++r) raw[s][r] = load_update<G, M, V, false>(e, span(s, r));
 #pragma unroll
         for (int s = 0; s < kBlocks; ++s)
 #pragma unroll
@@ -997,6 +1224,16 @@ __global__ __launch_bounds__(kLargeThreads) void muon_apply_large_kernel(List li
 
 // ---- host ----
 
+// The steps that run in fp64. An error of A_k grows 11.9 times a step in what is far below
+// the largest: fp32's 2^-24 in A_1 ends as up to 1e-4 of O, a twentieth of a bf16 output's
+// half step; in A_2 as up to 8e-6, 8e-8 of a weight that steps by a hundredth of itself.
+// What is orthogonalised for itself in fp32 stays in fp64: 64 matrices of 4096 x 64 take
+// @@ us instead of @@ with two steps.
+int exact_steps(const MuonCall &call, bool masters) {
+    const int most = !call.step && call.w == NF4_F32 ? call.iterations : call.w == NF4_F32 || masters ? 2 : 1;
+    return most < call.iterations ? most : call.iterations;
+}
+
 size_t round_up(size_t x, size_t to) { return (x + to - 1) / to * to; }
 
 // How a list is cut, and what lies where in the workspace. The longer sides are cut into
@@ -1008,7 +1245,7 @@ struct Plan {
     int32_t largest, smallest;   // of their shorter sides
     bool fits;
 };
-constexpr int64_t kShares = 2048;
+constexpr int64_t kShares = 2048, kApplyShares = 2048;
 
 template <typename F>
 Plan make_plan(const MuonMatrix *list, int32_t count, F &&each) {
@@ -1028,7 +1265,7 @@ Plan make_plan(const MuonMatrix *list, int32_t count, F &&each) {
     }
     // 64 rows a wave at least: the fp32 sums' length
     const int64_t gram_chunk = round_up(gram_rows / kShares < 128 ? 128 : gram_rows / kShares, 64);
-    const int64_t apply_chunk = round_up(apply_rows / kShares < 64 ? 64 : apply_rows / kShares, 64);
+    const int64_t apply_chunk = round_up(apply_rows / kApplyShares < 64 ? 64 : apply_rows / kApplyShares, 64);
     p.items = 0;
     p.gram_first = round_up(p.items + (size_t)p.count * sizeof(Item), 16);
     p.apply_first = round_up(p.gram_first + (size_t)p.count * 4, 16);
@@ -1083,11 +1320,9 @@ hipError_t run(const Plan &p, const List &list, const Scalars &c, const Space &w
     if (small) {
         muon_gram_kernel<G, M, false><<<dim3(p.gram_wgs), dim3(kThreads), 0, s>>>(list, c, ws);
         if (!note()) return r;
-        constexpr size_t kSmallLds = (3 * kSmall * kStride + 16) * sizeof(double);
+        constexpr size_t kSmallLds = (2 * kSmall * kStride + kWaves) * sizeof(double);
         if ((r = allow_lds(reinterpret_cast<const void *>(&muon_small_kernel), kSmallLds)) != hipSuccess) return r;
-        // a tile a wave, up to ten; the few of short sides leave waves to add up the partial sums
-        const int threads = p.largest <= 32 ? 256 : p.largest <= 48 ? 512 : kSmallThreads;
-        muon_small_kernel<<<dim3(p.count), dim3(threads), kSmallLds, s>>>(list, c, ws);
+        muon_small_kernel<<<dim3(p.count), dim3(kThreads), kSmallLds, s>>>(list, c, ws);
         if (!note()) return r;
     }
     if (large) {
@@ -1096,22 +1331,27 @@ hipError_t run(const Plan &p, const List &list, const Scalars &c, const Space &w
         const int nb = blocks_of(p.largest), pairs = 2 * nb * (2 * nb + 1) / 2;
         muon_start_kernel<<<dim3(p.count, nb * (nb + 1) / 2, kStartParts), dim3(kThreads), 0, s>>>(list, c, ws);
         if (!note()) return r;
-        auto launch = [&](const Products &x, int z) {
+        auto launch = [&](bool wide, const Products &x, int z) {
             if (r != hipSuccess) return;
-            muon_product_kernel<<<dim3(p.count, pairs, z), dim3(kThreads), 0, s>>>(list, c, ws, x);
+            if (wide) muon_product_kernel<<<dim3(p.count, pairs, z), dim3(kThreads), 0, s>>>(list, c, ws, x);
+            else muon_product32_kernel<<<dim3(p.count, pairs, z), dim3(64), 0, s>>>(list, c, ws, x);
             note();
         };
         int now = kP0;
         for (int it = 0; it < c.iterations; ++it) {
-            const bool last = it + 1 == c.iterations;
+            const bool last = it + 1 == c.iterations, wide = it < c.exact;
+            const bool narrow = wide && it + 1 == c.exact && !last;  // the next step is in fp32
             const int next = now == kP0 ? kP1 : kP0;
-            launch({{{kA, kA, kQ, it == 0 ? now : -1, true, last && it == 0}, {}}}, 1);
-            const Product step{kA, kQ, kT, -1, false, false}, grow{now, kQ, next, -1, false, last};
-            if (it > 0 && last) launch({{grow, {}}}, 1);
-            else if (it > 0) launch({{step, grow}}, 2);
-            else if (!last) launch({{step, {}}}, 1);
+            // Q; with the first step, P too
+            Product q{kA, kA, kQ, true, last && it == 0, false};
+            launch(wide, {{q, {}}}, 1);
+            const Product step{kA, kQ, kT, false, false, false}, grow{now, kQ, next, false, last, narrow};
+            const Product first{kA, kA, now, true, false, narrow};
+            if (it == 0 && !last) launch(wide, {{step, first}}, 2);
+            else if (it > 0 && last) launch(wide, {{grow, {}}}, 1);
+            else if (it > 0) launch(wide, {{step, grow}}, 2);
             if (it > 0) now = next;
-            if (!last) launch({{{kT, kQ, kA, -1, false, false}, {}}}, 1);
+            if (!last) launch(wide, {{{kT, kQ, kA, false, false, narrow}, {}}}, 1);
         }
         if (r != hipSuccess) return r;
     }
@@ -1178,7 +1418,8 @@ hipError_t launch_muon(const MuonMatrix *list, int32_t count, const MuonCall &ca
     Scalars c{};
     c.mu = (float)call.momentum, c.one_mu = (float)(1.0 - call.momentum), c.nesterov = call.nesterov;
     c.eps = call.eps, c.a = call.a, c.b = call.b, c.c = call.c, c.iterations = call.iterations;
-    c.step = call.step, c.w_bf16 = call.w == NF4_BF16;
+    c.exact = exact_steps(call, sizes.masters > 0);
+    c.step = call.step, c.w_bf16 = call.w == NF4_BF16, c.precise = !call.step && call.w == NF4_F32;
     const List l{items, gram_first, apply_first, sizes.count};
     const Space ws{reinterpret_cast<double *>(base + sizes.partial), reinterpret_cast<double *>(base + sizes.mats),
                    reinterpret_cast<double *>(base + sizes.norm), reinterpret_cast<uint16_t *>(base + sizes.p)};

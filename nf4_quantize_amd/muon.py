@@ -74,8 +74,8 @@ class NF4Muon(ListOptimizer):
     ``m`` is the list of the matrices' momenta in the order of the parameters. A step
     writes at these tensors' addresses, so ``bind_state`` replaces them, and a step
     refuses lists whose tensors are others (a parameter's ``data`` may change, its
-    shape may not). A matrix whose update's norm is not finite keeps its weight and
-    momentum."""
+    shape may not). A matrix whose update's norm is not finite, or 2^60 and more, keeps
+    its weight and momentum."""
 
     m = _taken("m")
 
@@ -162,7 +162,7 @@ def orthogonalize(updates, coefficients=COEFFICIENTS, iterations=5, eps=1e-7, ou
     X <- a X + b (X X^T) X + c (X X^T)^2 X (nf4_orthogonalize): its singular values
     come near 1. All are bfloat16 or all float32, with at most 256 rows or columns.
     Returns a list of new tensors, or ``outs`` (which may be the updates themselves).
-    A matrix whose norm is not finite becomes NaN."""
+    A matrix whose norm is not finite, or 2^60 and more, becomes NaN."""
     import torch
 
     updates = list(updates)
