@@ -12,6 +12,7 @@
 // instruction; the two passes over the long matrices split fp32 into bf16 parts.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "training_internal.h"
@@ -38,9 +39,17 @@ struct Item {
     uint32_t apply_first, apply_chunk;
     uint32_t p, pad;         // first element of P's parts, in units of 512
 };
-constexpr int kBatch = 34;
+// What of it the host sends, 80 a launch; the rest follows from the sizes.
+struct Sent {
+    const void *g;
+    void *m, *w;
+    float *master;
+    int32_t rows, cols;
+    float keep, step;
+};
+constexpr int kBatch = 80;
 struct Batch {
-    Item item[kBatch];
+    Sent item[kBatch];
 };
 static_assert(sizeof(Batch) + 64 <= 4096, "kernel arguments");
 
@@ -62,15 +71,84 @@ struct Space {
     uint16_t *p;              // bf16 parts, see put_p
 };
 
-__global__ __launch_bounds__(kThreads) void muon_table_kernel(Batch b, int32_t count, Item *items, uint32_t *gram_first,
-                                                              uint32_t *apply_first) {
-    constexpr int kWords = sizeof(Item) / 4;
-    const uint32_t *from = reinterpret_cast<const uint32_t *>(b.item);
-    uint32_t *to = reinterpret_cast<uint32_t *>(items);
-    for (int i = threadIdx.x; i < count * kWords; i += kThreads) to[i] = from[i];
-    if ((int)threadIdx.x < count) {
-        gram_first[threadIdx.x] = b.item[threadIdx.x].gram_first;
-        apply_first[threadIdx.x] = b.item[threadIdx.x].apply_first;
+// Where a matrix's shares begin: sums over the matrices before it.
+struct Offsets {
+    uint32_t gram, apply;
+    int64_t partial, mats;
+    uint32_t p;
+};
+__host__ __device__ inline int blocks_of(int side) { return (side + 63) / 64; }
+__host__ __device__ inline int p_blocks(int side) { return (side + 31) / 32; }  // operands of 32 columns of P
+__host__ __device__ inline int64_t p_elements(int side) { return 3 * 2 * (int64_t)p_blocks(side) * p_blocks(side) * 512; }
+// Tiles of 256 sums that a workgroup of the first pass leaves.
+__host__ __device__ inline int gram_tiles(int side) {
+    return side <= 16 ? 1 : side <= 32 ? 3 : side <= kSmall ? 10 : 16;
+}
+constexpr int kMats = 5;
+// The sizes of a matrix, and its shares into `o`.
+__host__ __device__ inline Item item_of(int32_t rows, int32_t cols, uint32_t gram_chunk, uint32_t apply_chunk, Offsets &o) {
+    Item e{};
+    e.tall = rows >= cols;
+    e.side = e.tall ? cols : rows, e.length = e.tall ? rows : cols;
+    e.total = rows * cols;
+    const int nb = blocks_of(e.side);
+    const int64_t edge = 64 * nb;
+    e.gram_pairs = nb * (nb + 1) / 2;
+    e.gram_chunk = gram_chunk, e.gram_chunks = (e.length + gram_chunk - 1) / gram_chunk;
+    e.apply_chunk = apply_chunk;
+    o.gram = e.gram_chunks * e.gram_pairs;
+    o.apply = (e.length + apply_chunk - 1) / apply_chunk;
+    o.partial = (int64_t)o.gram * gram_tiles(e.side) * 256;
+    o.mats = e.side > kSmall ? kMats * edge * edge : 0;
+    o.p = (uint32_t)(p_elements(e.side) / 512);
+    return e;
+}
+
+// The list into the workspace, from entry `done` on; with the last batch, where each
+// matrix's shares begin.
+__global__ __launch_bounds__(kThreads) void muon_table_kernel(Batch b, int32_t used, int32_t done, int32_t count,
+                                                              uint32_t gram_chunk, uint32_t apply_chunk, Item *items,
+                                                              uint32_t *gram_first, uint32_t *apply_first) {
+    for (int i = threadIdx.x; i < used; i += kThreads) {
+        const Sent &s = b.item[i];
+        Offsets o;
+        Item e = item_of(s.rows, s.cols, gram_chunk, apply_chunk, o);
+        e.g = s.g, e.m = s.m, e.w = s.w, e.master = s.master, e.keep = s.keep, e.step = s.step;
+        items[done + i] = e;
+    }
+    if (done + used < count) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x >= 64) return;
+    Offsets before{};
+    auto add = [](Offsets &x, const Offsets &y) {
+        x.gram += y.gram, x.apply += y.apply, x.partial += y.partial, x.mats += y.mats, x.p += y.p;
+    };
+    auto from = [](const Offsets &x, int lane) {
+        return Offsets{__shfl(x.gram, lane), __shfl(x.apply, lane), __shfl(x.partial, lane), __shfl(x.mats, lane), __shfl(x.p, lane)};
+    };
+    for (int base = 0; base < count; base += 64) {
+        const int i = base + threadIdx.x;
+        Offsets own{};
+        if (i >= done && i < count) item_of(b.item[i - done].rows, b.item[i - done].cols, gram_chunk, apply_chunk, own);
+        else if (i < count) item_of(items[i].tall ? items[i].length : items[i].side, items[i].tall ? items[i].side : items[i].length,
+                                    gram_chunk, apply_chunk, own);
+        Offsets at = own;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+            const Offsets other = from(at, max((int)threadIdx.x - o, 0));
+            if ((int)threadIdx.x >= o) add(at, other);
+        }
+        const Offsets all = from(at, 63);
+        if (i < count) {
+            Item &e = items[i];
+            e.gram_first = gram_first[i] = before.gram + at.gram - own.gram;
+            e.apply_first = apply_first[i] = before.apply + at.apply - own.apply;
+            e.partial = before.partial + at.partial - own.partial;
+            e.mats = before.mats + at.mats - own.mats;
+            e.p = before.p + at.p - own.p;
+        }
+        add(before, all);
     }
 }
 
@@ -413,11 +491,7 @@ __device__ __forceinline__ void gram_part(const Item &e, const Scalars &c, int b
     for (int i = threadIdx.x; i < kTiles * 256; i += kThreads) out[i] = part[i / 256][i % 256];
 }
 
-// Tiles of 256 sums that a workgroup leaves.
-__host__ __device__ inline int gram_width(int side) { return side <= 16 ? 1 : side <= 32 ? 2 : 4; }
-__host__ __device__ inline int gram_tiles(int side) {
-    return side <= 16 ? 1 : side <= 32 ? 3 : side <= kSmall ? 10 : 16;
-}
+__device__ __forceinline__ int gram_width(int side) { return side <= 16 ? 1 : side <= 32 ? 2 : 4; }
 __device__ __forceinline__ void pair_of(int pair, int &bi, int &bj) {
     bj = 0;
     while ((bj + 1) * (bj + 2) / 2 <= pair) ++bj;
@@ -427,7 +501,9 @@ __device__ __forceinline__ void pair_of(int pair, int &bi, int &bj) {
 template <typename G, typename M, bool kLarge>
 __global__ __launch_bounds__(kThreads, 2) void muon_gram_kernel(List list, Scalars c, Space ws) {
     __shared__ double part[kLarge ? 16 : 10][256];
-    const uint32_t wg = blockIdx.x;
+    // the pairs of blocks of the same rows run on one XCD and share its L2
+    const uint32_t xcd = blockIdx.x % 8, each = gridDim.x / 8;
+    const uint32_t wg = kLarge ? xcd * each + min(xcd, gridDim.x % 8) + blockIdx.x / 8 : blockIdx.x;
     const Item e = list.item[find(list.gram_first, list.count, wg)];
     if ((e.side > kSmall) != kLarge) return;
     const uint32_t own = wg - e.gram_first, chunk = own / e.gram_pairs, pair = own % e.gram_pairs;
@@ -464,21 +540,21 @@ __device__ __forceinline__ bool place_of(const Item &e, bool precise, int width,
     return ti != tj || r <= n;
 }
 
-// N sums of `count` partial sums each, `stride` apart, in their order: N times four loads
+// N sums of `count` partial sums each, `stride` apart, in their order: N times kAhead loads
 // in flight, none of them behind a branch. Number j is at from + at[j].
-template <int N>
+template <int N, int kAhead>
 __device__ __forceinline__ void chunk_totals(const double *from, const int (&at)[N], int64_t stride, uint32_t count,
                                              double (&x)[N]) {
 #pragma unroll
     for (int j = 0; j < N; ++j) x[j] = 0.0;
-    for (uint32_t k = 0; k < count; k += 4) {
-        double y[N][4];
+    for (uint32_t k = 0; k < count; k += kAhead) {
+        double y[N][kAhead];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kAhead; ++i)
 #pragma unroll
             for (int j = 0; j < N; ++j) y[j][i] = from[at[j] + min(k + i, count - 1) * stride];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kAhead; ++i)
 #pragma unroll
             for (int j = 0; j < N; ++j) x[j] += k + i < count ? y[j][i] : 0.0;
     }
@@ -501,8 +577,6 @@ __device__ __forceinline__ double block_total(double x, double *part) {
 // operand s, and rows so permuted that lane (k, n) of the product finds those same
 // columns of O in two operands' results: row 4 k + r of result i is row
 // 32 (i / 2) + 8 k + 4 (i % 2) + r of P.
-__host__ __device__ inline int p_blocks(int side) { return (side + 31) / 32; }  // operands of 32 columns
-__host__ __device__ inline int64_t p_elements(int side) { return 3 * 2 * (int64_t)p_blocks(side) * p_blocks(side) * 512; }
 __device__ __forceinline__ void put_p(uint16_t *p, int blocks, int row, int col, float x) {
     const int i = 2 * (row / 32) + row % 8 / 4, n = 4 * (row % 32 / 8) + row % 4;
     const int at = ((i * blocks + col / 32) * 64 + col % 32 / 8 * 16 + n) * 8 + col % 8;
@@ -712,18 +786,26 @@ __global__ __launch_bounds__(kThreads, 2) void muon_small_kernel(List list, Scal
     if (e.side > kSmall) return;
     const int tiles = gram_tiles(e.side), width = gram_width(e.side);
     const double *from = ws.partial + e.partial;
-    for (int tile = 0; tile < tiles; tile += 5) {
-        int at[5];
-        double x[5];
+    auto gather = [&](auto each, auto ahead) {
+        constexpr int kEach = decltype(each)::value;
+        for (int tile = 0; tile < tiles; tile += kEach) {
+            int at[kEach];
+            double x[kEach];
 #pragma unroll
-        for (int j = 0; j < 5; ++j) at[j] = min(tile + j, tiles - 1) * 256 + threadIdx.x;
-        chunk_totals<5>(from, at, (int64_t)tiles * 256, e.gram_chunks, x);
+            for (int j = 0; j < kEach; ++j) at[j] = (tile + j) * 256 + threadIdx.x;
+            chunk_totals<kEach, decltype(ahead)::value>(from, at, (int64_t)tiles * 256, e.gram_chunks, x);
 #pragma unroll
-        for (int j = 0; j < 5; ++j) {
-            int row, col;
-            if (tile + j < tiles && place_of(e, c.precise, width, true, at[j], row, col)) A[row][col] = x[j], A[col][row] = x[j];
+            for (int j = 0; j < kEach; ++j) {
+                int row, col;
+                if (place_of(e, c.precise, width, true, at[j], row, col)) A[row][col] = x[j], A[col][row] = x[j];
+            }
         }
-    }
+    };
+    // 1, 3 or 10 tiles
+    typedef std::integral_constant<int, 16> Sixteen;
+    if (tiles == 1) gather(std::integral_constant<int, 1>{}, Sixteen{});
+    else if (tiles == 3) gather(std::integral_constant<int, 3>{}, Sixteen{});
+    else gather(std::integral_constant<int, 5>{}, std::integral_constant<int, 8>{});
     __syncthreads();
     const double trace = block_total((int)threadIdx.x < e.side ? A[threadIdx.x][threadIdx.x] : 0.0, part);
     const double norm = norm_of(trace), inv = inverse(norm, c.eps);
@@ -737,35 +819,40 @@ __global__ __launch_bounds__(kThreads, 2) void muon_small_kernel(List list, Scal
 
 // ---- the iteration, shorter sides above 64: a launch a product ----
 
-__host__ __device__ inline int blocks_of(int side) { return (side + 63) / 64; }
-enum Mat { kA, kQ, kT, kP0, kP1, kMats };
+enum Mat { kA, kQ, kT, kP0, kP1 };
+static_assert(kP1 + 1 == kMats, "matrices of the iteration");
 
 __device__ __forceinline__ double *mat_of(const Item &e, const Space &ws, int which) {
     const int64_t edge = 64 * blocks_of(e.side);
     return ws.mats + e.mats + which * edge * edge;
 }
 
-// 64 x 64 sums of a pair of blocks are added up by kStartParts workgroups.
+// S, 64 x 64 of it by kStartParts workgroups, and its trace by one workgroup more. The
+// products of the first step bring S over the norm's square.
 constexpr int kStartParts = 4;
 __global__ __launch_bounds__(kThreads) void muon_start_kernel(List list, Scalars c, Space ws) {
     __shared__ double part[kWaves];
     const Item e = list.item[blockIdx.x];
-    if (e.side <= kSmall || blockIdx.y >= e.gram_pairs) return;
+    if (e.side <= kSmall || (blockIdx.y >= e.gram_pairs && blockIdx.y != gridDim.y - 1)) return;
     const double *from = ws.partial + e.partial;
     const int64_t stride = (int64_t)e.gram_pairs * 16 * 256;
     const int edge = 64 * blocks_of(e.side);
-    // the trace, by every workgroup: thread s takes element (s, s), in the pair of its block with itself
-    double diagonal[1] = {0.0};
-    if ((int)threadIdx.x < e.side) {
-        const int b = threadIdx.x / 64, d = threadIdx.x % 64, pair = b * (b + 1) / 2 + b;
-        // its tile, row and column: (4 r + i) in a tall matrix, (16 i + r) in a wide one
-        const int i = e.tall ? d % 4 : d / 16, r = e.tall ? d / 4 : d % 16;
-        const int reg = c.precise ? r / 4 : r % 4, group = c.precise ? r % 4 : r / 4;
-        const int at[1] = {((pair * 16) + i * 4 + i) * 256 + reg * 64 + group * 16 + r};
-        chunk_totals<1>(from, at, stride, e.gram_chunks, diagonal);
+    if (blockIdx.y == gridDim.y - 1) {
+        if (blockIdx.z != 0) return;
+        // thread s takes element (s, s), in the pair of its block with itself
+        double diagonal[1] = {0.0};
+        if ((int)threadIdx.x < e.side) {
+            const int b = threadIdx.x / 64, d = threadIdx.x % 64, pair = b * (b + 1) / 2 + b;
+            // its tile, row and column: (4 r + i) in a tall matrix, (16 i + r) in a wide one
+            const int i = e.tall ? d % 4 : d / 16, r = e.tall ? d / 4 : d % 16;
+            const int reg = c.precise ? r / 4 : r % 4, group = c.precise ? r % 4 : r / 4;
+            const int at[1] = {((pair * 16) + i * 4 + i) * 256 + reg * 64 + group * 16 + r};
+            chunk_totals<1, 16>(from, at, stride, e.gram_chunks, diagonal);
+        }
+        const double trace = block_total(diagonal[0], part);
+        if (threadIdx.x == 0) ws.norm[blockIdx.x] = norm_of(trace);
+        return;
     }
-    const double trace = block_total(diagonal[0], part);
-    const double norm = norm_of(trace), inv = inverse(norm, c.eps);
     int bi, bj;
     pair_of(blockIdx.y, bi, bj);
     double *A = mat_of(e, ws, kA);
@@ -774,17 +861,15 @@ __global__ __launch_bounds__(kThreads) void muon_start_kernel(List list, Scalars
     double sum[kEach];
 #pragma unroll
     for (int j = 0; j < kEach; ++j) at[j] = ((blockIdx.y * 16) + blockIdx.z * kEach + j) * 256 + threadIdx.x;
-    chunk_totals<kEach>(from, at, stride, e.gram_chunks, sum);
+    chunk_totals<kEach, 8>(from, at, stride, e.gram_chunks, sum);
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         int row, col;
         place_of(e, c.precise, 4, false, at[j] - (int)blockIdx.y * 16 * 256, row, col);
         row += 64 * bi, col += 64 * bj;
-        const double x = sum[j] * inv * inv;
         // a block with itself holds both of each pair: the upper one is taken
-        if (bi != bj || row <= col) A[(int64_t)row * edge + col] = x, A[(int64_t)col * edge + row] = x;
+        if (bi != bj || row <= col) A[(int64_t)row * edge + col] = sum[j], A[(int64_t)col * edge + row] = sum[j];
     }
-    if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) ws.norm[blockIdx.x] = norm;
 }
 
 // out = x y, with q: c out + b x + a I (x = y); with fin: over the norm, in parts, to P. blockIdx.z chooses one of two products. All matrices are
@@ -793,11 +878,12 @@ __global__ __launch_bounds__(kThreads) void muon_start_kernel(List list, Scalars
 struct Product {
     int32_t x, y, out;
     bool q, fin, narrow;  // narrow: out is fp32
+    bool first;           // x is S itself: over the norm's square
 };
 struct Products {
     Product of[2];
 };
-constexpr int kEdge = 32, kSlab = 64;
+constexpr int kEdge = 32, kSlab = 64, kSlabs = kMuonSide / kSlab;
 
 __global__ __launch_bounds__(kThreads) void muon_product_kernel(List list, Scalars c, Space ws, Products products) {
     __shared__ double xs[kEdge][kSlab + 2], ys[kEdge][kSlab + 2];
@@ -810,29 +896,34 @@ __global__ __launch_bounds__(kThreads) void muon_product_kernel(List list, Scala
     const double *x = mat_of(e, ws, d.x) + (int64_t)bi * kEdge * edge, *y = mat_of(e, ws, d.y) + (int64_t)bj * kEdge * edge;
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, n = lane % 16, k4 = lane / 16;
     const int ti = wave / 2, tj = wave % 2;
+    // everything in flight at once: the data come from another XCD's caches
+    const double norm = ws.norm[blockIdx.x];
     constexpr int kEach = kEdge * kSlab / 2 / kThreads;  // pairs of doubles of a thread and slab
     typedef double f64x2 __attribute__((ext_vector_type(2)));
-    f64x2 rx[kEach], ry[kEach];
-    auto load = [&](int k0) {
+    f64x2 rx[kSlabs][kEach], ry[kSlabs][kEach];
+    const int row0 = threadIdx.x / (kSlab / 2), col0 = threadIdx.x % (kSlab / 2) * 2;
+    constexpr int kRows = kThreads / (kSlab / 2);
 #pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-            const int i = j * kThreads + threadIdx.x, row = i / (kSlab / 2), col = i % (kSlab / 2) * 2;
-            rx[j] = *reinterpret_cast<const f64x2 *>(x + (int64_t)row * edge + k0 + col);
-            ry[j] = *reinterpret_cast<const f64x2 *>(y + (int64_t)row * edge + k0 + col);
-        }
-    };
-    load(0);
+    for (int s = 0; s < kSlabs; ++s)
+        if (s * kSlab < edge)
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                rx[s][j] = *reinterpret_cast<const f64x2 *>(x + (row0 + kRows * j) * edge + s * kSlab + col0);
+                ry[s][j] = *reinterpret_cast<const f64x2 *>(y + (row0 + kRows * j) * edge + s * kSlab + col0);
+            }
+    __builtin_amdgcn_sched_barrier(0);
     f64x4 acc[2] = {{0.0, 0.0, 0.0, 0.0}, {0.0, 0.0, 0.0, 0.0}};
-    for (int k0 = 0; k0 < edge; k0 += kSlab) {
+#pragma unroll
+    for (int s = 0; s < kSlabs; ++s) {
+        if (s * kSlab >= edge) break;
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
-            const int i = j * kThreads + threadIdx.x, row = i / (kSlab / 2), col = i % (kSlab / 2) * 2;
-            xs[row][col] = rx[j][0], xs[row][col + 1] = rx[j][1];
-            ys[row][col] = ry[j][0], ys[row][col + 1] = ry[j][1];
+            const int row = row0 + kRows * j;
+            xs[row][col0] = rx[s][j][0], xs[row][col0 + 1] = rx[s][j][1];
+            ys[row][col0] = ry[s][j][0], ys[row][col0 + 1] = ry[s][j][1];
         }
         __syncthreads();
-        if (k0 + kSlab < edge) load(k0 + kSlab);
 #pragma unroll
         for (int k = 0; k < kSlab; k += 8)
 #pragma unroll
@@ -840,7 +931,7 @@ __global__ __launch_bounds__(kThreads) void muon_product_kernel(List list, Scala
                 acc[j] = __builtin_amdgcn_mfma_f64_16x16x4f64(xs[16 * ti + n][k + 4 * j + k4], ys[16 * tj + n][k + 4 * j + k4],
                                                               acc[j], 0, 0, 0);
     }
-    const double inv = inverse(ws.norm[blockIdx.x], c.eps);
+    const double inv = inverse(norm, c.eps), s = d.first ? inv * inv : 1.0;
     double *out = mat_of(e, ws, d.out);
     const double *whole = mat_of(e, ws, d.x);
     const int blocks = p_blocks(e.side);
@@ -850,7 +941,8 @@ __global__ __launch_bounds__(kThreads) void muon_product_kernel(List list, Scala
         const int row = kEdge * bi + 16 * ti + 4 * r + k4, col = kEdge * bj + 16 * tj + n;
         const int64_t at = (int64_t)row * edge + col, mirror = (int64_t)col * edge + row;
         double v = acc[0][r] + acc[1][r];
-        if (d.q) v = c.c * v + c.b * whole[at] + (row == col ? c.a : 0.0);
+        if (d.q) v = c.c * s * s * v + c.b * s * whole[at] + (row == col ? c.a : 0.0);
+        else v *= s;
         if (d.fin) {
             if (row >= 32 * blocks || col >= 32 * blocks) continue;
             const float f = row < e.side && col < e.side ? (float)(v * inv) : 0.0f;
@@ -867,9 +959,9 @@ __global__ __launch_bounds__(kThreads) void muon_product_kernel(List list, Scala
     }
 }
 
-// The same on fp32 matrices in parts: a wave takes 32 x 32 of the upper triangle and reads
-// its operands from the caches, a row's eight columns a lane.
-__global__ __launch_bounds__(64) void muon_product32_kernel(List list, Scalars c, Space ws, Products products) {
+// The same on fp32 matrices in parts: a wave takes 16 x 16 of the upper triangle's 32 x 32
+// and reads its operands from the caches, a row's eight columns a lane, all at once.
+__global__ __launch_bounds__(kThreads) void muon_product32_kernel(List list, Scalars c, Space ws, Products products) {
     const Item e = list.item[blockIdx.x];
     const int edge = 64 * blocks_of(e.side), nb = edge / kEdge;
     if (e.side <= kSmall || (int)blockIdx.y >= nb * (nb + 1) / 2) return;
@@ -877,64 +969,58 @@ __global__ __launch_bounds__(64) void muon_product32_kernel(List list, Scalars c
     int bi, bj;
     pair_of(blockIdx.y, bi, bj);
     auto mat = [&](int which) { return reinterpret_cast<float *>(mat_of(e, ws, which)); };
-    const int n = threadIdx.x % 16, k = threadIdx.x / 16;
-    const float *x = mat(d.x) + (kEdge * bi + n) * edge + 8 * k, *y = mat(d.y) + (kEdge * bj + n) * edge + 8 * k;
-    f32x4 acc[2][2];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, n = lane % 16, k = lane / 16;
+    const int row0 = kEdge * bi + 16 * (wave / 2), col0 = kEdge * bj + 16 * (wave % 2);
+    const float *x = mat(d.x) + (row0 + n) * edge + 8 * k, *y = mat(d.y) + (col0 + n) * edge + 8 * k;
+    float whole[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (d.q)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+        for (int r = 0; r < 4; ++r) whole[r] = mat(d.x)[(row0 + 4 * k + r) * edge + col0 + n];
+    const double norm = ws.norm[blockIdx.x];
+    constexpr int kSteps = kMuonSide / 32;
+    f32x4 raw[kSteps][2][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // two steps of 32 columns at a time: 16 loads in flight
-    for (int k0 = 0; k0 < edge; k0 += 64) {
-        f32x4 raw[2][4][2];
+    for (int s = 0; s < kSteps; ++s)
+        if (32 * s < edge)
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float *from = (i < 2 ? x + 16 * i * edge : y + 16 * (i - 2) * edge) + k0 + 32 * s;
-                raw[s][i][0] = *reinterpret_cast<const f32x4 *>(from);
-                raw[s][i][1] = *reinterpret_cast<const f32x4 *>(from + 4);
+            for (int h = 0; h < 2; ++h) {
+                raw[s][0][h] = *reinterpret_cast<const f32x4 *>(x + 32 * s + 4 * h);
+                raw[s][1][h] = *reinterpret_cast<const f32x4 *>(y + 32 * s + 4 * h);
             }
+    __builtin_amdgcn_sched_barrier(0);
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            Operand<3> op[4];
+    for (int s = 0; s < kSteps; ++s) {
+        if (32 * s >= edge) break;
+        Operand<3> op[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v[8];
+        for (int i = 0; i < 2; ++i) {
+            float v[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = raw[s][i][j / 4][j % 4];
-                op[i] = operand_of<3>(v);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_f32<3>(op[i], op[2 + j], acc[i][j]);
+            for (int j = 0; j < 8; ++j) v[j] = raw[s][i][j / 4][j % 4];
+            op[i] = operand_of<3>(v);
         }
+        acc = mfma_f32<3>(op[0], op[1], acc);
     }
-    const double inv = inverse(ws.norm[blockIdx.x], c.eps);
+    const double inv = inverse(norm, c.eps);
     const int blocks = p_blocks(e.side);
     uint16_t *p = ws.p + (int64_t)e.p * 512;
-    const float *whole = mat(d.x);
     float *out = mat(d.out);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = kEdge * bi + 16 * i + 4 * k + r, col = kEdge * bj + 16 * j + n;
-                float v = acc[i][j][r];
-                if (d.q) v = (float)c.c * v + (float)c.b * whole[row * edge + col] + (row == col ? (float)c.a : 0.0f);
-                if (d.fin) {
-                    if (row >= 32 * blocks || col >= 32 * blocks) continue;
-                    const float f = row < e.side && col < e.side ? (float)(v * inv) : 0.0f;
-                    put_p(p, blocks, row, col, f);
-                    if (bi != bj) put_p(p, blocks, col, row, f);
-                } else {
-                    out[row * edge + col] = v;
-                    if (bi != bj) out[col * edge + row] = v;
-                }
-            }
+    for (int r = 0; r < 4; ++r) {
+        const int row = row0 + 4 * k + r, col = col0 + n;
+        float v = acc[r];
+        if (d.q) v = (float)c.c * v + (float)c.b * whole[r] + (row == col ? (float)c.a : 0.0f);
+        if (d.fin) {
+            if (row >= 32 * blocks || col >= 32 * blocks) continue;
+            const float f = row < e.side && col < e.side ? (float)(v * inv) : 0.0f;
+            put_p(p, blocks, row, col, f);
+            if (bi != bj) put_p(p, blocks, col, row, f);
+        } else {
+            out[row * edge + col] = v;
+            if (bi != bj) out[col * edge + row] = v;
+        }
+    }
 }
 
 // ---- O = U P and the step ----
@@ -1236,19 +1322,18 @@ int exact_steps(const MuonCall &call, bool masters) {
 
 size_t round_up(size_t x, size_t to) { return (x + to - 1) / to * to; }
 
-// How a list is cut, and what lies where in the workspace. The longer sides are cut into
-// about 2048 shares of each pass, so that the chip is full and few partial sums are left.
+// How a list is cut, and what lies where in the workspace. The longer sides are cut so
+// that the chip is full and few partial sums are left.
 struct Plan {
     size_t items, gram_first, apply_first, norm, partial, mats, p, bytes;  // offsets
-    uint32_t gram_wgs, apply_wgs;
+    uint32_t gram_wgs, apply_wgs, gram_chunk, apply_chunk;
     int32_t count, masters;      // matrices with elements, and with a master weight
     int32_t largest, smallest;   // of their shorter sides
     bool fits;
 };
-constexpr int64_t kShares = 2048, kApplyShares = 2048;
+constexpr int64_t kMinRows = 256;  // of a share of the first pass: 64 a wave
 
-template <typename F>
-Plan make_plan(const MuonMatrix *list, int32_t count, F &&each) {
+Plan make_plan(const MuonMatrix *list, int32_t count) {
     Plan p{};
     int64_t gram_rows = 0, apply_rows = 0;
     for (int32_t i = 0; i < count; ++i) {
@@ -1263,9 +1348,12 @@ Plan make_plan(const MuonMatrix *list, int32_t count, F &&each) {
         if (side > p.largest) p.largest = (int32_t)side;
         if (p.smallest == 0 || side < p.smallest) p.smallest = (int32_t)side;
     }
-    // 64 rows a wave at least: the fp32 sums' length
-    const int64_t gram_chunk = round_up(gram_rows / kShares < 128 ? 128 : gram_rows / kShares, 64);
-    const int64_t apply_chunk = round_up(apply_rows / kApplyShares < 64 ? 64 : apply_rows / kApplyShares, 64);
+    // Shares of each pass: 448 matrices of rank 64 take 842 us a step with 2048 shares of the
+    // first one, 850 with 1024, 14 of rank 256 337 and 328 (more partial sums to add up).
+    const int64_t shares = p.largest > kSmall ? 1024 : 2048;
+    const int64_t gram_chunk = round_up(std::max(gram_rows / shares, kMinRows), 64);
+    const int64_t apply_chunk = round_up(std::max<int64_t>(apply_rows / 2048, 64), 64);
+    p.gram_chunk = (uint32_t)gram_chunk, p.apply_chunk = (uint32_t)apply_chunk;
     p.items = 0;
     p.gram_first = round_up(p.items + (size_t)p.count * sizeof(Item), 16);
     p.apply_first = round_up(p.gram_first + (size_t)p.count * 4, 16);
@@ -1273,25 +1361,10 @@ Plan make_plan(const MuonMatrix *list, int32_t count, F &&each) {
     p.partial = round_up(p.norm + (size_t)p.count * 8, 256);
     int64_t partial = 0, mats = 0, wgs = 0, apply_wgs = 0, ps = 0;
     for (int32_t i = 0; i < count; ++i) {
-        const MuonMatrix &x = list[i];
-        Item e{};
-        e.tall = x.rows >= x.cols;
-        e.side = (int32_t)(e.tall ? x.cols : x.rows), e.length = (int32_t)(e.tall ? x.rows : x.cols);
-        e.total = (int32_t)(x.rows * x.cols);
-        if (e.side == 0) continue;
-        const int nb = blocks_of(e.side);
-        const int64_t edge = 64 * nb;
-        e.gram_pairs = nb * (nb + 1) / 2;
-        e.gram_chunk = (uint32_t)gram_chunk, e.gram_chunks = (uint32_t)((e.length + gram_chunk - 1) / gram_chunk);
-        e.apply_chunk = (uint32_t)apply_chunk;
-        e.gram_first = (uint32_t)wgs, e.apply_first = (uint32_t)apply_wgs;
-        e.partial = partial, e.mats = mats, e.p = (uint32_t)ps;
-        wgs += (int64_t)e.gram_chunks * e.gram_pairs;
-        apply_wgs += (e.length + apply_chunk - 1) / apply_chunk;
-        partial += (int64_t)e.gram_chunks * e.gram_pairs * gram_tiles(e.side) * 256;
-        if (e.side > kSmall) mats += kMats * edge * edge;
-        ps += p_elements(e.side) / 512;
-        each(i, e);
+        if (list[i].rows == 0 || list[i].cols == 0) continue;
+        Offsets o;
+        item_of((int32_t)list[i].rows, (int32_t)list[i].cols, p.gram_chunk, p.apply_chunk, o);
+        wgs += o.gram, apply_wgs += o.apply, partial += o.partial, mats += o.mats, ps += o.p;
     }
     p.mats = round_up(p.partial + (size_t)partial * 8, 256);
     p.p = round_up(p.mats + (size_t)mats * 8, 256);
@@ -1329,12 +1402,12 @@ hipError_t run(const Plan &p, const List &list, const Scalars &c, const Space &w
         muon_gram_kernel<G, M, true><<<dim3(p.gram_wgs), dim3(kThreads), 0, s>>>(list, c, ws);
         if (!note()) return r;
         const int nb = blocks_of(p.largest), pairs = 2 * nb * (2 * nb + 1) / 2;
-        muon_start_kernel<<<dim3(p.count, nb * (nb + 1) / 2, kStartParts), dim3(kThreads), 0, s>>>(list, c, ws);
+        muon_start_kernel<<<dim3(p.count, nb * (nb + 1) / 2 + 1, kStartParts), dim3(kThreads), 0, s>>>(list, c, ws);
         if (!note()) return r;
         auto launch = [&](bool wide, const Products &x, int z) {
             if (r != hipSuccess) return;
             if (wide) muon_product_kernel<<<dim3(p.count, pairs, z), dim3(kThreads), 0, s>>>(list, c, ws, x);
-            else muon_product32_kernel<<<dim3(p.count, pairs, z), dim3(64), 0, s>>>(list, c, ws, x);
+            else muon_product32_kernel<<<dim3(p.count, pairs, z), dim3(kThreads), 0, s>>>(list, c, ws, x);
             note();
         };
         int now = kP0;
@@ -1342,16 +1415,16 @@ hipError_t run(const Plan &p, const List &list, const Scalars &c, const Space &w
             const bool last = it + 1 == c.iterations, wide = it < c.exact;
             const bool narrow = wide && it + 1 == c.exact && !last;  // the next step is in fp32
             const int next = now == kP0 ? kP1 : kP0;
-            // Q; with the first step, P too
-            Product q{kA, kA, kQ, true, last && it == 0, false};
-            launch(wide, {{q, {}}}, 1);
-            const Product step{kA, kQ, kT, false, false, false}, grow{now, kQ, next, false, last, narrow};
-            const Product first{kA, kA, now, true, false, narrow};
-            if (it == 0 && !last) launch(wide, {{step, first}}, 2);
-            else if (it > 0 && last) launch(wide, {{grow, {}}}, 1);
-            else if (it > 0) launch(wide, {{step, grow}}, 2);
-            if (it > 0) now = next;
-            if (!last) launch(wide, {{{kT, kQ, kA, false, false, narrow}, {}}}, 1);
+            // Q; with the first step P is Q, computed once more
+            const bool first = it == 0;
+            launch(wide, {{{kA, kA, kQ, true, last && first, false, first}, {}}}, 1);
+            const Product step{kA, kQ, kT, false, false, false, first}, grow{now, kQ, next, false, last, narrow, false};
+            const Product start{kA, kA, now, true, false, narrow, true};
+            if (first && !last) launch(wide, {{step, start}}, 2);
+            else if (!first && last) launch(wide, {{grow, {}}}, 1);
+            else if (!first) launch(wide, {{step, grow}}, 2);
+            if (!first) now = next;
+            if (!last) launch(wide, {{{kT, kQ, kA, false, false, narrow, false}, {}}}, 1);
         }
         if (r != hipSuccess) return r;
     }
@@ -1382,39 +1455,31 @@ hipError_t run(const Plan &p, const List &list, const Scalars &c, const Space &w
 }  // namespace
 
 size_t muon_workspace(const MuonMatrix *list, int32_t count) {
-    const Plan p = make_plan(list, count, [](int32_t, const Item &) {});
+    const Plan p = make_plan(list, count);
     return p.fits ? p.bytes : (size_t)-1;
 }
 
 hipError_t launch_muon(const MuonMatrix *list, int32_t count, const MuonCall &call, void *workspace, hipStream_t s) {
-    // the table first, a batch a launch; offsets and sizes follow from the list alone
-    const Plan sizes = make_plan(list, count, [](int32_t, const Item &) {});
+    const Plan sizes = make_plan(list, count);
     if (sizes.count == 0) return hipSuccess;
     char *base = static_cast<char *>(workspace);
     Item *items = reinterpret_cast<Item *>(base + sizes.items);
     uint32_t *gram_first = reinterpret_cast<uint32_t *>(base + sizes.gram_first);
     uint32_t *apply_first = reinterpret_cast<uint32_t *>(base + sizes.apply_first);
     Batch b{};
-    int used = 0;
-    int32_t done = 0;
-    hipError_t err = hipSuccess;
-    auto flush = [&] {
-        if (used == 0 || err != hipSuccess) return;
-        muon_table_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(b, used, items + done, gram_first + done, apply_first + done);
-        err = hipGetLastError();
-        done += used, used = 0;
-    };
-    make_plan(list, count, [&](int32_t i, const Item &e) {
-        if (used == kBatch) flush();
-        Item &t = b.item[used++];
-        t = e;
+    int32_t used = 0, done = 0;
+    for (int32_t i = 0; i < count; ++i) {
         const MuonMatrix &x = list[i];
-        t.g = x.grad, t.m = x.m, t.w = x.w, t.master = x.master;
-        t.keep = (float)(1.0 - (double)x.lr * (double)x.weight_decay);
-        t.step = (float)((double)x.lr * (double)x.scale);
-    });
-    flush();
-    if (err != hipSuccess) return err;
+        if (x.rows == 0 || x.cols == 0) continue;
+        b.item[used++] = Sent{x.grad, x.m, x.w, x.master, (int32_t)x.rows, (int32_t)x.cols,
+                              (float)(1.0 - (double)x.lr * (double)x.weight_decay), (float)((double)x.lr * (double)x.scale)};
+        if (used < kBatch && done + used < sizes.count) continue;
+        muon_table_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(b, used, done, sizes.count, sizes.gram_chunk, sizes.apply_chunk, items,
+                                                             gram_first, apply_first);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+        done += used, used = 0;
+    }
     Scalars c{};
     c.mu = (float)call.momentum, c.one_mu = (float)(1.0 - call.momentum), c.nesterov = call.nesterov;
     c.eps = call.eps, c.a = call.a, c.b = call.b, c.c = call.c, c.iterations = call.iterations;
