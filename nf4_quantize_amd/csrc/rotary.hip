@@ -121,93 +121,154 @@ __device__ __forceinline__ Unit unit_of(const RotaryParams &p, int u) {
 
 enum RotaryKind { kTurn, kNormTurn, kNormTurnBack };
 
+constexpr int kMaxDim = 512, kMaxPairs = kMaxDim / 2;
+
 // A wave takes a token and every splits-th round of its heads: 64 / lanes heads a
-// round, queries first. Its cosines and sines serve all of them. U units a lane.
+// round, queries first. The next round's loads are in flight while it works on one. Its
+// lanes share the token's cosines and sines through LDS, a pair a lane (with each lane
+// computing those of its own pairs, eight lanes do the same work). U units a lane.
 template <typename T, int V, int U, RotaryKind kKind>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p) {
     constexpr bool kBack = kKind == kNormTurnBack, kNorm = kKind != kTurn;
     constexpr int E = 2 * V;
+    __shared__ float turns[kWaves][2][kMaxPairs], weights[kNorm ? 2 : 1][kNorm ? kMaxDim + 8 : 1];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int in_group = lane & (p.lanes - 1), group = lane / p.lanes, groups = 64 / p.lanes;
+    const int pairs = p.rotated / 2, total = p.steps[0] + p.steps[1];
+    float *cosines = turns[wave][0], *sines = turns[wave][1];
     Unit unit[U];
-    float w[2][kNorm ? U : 1][E], sums[2][kBack ? U : 1][E];
+    float sums[2][kBack ? U : 1][E];
 #pragma unroll
     for (int u = 0; u < U; ++u) unit[u] = unit_of<V>(p, in_group + u * 64);
-    if constexpr (kNorm)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const int d = j < V ? unit[u].lo + j : unit[u].hi + j - V;
-                    const bool live = p.w[i] != nullptr && (j < V ? unit[u].live_lo : unit[u].live_hi);
-                    w[i][u][j] = 1.0f;
-                    if (live) w[i][u][j] = p.off + (p.w_bf16 ? load1(static_cast<const Bf16 *>(p.w[i]) + d)
-                                                             : load1(static_cast<const float *>(p.w[i]) + d));
-                    if constexpr (kBack) sums[i][u][j] = 0.0f;
-                }
-    for (uint32_t item = blockIdx.x * kWaves + wave; item < p.items; item += gridDim.x * kWaves) {
-        const uint32_t row = item / p.splits, part = item % p.splits;
-        const uint32_t b = row / p.tokens, t = row % p.tokens;
-        int64_t position = t;
-        if (p.positions) {
-            const int64_t at = (int64_t)b * p.position_batch_stride + t;
-            position = p.i64 ? static_cast<const int64_t *>(p.positions)[at] : static_cast<const int32_t *>(p.positions)[at];
-        }
-        float c[U][V], s[U][V];
+    if constexpr (kBack)
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                c[u][j] = 1.0f, s[u][j] = 0.0f;
-                if (unit[u].pair + j < p.rotated / 2) {
-                    const uint64_t phase = (uint64_t)position * p.turns[unit[u].pair + j] + 0x80000000u;
-                    cos_sin((uint32_t)(phase >> 32), c[u][j], s[u][j]);
-                    c[u][j] *= p.scale, s[u][j] *= p.scale * p.sign;
+            for (int j = 0; j < E; ++j) sums[0][u][j] = sums[1][u][j] = 0.0f;
+
+    struct Place {
+        uint32_t item, b, t;
+        int step;
+    };
+    auto place = [&](uint32_t item) {
+        const uint32_t row = item / p.splits;
+        return Place{item, row / p.tokens, row % p.tokens, (int)(item % p.splits)};
+    };
+    struct Heads {
+        RawVec<T, V> lo[U], hi[U];
+    };
+    auto read = [&](const nf4_heads &h, const Place &at, int head, Heads &x) {
+        const T *from = static_cast<const T *>(h.data) + (at.b * h.batch_stride + at.t * h.token_stride + head * h.head_stride);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            x.lo[u] = load_vec<T, V>(from + (unit[u].live_lo ? unit[u].lo : 0));
+            x.hi[u] = load_vec<T, V>(from + (unit[u].live_hi ? unit[u].hi : 0));
+        }
+    };
+    Heads raw, raw_x;
+    int64_t position = 0;
+    auto load = [&](const Place &at) {
+        const int i = at.step < p.steps[0] ? 0 : 1;
+        const int head = min((at.step - (i ? p.steps[0] : 0)) * groups + group, p.heads[i] - 1);
+        read(p.in[i], at, head, raw);
+        if constexpr (kBack)
+            if (p.w[i]) read(p.x[i], at, head, raw_x);
+        if (at.step >= (int)p.splits) return;
+        position = at.t;  // a token's first round
+        if (p.positions) {
+            const int64_t k = (int64_t)at.b * p.position_batch_stride + at.t;
+            position = p.i64 ? static_cast<const int64_t *>(p.positions)[k] : static_cast<const int32_t *>(p.positions)[k];
+        }
+    };
+    auto values = [&](const Heads &h, float (&x)[U][E]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            vec_values<V>(h.lo[u], x[u]);
+            vec_values<V>(h.hi[u], x[u] + V);
+#pragma unroll
+            for (int j = 0; j < E; ++j) x[u][j] = (j < V ? unit[u].live_lo : unit[u].live_hi) ? x[u][j] : 0.0f;
+        }
+    };
+
+    Place at = place(blockIdx.x * kWaves + wave);
+    if (at.item < p.items) load(at);
+    uint64_t turn_of[kMaxPairs / 64];
+#pragma unroll
+    for (int k = 0; k < kMaxPairs / 64; ++k)
+        if (k * 64 < pairs) turn_of[k] = p.turns[min(k * 64 + lane, pairs - 1)];
+    // what is not rotated: pairs from `pairs` on
+    for (int k = pairs + lane; k < kMaxPairs; k += 64) cosines[k] = 1.0f, sines[k] = 0.0f;
+    if constexpr (kNorm) {
+        for (int k = threadIdx.x; k < 2 * p.dim; k += kThreads) {
+            const int i = k / p.dim, d = k % p.dim;
+            float w = 1.0f;
+            if (p.w[i]) w = p.off + (p.w_bf16 ? load1(static_cast<const Bf16 *>(p.w[i]) + d) : load1(static_cast<const float *>(p.w[i]) + d));
+            weights[i][d] = w;
+        }
+        __syncthreads();
+    }
+    float c[U][V], s[U][V];
+    auto turn = [&](float (&x)[U][E]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (p.half || V == 1) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float a = x[u][j], d = x[u][V + j];
+                    x[u][j] = a * c[u][j] - d * s[u][j], x[u][V + j] = d * c[u][j] + a * s[u][j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float a = x[u][2 * j], d = x[u][2 * j + 1];
+                    x[u][2 * j] = a * c[u][j] - d * s[u][j], x[u][2 * j + 1] = d * c[u][j] + a * s[u][j];
                 }
             }
-        auto turn = [&](float (&x)[U][E]) {
+        }
+    };
+    auto weight = [&](int i, int u, int j) { return weights[i][j < V ? unit[u].lo + j : unit[u].hi + j - V]; };
+    // dead vectors read the weights' last places: their elements are zero
+    if constexpr (kNorm)
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (p.half || V == 1) {
+        for (int u = 0; u < U; ++u) {
+            if (!unit[u].live_lo) unit[u].lo = 0;
+            if (!unit[u].live_hi) unit[u].hi = 0;
+        }
+
+    while (at.item < p.items) {
+        float x[U][E], n[U][E];
+        values(raw, x);
+        if constexpr (kBack) values(raw_x, n);
+        const int64_t here = position;
+        Place next = at;
+        next.step += p.splits;
+        if (next.step >= total) next = place(at.item + gridDim.x * kWaves);
+        if (next.item < p.items) load(next);
+        if (at.step < (int)p.splits) {
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float a = x[u][j], d = x[u][V + j];
-                        x[u][j] = a * c[u][j] - d * s[u][j], x[u][V + j] = d * c[u][j] + a * s[u][j];
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float a = x[u][2 * j], d = x[u][2 * j + 1];
-                        x[u][2 * j] = a * c[u][j] - d * s[u][j], x[u][2 * j + 1] = d * c[u][j] + a * s[u][j];
-                    }
+            for (int k = 0; k < kMaxPairs / 64; ++k)
+                if (k * 64 + lane < pairs) {
+                    const uint64_t phase = (uint64_t)here * turn_of[k] + 0x80000000u;
+                    float cosine, sine;
+                    cos_sin((uint32_t)(phase >> 32), cosine, sine);
+                    cosines[k * 64 + lane] = cosine * p.scale, sines[k * 64 + lane] = sine * (p.scale * p.sign);
                 }
-            }
-        };
-        auto load = [&](const nf4_heads &h, int head, float (&x)[U][E]) {
-            const T *from = static_cast<const T *>(h.data) + (b * h.batch_stride + t * h.token_stride + head * h.head_stride);
-            RawVec<T, V> lo[U], hi[U];
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                lo[u] = load_vec<T, V>(from + (unit[u].live_lo ? unit[u].lo : 0));
-                hi[u] = load_vec<T, V>(from + (unit[u].live_hi ? unit[u].hi : 0));
-            }
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                vec_values<V>(lo[u], x[u]);
-                vec_values<V>(hi[u], x[u] + V);
-#pragma unroll
-                for (int j = 0; j < E; ++j) x[u][j] = (j < V ? unit[u].live_lo : unit[u].live_hi) ? x[u][j] : 0.0f;
-            }
-        };
-        auto heads = [&](auto which, int round) {
+                for (int j = 0; j < V; ++j) {
+                    const int k = min(unit[u].pair, kMaxPairs - V) + j;
+                    c[u][j] = cosines[k], s[u][j] = sines[k];
+                }
+        }
+        auto heads = [&](auto which) {
             constexpr int i = decltype(which)::value;
-            const int head = round * groups + group;
+            const int head = (at.step - (i ? p.steps[0] : 0)) * groups + group;
             const bool live = head < p.heads[i];
-            const int from = live ? head : p.heads[i] - 1;
-            float x[U][E];
-            load(p.in[i], from, x);
             if constexpr (kKind == kTurn) {
                 turn(x);
             } else if constexpr (kKind == kNormTurn) {
@@ -221,21 +282,19 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p) {
 #pragma unroll
                     for (int u = 0; u < U; ++u)
 #pragma unroll
-                        for (int j = 0; j < E; ++j) x[u][j] *= r * w[i][u][j];
+                        for (int j = 0; j < E; ++j) x[u][j] *= r * weight(i, u, j);
                 }
                 turn(x);
             } else {
                 turn(x);  // the gradient of the normed head
                 if (p.w[i]) {
-                    float n[U][E];
-                    load(p.x[i], from, n);
                     float sum = 0.0f, dot = 0.0f;
 #pragma unroll
                     for (int u = 0; u < U; ++u)
 #pragma unroll
                         for (int j = 0; j < E; ++j) {
                             sum += n[u][j] * n[u][j];
-                            dot += x[u][j] * w[i][u][j] * n[u][j];
+                            dot += x[u][j] * weight(i, u, j) * n[u][j];
                         }
                     const float r = 1.0f / sqrtf(group_sum(sum, p.lanes) * p.inv_dim + p.eps);
                     const float mean = group_sum(dot, p.lanes) * p.inv_dim * r;
@@ -245,27 +304,27 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p) {
                         for (int j = 0; j < E; ++j) {
                             const float nr = n[u][j] * r;
                             sums[i][u][j] += live ? x[u][j] * nr : 0.0f;
-                            x[u][j] = r * (x[u][j] * w[i][u][j] - nr * mean);
+                            x[u][j] = r * (x[u][j] * weight(i, u, j) - nr * mean);
                         }
                 }
             }
             if (!live) return;
             const nf4_heads &h = p.out[i];
-            T *to = static_cast<T *>(h.data) + (b * h.batch_stride + t * h.token_stride + head * h.head_stride);
+            T *to = static_cast<T *>(h.data) + (at.b * h.batch_stride + at.t * h.token_stride + head * h.head_stride);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (unit[u].live_lo) store_vec<V>(to + unit[u].lo, x[u]);
                 if (unit[u].live_hi) store_vec<V>(to + unit[u].hi, x[u] + V);
             }
         };
-        int step = part;
-        for (; step < p.steps[0]; step += p.splits) heads(std::integral_constant<int, 0>{}, step);
-        for (; step < p.steps[0] + p.steps[1]; step += p.splits) heads(std::integral_constant<int, 1>{}, step - p.steps[0]);
+        if (at.step < p.steps[0]) heads(std::integral_constant<int, 0>{});
+        else heads(std::integral_constant<int, 1>{});
+        at = next;
     }
     if constexpr (kBack) {
         if (!p.partial) return;
         // the workgroup's sums: the wave's groups, then its waves
-        __shared__ float part[kWaves][2][U * 64 * E];
+        __shared__ float part[kWaves][2][kMaxDim];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -289,25 +348,32 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p) {
 }
 
 // The weights' gradients: columns of the workgroups' partial sums, 16 columns a
-// workgroup and 16 rows at a time.
-__global__ __launch_bounds__(kThreads) void rotary_sums_kernel(const float *partial, int32_t rows, int32_t dim, bool bf16,
-                                                               void *dw_q, void *dw_k) {
-    __shared__ float part[16][17];
+// workgroup and 64 rows at a time, eight of a thread's loads in flight.
+constexpr int kSumRows = 64;
+__global__ __launch_bounds__(16 * kSumRows) void rotary_sums_kernel(const float *partial, int32_t rows, int32_t dim, bool bf16,
+                                                                   void *dw_q, void *dw_k) {
+    __shared__ float part[kSumRows][17];
     const int col = threadIdx.x % 16, first = threadIdx.x / 16, k = blockIdx.x * 16 + col;
     float x = 0.0f;
-    if (k < 2 * dim)
-        for (int r = first; r < rows; r += 16) x += partial[(int64_t)r * 2 * dim + k];
+    for (int r = first; r < rows; r += 8 * kSumRows) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = partial[(int64_t)min(r + j * kSumRows, rows - 1) * 2 * dim + min(k, 2 * dim - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x += r + j * kSumRows < rows ? y[j] : 0.0f;
+    }
     part[first][col] = x;
     __syncthreads();
+    for (int o = kSumRows / 2; o > 0; o /= 2) {
+        if (first < o) part[first][col] += part[first + o][col];
+        __syncthreads();
+    }
     if (first != 0 || k >= 2 * dim) return;
-    x = 0.0f;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) x += part[r][col];
     void *dw = k < dim ? dw_q : dw_k;
     if (!dw) return;
     const int d = k < dim ? k : k - dim;
-    if (bf16) store1(static_cast<Bf16 *>(dw) + d, x);
-    else store1(static_cast<float *>(dw) + d, x);
+    if (bf16) store1(static_cast<Bf16 *>(dw) + d, part[0][col]);
+    else store1(static_cast<float *>(dw) + d, part[0][col]);
 }
 
 constexpr uint32_t kMostGroups = 1024;  // workgroups of a backward pass with weights: rows of partial sums
@@ -404,7 +470,7 @@ hipError_t launch_rotary(const nf4_rotary_shape &sh, const RotaryArgs &a, bool b
         if (r != hipSuccess) return r;
     }
     if (!sums) return hipSuccess;
-    rotary_sums_kernel<<<dim3((2 * sh.dim + 15) / 16), dim3(kThreads), 0, s>>>(p.partial, (int32_t)wgs, sh.dim, p.w_bf16,
+    rotary_sums_kernel<<<dim3((2 * sh.dim + 15) / 16), dim3(16 * kSumRows), 0, s>>>(p.partial, (int32_t)wgs, sh.dim, p.w_bf16,
                                                                              a.dw[0], a.dw[1]);
     return hipGetLastError();
 }
