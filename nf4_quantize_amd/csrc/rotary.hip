@@ -8,6 +8,7 @@
 // lane's own, so a rotation needs no other lane and a norm one sum over the group.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "training_internal.h"
@@ -65,7 +66,8 @@ __device__ __forceinline__ void vec_values(const RawVec<float, V> &r, float *x) 
 #pragma unroll
         for (int j = 0; j < V; ++j) x[j] = r.v[j];
 }
-template <int V>
+// kPast: past the caches.
+template <int V, bool kPast>
 __device__ __forceinline__ void store_vec(Bf16 *p, const float *x) {
     RawVec<Bf16, V> r;
     if constexpr (V == 1) r.v = (uint16_t)(pack_bf16x2(x[0], 0.0f) & 0xFFFFu);
@@ -73,16 +75,20 @@ __device__ __forceinline__ void store_vec(Bf16 *p, const float *x) {
     else
 #pragma unroll
         for (int j = 0; j < V / 2; ++j) r.v[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
-    *reinterpret_cast<decltype(r.v) *>(p) = r.v;
+    auto *to = reinterpret_cast<decltype(r.v) *>(p);
+    if constexpr (kPast) __builtin_nontemporal_store(r.v, to);
+    else *to = r.v;
 }
-template <int V>
+template <int V, bool kPast>
 __device__ __forceinline__ void store_vec(float *p, const float *x) {
     RawVec<float, V> r;
     if constexpr (V == 1) r.v = x[0];
     else
 #pragma unroll
         for (int j = 0; j < V; ++j) r.v[j] = x[j];
-    *reinterpret_cast<decltype(r.v) *>(p) = r.v;
+    auto *to = reinterpret_cast<decltype(r.v) *>(p);
+    if constexpr (kPast) __builtin_nontemporal_store(r.v, to);
+    else *to = r.v;
 }
 
 // Cosine and sine of phase 2^-32 turns. The phase is cut to an eighth of a turn
@@ -127,7 +133,7 @@ constexpr int kMaxDim = 512, kMaxPairs = kMaxDim / 2;
 // round, queries first. The next round's loads are in flight while it works on one. Its
 // lanes share the token's cosines and sines through LDS, a pair a lane (with each lane
 // computing those of its own pairs, eight lanes do the same work). U units a lane.
-template <typename T, int V, int U, RotaryKind kKind>
+template <typename T, int V, int U, RotaryKind kKind, bool kPast = false>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p) {
     constexpr bool kBack = kKind == kNormTurnBack, kNorm = kKind != kTurn;
     constexpr int E = 2 * V;
@@ -313,8 +319,8 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p) {
             T *to = static_cast<T *>(h.data) + (at.b * h.batch_stride + at.t * h.token_stride + head * h.head_stride);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (unit[u].live_lo) store_vec<V>(to + unit[u].lo, x[u]);
-                if (unit[u].live_hi) store_vec<V>(to + unit[u].hi, x[u] + V);
+                if (unit[u].live_lo) store_vec<V, kPast>(to + unit[u].lo, x[u]);
+                if (unit[u].live_hi) store_vec<V, kPast>(to + unit[u].hi, x[u] + V);
             }
         };
         if (at.step < p.steps[0]) heads(std::integral_constant<int, 0>{});
@@ -386,9 +392,12 @@ uint32_t plan(RotaryParams &p, uint32_t rows, int units, bool sums) {
     p.steps[0] = (p.heads[0] + groups - 1) / groups;
     p.steps[1] = (p.heads[1] + groups - 1) / groups;
     const uint32_t steps = p.steps[0] + p.steps[1];
-    // few tokens: a token's heads are shared by several waves
+    // Few tokens: a token's heads are shared by several waves, until there are 4096, and without
+    // sums up to 8192 while each keeps four rounds (4096 tokens of 72 normed heads: 26.6 us
+    // instead of 28.5; 3003 tokens of 8, of three rounds: 7.8 instead of 7.2).
     constexpr uint32_t kWant = 4096;
     p.splits = rows >= kWant ? 1 : (kWant + rows - 1) / rows;
+    if (!sums && rows * p.splits < 2 * kWant && steps >= 8 * p.splits) p.splits *= 2;
     if (p.splits > steps) p.splits = steps;
     p.items = rows * p.splits;
     const uint32_t wgs = (p.items + kWaves - 1) / kWaves;
@@ -397,18 +406,21 @@ uint32_t plan(RotaryParams &p, uint32_t rows, int units, bool sums) {
 }
 
 template <typename T, int V, int U>
-void launch_units(const RotaryParams &p, RotaryKind kind, uint32_t wgs, hipStream_t s) {
+void launch_units(const RotaryParams &p, RotaryKind kind, bool past, uint32_t wgs, hipStream_t s) {
     const dim3 grid(wgs), block(kThreads);
-    if (kind == kTurn) rotary_kernel<T, V, U, kTurn><<<grid, block, 0, s>>>(p);
+    constexpr bool kWidest = V * sizeof(T) == 16;
+    if (kWidest && past && kind == kTurn) rotary_kernel<T, V, U, kTurn, kWidest><<<grid, block, 0, s>>>(p);
+    else if (kWidest && past && kind == kNormTurn) rotary_kernel<T, V, U, kNormTurn, kWidest><<<grid, block, 0, s>>>(p);
+    else if (kind == kTurn) rotary_kernel<T, V, U, kTurn><<<grid, block, 0, s>>>(p);
     else if (kind == kNormTurn) rotary_kernel<T, V, U, kNormTurn><<<grid, block, 0, s>>>(p);
-    else rotary_kernel<T, V, U, kNormTurnBack><<<grid, block, 0, s>>>(p);
+    else if constexpr (V <= 4) rotary_kernel<T, V, U, kNormTurnBack><<<grid, block, 0, s>>>(p);
 }
 
-// Elements of a vector: the widest up to 16 bytes that divides the head, the two
+// Elements of a vector: the widest up to `most` elements and 16 bytes that divides the head, the two
 // halves of its rotated part, every stride, and the addresses.
-int vector_of(const nf4_rotary_shape &sh, const RotaryArgs &a) {
+int vector_of(const nf4_rotary_shape &sh, const RotaryArgs &a, int most) {
     const int size = sh.dtype == NF4_F32 ? 4 : 2;
-    int v = 16 / size;
+    int v = std::min(16 / size, most);
     for (; v > 1; v /= 2) {
         bool fits = sh.dim % v == 0 && (sh.layout == NF4_ROTARY_INTERLEAVED || sh.rotated / 2 % v == 0);
         for (int i = 0; i < 2; ++i)
@@ -443,6 +455,11 @@ hipError_t launch_rotary(const nf4_rotary_shape &sh, const RotaryArgs &a, bool b
     p.w_bf16 = sh.w_dtype == NF4_BF16;
     p.sign = backward ? -1.0f : 1.0f;
     p.inv_dim = 1.0f / (float)sh.dim, p.eps = sh.eps, p.off = sh.w_offset, p.scale = sh.scale;
+    // Whole vectors of outputs that the memory-side cache (256 MB) cannot hold with the inputs
+    // go past it: 335 MB 60 us plain and 50 past it, 151 MB 28.5 and 30.8. The backward pass of
+    // a norm is as fast with either.
+    const int64_t elements = sh.batch * sh.tokens * (int64_t)(sh.heads_q + sh.heads_k) * sh.dim;
+    const bool past = elements * (sh.dtype == NF4_F32 ? 8 : 4) > (int64_t(256) << 20);
     const bool norm = p.w[0] || p.w[1], sums = a.dw[0] || a.dw[1];
     p.partial = sums ? static_cast<float *>(workspace) : nullptr;
     const RotaryKind kind = !norm ? kTurn : backward ? kNormTurnBack : kNormTurn;
@@ -450,21 +467,23 @@ hipError_t launch_rotary(const nf4_rotary_shape &sh, const RotaryArgs &a, bool b
     uint32_t wgs = 0;
     if (rows > 0) {
         p.tokens = (uint32_t)sh.tokens;
-        const int v = vector_of(sh, a), units = units_of(sh, v);
+        // the backward pass of a norm has three values an element in registers: with eight a
+        // vector 201 of them and 59 us for 4096 tokens of 72 heads, with four 118 and 49 us
+        const int v = vector_of(sh, a, kind == kNormTurnBack ? 4 : 8), units = units_of(sh, v);
         wgs = plan(p, rows, units, sums);
         if (sh.dtype == NF4_F32) {
-            if (v == 4) launch_units<float, 4, 1>(p, kind, wgs, s);
-            else if (v == 2 && units <= 64) launch_units<float, 2, 1>(p, kind, wgs, s);
-            else if (v == 2) launch_units<float, 2, 2>(p, kind, wgs, s);
-            else if (units <= 64) launch_units<float, 1, 1>(p, kind, wgs, s);
-            else launch_units<float, 1, 4>(p, kind, wgs, s);
+            if (v == 4) launch_units<float, 4, 1>(p, kind, past, wgs, s);
+            else if (v == 2 && units <= 64) launch_units<float, 2, 1>(p, kind, past, wgs, s);
+            else if (v == 2) launch_units<float, 2, 2>(p, kind, past, wgs, s);
+            else if (units <= 64) launch_units<float, 1, 1>(p, kind, past, wgs, s);
+            else launch_units<float, 1, 4>(p, kind, past, wgs, s);
         } else {
-            if (v == 8) launch_units<Bf16, 8, 1>(p, kind, wgs, s);
-            else if (v == 4) launch_units<Bf16, 4, 1>(p, kind, wgs, s);
-            else if (v == 2 && units <= 64) launch_units<Bf16, 2, 1>(p, kind, wgs, s);
-            else if (v == 2) launch_units<Bf16, 2, 2>(p, kind, wgs, s);
-            else if (units <= 64) launch_units<Bf16, 1, 1>(p, kind, wgs, s);
-            else launch_units<Bf16, 1, 4>(p, kind, wgs, s);
+            if (v == 8) launch_units<Bf16, 8, 1>(p, kind, past, wgs, s);
+            else if (v == 4) launch_units<Bf16, 4, 1>(p, kind, past, wgs, s);
+            else if (v == 2 && units <= 64) launch_units<Bf16, 2, 1>(p, kind, past, wgs, s);
+            else if (v == 2) launch_units<Bf16, 2, 2>(p, kind, past, wgs, s);
+            else if (units <= 64) launch_units<Bf16, 1, 1>(p, kind, past, wgs, s);
+            else launch_units<Bf16, 1, 4>(p, kind, past, wgs, s);
         }
         const hipError_t r = hipGetLastError();
         if (r != hipSuccess) return r;

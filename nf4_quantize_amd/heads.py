@@ -6,11 +6,12 @@ kernels, torch supplies device memory and the current stream.
 """
 import ctypes
 import math
+import struct
 from fractions import Fraction
 
 import nf4_quantize_amd as _nq
 
-from .training import _addr, _changed, _code, _index_code, _size, _stream
+from .training import _addr, _changed, _code, _index_code, _size, _stream, _torch
 
 LAYOUTS = {"half": 0, "interleaved": 1}
 TWO_PI = Fraction("6.283185307179586476925286766559005768394338798750")
@@ -31,7 +32,8 @@ class nf4_heads(ctypes.Structure):
 def declare(L):
     """argtypes and restypes of this module's entry points."""
     p, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-    shape, heads = ctypes.POINTER(nf4_rotary_shape), ctypes.POINTER(nf4_heads)
+    heads = p  # addresses: building structure objects would take microseconds a call
+    shape = p
     for name, restype, args in (
             ("nf4_rotary_forward", i32, [shape, p, p, i32, i64, heads, heads, p, p, heads, heads, p]),
             ("nf4_rotary_backward_workspace_size", sz, [shape]),
@@ -115,6 +117,13 @@ def rotary_frequencies(dim, base=10000.0, scaling=None):
     return out, 1.0
 
 
+def _turns(f):
+    """round(2^64 f / 2 pi) modulo 2^64, f taken as it is."""
+    n, d = f.as_integer_ratio()
+    top, bottom = n * TWO_PI.denominator << 65, d * TWO_PI.numerator
+    return (top // bottom + 1 >> 1) % 2 ** 64
+
+
 class NF4Rotary:
     """The rotation that a model keeps: ``dim`` rotated elements a head (the first
     ones; a head may have more), their pairs' ``layout`` ("half": element i with
@@ -133,14 +142,14 @@ class NF4Rotary:
             scale = attention if scale is None else scale
         elif scaling is not None:
             raise ValueError("frequencies are given, or scaled")
-        self.dim, self.layout = int(dim), layout
+        self.dim, self.layout, self.code = int(dim), layout, LAYOUTS[layout]
         self.frequencies, self.scale = [float(f) for f in frequencies], 1.0 if scale is None else float(scale)
         if self.dim < 2 or self.dim % 2 or len(self.frequencies) != self.dim // 2:
             raise ValueError(f"{len(self.frequencies)} frequencies for {dim} rotated elements")
         if not all(map(math.isfinite, self.frequencies + [self.scale])):
             raise ValueError("frequencies and scale are finite")
         # in integers: 64-bit floats would leave far positions off by 2^-53 of their angle
-        turns = [round(Fraction(f) / TWO_PI * 2 ** 64) % 2 ** 64 for f in self.frequencies]
+        turns = [_turns(f) for f in self.frequencies]
         self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns], dtype=torch.int64).to(device)
 
 
@@ -149,14 +158,21 @@ class NF4Rotary:
 def _strides(x):
     """(batch, token, head) strides of [tokens x heads x dim] or [batch x tokens x heads x dim]; a
     dimension of one element has none."""
-    st = [0 if n < 2 else s for n, s in zip(x.shape, x.stride())]
-    if st[-1] not in (0, 1):
-        raise ValueError(f"a head's elements are consecutive, got strides {x.stride()}")
-    return (0, *st[:2]) if len(st) == 3 else st[:3]
+    shape, st = x.shape, x.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"a head's elements are consecutive, got strides {st}")
+    if len(shape) == 3:
+        return 0, st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
+    return st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0, st[2] if shape[2] > 1 else 0
+
+
+_HEADS = struct.Struct("4q")
+_SHAPE = struct.Struct("2q7i3f")
 
 
 def _heads(x):
-    return None if x is None else nf4_heads(x.data_ptr(), *_strides(x))
+    """An nf4_heads, as bytes."""
+    return None if x is None else _HEADS.pack(x.data_ptr(), *_strides(x))
 
 
 def _extent(x):
@@ -199,15 +215,16 @@ def _check_out(out, own, others, what):
         raise ValueError(f"{what} is the input itself, or memory that no input has")
 
 
-def _check(rope, positions, pairs, weights):
-    """Checks (tensor of queries, tensor of keys) pairs and weights; returns (shape without the norm's
-    numbers, positions' code, their batch stride, the device's index)."""
+def _check(rope, positions, pairs, weights, eps, w_offset):
+    """Checks (tensor of queries, tensor of keys) pairs and weights; returns (an nf4_rotary_shape as
+    bytes, the positions' code, their batch stride, the device's index)."""
     first = pairs[0][0] if pairs[0][0] is not None else pairs[0][1]
     if first is None:
         raise ValueError("neither queries nor keys")
-    if first.dim() not in (3, 4):
-        raise ValueError(f"[tokens x heads x dim] or [batch x tokens x heads x dim], got {tuple(first.shape)}")
-    index, lead, dim = first.get_device(), first.shape[:-2], first.shape[-1]
+    size = first.shape
+    if len(size) not in (3, 4):
+        raise ValueError(f"[tokens x heads x dim] or [batch x tokens x heads x dim], got {tuple(size)}")
+    index, lead, dim, dt = first.get_device(), size[:-2], size[-1], first.dtype
     if index < 0:
         raise ValueError("device tensors")
     heads = [0, 0]
@@ -215,42 +232,57 @@ def _check(rope, positions, pairs, weights):
         for i, x in enumerate(pair):
             if x is None:
                 continue
-            if x.shape[:-2] != lead or x.shape[-1] != dim or x.dtype != first.dtype or x.get_device() != index:
-                raise ValueError(f"queries, keys and their gradients differ in their heads alone: {tuple(first.shape)} "
-                                 f"{first.dtype} {first.device} and {tuple(x.shape)} {x.dtype} {x.device}")
-            if heads[i] and heads[i] != x.shape[-2]:
-                raise ValueError(f"{heads[i]} and {x.shape[-2]} heads")
-            heads[i] = x.shape[-2]
+            if x is not first:
+                s = x.shape
+                if s[:-2] != lead or s[-1] != dim or x.dtype != dt or x.get_device() != index:
+                    raise ValueError(f"queries, keys and their gradients differ in their heads alone: {tuple(size)} "
+                                     f"{dt} {first.device} and {tuple(s)} {x.dtype} {x.device}")
+            n = x.shape[-2]
+            if heads[i] and heads[i] != n:
+                raise ValueError(f"{heads[i]} and {n} heads")
+            heads[i] = n
     if rope.dim > dim:
         raise ValueError(f"{rope.dim} rotated elements in heads of {dim}")
     if rope.turns.get_device() != index:
         raise ValueError(f"the rotation is on {rope.turns.device}, the heads on {first.device}")
-    wt = first.dtype
-    given = [w for w in weights if w is not None]
-    for w in given:
-        if w.shape != (dim,) or w.dtype != given[0].dtype or w.get_device() != index or not w.is_contiguous():
+    wt = None
+    for w in weights:
+        if w is None:
+            continue
+        if w.shape != (dim,) or w.dtype != (wt or w.dtype) or w.get_device() != index or not w.is_contiguous():
             raise ValueError(f"norm weights are ({dim},), contiguous, of one dtype, on {first.device}")
         wt = w.dtype
     tokens, batch = lead[-1], (lead[0] if len(lead) == 2 else 1)
     code, stride = 1, 0
     if positions is not None:
-        code = _index_code(positions)
-        if positions.shape not in (lead, lead[-1:]):
-            raise ValueError(f"positions {tuple(positions.shape)} for tokens {tuple(lead)}")
+        code, at = _index_code(positions), positions.shape
+        if at != lead and at != lead[-1:]:
+            raise ValueError(f"positions {tuple(at)} for tokens {tuple(lead)}")
         if positions.get_device() != index or (tokens > 1 and positions.stride(-1) != 1):
             raise ValueError("positions: consecutive, on the heads' device")
-        if positions.dim() == 2 and batch > 1:
+        if len(at) == 2 and batch > 1:
             stride = positions.stride(0)
-    shape = nf4_rotary_shape(batch, tokens, heads[0], heads[1], dim, rope.dim, LAYOUTS[rope.layout], _code(first.dtype),
-                             _code(wt), 0.0, 0.0, rope.scale)
-    return shape, code, stride, index
+    return (_SHAPE.pack(batch, tokens, heads[0], heads[1], dim, rope.dim, rope.code, _code(dt), _code(wt or dt), eps, w_offset,
+                        rope.scale), code, stride, index)
 
 
 def _like(x):
     """An output in x's order in memory, without its gaps."""
-    import torch
+    return None if x is None else _torch("empty_like")(x)
 
-    return None if x is None else torch.empty_like(x)
+
+def _check_outs(q, k, q_out, k_out, weights):
+    """The given outputs, once they are looked over."""
+    inputs, given = [t for t in (q, k) if t is not None], []
+    for out, own, what in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if out is not None:
+            _check_out(out, own, inputs, what)
+            given.append(out)
+    if len(given) == 2 and not _apart(*given):
+        raise ValueError("q_out and k_out share memory")
+    if not all(_range_apart(out, w) for out in given for w in weights if w is not None):
+        raise ValueError("an output shares memory with a weight")
+    return given
 
 
 def rotary_forward(q, k, positions, rope, w_q=None, w_k=None, eps=1e-6, w_offset=0.0, q_out=None, k_out=None):
@@ -264,23 +296,15 @@ def rotary_forward(q, k, positions, rope, w_q=None, w_k=None, eps=1e-6, w_offset
     ``k_out=k`` rotate in place."""
     if q is None:
         raise ValueError("queries")
-    shape, code, stride, index = _check(rope, positions, ((q, k), (q_out, k_out)), (w_q, w_k))
+    shape, code, stride, index = _check(rope, positions, ((q, k), (q_out, k_out)), (w_q, w_k), eps, w_offset)
     if (k is None and (w_k is not None or k_out is not None)):
         raise ValueError("weights and an output of keys, without keys")
-    shape.eps, shape.w_offset = eps, w_offset
-    inputs = [t for t in (q, k) if t is not None]
-    given = []
-    for out, own, what in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        if out is not None:
-            _check_out(out, own, inputs, what)
-            given.append(out)
-    if len(given) == 2 and not _apart(*given):
-        raise ValueError("q_out and k_out share memory")
-    if not all(_range_apart(out, w) for out in given for w in (w_q, w_k) if w is not None):
-        raise ValueError("an output shares memory with a weight")
+    given = None
+    if q_out is not None or k_out is not None:
+        given = _check_outs(q, k, q_out, k_out, (w_q, w_k))
     q_out = _like(q) if q_out is None else q_out
     k_out = _like(k) if k_out is None else k_out
-    st = _nq.lib().nf4_rotary_forward(ctypes.byref(shape), rope.turns.data_ptr(), _addr(positions), code, stride, _heads(q),
+    st = _nq.lib().nf4_rotary_forward(shape, rope.turns.data_ptr(), _addr(positions), code, stride, _heads(q),
                                       _heads(k), _addr(w_q), _addr(w_k), _heads(q_out), _heads(k_out), _stream(index))
     _nq._check(st, "nf4_rotary_forward")
     if given:
@@ -306,15 +330,14 @@ def rotary_backward(dq_out, dk_out, positions, rope, q=None, k=None, w_q=None, w
         if w is not None and d is None:
             raise ValueError(f"weights of {what} without their gradient")
     live = ((dq_out, dk_out), (q if w_q is not None else None, k if w_k is not None else None))
-    shape, code, stride, index = _check(rope, positions, live, (w_q, w_k))
-    shape.eps, shape.w_offset = eps, w_offset
+    shape, code, stride, index = _check(rope, positions, live, (w_q, w_k), eps, w_offset)
     dq, dk = _like(dq_out), _like(dk_out)
     dw = [torch.empty_like(w) if w is not None and ask else None for w, ask in zip((w_q, w_k), want)]
     L, ws, size = _nq.lib(), None, 0
     if dw[0] is not None or dw[1] is not None:
-        size = _size(L.nf4_rotary_backward_workspace_size(ctypes.byref(shape)), "nf4_rotary_backward_workspace_size")
+        size = _size(L.nf4_rotary_backward_workspace_size(shape), "nf4_rotary_backward_workspace_size")
         ws = torch.empty(size, dtype=torch.uint8, device=rope.turns.device)
-    st = L.nf4_rotary_backward(ctypes.byref(shape), rope.turns.data_ptr(), _addr(positions), code, stride, _heads(dq_out),
+    st = L.nf4_rotary_backward(shape, rope.turns.data_ptr(), _addr(positions), code, stride, _heads(dq_out),
                                _heads(dk_out), _heads(live[1][0]), _heads(live[1][1]), _addr(w_q), _addr(w_k), _heads(dq),
                                _heads(dk), _addr(dw[0]), _addr(dw[1]), _addr(ws), size, _stream(index))
     _nq._check(st, "nf4_rotary_backward")

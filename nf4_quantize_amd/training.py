@@ -94,7 +94,8 @@ def _torch(name):
     if not _TORCH:
         import torch
 
-        _TORCH.update(stream=torch._C._cuda_getCurrentRawStream, changed=torch.autograd.graph.increment_version)
+        _TORCH.update(stream=torch._C._cuda_getCurrentRawStream, changed=torch.autograd.graph.increment_version,
+                      empty_like=torch.empty_like, int64=torch.int64, int32=torch.int32)
     return _TORCH[name]
 
 
@@ -494,11 +495,9 @@ def residual_norm_backward(dx, dh_out, y, h_out, rstd_pre, w_pre, rstd_post=None
 # ------------------------------------------------------------------ token embedding
 
 def _index_code(ids):
-    import torch
-
-    if ids.dtype == torch.int64:
+    if ids.dtype == _torch("int64"):
         return 1
-    if ids.dtype == torch.int32:
+    if ids.dtype == _torch("int32"):
         return 0
     raise TypeError(f"token numbers are int32 or int64, got {ids.dtype}")
 

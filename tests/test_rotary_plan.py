@@ -82,11 +82,20 @@ BAD_SHAPES = ((dict(batch=-1), SIZE), (dict(tokens=-1), SIZE), (dict(batch=1 << 
 def view(**c):
     f = dict(data=FAKE, batch_stride=768, token_stride=256, head_stride=64)
     f.update(c)
-    return heads.nf4_heads(**f)
+    return ctypes.byref(heads.nf4_heads(**f))
 
 
 BAD_VIEWS = ((None, NULL), (view(data=None), NULL), (view(data=FAKE + 1), ALIGN), (view(batch_stride=-1), SIZE),
              (view(token_stride=-1), SIZE), (view(head_stride=-1), SIZE), (view(head_stride=(1 << 40) + 1), SIZE))
+
+
+def test_structures():
+    """The bytes that the binding packs are the structures'."""
+    assert heads._SHAPE.size == ctypes.sizeof(heads.nf4_rotary_shape) == 56
+    assert heads._HEADS.size == ctypes.sizeof(heads.nf4_heads) == 32
+    fields = [(n, getattr(heads.nf4_rotary_shape, n).offset) for n, _ in heads.nf4_rotary_shape._fields_]
+    s = heads.nf4_rotary_shape.from_buffer_copy(heads._SHAPE.pack(*range(1, 10), 10.0, 11.0, 12.0))
+    assert [float(getattr(s, n)) for n, _ in fields] == [float(i) for i in range(1, 13)]
 
 
 def test_forward_refusals():
