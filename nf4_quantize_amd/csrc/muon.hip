@@ -341,7 +341,6 @@ __device__ __forceinline__ void update_of(const Item &e, const Raw<G, M, N> &r, 
 // mm, hl, lh leave 2^-26 of |x| |y|. That is 6 instructions of 16 cycles for 32 rows of
 // a 16 x 16 tile, 96 cycles; the fp32 instruction takes 8 of 32, 256 cycles. bf16 numbers
 // (kParts 1) take one.
-typedef short bf16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 bf16_operand;
 
 template <int kParts> struct Operand {
@@ -501,9 +500,7 @@ __device__ __forceinline__ void pair_of(int pair, int &bi, int &bj) {
 template <typename G, typename M, bool kLarge>
 __global__ __launch_bounds__(kThreads, 2) void muon_gram_kernel(List list, Scalars c, Space ws) {
     __shared__ double part[kLarge ? 16 : 10][256];
-    // the pairs of blocks of the same rows run on one XCD and share its L2
-    const uint32_t xcd = blockIdx.x % 8, each = gridDim.x / 8;
-    const uint32_t wg = kLarge ? xcd * each + min(xcd, gridDim.x % 8) + blockIdx.x / 8 : blockIdx.x;
+    const uint32_t wg = blockIdx.x;
     const Item e = list.item[find(list.gram_first, list.count, wg)];
     if ((e.side > kSmall) != kLarge) return;
     const uint32_t own = wg - e.gram_first, chunk = own / e.gram_pairs, pair = own % e.gram_pairs;
@@ -1191,11 +1188,13 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(List list, Scal
     const uint32_t wg = gridDim.x - 1 - blockIdx.x;  // the first pass's last reads may still be cached
     const int32_t index = find(list.apply_first, list.count, wg);
     const Item e = list.item[index];
-    if (e.side > kSmall || !takes<W>(e, c) || (c.step && !isfinite(ws.norm[index]))) return;
+    if (e.side > kSmall || !takes<W>(e, c)) return;
+    const double norm = ws.norm[index];  // asked for with P, and looked at after it
     const int begin = (wg - e.apply_first) * e.apply_chunk, end = min(begin + (int)e.apply_chunk, e.length);
     const u32x4 *p = reinterpret_cast<const u32x4 *>(ws.p + (int64_t)e.p * 512);
     for (int i = threadIdx.x; i < p_elements(e.side) / 8; i += kThreads) sp[i] = p[i];
     __syncthreads();
+    if (c.step && !isfinite(norm)) return;
     if (e.tall) {
         if (e.side <= 32) apply_tall<G, M, W, 1>(e, c, sp, begin, end);
         else apply_tall<G, M, W, 2>(e, c, sp, begin, end);
@@ -1313,8 +1312,9 @@ __global__ __launch_bounds__(kLargeThreads) void muon_apply_large_kernel(List li
 // The steps that run in fp64. An error of A_k grows 11.9 times a step in what is far below
 // the largest: fp32's 2^-24 in A_1 ends as up to 1e-4 of O, a twentieth of a bf16 output's
 // half step; in A_2 as up to 8e-6, 8e-8 of a weight that steps by a hundredth of itself.
-// What is orthogonalised for itself in fp32 stays in fp64: 64 matrices of 4096 x 64 take
-// @@ us instead of @@ with two steps.
+// What is orthogonalised for itself in fp32 stays in fp64: the iteration of 64 matrices of
+// 4096 x 64 takes 46 us instead of 34 with two steps, and errors are 0.4 of a plain fp32
+// iteration's instead of 1.1.
 int exact_steps(const MuonCall &call, bool masters) {
     const int most = !call.step && call.w == NF4_F32 ? call.iterations : call.w == NF4_F32 || masters ? 2 : 1;
     return most < call.iterations ? most : call.iterations;
@@ -1331,7 +1331,8 @@ struct Plan {
     int32_t largest, smallest;   // of their shorter sides
     bool fits;
 };
-constexpr int64_t kMinRows = 256;  // of a share of the first pass: 64 a wave
+// Rows of a share: in the first pass 64 a wave at least.
+constexpr int64_t kMinRows = 256, kMostRows = int64_t(1) << 29;
 
 Plan make_plan(const MuonMatrix *list, int32_t count) {
     Plan p{};
@@ -1351,8 +1352,8 @@ Plan make_plan(const MuonMatrix *list, int32_t count) {
     // Shares of each pass: 448 matrices of rank 64 take 842 us a step with 2048 shares of the
     // first one, 850 with 1024, 14 of rank 256 337 and 328 (more partial sums to add up).
     const int64_t shares = p.largest > kSmall ? 1024 : 2048;
-    const int64_t gram_chunk = round_up(std::max(gram_rows / shares, kMinRows), 64);
-    const int64_t apply_chunk = round_up(std::max<int64_t>(apply_rows / 2048, 64), 64);
+    const int64_t gram_chunk = round_up(std::clamp(gram_rows / shares, kMinRows, kMostRows), 64);
+    const int64_t apply_chunk = round_up(std::clamp<int64_t>(apply_rows / 2048, 64, kMostRows), 64);
     p.gram_chunk = (uint32_t)gram_chunk, p.apply_chunk = (uint32_t)apply_chunk;
     p.items = 0;
     p.gram_first = round_up(p.items + (size_t)p.count * sizeof(Item), 16);

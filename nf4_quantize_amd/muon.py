@@ -4,6 +4,7 @@ are in ``include/nf4.h`` (nf4_muon_step, nf4_orthogonalize); every step of the
 computation runs in the library's HIP kernels, torch supplies device memory and the
 current stream.
 """
+import array
 import ctypes
 import math
 
@@ -132,7 +133,7 @@ class NF4Muon(ListOptimizer):
         """One step with the parameters' ``.grad``, or with ``grads`` (a tensor for each
         parameter, all bfloat16 or all float32)."""
         grad_dtype, device = self._take_grads(grads, self._shapes)
-        if list(map(_shape_of, self._params)) != self._shapes:
+        if [p.shape for p in self._params] != self._shapes:
             self._bind()  # refuses
         config = nf4_muon_config(self.momentum, self.eps, *self.coefficients, self.nesterov, self.iterations)
         _nq._check(_nq.lib().nf4_muon_step(self._at, len(self._params), _code(self.dtype), grad_dtype, self._state_code,
@@ -153,10 +154,6 @@ class NF4Muon(ListOptimizer):
         self.steps = int(d["steps"])
 
 
-def _shape_of(t):
-    return t.shape
-
-
 def orthogonalize(updates, coefficients=COEFFICIENTS, iterations=5, eps=1e-7, outs=None, workspace=None):
     """Each matrix of the list over its norm (at least ``eps``), and ``iterations`` times
     X <- a X + b (X X^T) X + c (X X^T)^2 X (nf4_orthogonalize): its singular values
@@ -172,19 +169,23 @@ def orthogonalize(updates, coefficients=COEFFICIENTS, iterations=5, eps=1e-7, ou
     outs = list(outs) if given else [torch.empty_like(u, memory_format=torch.contiguous_format) for u in updates]
     if len(outs) != len(updates):
         raise ValueError(f"{len(outs)} outputs for {len(updates)} updates")
-    index, dt = _check_tensors(updates[0], *updates[1:], *outs, workspace), updates[0].dtype
-    code = _code(dt)
+    # the methods over the lists, as in an optimizer's step
+    T, every, dt = torch.Tensor, updates + outs, updates[0].dtype
+    code, shapes = _code(dt), [u.shape for u in updates]
+    if len(set(map(T.get_device, every))) != 1 or not all(map(T.is_contiguous, every)):
+        _check_tensors(*every)  # says what is wrong
+    index = _check_tensors(updates[0], workspace)
+    for shape in set(shapes):
+        _check_matrix(shape)
+    if {t.dtype for t in every} != {dt} or (given and [o.shape for o in outs] != shapes):
+        raise ValueError("updates and outputs have one dtype, and each pair one shape")
     e = np.zeros(len(updates), _ENTRY)
-    for u, o in zip(updates, outs):
-        _check_matrix(u.shape)
-        if u.dtype != dt or o.dtype != dt or o.shape != u.shape:
-            raise ValueError("updates and outputs have one dtype, and each pair one shape")
+    e["rows"], e["cols"] = zip(*shapes)
+    e["grad"], e["w"] = array.array("Q", map(T.data_ptr, updates)), array.array("Q", map(T.data_ptr, outs))
     if given:
         # an update that is not its own output must not be one; the same update may be there twice
         read = {(u.data_ptr(), u.nbytes): u for u, o in zip(updates, outs) if u.data_ptr() != o.data_ptr()}
         _check_apart(outs + list(read.values()))
-    e["rows"], e["cols"] = zip(*[u.shape for u in updates])
-    e["grad"], e["w"] = [u.data_ptr() for u in updates], [o.data_ptr() for o in outs]
     L = _nq.lib()
     if workspace is None:
         size = _size(L.nf4_muon_workspace_size(e.ctypes.data, len(e)), "nf4_muon_workspace_size")
