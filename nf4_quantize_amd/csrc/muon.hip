@@ -1081,11 +1081,12 @@ __device__ __forceinline__ f32x4 mfma_p(const Operand<3> &p, const Operand<kPart
 }
 
 // A matrix of up to 64 on its shorter side, P in LDS. In a tall matrix a wave takes 16
-// rows, a lane columns 32 s + 8 k .. + 7 of row n, of U and of O; in a wide one 16 kWideCols
-// columns, a lane kWideCols of them (from kWideCols n on) in rows 32 s + 8 k .. + 7. All of
+// rows, a lane columns 32 s + 8 k .. + 7 of row n, of U and of O; in a wide one 16 V
+// columns, a lane V of them (from V n on) in rows 32 s + 8 k .. + 7. All of
 // a turn's loads are issued before its first product. The barriers to the scheduler keep
 // the operands of P from being read all at once, which spills.
-constexpr int kWideCols = 4;
+template <typename W>
+constexpr int kWideCols = sizeof(W) == 4 ? 2 : 4;  // fp32 weights in fours spill: 323 us instead of 201
 
 template <typename G, typename M, typename W, int kBlocks>
 __device__ __forceinline__ void apply_tall(const Item &e, const Scalars &c, const u32x4 *p, int begin, int end) {
@@ -1127,7 +1128,7 @@ __device__ __forceinline__ void apply_tall(const Item &e, const Scalars &c, cons
 
 template <typename G, typename M, typename W, int kBlocks>
 __device__ __forceinline__ void apply_wide(const Item &e, const Scalars &c, const u32x4 *p, int begin, int end) {
-    constexpr int kParts = kPartsOf<G, M>, V = kWideCols;
+    constexpr int kParts = kPartsOf<G, M>, V = kWideCols<W>;
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, n = lane % 16, k = lane / 16;
     for (int col = begin + wave * 16 * V; col < end; col += 16 * V * kWaves) {
         const int l = col + V * n;
