@@ -8,8 +8,12 @@
 // S and once for the product with P, and the iteration runs on s x s matrices.
 // What S has to hold: an eigenvalue far below the largest grows by a^2 = 11.9 a step, and
 // so does its error, 2 10^4 times over the first four of five steps. S is therefore summed
-// in fp32 over 32 rows and in fp64 beyond, and the s x s products run on the fp64 matrix
-// instruction; the two passes over the long matrices split fp32 into bf16 parts.
+// in fp32 over 32 rows and in fp64 beyond, and the first of the s x s products run on the
+// fp64 matrix instruction (exact_steps says how many); the others, and the two passes over
+// the long matrices, split fp32 into bf16 parts.
+// 448 adapters of rank 64 (1.7e8 elements, bf16 with an fp32 momentum): 833 us a step. 20
+// bytes an element move, 516 us at the rate of a copy: the passes take 241 and 500 us, the
+// iteration 56. Lists whose bytes do not count are a chain of four launches, 25 us.
 #include <math.h>
 
 #include <algorithm>
@@ -23,7 +27,7 @@ namespace {
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256, kWaves = 4;
-constexpr int kSmall = 64;     // shorter sides up to here are iterated in one workgroup's LDS
+constexpr int kSmall = 64;     // shorter sides up to here are iterated by one workgroup
 
 // One matrix. `tall`: the longer side's index is the slow one (rows >= cols).
 struct Item {
@@ -105,7 +109,8 @@ __host__ __device__ inline Item item_of(int32_t rows, int32_t cols, uint32_t gra
 }
 
 // The list into the workspace, from entry `done` on; with the last batch, where each
-// matrix's shares begin.
+// matrix's shares begin, in a scan here: so 48 bytes an entry travel from the host. 1.6 us a
+// launch, 4.6 for the last one of 448 entries.
 __global__ __launch_bounds__(kThreads) void muon_table_kernel(Batch b, int32_t used, int32_t done, int32_t count,
                                                               uint32_t gram_chunk, uint32_t apply_chunk, Item *items,
                                                               uint32_t *gram_first, uint32_t *apply_first) {
@@ -497,6 +502,11 @@ __device__ __forceinline__ void pair_of(int pair, int &bi, int &bj) {
     bi = pair - bj * (bj + 1) / 2;
 }
 
+// A workgroup takes a share of one matrix's longer side and, above 64 columns, one pair of
+// blocks of 64 (of the upper triangle). Two workgroups a CU: with three the sums of ten
+// tiles spill. 448 adapters of rank 64: 241 us for 6 bytes an element, 4.2 TB/s; loads and
+// the making of operands take turns in a wave, and eight waves a CU do not hide all of it.
+// 14 bf16 matrices of rank 256, whose columns four workgroups read: 53 us.
 template <typename G, typename M, bool kLarge>
 __global__ __launch_bounds__(kThreads, 2) void muon_gram_kernel(List list, Scalars c, Space ws) {
     __shared__ double part[kLarge ? 16 : 10][256];
@@ -775,6 +785,9 @@ __device__ __forceinline__ void iterate(const Item &e, const Scalars &c, double 
         }
 }
 
+// The sums of a matrix's shares, its norm, and all its steps: a chain of dependent products in
+// one workgroup, bound by the latency of matrix instructions and LDS. 7.8 us for two matrices
+// of side 16, 56 us for 448 of side 64, two a CU.
 __global__ __launch_bounds__(kThreads, 2) void muon_small_kernel(List list, Scalars c, Space ws) {
     extern __shared__ double smem[];
     SmallMat &A = *reinterpret_cast<SmallMat *>(smem);
@@ -825,7 +838,8 @@ __device__ __forceinline__ double *mat_of(const Item &e, const Space &ws, int wh
 }
 
 // S, 64 x 64 of it by kStartParts workgroups, and its trace by one workgroup more. The
-// products of the first step bring S over the norm's square.
+// products of the first step bring S over the norm's square. Bound by the loads of partial
+// sums: 14 us for 14 matrices of side 256.
 constexpr int kStartParts = 4;
 __global__ __launch_bounds__(kThreads) void muon_start_kernel(List list, Scalars c, Space ws) {
     __shared__ double part[kWaves];
@@ -869,9 +883,14 @@ __global__ __launch_bounds__(kThreads) void muon_start_kernel(List list, Scalars
     }
 }
 
-// out = x y, with q: c out + b x + a I (x = y); with fin: over the norm, in parts, to P. blockIdx.z chooses one of two products. All matrices are
-// polynomials of one, so x y is symmetric: a workgroup takes 32 x 32 of the upper
-// triangle, writes both halves, and reads a column of y as its row.
+// out = x y, with q: c out + b x + a I (x = y); with fin: over the norm, in parts, to P.
+// blockIdx.z chooses one of two products. All matrices are polynomials of one, so x y is
+// symmetric: a workgroup takes 32 x 32 of the upper triangle, writes both halves, and reads
+// a column of y as its row.
+// 14 matrices of side 256 take 13.9 us a launch, and 13.4 in the fp32 parts below, which are
+// a fifth of the matrix instructions' time: a launch's length is that of its chain, from the
+// last one's stores through the memory-side cache to its loads, its products and its stores.
+// With all workgroups of a matrix on one XCD it is 15 us.
 struct Product {
     int32_t x, y, out;
     bool q, fin, narrow;  // narrow: out is fp32
@@ -1082,9 +1101,13 @@ __device__ __forceinline__ f32x4 mfma_p(const Operand<3> &p, const Operand<kPart
 
 // A matrix of up to 64 on its shorter side, P in LDS. In a tall matrix a wave takes 16
 // rows, a lane columns 32 s + 8 k .. + 7 of row n, of U and of O; in a wide one 16 V
-// columns, a lane V of them (from V n on) in rows 32 s + 8 k .. + 7. All of
-// a turn's loads are issued before its first product. The barriers to the scheduler keep
-// the operands of P from being read all at once, which spills.
+// columns, a lane V of them (from V n on) in rows 32 s + 8 k .. + 7. A turn's loads are all
+// issued before its first product. The barriers to the scheduler keep the operands of P from
+// being read all at once, which spills.
+// Bound by memory: 500 us for the 14 bytes an element of 448 adapters of rank 64, 490 without
+// any product. Wide matrices take 450, tall ones 555, whose instructions touch twice as many
+// lines (two fours a lane instead of an eight: 750). Loads of the next turn ahead of the products
+// change nothing.
 template <typename W>
 constexpr int kWideCols = sizeof(W) == 4 ? 2 : 4;  // fp32 weights in fours spill: 323 us instead of 201
 
@@ -1208,7 +1231,9 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(List list, Scal
 // A matrix of up to 256 on its shorter side, 64 places of the longer at a time: the
 // parts of U in LDS, read whole before anything is written; P from the caches; a wave
 // takes pairs of results, eight columns of O a lane as above. Place of lane n in
-// operand j: 16 j + n in a tall matrix, 4 n + j in a wide one.
+// operand j: 16 j + n in a tall matrix, 4 n + j in a wide one. The matrix instruction is busy
+// for a quarter of the time, loads and barriers take the rest: 53 us for 14 bf16 matrices of
+// rank 256 alone, 84 MB.
 constexpr int kLargeThreads = 512, kLargeWaves = kLargeThreads / 64;
 
 template <typename G, typename M, typename W>

@@ -6,6 +6,9 @@
 // the backward pass of a norm reads the input as well (6 bytes). A head lies in a
 // group of lanes, 2 V elements a lane: two vectors of V elements whose pairs are the
 // lane's own, so a rotation needs no other lane and a norm one sum over the group.
+// bf16 heads of 128: 16384 tokens of 40 take 50 us (6.7 TB/s, past the caches), 4096 of 72
+// with norms 26 us (5.7 TB/s), their gradients 49 us (4.6 TB/s) and 5 for the weights' sums.
+// One token takes 3 us, a launch and two loads one after the other.
 #include <math.h>
 
 #include <algorithm>
@@ -132,7 +135,10 @@ constexpr int kMaxDim = 512, kMaxPairs = kMaxDim / 2;
 // A wave takes a token and every splits-th round of its heads: 64 / lanes heads a
 // round, queries first. The next round's loads are in flight while it works on one. Its
 // lanes share the token's cosines and sines through LDS, a pair a lane (with each lane
-// computing those of its own pairs, eight lanes do the same work). U units a lane.
+// computing those of its own pairs, eight lanes do the same work). That and the loads ahead
+// took 16384 tokens of 40 heads from 72 to 60 us, stores past the caches to 50. U units a lane.
+// The gradient of a norm holds three values and the sums of an element: 16 waves a CU, not
+// enough to keep the loads of a whole round ahead for all of them, hence 4.6 TB/s.
 template <typename T, int V, int U, RotaryKind kKind, bool kPast = false>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p) {
     constexpr bool kBack = kKind == kNormTurnBack, kNorm = kKind != kTurn;
@@ -354,7 +360,8 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryParams p) {
 }
 
 // The weights' gradients: columns of the workgroups' partial sums, 16 columns a
-// workgroup and 64 rows at a time, eight of a thread's loads in flight.
+// workgroup and 64 rows at a time, eight of a thread's loads in flight: 4.7 us for 1024 rows,
+// all of it latency.
 constexpr int kSumRows = 64;
 __global__ __launch_bounds__(16 * kSumRows) void rotary_sums_kernel(const float *partial, int32_t rows, int32_t dim, bool bf16,
                                                                    void *dw_q, void *dw_k) {

@@ -76,7 +76,9 @@ class NF4Muon(ListOptimizer):
     writes at these tensors' addresses, so ``bind_state`` replaces them, and a step
     refuses lists whose tensors are others (a parameter's ``data`` may change, its
     shape may not). A matrix whose update's norm is not finite, or 2^60 and more, keeps
-    its weight and momentum."""
+    its weight and momentum. A step that is captured into a graph keeps the rates and
+    addresses of its capture, gradients' ones too; steps of one optimizer, replays among
+    them, run one after another."""
 
     m = _taken("m")
 
