@@ -503,10 +503,11 @@ __device__ __forceinline__ void pair_of(int pair, int &bi, int &bj) {
 }
 
 // A workgroup takes a share of one matrix's longer side and, above 64 columns, one pair of
-// blocks of 64 (of the upper triangle). Two workgroups a CU: with three the sums of ten
+// blocks of 64 (of the upper triangle; a block with itself is read once and has ten tiles, not
+// sixteen: 112 matrices of rank 128 with a momentum 297 us instead of 403). Two workgroups a CU: with three the sums of ten
 // tiles spill. 448 adapters of rank 64: 241 us for 6 bytes an element, 4.2 TB/s; loads and
 // the making of operands take turns in a wave, and eight waves a CU do not hide all of it.
-// 14 bf16 matrices of rank 256, whose columns four workgroups read: 53 us.
+// 14 bf16 matrices of rank 256, whose columns four workgroups read: 50 us.
 template <typename G, typename M, bool kLarge>
 __global__ __launch_bounds__(kThreads, 2) void muon_gram_kernel(List list, Scalars c, Space ws) {
     __shared__ double part[kLarge ? 16 : 10][256];
@@ -519,7 +520,8 @@ __global__ __launch_bounds__(kThreads, 2) void muon_gram_kernel(List list, Scala
     if constexpr (kLarge) {
         int bi, bj;
         pair_of(pair, bi, bj);
-        gram_part<G, M, 4, 4, false>(e, c, bi, bj, begin, end, out, part);
+        if (bi == bj) gram_part<G, M, 4, 4, true>(e, c, bi, bj, begin, end, out, part);
+        else gram_part<G, M, 4, 4, false>(e, c, bi, bj, begin, end, out, part);
     } else {
         if (e.side <= 16) gram_part<G, M, 1, 1, true>(e, c, 0, 0, begin, end, out, part);
         else if (e.side <= 32) gram_part<G, M, 2, 2, true>(e, c, 0, 0, begin, end, out, part);
@@ -527,8 +529,9 @@ __global__ __launch_bounds__(kThreads, 2) void muon_gram_kernel(List list, Scala
     }
 }
 
-// Where sum i of a pair of blocks lies in it; false for the half of a tile on the diagonal
-// that its other half has too (rounded otherwise: one of the two is taken).
+// Where sum i of a pair of blocks lies in it; in a block with itself (diag) false for the half
+// of a tile on the diagonal that its other half has too (rounded otherwise: one of the two is
+// taken).
 __device__ __forceinline__ bool place_of(const Item &e, bool precise, int width, bool diag, int i, int &row, int &col) {
     int t = i / 256;
     const int reg = i / 64 % 4, lane = i % 64;
@@ -544,7 +547,7 @@ __device__ __forceinline__ bool place_of(const Item &e, bool precise, int width,
     const int r = precise ? 4 * reg + lane / 16 : 4 * (lane / 16) + reg, n = lane % 16;
     row = e.tall ? width * r + ti : 16 * ti + r;
     col = e.tall ? width * n + tj : 16 * tj + n;
-    return ti != tj || r <= n;
+    return !diag || ti != tj || r <= n;
 }
 
 // N sums of `count` partial sums each, `stride` apart, in their order: N times kAhead loads
@@ -854,10 +857,10 @@ __global__ __launch_bounds__(kThreads) void muon_start_kernel(List list, Scalars
         double diagonal[1] = {0.0};
         if ((int)threadIdx.x < e.side) {
             const int b = threadIdx.x / 64, d = threadIdx.x % 64, pair = b * (b + 1) / 2 + b;
-            // its tile, row and column: (4 r + i) in a tall matrix, (16 i + r) in a wide one
+            // its row and column in tile (i, i): (4 r + i) in a tall matrix, (16 i + r) in a wide one
             const int i = e.tall ? d % 4 : d / 16, r = e.tall ? d / 4 : d % 16;
             const int reg = c.precise ? r / 4 : r % 4, group = c.precise ? r % 4 : r / 4;
-            const int at[1] = {((pair * 16) + i * 4 + i) * 256 + reg * 64 + group * 16 + r};
+            const int at[1] = {((pair * 16) + i * (9 - i) / 2) * 256 + reg * 64 + group * 16 + r};
             chunk_totals<1, 16>(from, at, stride, e.gram_chunks, diagonal);
         }
         const double trace = block_total(diagonal[0], part);
@@ -875,11 +878,12 @@ __global__ __launch_bounds__(kThreads) void muon_start_kernel(List list, Scalars
     chunk_totals<kEach, 8>(from, at, stride, e.gram_chunks, sum);
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
+        const int i = at[j] - (int)blockIdx.y * 16 * 256;
+        if (bi == bj && i >= 10 * 256) break;  // a block with itself has ten tiles
         int row, col;
-        place_of(e, c.precise, 4, false, at[j] - (int)blockIdx.y * 16 * 256, row, col);
+        if (!place_of(e, c.precise, 4, bi == bj, i, row, col)) continue;
         row += 64 * bi, col += 64 * bj;
-        // a block with itself holds both of each pair: the upper one is taken
-        if (bi != bj || row <= col) A[(int64_t)row * edge + col] = sum[j], A[(int64_t)col * edge + row] = sum[j];
+        A[(int64_t)row * edge + col] = sum[j], A[(int64_t)col * edge + row] = sum[j];
     }
 }
 
@@ -1232,12 +1236,14 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(List list, Scal
 // parts of U in LDS, read whole before anything is written; P from the caches; a wave
 // takes pairs of results, eight columns of O a lane as above. Place of lane n in
 // operand j: 16 j + n in a tall matrix, 4 n + j in a wide one. The matrix instruction is busy
-// for a quarter of the time, loads and barriers take the rest: 53 us for 14 bf16 matrices of
-// rank 256 alone, 84 MB.
+// for a quarter of the time, loads and barriers take the rest: 54 us for 14 bf16 matrices of
+// rank 256 alone, 84 MB. With a momentum, 112 matrices of rank 128: 380 us, with the 155
+// registers that it takes unasked, and so one workgroup a CU, 509; of rank 256 976 and 1037.
+// Two places of 16 a wave, so that with 128 columns none is idle: 391.
 constexpr int kLargeThreads = 512, kLargeWaves = kLargeThreads / 64;
 
 template <typename G, typename M, typename W>
-__global__ __launch_bounds__(kLargeThreads) void muon_apply_large_kernel(List list, Scalars c, Space ws) {
+__global__ __launch_bounds__(kLargeThreads, 4) void muon_apply_large_kernel(List list, Scalars c, Space ws) {
     extern __shared__ u32x4 us[];  // [part][place's operand j][operand s][lane]
     constexpr int kParts = kPartsOf<G, M>;
     const uint32_t wg = gridDim.x - 1 - blockIdx.x;
